@@ -1,4 +1,5 @@
-"""ctypes view of the C ABI in include/spec_verify.h (libspecverify.so, built in-tree).
+"""ctypes view of the C ABI in include/spec_verify.h and include/spec_attend.h (libspecverify.so,
+built in-tree).
 
 There is no fallback: if the library is missing or fails to load, importing this module
 raises, and nothing in the package computes any part of the verifier on the CPU.
@@ -12,6 +13,7 @@ from .build import LIB_PATH
 
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
@@ -64,11 +66,37 @@ class SpecCompactArgs(ctypes.Structure):
     ]
 
 
+class SpecKvAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", _i32), ("total_rows", _i32), ("n_q_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+        ("rot_dim", _i32), ("interleaved", _i32), ("page_size", _i32), ("max_blocks", _i32), ("n_pages", _i32),
+        ("n_pos", _i32), ("dtype", ctypes.c_int),
+        ("q", _p), ("k", _p), ("v", _p), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+        ("q_out", _p), ("q_out_stride", _i64), ("cos_sin", _p), ("k_cache", _p), ("v_cache", _p),
+        ("page_stride", _i64), ("slot_stride", _i64), ("head_stride", _i64),
+        ("row_off", _p), ("kv_len", _p), ("block_table", _p), ("req_status", _p),
+    ]
+
+
+class SpecAttendArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", _i32), ("total_rows", _i32), ("n_q_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+        ("page_size", _i32), ("max_blocks", _i32), ("n_pages", _i32), ("window", _i32), ("n_sink", _i32),
+        ("shared_len", _i32), ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
+        ("q", _p), ("q_stride", _i64), ("k_cache", _p), ("v_cache", _p),
+        ("page_stride", _i64), ("slot_stride", _i64), ("head_stride", _i64),
+        ("row_off", _p), ("kv_len", _p), ("block_table", _p), ("shared_table", _p),
+        ("out", _p), ("out_stride", _i64), ("lse", _p), ("req_status", _p),
+    ]
+
+
 # every symbol include/spec_verify.h declares
 EXPORTS = ("spec_verify_workspace_size", "spec_verify", "spec_verify_noalloc", "spec_verify_plan",
            "spec_verify_round", "spec_compact",
            "spec_gamma_objective", "spec_choose_gamma", "spec_choose_gamma_depth", "spec_depth_objective",
            "spec_version")
+# every symbol include/spec_attend.h declares
+ATTEND_EXPORTS = ("spec_kv_append", "spec_attend_workspace_size", "spec_attend", "spec_attend_plan")
 
 
 def load_library(path: str):
@@ -103,6 +131,14 @@ def load_library(path: str):
     lib.spec_depth_objective.restype = ctypes.c_double
     lib.spec_version.argtypes = []
     lib.spec_version.restype = ctypes.c_char_p
+    lib.spec_kv_append.argtypes = [ctypes.POINTER(SpecKvAppendArgs), _p]
+    lib.spec_kv_append.restype = ctypes.c_int
+    lib.spec_attend_workspace_size.argtypes = [ctypes.POINTER(SpecAttendArgs)]
+    lib.spec_attend_workspace_size.restype = ctypes.c_size_t
+    lib.spec_attend.argtypes = [ctypes.POINTER(SpecAttendArgs), _p, ctypes.c_size_t, _p]
+    lib.spec_attend.restype = ctypes.c_int
+    lib.spec_attend_plan.argtypes = [ctypes.POINTER(SpecAttendArgs)]
+    lib.spec_attend_plan.restype = ctypes.c_char_p
     if hasattr(lib, "spec_debug_fetch"):  # the debug build (include/spec_debug.h)
         lib.spec_debug_fetch.argtypes = [_p]
         lib.spec_debug_fetch.restype = ctypes.c_int

@@ -12,7 +12,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import SpecCompactArgs, SpecVerifyArgs, check, lib
+from ._lib import SpecAttendArgs, SpecCompactArgs, SpecKvAppendArgs, SpecVerifyArgs, check, lib
 
 _DTYPE = {torch.float32: _lib.SPEC_F32, torch.bfloat16: _lib.SPEC_BF16}
 
@@ -288,6 +288,160 @@ def depth_objective(n_reached, n_accepted, alpha_prev: float, c: float, gamma: i
     assert nr.shape == na.shape
     return float(lib.spec_depth_objective(nr.ctypes.data_as(ctypes.c_void_p), na.ctypes.data_as(ctypes.c_void_p),
                                           int(nr.size), float(alpha_prev), float(c), int(gamma)))
+
+
+def _rows_of(t, T: int, heads: int, D: int, dtype):
+    """Pointer and row stride (elements) of [T][heads][D] rows whose heads are contiguous."""
+    assert t.dtype == dtype and t.is_cuda and t.shape == (T, heads, D), (t.dtype, t.shape, (T, heads, D))
+    assert (D == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == D), "a row's heads must be contiguous"
+    return _ptr(t), (t.stride(0) if T > 1 else heads * D)
+
+
+def _bind_cache(a, k_cache, v_cache, Hkv: int, D: int, dtype):
+    """The paged cache as [n_pages, page_size, Hkv, D] tensors of any strides (elements of a head
+    contiguous), the same for keys and values."""
+    assert k_cache.dtype == dtype and v_cache.dtype == dtype and k_cache.is_cuda and v_cache.is_cuda
+    assert k_cache.dim() == 4 and k_cache.shape[2:] == (Hkv, D), (k_cache.shape, (Hkv, D))
+    assert k_cache.shape == v_cache.shape and k_cache.stride() == v_cache.stride(), "keys and values alike"
+    assert D == 1 or k_cache.stride(3) == 1
+    a.n_pages, a.page_size = int(k_cache.shape[0]), int(k_cache.shape[1])
+    a.page_stride, a.slot_stride, a.head_stride = k_cache.stride()[:3]
+    a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+
+
+def _bind_requests(a, B: int, row_off, kv_len, block_table):
+    assert _i32(row_off).shape == (B + 1,) and _i32(kv_len).shape == (B,)
+    assert _i32(block_table).dim() == 2 and block_table.shape[0] == B
+    a.row_off, a.kv_len, a.block_table = _ptr(row_off), _ptr(kv_len), _ptr(block_table)
+    a.max_blocks = int(block_table.shape[1])
+
+
+@dataclass
+class AppendOutputs:
+    q: torch.Tensor           # [T, Hq, D] rotated queries
+    req_status: torch.Tensor
+
+
+class KvAppender:
+    """A prepared spec_kv_append call for one batch shape: a round's keys (rotated) and values go to
+    the paged cache, its queries (rotated) to ``out.q``. rot_dim None rotates whole heads."""
+
+    def __init__(self, B: int, total_rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype, *,
+                 rot_dim: int | None = None, interleaved: bool = False, device=None):
+        device = torch.device(device or "cuda")
+        self.B, self.T, self.Hq, self.Hkv, self.D, self.dtype = B, total_rows, Hq, Hkv, D, dtype
+        self.out = AppendOutputs(q=torch.empty(total_rows, Hq, D, dtype=dtype, device=device),
+                                 req_status=torch.empty(B, dtype=torch.int32, device=device))
+        self.args = SpecKvAppendArgs()
+        a = self.args
+        a.B, a.total_rows, a.n_q_heads, a.n_kv_heads, a.head_dim = B, total_rows, Hq, Hkv, D
+        a.rot_dim, a.interleaved, a.dtype = D if rot_dim is None else rot_dim, int(interleaved), _DTYPE[dtype]
+        a.req_status = _ptr(self.out.req_status)
+        self._keep = ()
+
+    def bind(self, q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, *, q_out=None):
+        """q [T, Hq, D], k and v [T, Hkv, D] (slices of one projection are fine), cos_sin
+        [n_pos, rot_dim] float32 (cosines, then sines), k_cache and v_cache [n_pages, page_size, Hkv,
+        D], block_table [B, max_blocks]. q_out may be q itself."""
+        a, T, D = self.args, self.T, self.D
+        if q_out is not None:
+            self.out.q = q_out
+        if self.Hq:
+            a.q, a.q_stride = _rows_of(q, T, self.Hq, D, self.dtype)
+            a.q_out, a.q_out_stride = _rows_of(self.out.q, T, self.Hq, D, self.dtype)
+        a.k, a.k_stride = _rows_of(k, T, self.Hkv, D, self.dtype)
+        a.v, a.v_stride = _rows_of(v, T, self.Hkv, D, self.dtype)
+        if a.rot_dim:
+            assert cos_sin.dtype == torch.float32 and cos_sin.is_cuda and cos_sin.is_contiguous()
+            assert cos_sin.dim() == 2 and cos_sin.shape[1] == a.rot_dim, (cos_sin.shape, a.rot_dim)
+            a.cos_sin, a.n_pos = _ptr(cos_sin), int(cos_sin.shape[0])
+        _bind_cache(a, k_cache, v_cache, self.Hkv, D, self.dtype)
+        _bind_requests(a, self.B, row_off, kv_len, block_table)
+        self._keep = (q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, q_out)
+        return self
+
+    def run(self, stream=None) -> AppendOutputs:
+        check(lib.spec_kv_append(ctypes.byref(self.args), _stream_handle(stream)), "spec_kv_append")
+        return self.out
+
+
+def kv_append(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, *, rot_dim: int | None = None,
+              interleaved: bool = False, q_out=None, stream=None) -> AppendOutputs:
+    """Appends a round's rows to the paged cache (see include/spec_attend.h)."""
+    T, Hkv, D = k.shape
+    c = KvAppender(row_off.numel() - 1, T, q.shape[1] if q is not None else 0, Hkv, D, k.dtype, rot_dim=rot_dim,
+                   interleaved=interleaved, device=k.device)
+    c.bind(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, q_out=q_out)
+    return c.run(stream)
+
+
+@dataclass
+class AttendOutputs:
+    out: torch.Tensor         # [T, Hq, D]
+    lse: torch.Tensor         # [T, Hq] float32, natural logarithm
+    req_status: torch.Tensor
+
+
+class Attention:
+    """A prepared spec_attend call for one batch shape: attention of the round's rows over the paged
+    cache. window 0: every earlier position; n_sink first positions stay visible behind a window;
+    the first shared_len positions of all requests lie in the pages of the shared table."""
+
+    def __init__(self, B: int, total_rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype, *, window: int = 0,
+                 n_sink: int = 0, shared_len: int = 0, scale: float | None = None, device=None):
+        self.device = torch.device(device or "cuda")
+        self.B, self.T, self.Hq, self.Hkv, self.D, self.dtype = B, total_rows, Hq, Hkv, D, dtype
+        self.out = AttendOutputs(out=torch.empty(total_rows, Hq, D, dtype=dtype, device=self.device),
+                                 lse=torch.empty(total_rows, Hq, dtype=torch.float32, device=self.device),
+                                 req_status=torch.empty(B, dtype=torch.int32, device=self.device))
+        self.args = SpecAttendArgs()
+        a = self.args
+        a.B, a.total_rows, a.n_q_heads, a.n_kv_heads, a.head_dim = B, total_rows, Hq, Hkv, D
+        a.window, a.n_sink, a.shared_len, a.dtype = window, n_sink, shared_len, _DTYPE[dtype]
+        a.scale = D ** -0.5 if scale is None else scale
+        a.lse, a.req_status = _ptr(self.out.lse), _ptr(self.out.req_status)
+        self.workspace, self.ws_bytes = None, 0
+        self._keep = ()
+
+    def bind(self, q, k_cache, v_cache, row_off, kv_len, block_table, *, shared_table=None, out=None):
+        """q [T, Hq, D], k_cache and v_cache [n_pages, page_size, Hkv, D] of any strides, block_table
+        [B, max_blocks], shared_table [ceil(shared_len / page_size)]."""
+        a = self.args
+        if out is not None:
+            self.out.out = out
+        a.q, a.q_stride = _rows_of(q, self.T, self.Hq, self.D, self.dtype)
+        a.out, a.out_stride = _rows_of(self.out.out, self.T, self.Hq, self.D, self.dtype)
+        _bind_cache(a, k_cache, v_cache, self.Hkv, self.D, self.dtype)
+        _bind_requests(a, self.B, row_off, kv_len, block_table)
+        if a.shared_len:
+            assert _i32(shared_table).numel() * a.page_size >= a.shared_len
+        a.shared_table = _ptr(shared_table)
+        self.ws_bytes = int(lib.spec_attend_workspace_size(ctypes.byref(a)))
+        if self.workspace is None or self.workspace.numel() < self.ws_bytes:
+            self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self._keep = (q, k_cache, v_cache, row_off, kv_len, block_table, shared_table, out)
+        return self
+
+    def plan(self) -> str | None:
+        """The kernel that serves the bound call, or None when its sizes are invalid."""
+        name = lib.spec_attend_plan(ctypes.byref(self.args))
+        return None if name is None else name.decode()
+
+    def run(self, stream=None) -> AttendOutputs:
+        rc = lib.spec_attend(ctypes.byref(self.args), ctypes.c_void_p(self.workspace.data_ptr()),
+                             self.workspace.numel(), _stream_handle(stream))
+        check(rc, "spec_attend")
+        return self.out
+
+
+def attend(q, k_cache, v_cache, row_off, kv_len, block_table, *, window: int = 0, n_sink: int = 0,
+           shared_len: int = 0, shared_table=None, scale: float | None = None, stream=None) -> AttendOutputs:
+    """Attention of a round's rows over the paged cache (see include/spec_attend.h)."""
+    T, Hq, D = q.shape
+    a = Attention(row_off.numel() - 1, T, Hq, k_cache.shape[2], D, q.dtype, window=window, n_sink=n_sink,
+                  shared_len=shared_len, scale=scale, device=q.device)
+    a.bind(q, k_cache, v_cache, row_off, kv_len, block_table, shared_table=shared_table)
+    return a.run(stream)
 
 
 def gamma_objective(alpha: float, c: float, gamma: int) -> float:

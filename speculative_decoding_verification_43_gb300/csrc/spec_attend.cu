@@ -1,0 +1,386 @@
+// Attention of a round's rows over the paged cache (spec_attend). See include/spec_attend.h for the
+// contract, spec_attend_plan.cuh for how the work is cut.
+//
+// out = sum_x softmax_x(s_x) v_x needs one pass over the keys: with a running maximum m, sum
+// l = sum 2^(s_x - m) and output o = sum 2^(s_x - m) v_x, a larger maximum m' rescales l and o by
+// 2^(m - m'). Parts taken over different keys join alike: with M = max m_i, out = sum o_i 2^(m_i - M) /
+// sum l_i 2^(m_i - M).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "spec_attend.h"
+#include "spec_attend_fma.cuh"
+#include "spec_attend_plan.cuh"
+#include "spec_device.cuh"
+#include "spec_paged.cuh"
+
+namespace spec {
+
+constexpr int kSMs = 152;
+
+// ---------------------------------------------------------------- joining the parts
+
+constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * kWarp, kJoinRows = 16;
+
+// Parts of one row: part x < n of a run of workers, w0 + x. Along a run a worker's first unit is its own
+// or the item's start.
+struct PartRun {
+    int w0, n, workers;
+    int64_t total, start;  // units of the class, the item's first unit
+    int64_t base;          // shared-prefix calls: rows of the items before, + the row
+    int pitch;
+    bool pairs;            // parts sit in two slots per worker (calls without a shared prefix)
+
+    // Row of part x in the workspace, or -1 for a worker without units.
+    __device__ __forceinline__ int64_t row(int x) const {
+        const int w = w0 + x;
+        const int64_t u0 = first_unit(total, w, workers);
+        if (first_unit(total, w + 1, workers) == u0) return -1;
+        if (!pairs) return base + static_cast<int64_t>(w) * pitch;
+        return base + static_cast<int64_t>(2 * w + (u0 < start ? 1 : 0)) * pitch;
+    }
+};
+
+// Joins the parts of one row and writes it; a warp per row.
+template <typename E>
+__device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a, const PartRun &b, int t, int h,
+                                         int lane) {
+    const int n = a.n + b.n;
+    float M = -INFINITY;
+    for (int x = lane; x < n; x += kWarp) {
+        const int64_t r = x < a.n ? a.row(x) : b.row(x - a.n);
+        if (r >= 0 && SPEC_IN(r, P.part_rows, DBG_ATTEND)) M = fmaxf(M, P.part_ml[r].x);
+    }
+    M = warp_max(M);
+    float4 o[2] = {};
+    float L = 0.0f;
+    if (M != -INFINITY) {
+        for (int x0 = 0; x0 < n; x0 += kWarp) {
+            const int x = x0 + lane;
+            int64_t r = -1;
+            float w = 0.0f;
+            if (x < n) {
+                r = x < a.n ? a.row(x) : b.row(x - a.n);
+                if (r >= 0 && SPEC_IN(r, P.part_rows, DBG_ATTEND)) {
+                    const float2 ml = P.part_ml[r];
+                    w = ex2(ml.x - M);
+                    L += w * ml.y;
+                }
+            }
+            const int cnt = min(kWarp, n - x0);
+#pragma unroll 4
+            for (int j = 0; j < cnt; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+                const int64_t rj = __shfl_sync(0xffffffffu, r, j);
+                if (wj == 0.0f) continue;  // takes no part (or holds nothing)
+                const float *src = P.part_o + rj * P.D;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int d = c * 128 + 4 * lane;
+                    if (d >= P.D) continue;
+                    const float4 v = *reinterpret_cast<const float4 *>(src + d);
+                    o[c].x = fmaf(wj, v.x, o[c].x);
+                    o[c].y = fmaf(wj, v.y, o[c].y);
+                    o[c].z = fmaf(wj, v.z, o[c].z);
+                    o[c].w = fmaf(wj, v.w, o[c].w);
+                }
+            }
+        }
+        L = warp_sum(L);
+    }
+    if (!SPEC_IN(t, P.T, DBG_ATTEND)) return;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    E *dst = static_cast<E *>(P.out) + t * P.out_stride + static_cast<int64_t>(h) * P.D;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int d = c * 128 + 4 * lane;
+        if (d < P.D) fma::store4(dst + d, make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv));
+    }
+    if (lane == 0 && P.lse)
+        P.lse[static_cast<int64_t>(t) * P.Hq + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The run of workers that share units [start, start + units).
+__device__ __forceinline__ void run_of(PartRun &r, int64_t total, int workers, int64_t start, int64_t units) {
+    r.total = total;
+    r.workers = workers;
+    r.start = start;
+    r.w0 = unit_owner(total, start, workers);
+    r.n = unit_owner(total, start + units - 1, workers) - r.w0 + 1;
+}
+
+// Blocks [0, B): request i's status goes out, and the rows of a request in error become 0 / -inf.
+// Then, without a shared prefix, kJoinRows rows a block for every border between two workers that is the
+// first to cut an item; with one, kJoinRows rows (of all query heads) a block.
+template <typename E, int RT, int KT>
+__global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const AttendParams P) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    if (blockIdx.x < static_cast<unsigned>(P.B)) {
+        const int i = blockIdx.x;
+        int bad = 0;
+        for (int w = threadIdx.x; w < P.own_workers + P.prefix_workers; w += kJoinThreads) bad |= P.err[w];
+        const int st = P.status[i] | (__syncthreads_or(bad) ? SPEC_REQ_TIMEOUT : 0);
+        if (threadIdx.x == 0 && P.req_status) P.req_status[i] = st;
+        if (st == SPEC_REQ_OK) return;
+        const ReqRows q = load_request(P, i);
+        const int per = P.Hq * P.D;
+        for (int j = 0; j < q.n; ++j) {
+            E *o = static_cast<E *>(P.out) + (q.r0 + j) * P.out_stride;
+            for (int d = 4 * threadIdx.x; d < per; d += 4 * kJoinThreads)
+                fma::store4(o + d, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+            if (P.lse)
+                for (int h = threadIdx.x; h < P.Hq; h += kJoinThreads)
+                    P.lse[static_cast<int64_t>(q.r0 + j) * P.Hq + h] = -INFINITY;
+        }
+        return;
+    }
+    const int blk = blockIdx.x - P.B;
+    const int64_t total = P.unit_prefix[P.B];
+    PartRun own = {}, pre = {};
+    if (P.shared_len == 0) {
+        if (total == 0) return;
+        const int per = (P.own_pitch + kJoinRows - 1) / kJoinRows;
+        const int c = blk / per + 1;  // the border between workers c - 1 and c
+        const int64_t u = first_unit(total, c, P.own_workers);
+        if (u >= total || u == first_unit(total, c - 1, P.own_workers)) return;
+        // the item with unit u
+        int lo = 0, n = P.B;
+        while (n > 1) {
+            const int half = n / 2;
+            if (P.unit_prefix[lo + half] <= u) {
+                lo += half;
+                n -= half;
+            } else {
+                n = half;
+            }
+        }
+        const ReqRows q = load_request(P, lo);
+        const int per_head = own_units<RT, KT>(P, q);
+        const int64_t rem = u - P.unit_prefix[lo];
+        const int head = static_cast<int>(rem / per_head);
+        int64_t start = P.unit_prefix[lo] + static_cast<int64_t>(head) * per_head;
+        int k = 0, units = 0;
+        for (;; ++k) {
+            units = max(own_tiles<RT, KT>(P, q, k).n, 1);
+            if (u < start + units) break;
+            start += units;
+        }
+        // nothing is cut here, or an earlier border has the item
+        if (start == u || first_unit(total, c - 1, P.own_workers) > start) return;
+        if (P.status[lo] != SPEC_REQ_OK) return;
+        run_of(own, total, P.own_workers, start, units);
+        own.pairs = true;
+        own.pitch = P.own_pitch;
+        const int first = (blk % per) * kJoinRows;
+        const int rows = min(RT, q.n * P.G - k * RT);
+        for (int r = first + warp; r < min(first + kJoinRows, rows); r += kJoinWarps) {
+            own.base = r;
+            const int j = (k * RT + r) / P.G, g = k * RT + r - j * P.G;
+            join_row<E>(P, own, pre, q.r0 + j, head * P.G + g, lane);
+        }
+        return;
+    }
+    const Totals t = batch_totals<RT, KT>(P, lane, false);
+    const int pre_units = max(prefix_tiles<KT>(P, t).n, 1);
+    const int tiles = (P.T * P.G + RT - 1) / RT;
+    for (int x = 0; x < kJoinRows / kJoinWarps; ++x) {
+        const int64_t row = static_cast<int64_t>(blk) * kJoinRows + x * kJoinWarps + warp;
+        if (row >= static_cast<int64_t>(P.T) * P.Hq) return;
+        const int tok = static_cast<int>(row / P.Hq), h = static_cast<int>(row - static_cast<int64_t>(tok) * P.Hq);
+        const int head = h / P.G, g = h - head * P.G;
+        const int i = find_request(P.row_off, P.B, tok, lane);
+        const ReqRows q = load_request(P, i);
+        if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) continue;
+        {
+            const int pr = tok * P.G + g, k = pr / RT;
+            const int64_t start = (static_cast<int64_t>(head) * tiles + k) * pre_units;
+            run_of(pre, static_cast<int64_t>(P.Hkv) * tiles * pre_units, P.prefix_workers, start, pre_units);
+            pre.pitch = P.prefix_pitch;
+            pre.base = static_cast<int64_t>(head) * P.T * P.G + pr;
+        }
+        {
+            const int pr = (tok - q.r0) * P.G + g, k = pr / RT;
+            int64_t start = P.unit_prefix[i] + static_cast<int64_t>(head) * own_units<RT, KT>(P, q);
+            for (int y = 0; y < k; ++y) start += max(own_tiles<RT, KT>(P, q, y).n, 1);
+            run_of(own, total, P.own_workers, start, max(own_tiles<RT, KT>(P, q, k).n, 1));
+            own.pitch = P.own_pitch;
+            own.base = static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
+                       (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + pr;
+        }
+        join_row<E>(P, pre, own, tok, h, lane);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct AttendLayout {
+    size_t status, unit_prefix, err, ml, o, total;
+};
+
+static AttendLayout attend_layout(const AttendParams &P) {
+    AttendLayout L = {};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = (off + bytes + 255) / 256 * 256;
+        return o;
+    };
+    L.status = take(static_cast<size_t>(P.B) * 4);
+    L.unit_prefix = take((static_cast<size_t>(P.B) + 1) * 8);
+    L.err = take(static_cast<size_t>(P.own_workers + P.prefix_workers) * 4);
+    L.ml = take(static_cast<size_t>(P.part_rows) * 8);
+    L.o = take(static_cast<size_t>(P.part_rows) * P.D * 4);
+    L.total = off;
+    return L;
+}
+
+// The sizes of a call, checked; workers and parts of the kernel that serves it.
+static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
+    if (!a) return SPEC_ERR_INVALID_ARG;
+    if (a->B < 1 || a->total_rows < 0 || a->n_kv_heads < 1 || a->n_q_heads < 1 || a->n_q_heads % a->n_kv_heads != 0 ||
+        a->head_dim < 1 || a->page_size < 1 || a->max_blocks < 1 || a->n_pages < 1 || a->window < 0 || a->n_sink < 0 ||
+        a->shared_len < 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+    if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return SPEC_ERR_INVALID_ARG;
+    const int vec = a->dtype == SPEC_BF16 ? 8 : 4;
+    if (a->head_dim > 256 || a->head_dim % vec != 0) return SPEC_ERR_UNSUPPORTED;
+    // packed rows and positions are 32-bit
+    if (static_cast<int64_t>(a->total_rows) * a->n_q_heads > INT_MAX / 4 ||
+        static_cast<int64_t>(a->max_blocks) * a->page_size > INT_MAX / 2 || a->shared_len > INT_MAX / 2 ||
+        a->n_q_heads > 65536)
+        return SPEC_ERR_UNSUPPORTED;
+    P.B = a->B;
+    P.T = a->total_rows;
+    P.Hq = a->n_q_heads;
+    P.Hkv = a->n_kv_heads;
+    P.G = a->n_q_heads / a->n_kv_heads;
+    P.D = a->head_dim;
+    P.page_size = a->page_size;
+    P.page_shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (a->page_size == 1 << s) P.page_shift = s;
+    P.max_blocks = a->max_blocks;
+    P.n_pages = a->n_pages;
+    P.window = a->window;
+    P.n_sink = a->n_sink;
+    P.shared_len = a->shared_len;
+    P.scale_log2 = a->scale * 1.4426950408889634f;
+
+    const int rt = fma::kRT;
+    P.own_workers = kSMs * fma::ctas_per_sm(P.D);
+    P.prefix_workers = P.shared_len > 0 ? P.own_workers : 0;
+    const int64_t head_rows = static_cast<int64_t>(P.T) * P.G;
+    P.own_pitch = P.prefix_pitch = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rt, head_rows)));
+    if (P.shared_len > 0)
+        P.part_rows = 2 * static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.own_workers) * P.own_pitch +
+                      static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch;
+    else
+        P.part_rows = 2 * static_cast<int64_t>(P.own_workers) * P.own_pitch;
+    return SPEC_OK;
+}
+
+template <typename E, int NC, bool PREFIX>
+static cudaError_t launch_fma(const AttendParams &P, cudaStream_t stream) {
+    const int smem = fma::smem_floats(P.D) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(fma::spec_attend_fma_kernel<E, NC, PREFIX>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_after(fma::spec_attend_fma_kernel<E, NC, PREFIX>,
+                        dim3(static_cast<unsigned>(PREFIX ? P.prefix_workers : P.own_workers)), dim3(fma::kThreads),
+                        static_cast<size_t>(smem), stream, P);
+}
+
+template <typename E, int RT, int KT>
+static cudaError_t launch_join(const AttendParams &P, cudaStream_t stream) {
+    const int64_t blocks =
+        P.shared_len > 0
+            ? (static_cast<int64_t>(P.T) * P.Hq + kJoinRows - 1) / kJoinRows
+            : static_cast<int64_t>(P.own_workers - 1) * ((P.own_pitch + kJoinRows - 1) / kJoinRows);
+    return launch_after(spec_attend_join_kernel<E, RT, KT>, dim3(static_cast<unsigned>(P.B + blocks)),
+                        dim3(kJoinThreads), 0, stream, P);
+}
+
+template <typename E>
+static cudaError_t enqueue_fma(const AttendParams &P, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    const bool wide = P.D > 128;
+    if (P.shared_len > 0) e = wide ? launch_fma<E, 2, true>(P, stream) : launch_fma<E, 1, true>(P, stream);
+    if (e == cudaSuccess) e = wide ? launch_fma<E, 2, false>(P, stream) : launch_fma<E, 1, false>(P, stream);
+    if (e == cudaSuccess) e = launch_join<E, fma::kRT, fma::kKT>(P, stream);
+    return e;
+}
+
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t spec_attend_workspace_size(const spec_attend_args *a) {
+    AttendParams P = {};
+    return attend_sizes(a, P) == SPEC_OK ? attend_layout(P).total : 0;
+}
+
+extern "C" const char *spec_attend_plan(const spec_attend_args *a) {
+    AttendParams P = {};
+    if (attend_sizes(a, P) != SPEC_OK) return nullptr;
+    return "spec_attend_fma_kernel";
+}
+
+extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream) {
+    AttendParams P = {};
+    const spec_status st = attend_sizes(a, P);
+    if (st != SPEC_OK) return st;
+    if (!a->row_off || !a->kv_len || !a->block_table || !a->k_cache || !a->v_cache) return SPEC_ERR_INVALID_ARG;
+    if (P.T > 0 && (!a->q || !a->out)) return SPEC_ERR_INVALID_ARG;
+    if (P.shared_len > 0 && !a->shared_table) return SPEC_ERR_INVALID_ARG;
+    const int64_t width = static_cast<int64_t>(P.Hq) * P.D;
+    if (P.T > 1 && (a->q_stride < width || a->out_stride < width)) return SPEC_ERR_INVALID_ARG;
+    if (a->page_stride < 0 || a->slot_stride < 0 || a->head_stride < 0) return SPEC_ERR_INVALID_ARG;
+    const int vec = a->dtype == SPEC_BF16 ? 8 : 4;
+    auto aligned = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    if ((a->q_stride | a->out_stride | a->page_stride | a->slot_stride | a->head_stride) % vec != 0 || !aligned(a->q) ||
+        !aligned(a->out) || !aligned(a->k_cache) || !aligned(a->v_cache))
+        return SPEC_ERR_UNSUPPORTED;
+    const AttendLayout L = attend_layout(P);
+    if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return SPEC_ERR_WORKSPACE;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    P.q = a->q;
+    P.k_cache = a->k_cache;
+    P.v_cache = a->v_cache;
+    P.q_stride = a->q_stride;
+    P.page_stride = a->page_stride;
+    P.slot_stride = a->slot_stride;
+    P.head_stride = a->head_stride;
+    P.row_off = a->row_off;
+    P.kv_len = a->kv_len;
+    P.block_table = a->block_table;
+    P.shared_table = a->shared_table;
+    P.out = a->out;
+    P.out_stride = a->out_stride;
+    P.lse = a->lse;
+    P.req_status = a->req_status;
+    P.status = reinterpret_cast<int32_t *>(ws + L.status);
+    P.unit_prefix = reinterpret_cast<int64_t *>(ws + L.unit_prefix);
+    P.err = reinterpret_cast<int32_t *>(ws + L.err);
+    P.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
+    P.part_o = reinterpret_cast<float *>(ws + L.o);
+    const cudaError_t e =
+        a->dtype == SPEC_BF16 ? enqueue_fma<__nv_bfloat16>(P, stream) : enqueue_fma<float>(P, stream);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+#ifdef SPEC_DEBUG
+namespace spec {
+// The debug words of this translation unit's kernels.
+cudaError_t debug_take_attend(unsigned int out[4]) { return spec_dbg_take(out); }
+}  // namespace spec
+#endif

@@ -1,0 +1,316 @@
+// How the attention of a ragged batch over the paged cache is cut into work, computed on the device
+// (lengths and offsets are device arrays).
+//
+// Rows that share a key/value head are packed: row r of a request's head is (row j, query head g of
+// the group) = (r / G, r % G). An item is up to RT packed rows of one head; its keys, in tiles of KT
+// positions, are its units. Units are numbered item after item, and worker w of NW takes the units
+// [total w / NW, total (w+1) / NW): every worker gets the same number of tiles whatever the lengths
+// are, a long context is split over many workers, and the cut depends on the inputs alone. An item
+// that falls to several workers leaves a part (output, maximum, sum) per worker, and the joining
+// kernel adds the parts in the order of the workers.
+//
+// Two classes of items. A call without a shared prefix has "own" items: a request's rows over its
+// positions. With one, the own items begin at shared_len, and "prefix" items take the rows of the
+// whole batch over the positions below it.
+#pragma once
+
+#include <climits>
+#include <cstdint>
+
+#include "spec_attend.h"
+#include "spec_device.cuh"
+#include "spec_paged.cuh"
+
+namespace spec {
+
+struct AttendParams {
+    int32_t B, T, Hq, Hkv, G, D;
+    int32_t page_size, page_shift;  // page_shift >= 0: page_size is 1 << page_shift
+    int32_t max_blocks, n_pages, window, n_sink, shared_len;
+    float scale_log2;  // scale * log2(e): the softmax is taken in base 2
+    const void *q, *k_cache, *v_cache;
+    int64_t q_stride, page_stride, slot_stride, head_stride;
+    const int32_t *row_off, *kv_len, *block_table, *shared_table;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    int32_t *req_status;
+    // workspace
+    int32_t *status;       // [B]
+    int64_t *unit_prefix;  // [B+1] units of the own items before each request
+    float2 *part_ml;       // [part rows] maximum (base 2, scaled) and sum
+    float *part_o;         // [part rows][D] unnormalised output
+    int32_t *err;          // [workers of both classes] 1: a bounded wait gave up
+    int32_t own_workers, prefix_workers;
+    int32_t own_pitch, prefix_pitch;  // rows of a worker's part
+    int64_t part_rows;
+};
+
+// ---------------------------------------------------------------- positions and pages
+
+struct ReqRows {
+    int r0, n, kv;  // first row, rows, positions; n = 0 / kv = 0 where the batch is inconsistent
+};
+__device__ __forceinline__ ReqRows load_request(const AttendParams &P, int i) {
+    const int r0 = P.row_off[i], r1 = P.row_off[i + 1];
+    int kv = P.kv_len[i];
+    if (r0 < 0 || r1 < r0 || r1 > P.T) return {0, 0, 0};
+    if (kv < 0 || kv > static_cast<int64_t>(P.max_blocks) * P.page_size) kv = 0;
+    return {r0, r1 - r0, kv};
+}
+
+// Element offset of position x's slot (head 0), or -1 when it has no page.
+__device__ __forceinline__ int64_t slot_offset(const AttendParams &P, const int32_t *table, int x) {
+    const int b = P.page_shift >= 0 ? x >> P.page_shift : x / P.page_size;
+    const int page = table[b];
+    if (page < 0 || page >= P.n_pages) return -1;
+    return page * P.page_stride + (x - b * P.page_size) * P.slot_stride;
+}
+
+// The key tiles an item visits: of the tiles of KT positions from lo, the first s (the sinks), then
+// those from w_first on (the window); n in all. Positions in [lo, hi) at or above win, or below the
+// sinks, are seen by some row of the item; pad is one of them.
+struct KeyTiles {
+    int lo, hi, win, s, w_first, n, pad;
+};
+template <int KT>
+__device__ __forceinline__ KeyTiles key_tiles(const AttendParams &P, int lo, int hi, int pmin) {
+    KeyTiles t = {lo, hi, lo, 0, 0, 0, lo};
+    if (hi <= lo) return t;
+    const int total = (hi - lo + KT - 1) / KT;
+    if (P.window > 0) {
+        t.win = max(lo, pmin - P.window + 1);
+        const int sinks = max(min(P.n_sink, hi) - lo, 0);
+        t.w_first = t.win < hi ? (t.win - lo) / KT : total;
+        t.s = min((sinks + KT - 1) / KT, t.w_first);
+        t.pad = sinks > 0 ? lo : t.win;
+    }
+    t.n = t.s + total - t.w_first;
+    return t;
+}
+template <int KT>
+__device__ __forceinline__ int tile_begin(const KeyTiles &t, int i) {
+    return t.lo + (i < t.s ? i : i - t.s + t.w_first) * KT;
+}
+// True when some row of the item may see position x.
+__device__ __forceinline__ bool item_sees(const AttendParams &P, const KeyTiles &t, int x) {
+    return x < t.hi && (x >= t.win || x < P.n_sink);
+}
+
+// ---------------------------------------------------------------- items and units
+
+template <int RT, int KT>
+__device__ __forceinline__ KeyTiles own_tiles(const AttendParams &P, const ReqRows &q, int k) {
+    const int base = q.kv - q.n;
+    const int last = min((k + 1) * RT, q.n * P.G) - 1;
+    return key_tiles<KT>(P, P.shared_len, base + last / P.G + 1, max(base + k * RT / P.G, 0));
+}
+// Units of one head of a request (an item without keys is one unit: its rows are written too).
+template <int RT, int KT>
+__device__ __forceinline__ int own_units(const AttendParams &P, const ReqRows &q) {
+    int u = 0;
+    for (int k = 0; k * RT < q.n * P.G; ++k) u += max(own_tiles<RT, KT>(P, q, k).n, 1);
+    return u;
+}
+
+// The batch as a whole, by one warp.
+struct Totals {
+    int64_t own_units;
+    int pmin, pmax;  // least and greatest position of the rows (padding aside)
+};
+template <int RT, int KT>
+__device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane, bool units) {
+    Totals t = {0, INT_MAX, -1};
+    for (int i = lane; i < P.B; i += kWarp) {
+        const ReqRows q = load_request(P, i);
+        if (q.n > 0 && q.kv > 0) {
+            t.pmin = min(t.pmin, max(q.kv - q.n, 0));
+            t.pmax = max(t.pmax, q.kv - 1);
+        }
+        if (units) t.own_units += static_cast<int64_t>(P.Hkv) * own_units<RT, KT>(P, q);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        t.own_units += __shfl_xor_sync(0xffffffffu, t.own_units, o);
+        t.pmin = min(t.pmin, __shfl_xor_sync(0xffffffffu, t.pmin, o));
+        t.pmax = max(t.pmax, __shfl_xor_sync(0xffffffffu, t.pmax, o));
+    }
+    return t;
+}
+template <int KT>
+__device__ __forceinline__ KeyTiles prefix_tiles(const AttendParams &P, const Totals &t) {
+    return key_tiles<KT>(P, 0, min(P.shared_len, t.pmax + 1), t.pmin);
+}
+
+__device__ __forceinline__ int64_t first_unit(int64_t total, int w, int workers) { return total * w / workers; }
+// The worker that unit u falls to.
+__device__ __forceinline__ int unit_owner(int64_t total, int64_t u, int workers) {
+    return static_cast<int>(((u + 1) * workers + total - 1) / total) - 1;
+}
+
+// A run of units of one item, as a worker takes it.
+struct Segment {
+    int row0;        // first packed row (own: within the request's head; prefix: within the batch)
+    int nrows;       // packed rows, at most RT
+    int t0;          // first row of the request in the batch (prefix: 0)
+    int base;        // position of row t0 (prefix: unused, rows have their own)
+    int head;        // key/value head
+    int req;         // request, -1 for prefix items
+    int tile, ntile; // first tile and number of tiles of this run
+    int64_t part;    // first row of its part in the workspace, or -1: the whole item, written out
+    KeyTiles keys;
+};
+
+// Walks a worker's segments. Used by whole warps; every lane holds the same state.
+template <int RT, int KT, bool PREFIX>
+struct Walker {
+    int64_t u, u_end, u_first;
+    int worker;
+    int i, head, k, tile;  // request, head, row tile, tile within the item
+    int head_tiles;        // row tiles of a head
+    ReqRows q;
+    KeyTiles shared;       // prefix items: all alike
+
+    __device__ __forceinline__ void start(const AttendParams &P, int w, int lane) {
+        worker = w;
+        const Totals t = batch_totals<RT, KT>(P, lane, !PREFIX);
+        head = k = tile = i = 0;
+        q = {0, 0, 0};
+        if constexpr (PREFIX) {
+            shared = prefix_tiles<KT>(P, t);
+            q.n = P.T;
+            head_tiles = (P.T * P.G + RT - 1) / RT;
+            const int per = max(shared.n, 1);
+            const int64_t total = static_cast<int64_t>(P.Hkv) * head_tiles * per;
+            u = first_unit(total, w, P.prefix_workers);
+            u_end = first_unit(total, w + 1, P.prefix_workers);
+            const int64_t item = u / per;
+            tile = static_cast<int>(u - item * per);
+            head = static_cast<int>(item / head_tiles);
+            k = static_cast<int>(item - static_cast<int64_t>(head) * head_tiles);
+        } else {
+            const int64_t total = t.own_units;
+            u = first_unit(total, w, P.own_workers);
+            u_end = first_unit(total, w + 1, P.own_workers);
+            const bool record = w == 0;  // worker 0 leaves the requests' units to the joining kernel
+            int64_t before = 0;
+            bool found = u >= u_end;
+            int64_t rem = 0;
+            for (int i0 = 0; i0 < P.B && (record || !found); i0 += kWarp) {
+                const int r = i0 + lane;
+                int64_t mine = 0;
+                if (r < P.B) mine = static_cast<int64_t>(P.Hkv) * own_units<RT, KT>(P, load_request(P, r));
+                int64_t incl = mine;
+#pragma unroll
+                for (int o = 1; o < kWarp; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += x;
+                }
+                if (record && r < P.B && SPEC_IN(r + 1, P.B + 1, DBG_ATTEND))
+                    P.unit_prefix[r + 1] = before + incl;
+                const unsigned hit = __ballot_sync(0xffffffffu, u < before + incl);
+                if (!found && hit) {
+                    const int l = __ffs(hit) - 1;
+                    i = i0 + l;
+                    rem = u - before - __shfl_sync(0xffffffffu, incl - mine, l);
+                    found = true;
+                }
+                before += __shfl_sync(0xffffffffu, incl, kWarp - 1);
+            }
+            if (record && lane == 0) P.unit_prefix[0] = 0;
+            if (u < u_end) {
+                q = load_request(P, i);
+                head_tiles = (q.n * P.G + RT - 1) / RT;
+                const int per_head = own_units<RT, KT>(P, q);
+                head = static_cast<int>(rem / per_head);
+                rem -= static_cast<int64_t>(head) * per_head;
+                for (;; ++k) {
+                    const int nt = max(own_tiles<RT, KT>(P, q, k).n, 1);
+                    if (rem < nt || k + 1 >= head_tiles) break;
+                    rem -= nt;
+                }
+                tile = static_cast<int>(rem);
+            }
+        }
+        u_first = u;
+    }
+
+    // The next segment, or false at the end of the worker's units.
+    __device__ __forceinline__ bool next(const AttendParams &P, Segment &s) {
+        if (u >= u_end) return false;
+        s.keys = PREFIX ? shared : own_tiles<RT, KT>(P, q, k);
+        const int units = max(s.keys.n, 1);
+        const int take = static_cast<int>(min(static_cast<int64_t>(units - tile), u_end - u));
+        s.row0 = k * RT;
+        s.nrows = min(RT, q.n * P.G - s.row0);
+        s.t0 = q.r0;
+        s.base = q.kv - q.n;
+        s.head = head;
+        s.req = PREFIX ? -1 : i;
+        s.tile = tile;
+        s.ntile = min(take, s.keys.n);
+        const bool whole = take == units;
+        if (P.shared_len > 0) {
+            // along a class's units either the item or the worker grows from one part to the next, so
+            // (rows of the items before) + worker * pitch gives every part rows of its own
+            const int64_t rows = (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + s.row0;
+            s.part = rows + static_cast<int64_t>(worker) * (PREFIX ? P.prefix_pitch : P.own_pitch);
+            if (!PREFIX)
+                s.part += static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch;
+        } else {
+            // only a worker's first and last segment can be part of an item
+            s.part = whole ? -1 : static_cast<int64_t>(2 * worker + (u == u_first ? 0 : 1)) * P.own_pitch;
+        }
+        u += take;
+        tile += take;
+        if (tile >= units) {
+            tile = 0;
+            if (++k >= head_tiles) {
+                k = 0;
+                if (++head >= P.Hkv) {
+                    head = 0;
+                    if (!PREFIX && u < u_end) {
+                        do {
+                            q = load_request(P, ++i);
+                        } while (q.n == 0 && i + 1 < P.B);
+                        head_tiles = (q.n * P.G + RT - 1) / RT;
+                    }
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------- requests' status
+
+// Status of request i, by one warp: consistent offsets and lengths, and a page for every position
+// that a row sees.
+__device__ __forceinline__ int attend_status(const AttendParams &P, int i, int lane) {
+    const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
+    if (r0 < 0 || r1 < r0 || r1 > P.T || kv < 0) return SPEC_REQ_BAD_SHAPE;
+    if (r1 == r0 || kv == 0) return SPEC_REQ_OK;
+    if (kv > static_cast<int64_t>(P.max_blocks) * P.page_size) return SPEC_REQ_BAD_BLOCKS;
+    bool bad = false;
+    // positions [a, b) through a table
+    auto scan = [&](const int32_t *table, int a, int b) {
+        if (a >= b) return;
+        for (int x = a / P.page_size + lane; x <= (b - 1) / P.page_size; x += kWarp) {
+            const int page = table[x];
+            bad |= page < 0 || page >= P.n_pages;
+        }
+    };
+    const int32_t *table = P.block_table + static_cast<int64_t>(i) * P.max_blocks;
+    const int win = P.window > 0 ? max(max(kv - (r1 - r0), 0) - P.window + 1, 0) : 0;
+    const int sinks = min(min(P.n_sink, win), kv);
+    const int L = P.shared_len;
+    scan(table, max(win, L), kv);
+    scan(table, L, sinks);
+    if (L > 0) {
+        scan(P.shared_table, win, min(L, kv));
+        scan(P.shared_table, 0, min(sinks, L));
+    }
+    return __any_sync(0xffffffffu, bad) ? SPEC_REQ_BAD_BLOCKS : SPEC_REQ_OK;
+}
+
+}  // namespace spec

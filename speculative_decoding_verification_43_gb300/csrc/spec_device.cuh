@@ -302,6 +302,8 @@ enum : int {
     DBG_OUT_REQS = 5,   // per-request outputs and counters
     DBG_PACKED = 6,     // the compaction's packed outputs
     DBG_CUT = 7,        // the truncation kernel's rows and cuts
+    DBG_CACHE = 8,      // the paged cache's pages and the elements within a head
+    DBG_ATTEND = 9,     // the attention kernels' rows, outputs and workspace
 };
 #ifdef SPEC_DEBUG
 static __device__ unsigned int g_spec_dbg[4];  // first code, its line, its index, failures

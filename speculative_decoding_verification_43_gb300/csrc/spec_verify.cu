@@ -253,18 +253,23 @@ extern "C" const char *spec_version(void) { return "spec-verify-gb300 0.1 (sm_10
 
 namespace spec {
 cudaError_t debug_take_compact(unsigned int out[4]);
+cudaError_t debug_take_append(unsigned int out[4]);
+cudaError_t debug_take_attend(unsigned int out[4]);
 }
 
 extern "C" spec_status spec_debug_fetch(unsigned int *out) {
     if (!out) return SPEC_ERR_INVALID_ARG;
-    unsigned int a[4] = {0u, 0u, 0u, 0u}, b[4] = {0u, 0u, 0u, 0u};
+    unsigned int w[4][4] = {};
     if (cudaDeviceSynchronize() != cudaSuccess) return SPEC_ERR_CUDA;
-    if (spec::spec_dbg_take(a) != cudaSuccess || spec::debug_take_compact(b) != cudaSuccess) return SPEC_ERR_CUDA;
-    const unsigned int *first = a[0] ? a : b;
-    out[0] = first[0];
-    out[1] = first[1];
-    out[2] = first[2];
-    out[3] = a[3] + b[3];
+    if (spec::spec_dbg_take(w[0]) != cudaSuccess || spec::debug_take_compact(w[1]) != cudaSuccess ||
+        spec::debug_take_append(w[2]) != cudaSuccess || spec::debug_take_attend(w[3]) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    for (int k = 0; k < 4; ++k) out[k] = 0u;
+    for (const auto &u : w) {
+        if (out[0] == 0u)
+            for (int k = 0; k < 3; ++k) out[k] = u[k];
+        out[3] += u[3];
+    }
     return SPEC_OK;
 }
 #else
