@@ -15,6 +15,7 @@
 
 #include "spec_attend.h"
 #include "spec_attend_fma.cuh"
+#include "spec_attend_mma.cuh"
 #include "spec_attend_plan.cuh"
 #include "spec_device.cuh"
 #include "spec_paged.cuh"
@@ -117,7 +118,7 @@ __device__ __forceinline__ void run_of(PartRun &r, int64_t total, int workers, i
 // Blocks [0, B): request i's status goes out, and the rows of a request in error become 0 / -inf.
 // Then, without a shared prefix, kJoinRows rows a block for every border between two workers that is the
 // first to cut an item; with one, kJoinRows rows (of all query heads) a block.
-template <typename E, int RT, int KT>
+template <typename E, int KT>
 __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const AttendParams P) {
     griddep_launch_dependents();
     griddep_wait();
@@ -162,13 +163,13 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
             }
         }
         const ReqRows q = load_request(P, lo);
-        const int per_head = own_units<RT, KT>(P, q);
+        const int per_head = own_units<KT>(P, q);
         const int64_t rem = u - P.unit_prefix[lo];
         const int head = static_cast<int>(rem / per_head);
         int64_t start = P.unit_prefix[lo] + static_cast<int64_t>(head) * per_head;
         int k = 0, units = 0;
         for (;; ++k) {
-            units = max(own_tiles<RT, KT>(P, q, k).n, 1);
+            units = max(own_tiles<KT>(P, q, k).n, 1);
             if (u < start + units) break;
             start += units;
         }
@@ -179,17 +180,17 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
         own.pairs = true;
         own.pitch = P.own_pitch;
         const int first = (blk % per) * kJoinRows;
-        const int rows = min(RT, q.n * P.G - k * RT);
+        const int r0 = k << P.own_rt_log2, rows = min(1 << P.own_rt_log2, q.n * P.G - r0);
         for (int r = first + warp; r < min(first + kJoinRows, rows); r += kJoinWarps) {
             own.base = r;
-            const int j = (k * RT + r) / P.G, g = k * RT + r - j * P.G;
+            const int j = (r0 + r) / P.G, g = r0 + r - j * P.G;
             join_row<E>(P, own, pre, q.r0 + j, head * P.G + g, lane);
         }
         return;
     }
-    const Totals t = batch_totals<RT, KT>(P, lane, false);
+    const Totals t = batch_totals<KT>(P, lane, false);
     const int pre_units = max(prefix_tiles<KT>(P, t).n, 1);
-    const int tiles = (P.T * P.G + RT - 1) / RT;
+    const int tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
     for (int x = 0; x < kJoinRows / kJoinWarps; ++x) {
         const int64_t row = static_cast<int64_t>(blk) * kJoinRows + x * kJoinWarps + warp;
         if (row >= static_cast<int64_t>(P.T) * P.Hq) return;
@@ -199,17 +200,17 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
         const ReqRows q = load_request(P, i);
         if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) continue;
         {
-            const int pr = tok * P.G + g, k = pr / RT;
+            const int pr = tok * P.G + g, k = pr >> P.prefix_rt_log2;
             const int64_t start = (static_cast<int64_t>(head) * tiles + k) * pre_units;
             run_of(pre, static_cast<int64_t>(P.Hkv) * tiles * pre_units, P.prefix_workers, start, pre_units);
             pre.pitch = P.prefix_pitch;
             pre.base = static_cast<int64_t>(head) * P.T * P.G + pr;
         }
         {
-            const int pr = (tok - q.r0) * P.G + g, k = pr / RT;
-            int64_t start = P.unit_prefix[i] + static_cast<int64_t>(head) * own_units<RT, KT>(P, q);
-            for (int y = 0; y < k; ++y) start += max(own_tiles<RT, KT>(P, q, y).n, 1);
-            run_of(own, total, P.own_workers, start, max(own_tiles<RT, KT>(P, q, k).n, 1));
+            const int pr = (tok - q.r0) * P.G + g, k = pr >> P.own_rt_log2;
+            int64_t start = P.unit_prefix[i] + static_cast<int64_t>(head) * own_units<KT>(P, q);
+            for (int y = 0; y < k; ++y) start += max(own_tiles<KT>(P, q, y).n, 1);
+            run_of(own, total, P.own_workers, start, max(own_tiles<KT>(P, q, k).n, 1));
             own.pitch = P.own_pitch;
             own.base = static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
                        (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + pr;
@@ -274,17 +275,99 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
     P.shared_len = a->shared_len;
     P.scale_log2 = a->scale * 1.4426950408889634f;
 
-    const int rt = fma::kRT;
-    P.own_workers = kSMs * fma::ctas_per_sm(P.D);
-    P.prefix_workers = P.shared_len > 0 ? P.own_workers : 0;
+    return SPEC_OK;
+}
+
+// Workers and parts of the kernel that serves the call.
+static void attend_work(AttendParams &P, bool tensor) {
     const int64_t head_rows = static_cast<int64_t>(P.T) * P.G;
-    P.own_pitch = P.prefix_pitch = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rt, head_rows)));
+    if (tensor) {
+        // one accumulator holds 128 rows. Beyond that (own items: on average over the requests) items of
+        // 256 rows share their tiles between both accumulators of an SM; below it each accumulator is
+        // a worker.
+        const bool own_pair = head_rows > 128 * static_cast<int64_t>(P.B), prefix_pair = head_rows > 128;
+        P.own_rt_log2 = own_pair ? 8 : 7;
+        P.own_workers = own_pair ? kSMs : 2 * kSMs;
+        P.prefix_rt_log2 = prefix_pair ? 8 : 7;
+        P.prefix_workers = prefix_pair ? kSMs : 2 * kSMs;
+    } else {
+        P.own_rt_log2 = P.prefix_rt_log2 = fma::kRTLog2;
+        P.own_workers = P.prefix_workers = kSMs * fma::ctas_per_sm(P.D);
+    }
+    if (P.shared_len == 0) P.prefix_workers = 0;
+    P.own_pitch = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(1 << P.own_rt_log2, head_rows)));
+    P.prefix_pitch = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(1 << P.prefix_rt_log2, head_rows)));
     if (P.shared_len > 0)
         P.part_rows = 2 * static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.own_workers) * P.own_pitch +
                       static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch;
     else
         P.part_rows = 2 * static_cast<int64_t>(P.own_workers) * P.own_pitch;
-    return SPEC_OK;
+}
+
+// The cache as two-dimensional tensor maps of slots, where its strides allow it: pages a whole number of
+// slots apart, heads inside a slot or a whole number of slots apart. bf16, head sizes the matrix
+// instructions take.
+static bool cache_map(const spec_attend_args *a, mma::CacheMap &M, int64_t &rows, int64_t &cols) {
+    if (a->dtype != SPEC_BF16 || a->head_dim % 16 != 0 || a->head_dim > 128) return false;
+    const int64_t slot = a->slot_stride, D = a->head_dim, heads = a->n_kv_heads;
+    if (slot <= 0 || (a->n_pages > 1 && a->page_stride % slot != 0)) return false;
+    const int64_t page_rows = a->n_pages > 1 ? a->page_stride / slot : 0;
+    int64_t head_rows = 0, head_cols = 0;
+    cols = D;
+    if ((heads - 1) * a->head_stride + D <= slot) {
+        head_cols = heads > 1 ? a->head_stride : 0;
+        cols = (heads - 1) * a->head_stride + D;
+    } else if (a->head_stride % slot == 0 && D <= slot) {
+        head_rows = a->head_stride / slot;
+    } else {
+        return false;
+    }
+    rows = (a->n_pages - 1) * page_rows + (heads - 1) * head_rows + a->page_size;
+    if (rows > INT_MAX / 2 || cols > INT_MAX / 2 || slot * 2 >= (1ll << 40)) return false;
+    M.page_rows = static_cast<int32_t>(page_rows);
+    M.head_rows = static_cast<int32_t>(head_rows);
+    M.head_cols = static_cast<int32_t>(head_cols);
+    return true;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's call that fills a tensor map in (looked up once).
+static EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+static bool encode_map(CUtensorMap &map, const void *cache, int64_t rows, int64_t cols, int64_t slot_stride) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(slot_stride) * 2};
+    const cuuint32_t box[2] = {64, 1}, step[2] = {1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(cache), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool PAIR, bool PREFIX>
+static cudaError_t launch_mma(const AttendParams &P, const mma::CacheMap &M, const CUtensorMap &k, const CUtensorMap &v,
+                              cudaStream_t stream) {
+    const int smem = mma::smem_bytes(P.D);
+    const cudaError_t e = cudaFuncSetAttribute(mma::spec_attend_mma_kernel<PAIR, PREFIX>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_after(mma::spec_attend_mma_kernel<PAIR, PREFIX>, dim3(kSMs), dim3(mma::kThreads),
+                        static_cast<size_t>(smem), stream, P, M, k, v, mma::stages(P.D));
 }
 
 template <typename E, int NC, bool PREFIX>
@@ -298,14 +381,25 @@ static cudaError_t launch_fma(const AttendParams &P, cudaStream_t stream) {
                         static_cast<size_t>(smem), stream, P);
 }
 
-template <typename E, int RT, int KT>
+template <typename E, int KT>
 static cudaError_t launch_join(const AttendParams &P, cudaStream_t stream) {
     const int64_t blocks =
         P.shared_len > 0
             ? (static_cast<int64_t>(P.T) * P.Hq + kJoinRows - 1) / kJoinRows
             : static_cast<int64_t>(P.own_workers - 1) * ((P.own_pitch + kJoinRows - 1) / kJoinRows);
-    return launch_after(spec_attend_join_kernel<E, RT, KT>, dim3(static_cast<unsigned>(P.B + blocks)),
+    return launch_after(spec_attend_join_kernel<E, KT>, dim3(static_cast<unsigned>(P.B + blocks)),
                         dim3(kJoinThreads), 0, stream, P);
+}
+
+static cudaError_t enqueue_mma(const AttendParams &P, const mma::CacheMap &M, const CUtensorMap &k,
+                               const CUtensorMap &v, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    if (P.shared_len > 0)
+        e = P.prefix_rt_log2 == 8 ? launch_mma<true, true>(P, M, k, v, stream) : launch_mma<false, true>(P, M, k, v, stream);
+    if (e == cudaSuccess)
+        e = P.own_rt_log2 == 8 ? launch_mma<true, false>(P, M, k, v, stream) : launch_mma<false, false>(P, M, k, v, stream);
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, mma::kKT>(P, stream);
+    return e;
 }
 
 template <typename E>
@@ -314,7 +408,7 @@ static cudaError_t enqueue_fma(const AttendParams &P, cudaStream_t stream) {
     const bool wide = P.D > 128;
     if (P.shared_len > 0) e = wide ? launch_fma<E, 2, true>(P, stream) : launch_fma<E, 1, true>(P, stream);
     if (e == cudaSuccess) e = wide ? launch_fma<E, 2, false>(P, stream) : launch_fma<E, 1, false>(P, stream);
-    if (e == cudaSuccess) e = launch_join<E, fma::kRT, fma::kKT>(P, stream);
+    if (e == cudaSuccess) e = launch_join<E, fma::kKT>(P, stream);
     return e;
 }
 
@@ -324,13 +418,21 @@ using namespace spec;
 
 extern "C" size_t spec_attend_workspace_size(const spec_attend_args *a) {
     AttendParams P = {};
-    return attend_sizes(a, P) == SPEC_OK ? attend_layout(P).total : 0;
+    if (attend_sizes(a, P) != SPEC_OK) return 0;
+    // either kernel may serve the call: which one follows from the strides
+    attend_work(P, false);
+    const size_t fma_bytes = attend_layout(P).total;
+    if (a->dtype != SPEC_BF16) return fma_bytes;
+    attend_work(P, true);
+    return std::max(fma_bytes, attend_layout(P).total);
 }
 
 extern "C" const char *spec_attend_plan(const spec_attend_args *a) {
     AttendParams P = {};
     if (attend_sizes(a, P) != SPEC_OK) return nullptr;
-    return "spec_attend_fma_kernel";
+    mma::CacheMap M = {};
+    int64_t rows = 0, cols = 0;
+    return cache_map(a, M, rows, cols) ? "spec_attend_mma_kernel" : "spec_attend_fma_kernel";
 }
 
 extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, size_t workspace_bytes,
@@ -349,8 +451,12 @@ extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, s
     if ((a->q_stride | a->out_stride | a->page_stride | a->slot_stride | a->head_stride) % vec != 0 || !aligned(a->q) ||
         !aligned(a->out) || !aligned(a->k_cache) || !aligned(a->v_cache))
         return SPEC_ERR_UNSUPPORTED;
+    mma::CacheMap M = {};
+    int64_t map_rows = 0, map_cols = 0;
+    const bool tensor = cache_map(a, M, map_rows, map_cols);
+    attend_work(P, tensor);
     const AttendLayout L = attend_layout(P);
-    if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+    if (!workspace || workspace_bytes < spec_attend_workspace_size(a) || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
         return SPEC_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     P.q = a->q;
@@ -373,6 +479,13 @@ extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, s
     P.err = reinterpret_cast<int32_t *>(ws + L.err);
     P.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     P.part_o = reinterpret_cast<float *>(ws + L.o);
+    if (tensor) {
+        CUtensorMap k, v;
+        if (!encode_map(k, a->k_cache, map_rows, map_cols, a->slot_stride) ||
+            !encode_map(v, a->v_cache, map_rows, map_cols, a->slot_stride))
+            return SPEC_ERR_CUDA;
+        return enqueue_mma(P, M, k, v, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    }
     const cudaError_t e =
         a->dtype == SPEC_BF16 ? enqueue_fma<__nv_bfloat16>(P, stream) : enqueue_fma<float>(P, stream);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

@@ -15,7 +15,7 @@
 namespace spec {
 namespace fma {
 
-constexpr int kRT = 16, kKT = 32, kWarps = 4, kThreads = kWarps * kWarp, kRows = kRT / kWarps;
+constexpr int kRTLog2 = 4, kRT = 1 << kRTLog2, kKT = 32, kWarps = 4, kThreads = kWarps * kWarp, kRows = kRT / kWarps;
 
 // Shared memory: queries, two tiles of keys and values, the weights.
 __host__ __device__ constexpr int smem_floats(int D) {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
     griddep_launch_dependents();
     griddep_wait();
 
-    Walker<kRT, kKT, PREFIX> walk;
+    Walker<kKT, PREFIX> walk;
     walk.start(P, blockIdx.x, lane);
     Segment s;
     while (walk.next(P, s)) {

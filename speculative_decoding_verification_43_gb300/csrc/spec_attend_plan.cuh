@@ -42,7 +42,8 @@ struct AttendParams {
     float *part_o;         // [part rows][D] unnormalised output
     int32_t *err;          // [workers of both classes] 1: a bounded wait gave up
     int32_t own_workers, prefix_workers;
-    int32_t own_pitch, prefix_pitch;  // rows of a worker's part
+    int32_t own_rt_log2, prefix_rt_log2;  // packed rows of an item (RT), as a power of two
+    int32_t own_pitch, prefix_pitch;      // rows of a worker's part
     int64_t part_rows;
 };
 
@@ -99,17 +100,20 @@ __device__ __forceinline__ bool item_sees(const AttendParams &P, const KeyTiles 
 
 // ---------------------------------------------------------------- items and units
 
-template <int RT, int KT>
+template <int KT>
 __device__ __forceinline__ KeyTiles own_tiles(const AttendParams &P, const ReqRows &q, int k) {
-    const int base = q.kv - q.n;
-    const int last = min((k + 1) * RT, q.n * P.G) - 1;
-    return key_tiles<KT>(P, P.shared_len, base + last / P.G + 1, max(base + k * RT / P.G, 0));
+    const int base = q.kv - q.n, r0 = k << P.own_rt_log2;
+    const int last = min(r0 + (1 << P.own_rt_log2), q.n * P.G) - 1;
+    return key_tiles<KT>(P, P.shared_len, base + last / P.G + 1, max(base + r0 / P.G, 0));
 }
+// Row tiles of n rows of G query heads.
+__device__ __forceinline__ int row_tiles(int rows, int rt_log2) { return (rows + (1 << rt_log2) - 1) >> rt_log2; }
 // Units of one head of a request (an item without keys is one unit: its rows are written too).
-template <int RT, int KT>
+template <int KT>
 __device__ __forceinline__ int own_units(const AttendParams &P, const ReqRows &q) {
     int u = 0;
-    for (int k = 0; k * RT < q.n * P.G; ++k) u += max(own_tiles<RT, KT>(P, q, k).n, 1);
+    const int tiles = row_tiles(q.n * P.G, P.own_rt_log2);
+    for (int k = 0; k < tiles; ++k) u += max(own_tiles<KT>(P, q, k).n, 1);
     return u;
 }
 
@@ -118,7 +122,7 @@ struct Totals {
     int64_t own_units;
     int pmin, pmax;  // least and greatest position of the rows (padding aside)
 };
-template <int RT, int KT>
+template <int KT>
 __device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane, bool units) {
     Totals t = {0, INT_MAX, -1};
     for (int i = lane; i < P.B; i += kWarp) {
@@ -127,7 +131,7 @@ __device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane, 
             t.pmin = min(t.pmin, max(q.kv - q.n, 0));
             t.pmax = max(t.pmax, q.kv - 1);
         }
-        if (units) t.own_units += static_cast<int64_t>(P.Hkv) * own_units<RT, KT>(P, q);
+        if (units) t.own_units += static_cast<int64_t>(P.Hkv) * own_units<KT>(P, q);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -157,12 +161,13 @@ struct Segment {
     int head;        // key/value head
     int req;         // request, -1 for prefix items
     int tile, ntile; // first tile and number of tiles of this run
+    int pmin, pmax;  // bounds of the rows' positions (padding aside)
     int64_t part;    // first row of its part in the workspace, or -1: the whole item, written out
     KeyTiles keys;
 };
 
 // Walks a worker's segments. Used by whole warps; every lane holds the same state.
-template <int RT, int KT, bool PREFIX>
+template <int KT, bool PREFIX>
 struct Walker {
     int64_t u, u_end, u_first;
     int worker;
@@ -170,16 +175,19 @@ struct Walker {
     int head_tiles;        // row tiles of a head
     ReqRows q;
     KeyTiles shared;       // prefix items: all alike
+    int pmin, pmax;
 
     __device__ __forceinline__ void start(const AttendParams &P, int w, int lane) {
         worker = w;
-        const Totals t = batch_totals<RT, KT>(P, lane, !PREFIX);
+        const Totals t = batch_totals<KT>(P, lane, !PREFIX);
         head = k = tile = i = 0;
         q = {0, 0, 0};
         if constexpr (PREFIX) {
             shared = prefix_tiles<KT>(P, t);
+            pmin = t.pmin;
+            pmax = t.pmax;
             q.n = P.T;
-            head_tiles = (P.T * P.G + RT - 1) / RT;
+            head_tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
             const int per = max(shared.n, 1);
             const int64_t total = static_cast<int64_t>(P.Hkv) * head_tiles * per;
             u = first_unit(total, w, P.prefix_workers);
@@ -199,7 +207,7 @@ struct Walker {
             for (int i0 = 0; i0 < P.B && (record || !found); i0 += kWarp) {
                 const int r = i0 + lane;
                 int64_t mine = 0;
-                if (r < P.B) mine = static_cast<int64_t>(P.Hkv) * own_units<RT, KT>(P, load_request(P, r));
+                if (r < P.B) mine = static_cast<int64_t>(P.Hkv) * own_units<KT>(P, load_request(P, r));
                 int64_t incl = mine;
 #pragma unroll
                 for (int o = 1; o < kWarp; o <<= 1) {
@@ -220,12 +228,12 @@ struct Walker {
             if (record && lane == 0) P.unit_prefix[0] = 0;
             if (u < u_end) {
                 q = load_request(P, i);
-                head_tiles = (q.n * P.G + RT - 1) / RT;
-                const int per_head = own_units<RT, KT>(P, q);
+                head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
+                const int per_head = own_units<KT>(P, q);
                 head = static_cast<int>(rem / per_head);
                 rem -= static_cast<int64_t>(head) * per_head;
                 for (;; ++k) {
-                    const int nt = max(own_tiles<RT, KT>(P, q, k).n, 1);
+                    const int nt = max(own_tiles<KT>(P, q, k).n, 1);
                     if (rem < nt || k + 1 >= head_tiles) break;
                     rem -= nt;
                 }
@@ -238,17 +246,20 @@ struct Walker {
     // The next segment, or false at the end of the worker's units.
     __device__ __forceinline__ bool next(const AttendParams &P, Segment &s) {
         if (u >= u_end) return false;
-        s.keys = PREFIX ? shared : own_tiles<RT, KT>(P, q, k);
+        s.keys = PREFIX ? shared : own_tiles<KT>(P, q, k);
         const int units = max(s.keys.n, 1);
         const int take = static_cast<int>(min(static_cast<int64_t>(units - tile), u_end - u));
-        s.row0 = k * RT;
-        s.nrows = min(RT, q.n * P.G - s.row0);
+        const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2;
+        s.row0 = k << rt_log2;
+        s.nrows = min(1 << rt_log2, q.n * P.G - s.row0);
         s.t0 = q.r0;
         s.base = q.kv - q.n;
         s.head = head;
         s.req = PREFIX ? -1 : i;
         s.tile = tile;
         s.ntile = min(take, s.keys.n);
+        s.pmin = PREFIX ? pmin : max(s.base + s.row0 / P.G, 0);
+        s.pmax = PREFIX ? pmax : s.base + (s.row0 + s.nrows - 1) / P.G;
         const bool whole = take == units;
         if (P.shared_len > 0) {
             // along a class's units either the item or the worker grows from one part to the next, so
@@ -273,7 +284,7 @@ struct Walker {
                         do {
                             q = load_request(P, ++i);
                         } while (q.n == 0 && i + 1 < P.B);
-                        head_tiles = (q.n * P.G + RT - 1) / RT;
+                        head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
                     }
                 }
             }
