@@ -15,8 +15,9 @@
 
 #include "spec_attend.h"
 #include "spec_attend_fma.cuh"
-#include "spec_attend_mma.cuh"
+#include "spec_attend_pair.cuh"
 #include "spec_attend_plan.cuh"
+#include "spec_attend_round.cuh"
 #include "spec_device.cuh"
 #include "spec_paged.cuh"
 
@@ -28,22 +29,15 @@ constexpr int kSMs = 152;
 
 constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * kWarp, kJoinRows = 16;
 
-// Parts of one row: part x < n of a run of workers, w0 + x. Along a run a worker's first unit is its own
-// or the item's start.
+// Parts of one row: part x < n comes from worker w0 + x.
 struct PartRun {
-    int w0, n, workers;
-    int64_t total, start;  // units of the class, the item's first unit
-    int64_t base;          // shared-prefix calls: rows of the items before, + the row
+    int w0, n;
+    int64_t base;  // part 0's row in the workspace, the first and the later workers' parts apart
+    int64_t later;
     int pitch;
-    bool pairs;            // parts sit in two slots per worker (calls without a shared prefix)
 
-    // Row of part x in the workspace, or -1 for a worker without units.
     __device__ __forceinline__ int64_t row(int x) const {
-        const int w = w0 + x;
-        const int64_t u0 = first_unit(total, w, workers);
-        if (first_unit(total, w + 1, workers) == u0) return -1;
-        if (!pairs) return base + static_cast<int64_t>(w) * pitch;
-        return base + static_cast<int64_t>(2 * w + (u0 < start ? 1 : 0)) * pitch;
+        return (x == 0 ? base : later) + static_cast<int64_t>(x) * pitch;
     }
 };
 
@@ -55,7 +49,7 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
     float M = -INFINITY;
     for (int x = lane; x < n; x += kWarp) {
         const int64_t r = x < a.n ? a.row(x) : b.row(x - a.n);
-        if (r >= 0 && SPEC_IN(r, P.part_rows, DBG_ATTEND)) M = fmaxf(M, P.part_ml[r].x);
+        if (SPEC_IN(r, P.part_rows, DBG_ATTEND)) M = fmaxf(M, P.part_ml[r].x);
     }
     M = warp_max(M);
     float4 o[2] = {};
@@ -63,11 +57,11 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
     if (M != -INFINITY) {
         for (int x0 = 0; x0 < n; x0 += kWarp) {
             const int x = x0 + lane;
-            int64_t r = -1;
+            int64_t r = 0;
             float w = 0.0f;
             if (x < n) {
                 r = x < a.n ? a.row(x) : b.row(x - a.n);
-                if (r >= 0 && SPEC_IN(r, P.part_rows, DBG_ATTEND)) {
+                if (SPEC_IN(r, P.part_rows, DBG_ATTEND)) {
                     const float2 ml = P.part_ml[r];
                     w = ex2(ml.x - M);
                     L += w * ml.y;
@@ -78,7 +72,7 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
             for (int j = 0; j < cnt; ++j) {
                 const float wj = __shfl_sync(0xffffffffu, w, j);
                 const int64_t rj = __shfl_sync(0xffffffffu, r, j);
-                if (wj == 0.0f) continue;  // takes no part (or holds nothing)
+                if (wj == 0.0f) continue;  // holds nothing
                 const float *src = P.part_o + rj * P.D;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -104,15 +98,6 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
     }
     if (lane == 0 && P.lse)
         P.lse[static_cast<int64_t>(t) * P.Hq + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-}
-
-// The run of workers that share units [start, start + units).
-__device__ __forceinline__ void run_of(PartRun &r, int64_t total, int workers, int64_t start, int64_t units) {
-    r.total = total;
-    r.workers = workers;
-    r.start = start;
-    r.w0 = unit_owner(total, start, workers);
-    r.n = unit_owner(total, start + units - 1, workers) - r.w0 + 1;
 }
 
 // Blocks [0, B): request i's status goes out, and the rows of a request in error become 0 / -inf.
@@ -143,14 +128,15 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
         return;
     }
     const int blk = blockIdx.x - P.B;
-    const int64_t total = P.unit_prefix[P.B];
+    const int total = P.unit_prefix[P.B];
     PartRun own = {}, pre = {};
     if (P.shared_len == 0) {
         if (total == 0) return;
         const int per = (P.own_pitch + kJoinRows - 1) / kJoinRows;
         const int c = blk / per + 1;  // the border between workers c - 1 and c
-        const int64_t u = first_unit(total, c, P.own_workers);
-        if (u >= total || u == first_unit(total, c - 1, P.own_workers)) return;
+        const Shares share(total, P.own_workers);
+        if (c >= share.workers) return;
+        const int u = share.first(c);
         // the item with unit u
         int lo = 0, n = P.B;
         while (n > 1) {
@@ -164,9 +150,8 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
         }
         const ReqRows q = load_request(P, lo);
         const int per_head = own_units<KT>(P, q);
-        const int64_t rem = u - P.unit_prefix[lo];
-        const int head = static_cast<int>(rem / per_head);
-        int64_t start = P.unit_prefix[lo] + static_cast<int64_t>(head) * per_head;
+        const int head = (u - P.unit_prefix[lo]) / per_head;
+        int start = P.unit_prefix[lo] + head * per_head;
         int k = 0, units = 0;
         for (;; ++k) {
             units = max(own_tiles<KT>(P, q, k).n, 1);
@@ -174,23 +159,29 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
             start += units;
         }
         // nothing is cut here, or an earlier border has the item
-        if (start == u || first_unit(total, c - 1, P.own_workers) > start) return;
+        const int before = share.first(c - 1);
+        if (start == u || before > start) return;
         if (P.status[lo] != SPEC_REQ_OK) return;
-        run_of(own, total, P.own_workers, start, units);
-        own.pairs = true;
-        own.pitch = P.own_pitch;
+        // the item begins in worker c - 1: in its first segment (slot 0) when that starts with it, else in its
+        // last (slot 1); the others begin with it
+        own.w0 = c - 1;
+        own.n = share.owner(start + units - 1) - own.w0 + 1;
+        own.pitch = 2 * P.own_pitch;
         const int first = (blk % per) * kJoinRows;
         const int r0 = k << P.own_rt_log2, rows = min(1 << P.own_rt_log2, q.n * P.G - r0);
         for (int r = first + warp; r < min(first + kJoinRows, rows); r += kJoinWarps) {
-            own.base = r;
+            own.later = static_cast<int64_t>(2 * own.w0) * P.own_pitch + r;
+            own.base = own.later + (before < start ? P.own_pitch : 0);
             const int j = (r0 + r) / P.G, g = r0 + r - j * P.G;
             join_row<E>(P, own, pre, q.r0 + j, head * P.G + g, lane);
         }
         return;
     }
-    const Totals t = batch_totals<KT>(P, lane, false);
+    const Totals t = batch_totals<KT>(P, lane);
     const int pre_units = max(prefix_tiles<KT>(P, t).n, 1);
     const int tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
+    const Shares share(total, P.own_workers);
+    const Shares pre_share(P.Hkv * tiles * pre_units, P.prefix_workers);
     for (int x = 0; x < kJoinRows / kJoinWarps; ++x) {
         const int64_t row = static_cast<int64_t>(blk) * kJoinRows + x * kJoinWarps + warp;
         if (row >= static_cast<int64_t>(P.T) * P.Hq) return;
@@ -201,19 +192,24 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
         if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) continue;
         {
             const int pr = tok * P.G + g, k = pr >> P.prefix_rt_log2;
-            const int64_t start = (static_cast<int64_t>(head) * tiles + k) * pre_units;
-            run_of(pre, static_cast<int64_t>(P.Hkv) * tiles * pre_units, P.prefix_workers, start, pre_units);
+            const int start = (head * tiles + k) * pre_units;
+            pre.w0 = pre_share.owner(start);
+            pre.n = pre_share.owner(start + pre_units - 1) - pre.w0 + 1;
             pre.pitch = P.prefix_pitch;
-            pre.base = static_cast<int64_t>(head) * P.T * P.G + pr;
+            pre.base = pre.later =
+                static_cast<int64_t>(head) * P.T * P.G + pr + static_cast<int64_t>(pre.w0) * P.prefix_pitch;
         }
         {
             const int pr = (tok - q.r0) * P.G + g, k = pr >> P.own_rt_log2;
-            int64_t start = P.unit_prefix[i] + static_cast<int64_t>(head) * own_units<KT>(P, q);
+            int start = P.unit_prefix[i] + head * own_units<KT>(P, q);
             for (int y = 0; y < k; ++y) start += max(own_tiles<KT>(P, q, y).n, 1);
-            run_of(own, total, P.own_workers, start, max(own_tiles<KT>(P, q, k).n, 1));
+            own.w0 = share.owner(start);
+            own.n = share.owner(start + max(own_tiles<KT>(P, q, k).n, 1) - 1) - own.w0 + 1;
             own.pitch = P.own_pitch;
-            own.base = static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
-                       (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + pr;
+            own.base = own.later = static_cast<int64_t>(P.T) * P.Hq +
+                                   static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
+                                   (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + pr +
+                                   static_cast<int64_t>(own.w0) * P.own_pitch;
         }
         join_row<E>(P, pre, own, tok, h, lane);
     }
@@ -234,7 +230,7 @@ static AttendLayout attend_layout(const AttendParams &P) {
         return o;
     };
     L.status = take(static_cast<size_t>(P.B) * 4);
-    L.unit_prefix = take((static_cast<size_t>(P.B) + 1) * 8);
+    L.unit_prefix = take((static_cast<size_t>(P.B) + 1) * 4);
     L.err = take(static_cast<size_t>(P.own_workers + P.prefix_workers) * 4);
     L.ml = take(static_cast<size_t>(P.part_rows) * 8);
     L.o = take(static_cast<size_t>(P.part_rows) * P.D * 4);
@@ -258,6 +254,11 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
         static_cast<int64_t>(a->max_blocks) * a->page_size > INT_MAX / 2 || a->shared_len > INT_MAX / 2 ||
         a->n_q_heads > 65536)
         return SPEC_ERR_UNSUPPORTED;
+    // and so are the units of work, at their most with the smallest items and tiles (16 rows, 32 positions)
+    const int64_t most_tiles = std::max<int64_t>(static_cast<int64_t>(a->max_blocks) * a->page_size, a->shared_len) / 32 + 2;
+    const int64_t head_tiles =
+        static_cast<int64_t>(a->total_rows) * (a->n_q_heads / a->n_kv_heads) / fma::kRT + a->B + 1;
+    if (head_tiles * a->n_kv_heads > INT_MAX / most_tiles) return SPEC_ERR_UNSUPPORTED;
     P.B = a->B;
     P.T = a->total_rows;
     P.Hq = a->n_q_heads;
@@ -278,21 +279,28 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
     return SPEC_OK;
 }
 
-// Workers and parts of the kernel that serves the call.
+// Rows of an item (as a power of two) and workers for `rows` packed rows of a head over `groups` requests
+// on the tensor cores: the round kernel's items of 32 or 64 rows while that holds an average request,
+// give or take, else the pair kernel's of 256.
+static void tensor_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
+    rt_log2 = rows <= 24 * groups ? 5 : rows <= 96 * groups ? 6 : pair::kRTLog2;
+    workers = rt_log2 == pair::kRTLog2 ? kSMs : kSMs * round_::kPerSM;
+}
+
+// Workers and parts of the kernels that serve the call.
 static void attend_work(AttendParams &P, bool tensor) {
     const int64_t head_rows = static_cast<int64_t>(P.T) * P.G;
     if (tensor) {
-        // one accumulator holds 128 rows. Beyond that (own items: on average over the requests) items of
-        // 256 rows share their tiles between both accumulators of an SM; below it each accumulator is
-        // a worker.
-        const bool own_pair = head_rows > 128 * static_cast<int64_t>(P.B), prefix_pair = head_rows > 128;
-        P.own_rt_log2 = own_pair ? 8 : 7;
-        P.own_workers = own_pair ? kSMs : 2 * kSMs;
-        P.prefix_rt_log2 = prefix_pair ? 8 : 7;
-        P.prefix_workers = prefix_pair ? kSMs : 2 * kSMs;
+        tensor_class(head_rows, P.B, P.own_rt_log2, P.own_workers);
+        tensor_class(head_rows, 1, P.prefix_rt_log2, P.prefix_workers);
+        // boxes of slots: the largest power of two that divides the page, from 8 to a tile
+        P.box_log2 = 0;
+        for (int b = 3; b <= 7; ++b)
+            if (P.page_size % (1 << b) == 0) P.box_log2 = b;
     } else {
         P.own_rt_log2 = P.prefix_rt_log2 = fma::kRTLog2;
         P.own_workers = P.prefix_workers = kSMs * fma::ctas_per_sm(P.D);
+        P.box_log2 = 0;
     }
     if (P.shared_len == 0) P.prefix_workers = 0;
     P.own_pitch = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(1 << P.own_rt_log2, head_rows)));
@@ -307,7 +315,7 @@ static void attend_work(AttendParams &P, bool tensor) {
 // The cache as two-dimensional tensor maps of slots, where its strides allow it: pages a whole number of
 // slots apart, heads inside a slot or a whole number of slots apart. bf16, head sizes the matrix
 // instructions take.
-static bool cache_map(const spec_attend_args *a, mma::CacheMap &M, int64_t &rows, int64_t &cols) {
+static bool cache_map(const spec_attend_args *a, tiles::CacheMap &M, int64_t &rows, int64_t &cols) {
     if (a->dtype != SPEC_BF16 || a->head_dim % 16 != 0 || a->head_dim > 128) return false;
     const int64_t slot = a->slot_stride, D = a->head_dim, heads = a->n_kv_heads;
     if (slot <= 0 || (a->n_pages > 1 && a->page_stride % slot != 0)) return false;
@@ -348,26 +356,44 @@ static EncodeTiled encode_tiled() {
     return fn;
 }
 
-static bool encode_map(CUtensorMap &map, const void *cache, int64_t rows, int64_t cols, int64_t slot_stride) {
+// box_rows: slots of a copied box (1 for gathering copies).
+static bool encode_map(CUtensorMap &map, const void *cache, int64_t rows, int64_t cols, int64_t slot_stride, int box_rows) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(slot_stride) * 2};
-    const cuuint32_t box[2] = {64, 1}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
     return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(cache), dims, strides, box, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool PAIR, bool PREFIX>
-static cudaError_t launch_mma(const AttendParams &P, const mma::CacheMap &M, const CUtensorMap &k, const CUtensorMap &v,
-                              cudaStream_t stream) {
-    const int smem = mma::smem_bytes(P.D);
-    const cudaError_t e = cudaFuncSetAttribute(mma::spec_attend_mma_kernel<PAIR, PREFIX>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+struct CacheMaps {
+    tiles::CacheMap where;
+    CUtensorMap k, v;
+};
+
+template <typename Kernel>
+static cudaError_t launch_tensor(Kernel *kernel, int ctas, int threads, int smem, int stages, const AttendParams &P,
+                                 const CacheMaps &M, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(mma::spec_attend_mma_kernel<PAIR, PREFIX>, dim3(kSMs), dim3(mma::kThreads),
-                        static_cast<size_t>(smem), stream, P, M, k, v, mma::stages(P.D));
+    return launch_after(kernel, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
+                        static_cast<size_t>(smem), stream, P, M.where, M.k, M.v, stages);
+}
+
+// One class of items on the tensor cores.
+template <bool PREFIX>
+static cudaError_t launch_class(const AttendParams &P, const CacheMaps &M, cudaStream_t stream) {
+    const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2, workers = PREFIX ? P.prefix_workers : P.own_workers;
+    if (rt_log2 == 5)
+        return launch_tensor(round_::spec_attend_round_kernel<32, PREFIX>, workers, round_::kThreads,
+                             round_::smem_bytes<32>(P.D), round_::stages<32>(P.D), P, M, stream);
+    if (rt_log2 == 6)
+        return launch_tensor(round_::spec_attend_round_kernel<64, PREFIX>, workers, round_::kThreads,
+                             round_::smem_bytes<64>(P.D), round_::stages<64>(P.D), P, M, stream);
+    return launch_tensor(pair::spec_attend_pair_kernel<PREFIX>, workers, pair::kThreads, pair::smem_bytes(P.D),
+                         pair::stages(P.D), P, M, stream);
 }
 
 template <typename E, int NC, bool PREFIX>
@@ -391,14 +417,11 @@ static cudaError_t launch_join(const AttendParams &P, cudaStream_t stream) {
                         dim3(kJoinThreads), 0, stream, P);
 }
 
-static cudaError_t enqueue_mma(const AttendParams &P, const mma::CacheMap &M, const CUtensorMap &k,
-                               const CUtensorMap &v, cudaStream_t stream) {
+static cudaError_t enqueue_tensor(const AttendParams &P, const CacheMaps &M, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
-    if (P.shared_len > 0)
-        e = P.prefix_rt_log2 == 8 ? launch_mma<true, true>(P, M, k, v, stream) : launch_mma<false, true>(P, M, k, v, stream);
-    if (e == cudaSuccess)
-        e = P.own_rt_log2 == 8 ? launch_mma<true, false>(P, M, k, v, stream) : launch_mma<false, false>(P, M, k, v, stream);
-    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, mma::kKT>(P, stream);
+    if (P.shared_len > 0) e = launch_class<true>(P, M, stream);
+    if (e == cudaSuccess) e = launch_class<false>(P, M, stream);
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, tiles::kKT>(P, stream);
     return e;
 }
 
@@ -430,9 +453,11 @@ extern "C" size_t spec_attend_workspace_size(const spec_attend_args *a) {
 extern "C" const char *spec_attend_plan(const spec_attend_args *a) {
     AttendParams P = {};
     if (attend_sizes(a, P) != SPEC_OK) return nullptr;
-    mma::CacheMap M = {};
+    tiles::CacheMap M = {};
     int64_t rows = 0, cols = 0;
-    return cache_map(a, M, rows, cols) ? "spec_attend_mma_kernel" : "spec_attend_fma_kernel";
+    if (!cache_map(a, M, rows, cols)) return "spec_attend_fma_kernel";
+    attend_work(P, true);
+    return P.own_rt_log2 == pair::kRTLog2 ? "spec_attend_pair_kernel" : "spec_attend_round_kernel";
 }
 
 extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, size_t workspace_bytes,
@@ -451,9 +476,9 @@ extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, s
     if ((a->q_stride | a->out_stride | a->page_stride | a->slot_stride | a->head_stride) % vec != 0 || !aligned(a->q) ||
         !aligned(a->out) || !aligned(a->k_cache) || !aligned(a->v_cache))
         return SPEC_ERR_UNSUPPORTED;
-    mma::CacheMap M = {};
+    CacheMaps M = {};
     int64_t map_rows = 0, map_cols = 0;
-    const bool tensor = cache_map(a, M, map_rows, map_cols);
+    const bool tensor = cache_map(a, M.where, map_rows, map_cols);
     attend_work(P, tensor);
     const AttendLayout L = attend_layout(P);
     if (!workspace || workspace_bytes < spec_attend_workspace_size(a) || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
@@ -475,16 +500,16 @@ extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, s
     P.lse = a->lse;
     P.req_status = a->req_status;
     P.status = reinterpret_cast<int32_t *>(ws + L.status);
-    P.unit_prefix = reinterpret_cast<int64_t *>(ws + L.unit_prefix);
+    P.unit_prefix = reinterpret_cast<int32_t *>(ws + L.unit_prefix);
     P.err = reinterpret_cast<int32_t *>(ws + L.err);
     P.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     P.part_o = reinterpret_cast<float *>(ws + L.o);
     if (tensor) {
-        CUtensorMap k, v;
-        if (!encode_map(k, a->k_cache, map_rows, map_cols, a->slot_stride) ||
-            !encode_map(v, a->v_cache, map_rows, map_cols, a->slot_stride))
+        const int box = 1 << P.box_log2;
+        if (!encode_map(M.k, a->k_cache, map_rows, map_cols, a->slot_stride, box) ||
+            !encode_map(M.v, a->v_cache, map_rows, map_cols, a->slot_stride, box))
             return SPEC_ERR_CUDA;
-        return enqueue_mma(P, M, k, v, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+        return enqueue_tensor(P, M, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
     }
     const cudaError_t e =
         a->dtype == SPEC_BF16 ? enqueue_fma<__nv_bfloat16>(P, stream) : enqueue_fma<float>(P, stream);

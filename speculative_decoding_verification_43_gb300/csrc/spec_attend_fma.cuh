@@ -64,7 +64,7 @@ struct Rows {
 // One tile for NR of the warp's rows. full: every row sees every key of the tile.
 template <int NR, int NC>
 __device__ __forceinline__ void tile_step(const AttendParams &P, Rows<NC> &R, const float *sQ, const float *sK,
-                                          const float *sV, float *sP, int x0, int hi, int warp, int lane) {
+                                          const float *sV, float *sP, int x0, const KeyTiles &keys, int warp, int lane) {
     const int D = P.D;
     float s[NR];
 #pragma unroll
@@ -84,7 +84,7 @@ __device__ __forceinline__ void tile_step(const AttendParams &P, Rows<NC> &R, co
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const int p = R.pos[r];
-        const bool vis = x < hi && x <= p && (P.window == 0 || x > p - P.window || x < P.n_sink);
+        const bool vis = x >= keys.from && x < keys.hi && x <= p && (P.window == 0 || x > p - P.window || x < P.n_sink);
         seen[r] = __ballot_sync(0xffffffffu, vis);
         all &= seen[r];
         const float z = vis ? s[r] * P.scale_log2 : -INFINITY;
@@ -213,10 +213,10 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
             const int x0 = tile_begin<kKT>(s.keys, s.tile + t);
             const float *k = sK + b * kKT * (D + 4), *v = sV + b * kKT * D;
             switch (nr) {
-                case 1: tile_step<1, NC>(P, R, sQ, k, v, sP, x0, s.keys.hi, warp, lane); break;
-                case 2: tile_step<2, NC>(P, R, sQ, k, v, sP, x0, s.keys.hi, warp, lane); break;
-                case 3: tile_step<3, NC>(P, R, sQ, k, v, sP, x0, s.keys.hi, warp, lane); break;
-                case 4: tile_step<4, NC>(P, R, sQ, k, v, sP, x0, s.keys.hi, warp, lane); break;
+                case 1: tile_step<1, NC>(P, R, sQ, k, v, sP, x0, s.keys, warp, lane); break;
+                case 2: tile_step<2, NC>(P, R, sQ, k, v, sP, x0, s.keys, warp, lane); break;
+                case 3: tile_step<3, NC>(P, R, sQ, k, v, sP, x0, s.keys, warp, lane); break;
+                case 4: tile_step<4, NC>(P, R, sQ, k, v, sP, x0, s.keys, warp, lane); break;
                 default: break;
             }
             __syncthreads();
@@ -251,11 +251,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
             }
         }
     }
-    if constexpr (!PREFIX)
-        for (int i = blockIdx.x * kWarps + warp; i < P.B; i += gridDim.x * kWarps) {
-            const int st = attend_status(P, i, lane);
-            if (lane == 0 && SPEC_IN(i, P.B, DBG_ATTEND)) P.status[i] = st;
-        }
+    if (!PREFIX && warp == kWarps - 1) keep_books<kKT>(P, lane);
     if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = 0;
 }
 

@@ -1,0 +1,431 @@
+// Attention of many rows on the tensor cores (bf16, head sizes that are multiples of 16 up to 128): long
+// prompts, and the shared prefix, whose rows are those of the whole batch.
+//
+// One CTA per SM, an item of 256 packed rows in two accumulators of 128 that use the same tiles. Per
+// tile of 128 keys and accumulator:
+//   S = Q K^T      tcgen05.mma, both operands in shared memory, S (fp32) in tensor memory
+//   P = 2^(S - m)  a warpgroup, one row per thread; P (bf16) goes back over S's columns
+//   O += P V       tcgen05.mma, P read from tensor memory, V from shared memory
+// One accumulator's products run while the other's softmax does.
+// A row's m is a reference, not the running maximum: O and the sum are rescaled only when the maximum
+// has grown by more than 2^8 beyond it (P then stays below 2^8, whose bf16 rounding is relative all the
+// same), so the output hardly ever leaves tensor memory before the end.
+//
+// Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 keeps the books (the requests' status), 10 and
+// 11 issue matrix instructions (for accumulator 0 and 1).
+#pragma once
+
+#include "spec_attend_tiles.cuh"
+
+namespace spec {
+namespace pair {
+
+using namespace tiles;
+
+constexpr int kRTLog2 = 8, kRows = 128;  // rows of an item, of an accumulator
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.0f;           // log2 growth of the maximum that O and the sum absorb
+
+struct Shared {
+    Pipe<kMaxStages> pipe;
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], agree[2], drain[2];
+    uint32_t bad[2][2][4];  // per warp: its quarter of the values holds one that is not finite
+    uint32_t skip[2];       // the warpgroup has done this tile's second product itself
+    uint32_t tmem;
+};
+
+__host__ constexpr int stages(int D) {
+    const int n = (227 * 1024 - 1024 - static_cast<int>(sizeof(Shared)) - 2 * tile_bytes(D)) / tile_bytes(D);
+    return n < kMaxStages ? n : kMaxStages;
+}
+__host__ constexpr int smem_bytes(int D) {
+    return 1024 + (2 + stages(D)) * tile_bytes(D) + static_cast<int>(sizeof(Shared));
+}
+
+// ---------------------------------------------------------------- matrix instructions (one thread)
+
+__device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsigned char *q_tile, unsigned char *ring_mem,
+                                         int w, int n_stages) {
+    const int tb = tile_bytes(P.D);
+    int32_t *ab = &sh.pipe.abort;
+    const uint32_t s_col = sh.tmem + w * 256, o_col = s_col + 128, p_col = s_col;
+    const uint32_t q_addr = smem_addr(q_tile), t_addr = smem_addr(ring_mem);
+    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    uint32_t q_phase = 0, p_phase = 0;
+    const uint32_t pv_shape = mma_shape(P.D, false, true);
+    auto score = [&](int n) {  // S = Q K^T
+        const uint32_t k_addr = t_addr + ring.slot * tb;
+        const uint32_t shape = mma_shape(n, false, false);
+        for (int d = 0; d < P.D; d += 16) {
+            const uint32_t at = (d >> 6) * kBlock + (d & 63) * 2;
+            mma_ss(s_col, smem_operand(q_addr + at, 16), smem_operand(k_addr + at, 16), shape, d > 0);
+        }
+        mma_commit(&sh.s_full[w]);
+        mma_commit(&sh.pipe.empty[ring.slot]);
+        ring.step();
+    };
+    for (;;) {
+        if (!wait_one(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
+        const Segment &s = sh.pipe.desc[desc.slot];
+        if (s.nrows == 0) return;
+        const int nt = s.ntile;
+        if (nt > 0 && s.nrows <= w * kRows) {
+            for (int t = 0; t < 2 * nt; ++t) {  // no rows for this accumulator: let the tiles go by
+                if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                mbar_arrive(&sh.pipe.empty[ring.slot]);
+                ring.step();
+            }
+        } else if (nt > 0) {
+            if (!wait_one(ab, &sh.q_full[w], q_phase)) return;
+            q_phase ^= 1u;
+            if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+            tc_fence_after();
+            int n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile));
+            score(n);
+            for (int t = 0; t < nt; ++t) {
+                if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                if (!wait_one(ab, &sh.p_full[w], p_phase)) return;
+                p_phase ^= 1u;
+                tc_fence_after();
+                if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w])) {  // O += P V
+                    const uint32_t v_addr = t_addr + ring.slot * tb;
+                    for (int k = 0; k < n; k += 16)
+                        mma_ts(o_col, p_col + k / 2, smem_operand(v_addr + k * 128, kBlock), pv_shape, t > 0 || k > 0);
+                }
+                mma_commit(&sh.pipe.empty[ring.slot]);
+                ring.step();
+                if (t + 1 < nt) {
+                    if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                    tc_fence_after();
+                    // S and P share columns: matrix instructions of one thread run in the order of
+                    // their issue, so this one follows the product that reads P
+                    n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile + t + 1));
+                    score(n);
+                } else {
+                    mma_commit(&sh.o_full[w]);
+                }
+            }
+        }
+        mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        desc.step();
+    }
+}
+
+// ---------------------------------------------------------------- softmax (one row per thread)
+
+// The second product of a tile with values that are not finite, on the fp32 units: the row's weights
+// are in tensor memory already, O is complete up to the tile before. first: O holds nothing yet.
+__device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr, const unsigned char *v_tile, int x0, int n,
+                                        int from, int lim, int wlo, int sinks, bool first) {
+#pragma unroll 1
+    for (int d = 0; d < D; d += 16) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(o, o_addr + d);
+        tmem_wait_ld();
+        if (first)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < n; k += 32) {
+            float p[16];
+            __syncwarp();
+            tmem_ld16(p, p_addr + k / 2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int x = x0 + k + e;
+                if (k + e < n && x >= from && x <= lim && (x >= wlo || x < sinks)) {
+                    const uint32_t pw = __float_as_uint(p[e / 2]);
+                    const float w = __uint_as_float(e % 2 ? pw & 0xffff0000u : pw << 16);
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) o[i] = fmaf(w, tile_value(v_tile, k + e, d + i), o[i]);
+                }
+            }
+        }
+        uint32_t ow[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e]);
+        __syncwarp();
+        tmem_st16(o_addr + d, ow);
+        tmem_wait_st();
+    }
+}
+
+template <bool PREFIX>
+__device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, unsigned char *q_tile,
+                                             unsigned char *ring_mem, int w, int n_stages) {
+    const int tid = threadIdx.x % 128, warp = tid / kWarp, lane = tid % kWarp;
+    const int tb = tile_bytes(P.D);
+    int32_t *ab = &sh.pipe.abort;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t s_addr = sh.tmem + w * 256 + lanes, o_addr = s_addr + 128;
+    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    uint32_t s_phase = 0, o_phase = 0, agree_phase = 0;
+    for (;;) {
+        if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
+        const Segment &s = sh.pipe.desc[desc.slot];
+        if (s.nrows == 0) return;
+        const int off = w * kRows;
+        const int mine = min(max(s.nrows - off, 0), kRows);  // rows of this accumulator
+        const bool have = tid < mine;
+        const bool warp_has = warp * kWarp < mine;
+        const int nt = s.ntile;
+        // this thread's row
+        const int pr = s.row0 + off + tid, j = pr / P.G, g = pr - j * P.G;
+        const int t = s.t0 + j, h = s.head * P.G + g;
+        float m = -INFINITY, l = 0.0f;  // reference (scores, unscaled) and sum
+        bool dead = true;               // no position, or no keys at all
+        if (mine > 0 && nt > 0) {
+            // its query into the swizzled tile
+            if (have && SPEC_IN(t, P.T, DBG_ATTEND)) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) +
+                                                                   t * P.q_stride + static_cast<int64_t>(h) * P.D);
+#pragma unroll 4
+                for (int c = 0; c < P.D / 8; ++c)
+                    *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * kBlock + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
+                        src[c];
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.q_full[w]);
+            int p = -1;
+            if (have) {
+                if constexpr (PREFIX) {
+                    int lo = 0, n = P.B;  // the row's request
+                    while (n > 1) {
+                        const int half = n / 2;
+                        if (P.row_off[lo + half] <= t) {
+                            lo += half;
+                            n -= half;
+                        } else {
+                            n = half;
+                        }
+                    }
+                    const ReqRows q = load_request(P, lo);
+                    if (t >= q.r0 && t < q.r0 + q.n) p = q.kv - q.n + (t - q.r0);
+                } else {
+                    p = s.base + j;
+                }
+            }
+            dead = p < 0;
+            const int lim = min(p, s.keys.hi - 1), wlo = P.window > 0 ? p - P.window + 1 : 0;
+            for (int i = 0; i < nt; ++i) {
+                const int x0 = tile_begin<kKT>(s.keys, s.tile + i), n = tile_keys(s.keys, x0);
+                const bool edge = edge_tile(P, s, x0);
+                const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
+                const uint32_t v_phase = ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase;
+                bool skip = false;
+                if (edge) {
+                    if (!wait_warp(ab, &sh.pipe.full[v_slot], v_phase)) return;
+                    const bool bad =
+                        __any_sync(0xffffffffu, clean_values(P, s.keys, ring_mem + v_slot * tb, x0, n, tid));
+                    fence_proxy_async_smem();
+                    // the four warps' findings (two sets, used in turn)
+                    volatile uint32_t *found = sh.bad[w][agree_phase];
+                    __syncwarp();
+                    if (lane == 0) {
+                        found[warp] = bad;
+                        mbar_arrive(&sh.agree[w]);
+                    }
+                    if (!wait_warp(ab, &sh.agree[w], agree_phase)) return;
+                    agree_phase ^= 1u;
+                    skip = (found[0] | found[1] | found[2] | found[3]) != 0;
+                }
+                if (!wait_warp(ab, &sh.s_full[w], s_phase)) return;
+                s_phase ^= 1u;
+                tc_fence_after();
+                if (warp_has) {
+                    float z[kKT];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c * 32 < n) tmem_ld32(z + 32 * c, s_addr + 32 * c);
+                    tmem_wait_ld();
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < kKT; ++e) {
+                            const int x = x0 + e;
+                            if (!(x >= s.keys.from && x <= lim && (x >= wlo || x < P.n_sink))) z[e] = -INFINITY;
+                        }
+                    }
+                    float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+                    for (int e = 4; e < kKT; e += 8)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            mx[a] = e + 4 + a < kKT ? fmaxf(mx[a], fmaxf(z[e + a], z[e + 4 + a])) : fmaxf(mx[a], z[e + a]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // a new reference when the old one is too low (or there was none)
+                    const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack);
+                    if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                        const float a = grow && m != -INFINITY ? ex2((m - top) * P.scale_log2) : 1.0f;
+                        l *= a;
+                        // S is complete, and with it the product of the tile before: O is at rest
+#pragma unroll 1
+                        for (int d = 0; d < P.D; d += 16) {
+                            float o[16];
+                            uint32_t ow[16];
+                            tmem_ld16(o, o_addr + d);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * a);
+                            tmem_st16(o_addr + d, ow);
+                        }
+                        tmem_wait_st();
+                    }
+                    if (grow) m = top;
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+                    const float2 rf = make_float2(-ref * P.scale_log2, -ref * P.scale_log2);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c * 32 < n) {
+                            uint32_t pw[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 y = fma2(make_float2(z[32 * c + 2 * e], z[32 * c + 2 * e + 1]), sc, rf);
+                                y.x = ex2(y.x);
+                                y.y = ex2(y.y);
+                                sum[e & 1] = add2(sum[e & 1], y);
+                                pw[e] = pack_bf16(y.x, y.y);
+                            }
+                            tmem_st16(s_addr + 16 * c, pw);
+                        }
+                    }
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+                    tmem_wait_st();
+                    if (skip)
+                        mixed_tile(P.D, s_addr, o_addr, ring_mem + v_slot * tb, x0, n, s.keys.from, lim, wlo, P.n_sink,
+                                   i == 0);
+                }
+                if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[w]);
+                ring.step();
+                ring.step();
+            }
+            if (!wait_warp(ab, &sh.o_full[w], o_phase)) return;
+            o_phase ^= 1u;
+            tc_fence_after();
+        } else {
+            for (int i = 0; i < 2 * nt; ++i) ring.step();
+        }
+        if (dead) {
+            m = -INFINITY;
+            l = 0.0f;
+        }
+        const bool none = l == 0.0f;
+        const float inv = s.part >= 0 ? 1.0f : 1.0f / l;
+        if (warp_has) {
+#pragma unroll 1
+            for (int d = 0; d < P.D; d += 16) {
+                float o[16];
+                __syncwarp();
+                if (nt > 0) {
+                    tmem_ld16(o, o_addr + d);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * inv;
+                if (!have) continue;
+                if (s.part >= 0) {
+                    if (SPEC_IN(s.part + off + tid, P.part_rows, DBG_ATTEND)) {
+                        float4 *dst = reinterpret_cast<float4 *>(P.part_o + (s.part + off + tid) * P.D + d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                } else if (SPEC_IN(t, P.T, DBG_ATTEND)) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.out) + t * P.out_stride +
+                                                           static_cast<int64_t>(h) * P.D + d);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                            pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                }
+            }
+            if (have) {
+                const float ms = m * P.scale_log2;
+                if (s.part >= 0) {
+                    // a sum that is not a number must reach the joined row, whatever the other parts' maxima
+                    if (SPEC_IN(s.part + off + tid, P.part_rows, DBG_ATTEND))
+                        P.part_ml[s.part + off + tid] = make_float2(isnan(l) ? INFINITY : ms, l);
+                } else if (P.lse && SPEC_IN(t, P.T, DBG_ATTEND)) {
+                    P.lse[static_cast<int64_t>(t) * P.Hq + h] =
+                        none ? -INFINITY : (ms + log2f(l)) * 0.6931471805599453f;
+                }
+            }
+        }
+        tc_fence_before();  // O may be written again once the next segment's P is ready
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        desc.step();
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <bool PREFIX>
+__global__ void __launch_bounds__(kThreads, 1)
+    spec_attend_pair_kernel(const __grid_constant__ AttendParams P, const CacheMap M, const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap, const int n_stages) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const int tb = tile_bytes(P.D);
+    unsigned char *ring_mem = base + 2 * tb;
+    Shared &sh = *reinterpret_cast<Shared *>(ring_mem + n_stages * tb);
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+
+    griddep_launch_dependents();
+    if (warp == 10) tmem_alloc(&sh.tmem, 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < n_stages; ++i) {
+            mbar_init(&sh.pipe.full[i], 1);
+            mbar_init(&sh.pipe.empty[i], 2);  // both accumulators
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.pipe.desc_full[i], 1);
+            mbar_init(&sh.pipe.desc_empty[i], 10);  // eight softmax warps and two issuing threads
+            mbar_init(&sh.q_full[i], 128);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.o_full[i], 1);
+            mbar_init(&sh.agree[i], 4);
+            mbar_init(&sh.drain[i], 1);
+            sh.skip[i] = 0;
+        }
+        sh.pipe.abort = 0;
+        fence_mbar_init();
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+
+    if (warp < 8) {
+        softmax_role<PREFIX>(P, sh, base + (warp / 4) * tb, ring_mem, warp / 4, n_stages);
+    } else if (warp == 8) {
+        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
+    } else if (warp == 9) {
+        if constexpr (!PREFIX) keep_books<kKT>(P, lane);
+    } else if (lane == 0) {
+        const int w = warp - 10;
+        mma_role(P, sh, base + w * tb, ring_mem, w, n_stages);
+        // nothing this thread issued is in flight when the CTA ends
+        mma_commit(&sh.drain[w]);
+#pragma unroll 1
+        for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain[w], 0, kHintNs); ++t) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 10) tmem_free(sh.tmem, 512);
+    if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = sh.pipe.abort;
+}
+
+}  // namespace pair
+}  // namespace spec

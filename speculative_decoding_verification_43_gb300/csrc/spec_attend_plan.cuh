@@ -3,9 +3,9 @@
 //
 // Rows that share a key/value head are packed: row r of a request's head is (row j, query head g of
 // the group) = (r / G, r % G). An item is up to RT packed rows of one head; its keys, in tiles of KT
-// positions, are its units. Units are numbered item after item, and worker w of NW takes the units
-// [total w / NW, total (w+1) / NW): every worker gets the same number of tiles whatever the lengths
-// are, a long context is split over many workers, and the cut depends on the inputs alone. An item
+// positions, are its units. Units are numbered item after item, and worker w of NW takes its
+// share of consecutive units: every worker gets the same number of tiles, give or take one, whatever the
+// lengths are, a long context is split over many workers, and the cut depends on the inputs alone. An item
 // that falls to several workers leaves a part (output, maximum, sum) per worker, and the joining
 // kernel adds the parts in the order of the workers.
 //
@@ -26,6 +26,7 @@ namespace spec {
 struct AttendParams {
     int32_t B, T, Hq, Hkv, G, D;
     int32_t page_size, page_shift;  // page_shift >= 0: page_size is 1 << page_shift
+    int32_t box_log2;               // slots copied as one box (a divisor of page_size), as a power of two
     int32_t max_blocks, n_pages, window, n_sink, shared_len;
     float scale_log2;  // scale * log2(e): the softmax is taken in base 2
     const void *q, *k_cache, *v_cache;
@@ -37,7 +38,7 @@ struct AttendParams {
     int32_t *req_status;
     // workspace
     int32_t *status;       // [B]
-    int64_t *unit_prefix;  // [B+1] units of the own items before each request
+    int32_t *unit_prefix;  // [B+1] units of the own items before each request
     float2 *part_ml;       // [part rows] maximum (base 2, scaled) and sum
     float *part_o;         // [part rows][D] unnormalised output
     int32_t *err;          // [workers of both classes] 1: a bounded wait gave up
@@ -69,22 +70,23 @@ __device__ __forceinline__ int64_t slot_offset(const AttendParams &P, const int3
 }
 
 // The key tiles an item visits: of the tiles of KT positions from lo, the first s (the sinks), then
-// those from w_first on (the window); n in all. Positions in [lo, hi) at or above win, or below the
-// sinks, are seen by some row of the item; pad is one of them.
+// those from w_first on (the window); n in all. Some row of the item sees a position of [from, hi) that is
+// at or above win, or below the sinks. lo is from, rounded down so that a copied box of slots
+// (P.box_log2) lies in one page.
 struct KeyTiles {
-    int lo, hi, win, s, w_first, n, pad;
+    int lo, from, hi, win, s, w_first, n;
 };
 template <int KT>
-__device__ __forceinline__ KeyTiles key_tiles(const AttendParams &P, int lo, int hi, int pmin) {
-    KeyTiles t = {lo, hi, lo, 0, 0, 0, lo};
-    if (hi <= lo) return t;
+__device__ __forceinline__ KeyTiles key_tiles(const AttendParams &P, int from, int hi, int pmin) {
+    const int lo = from >> P.box_log2 << P.box_log2;
+    KeyTiles t = {lo, from, hi, from, 0, 0, 0};
+    if (hi <= from) return t;
     const int total = (hi - lo + KT - 1) / KT;
     if (P.window > 0) {
-        t.win = max(lo, pmin - P.window + 1);
-        const int sinks = max(min(P.n_sink, hi) - lo, 0);
+        t.win = max(from, pmin - P.window + 1);
+        const int sinks = min(P.n_sink, hi) - lo;
         t.w_first = t.win < hi ? (t.win - lo) / KT : total;
-        t.s = min((sinks + KT - 1) / KT, t.w_first);
-        t.pad = sinks > 0 ? lo : t.win;
+        t.s = P.n_sink > from ? min((sinks + KT - 1) / KT, t.w_first) : 0;
     }
     t.n = t.s + total - t.w_first;
     return t;
@@ -93,18 +95,20 @@ template <int KT>
 __device__ __forceinline__ int tile_begin(const KeyTiles &t, int i) {
     return t.lo + (i < t.s ? i : i - t.s + t.w_first) * KT;
 }
-// True when some row of the item may see position x.
-__device__ __forceinline__ bool item_sees(const AttendParams &P, const KeyTiles &t, int x) {
-    return x < t.hi && (x >= t.win || x < P.n_sink);
+// True when some row of the item may see a position of [x, x + n).
+__device__ __forceinline__ bool item_sees(const AttendParams &P, const KeyTiles &t, int x, int n = 1) {
+    const int a = max(x, t.from), b = min(x + n, t.hi);
+    return a < b && (b > t.win || a < P.n_sink);
 }
 
 // ---------------------------------------------------------------- items and units
+// Unit numbers are 32-bit: the host refuses sizes that could have more.
 
 template <int KT>
 __device__ __forceinline__ KeyTiles own_tiles(const AttendParams &P, const ReqRows &q, int k) {
-    const int base = q.kv - q.n, r0 = k << P.own_rt_log2;
-    const int last = min(r0 + (1 << P.own_rt_log2), q.n * P.G) - 1;
-    return key_tiles<KT>(P, P.shared_len, base + last / P.G + 1, max(base + r0 / P.G, 0));
+    const int base = q.kv - q.n, r0 = k << P.own_rt_log2, r1 = r0 + (1 << P.own_rt_log2), end = q.n * P.G;
+    const int j0 = k == 0 ? 0 : r0 / P.G, j1 = r1 >= end ? q.n - 1 : (r1 - 1) / P.G;
+    return key_tiles<KT>(P, P.shared_len, base + j1 + 1, max(base + j0, 0));
 }
 // Row tiles of n rows of G query heads.
 __device__ __forceinline__ int row_tiles(int rows, int rt_log2) { return (rows + (1 << rt_log2) - 1) >> rt_log2; }
@@ -117,45 +121,76 @@ __device__ __forceinline__ int own_units(const AttendParams &P, const ReqRows &q
     return u;
 }
 
-// The batch as a whole, by one warp.
+// A class's units over its workers: as many workers as there are units at most, the first `more` of them
+// with one unit more than the others' `each`.
+struct Shares {
+    int each, more, workers;
+    __device__ __forceinline__ Shares(int total, int limit) {
+        workers = min(total, limit);
+        each = workers > 0 ? total / workers : 0;
+        more = total - each * workers;
+    }
+    // The first unit of worker w (total, past the last one).
+    __device__ __forceinline__ int first(int w) const {
+        const int x = min(w, workers);
+        return each * x + min(x, more);
+    }
+    // The worker of unit u.
+    __device__ __forceinline__ int owner(int u) const {
+        const int longer = more * (each + 1);
+        return u < longer ? u / (each + 1) : more + (u - longer) / each;
+    }
+};
+
+// The batch as a whole, by one warp: units of the own items, least and greatest position of the rows
+// (padding aside). Lane l has requests [l * per, (l + 1) * per), and `before` units lie before them.
 struct Totals {
-    int64_t own_units;
-    int pmin, pmax;  // least and greatest position of the rows (padding aside)
+    int units, before, per, pmin, pmax;
 };
 template <int KT>
-__device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane, bool units) {
-    Totals t = {0, INT_MAX, -1};
-    for (int i = lane; i < P.B; i += kWarp) {
+__device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane) {
+    Totals t = {0, 0, (P.B + kWarp - 1) / kWarp, INT_MAX, -1};
+    int mine = 0;
+    for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
         const ReqRows q = load_request(P, i);
         if (q.n > 0 && q.kv > 0) {
             t.pmin = min(t.pmin, max(q.kv - q.n, 0));
             t.pmax = max(t.pmax, q.kv - 1);
         }
-        if (units) t.own_units += static_cast<int64_t>(P.Hkv) * own_units<KT>(P, q);
+        mine += P.Hkv * own_units<KT>(P, q);
     }
+    int incl = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        t.own_units += __shfl_xor_sync(0xffffffffu, t.own_units, o);
-        t.pmin = min(t.pmin, __shfl_xor_sync(0xffffffffu, t.pmin, o));
-        t.pmax = max(t.pmax, __shfl_xor_sync(0xffffffffu, t.pmax, o));
+    for (int o = 1; o < kWarp; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
     }
+    t.before = incl - mine;
+    t.units = __shfl_sync(0xffffffffu, incl, kWarp - 1);
+    t.pmin = __reduce_min_sync(0xffffffffu, t.pmin);
+    t.pmax = __reduce_max_sync(0xffffffffu, t.pmax);
     return t;
+}
+// Leaves the units before each request, and those of all, to the joining kernel (one warp).
+template <int KT>
+__device__ __forceinline__ void record_units(const AttendParams &P, int lane) {
+    const Totals t = batch_totals<KT>(P, lane);
+    int u = t.before;
+    for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
+        if (SPEC_IN(i, P.B, DBG_ATTEND)) P.unit_prefix[i] = u;
+        u += P.Hkv * own_units<KT>(P, load_request(P, i));
+    }
+    if (lane == 0) P.unit_prefix[P.B] = t.units;
 }
 template <int KT>
 __device__ __forceinline__ KeyTiles prefix_tiles(const AttendParams &P, const Totals &t) {
     return key_tiles<KT>(P, 0, min(P.shared_len, t.pmax + 1), t.pmin);
 }
 
-__device__ __forceinline__ int64_t first_unit(int64_t total, int w, int workers) { return total * w / workers; }
-// The worker that unit u falls to.
-__device__ __forceinline__ int unit_owner(int64_t total, int64_t u, int workers) {
-    return static_cast<int>(((u + 1) * workers + total - 1) / total) - 1;
-}
-
 // A run of units of one item, as a worker takes it.
 struct Segment {
     int row0;        // first packed row (own: within the request's head; prefix: within the batch)
-    int nrows;       // packed rows, at most RT
+    int nrows;       // packed rows, at most RT (0: the worker has no more)
     int t0;          // first row of the request in the batch (prefix: 0)
     int base;        // position of row t0 (prefix: unused, rows have their own)
     int head;        // key/value head
@@ -169,7 +204,7 @@ struct Segment {
 // Walks a worker's segments. Used by whole warps; every lane holds the same state.
 template <int KT, bool PREFIX>
 struct Walker {
-    int64_t u, u_end, u_first;
+    int u, u_end, u_first;
     int worker;
     int i, head, k, tile;  // request, head, row tile, tile within the item
     int head_tiles;        // row tiles of a head
@@ -179,8 +214,8 @@ struct Walker {
 
     __device__ __forceinline__ void start(const AttendParams &P, int w, int lane) {
         worker = w;
-        const Totals t = batch_totals<KT>(P, lane, !PREFIX);
-        head = k = tile = i = 0;
+        const Totals t = batch_totals<KT>(P, lane);
+        head = k = tile = i = head_tiles = 0;
         q = {0, 0, 0};
         if constexpr (PREFIX) {
             shared = prefix_tiles<KT>(P, t);
@@ -189,55 +224,38 @@ struct Walker {
             q.n = P.T;
             head_tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
             const int per = max(shared.n, 1);
-            const int64_t total = static_cast<int64_t>(P.Hkv) * head_tiles * per;
-            u = first_unit(total, w, P.prefix_workers);
-            u_end = first_unit(total, w + 1, P.prefix_workers);
-            const int64_t item = u / per;
-            tile = static_cast<int>(u - item * per);
-            head = static_cast<int>(item / head_tiles);
-            k = static_cast<int>(item - static_cast<int64_t>(head) * head_tiles);
-        } else {
-            const int64_t total = t.own_units;
-            u = first_unit(total, w, P.own_workers);
-            u_end = first_unit(total, w + 1, P.own_workers);
-            const bool record = w == 0;  // worker 0 leaves the requests' units to the joining kernel
-            int64_t before = 0;
-            bool found = u >= u_end;
-            int64_t rem = 0;
-            for (int i0 = 0; i0 < P.B && (record || !found); i0 += kWarp) {
-                const int r = i0 + lane;
-                int64_t mine = 0;
-                if (r < P.B) mine = static_cast<int64_t>(P.Hkv) * own_units<KT>(P, load_request(P, r));
-                int64_t incl = mine;
-#pragma unroll
-                for (int o = 1; o < kWarp; o <<= 1) {
-                    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += x;
-                }
-                if (record && r < P.B && SPEC_IN(r + 1, P.B + 1, DBG_ATTEND))
-                    P.unit_prefix[r + 1] = before + incl;
-                const unsigned hit = __ballot_sync(0xffffffffu, u < before + incl);
-                if (!found && hit) {
-                    const int l = __ffs(hit) - 1;
-                    i = i0 + l;
-                    rem = u - before - __shfl_sync(0xffffffffu, incl - mine, l);
-                    found = true;
-                }
-                before += __shfl_sync(0xffffffffu, incl, kWarp - 1);
-            }
-            if (record && lane == 0) P.unit_prefix[0] = 0;
+            const Shares share(P.Hkv * head_tiles * per, P.prefix_workers);
+            u = share.first(w);
+            u_end = share.first(w + 1);
             if (u < u_end) {
-                q = load_request(P, i);
+                const int item = u / per;
+                tile = u - item * per;
+                head = item / head_tiles;
+                k = item - head * head_tiles;
+            }
+        } else {
+            const Shares share(t.units, P.own_workers);
+            u = share.first(w);
+            u_end = share.first(w + 1);
+            if (u < u_end) {
+                // the lane whose requests have unit u (the last one with no more before it), then the request
+                const int l = __popc(__ballot_sync(0xffffffffu, t.before <= u)) - 1;
+                int rem = u - __shfl_sync(0xffffffffu, t.before, l), per_head;
+                for (i = l * t.per;; ++i) {
+                    q = load_request(P, i);
+                    per_head = own_units<KT>(P, q);
+                    if (rem < P.Hkv * per_head || i + 1 >= P.B) break;
+                    rem -= P.Hkv * per_head;
+                }
                 head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
-                const int per_head = own_units<KT>(P, q);
-                head = static_cast<int>(rem / per_head);
-                rem -= static_cast<int64_t>(head) * per_head;
-                for (;; ++k) {
+                head = rem / per_head;
+                rem -= head * per_head;
+                for (; k + 1 < head_tiles; ++k) {
                     const int nt = max(own_tiles<KT>(P, q, k).n, 1);
-                    if (rem < nt || k + 1 >= head_tiles) break;
+                    if (rem < nt) break;
                     rem -= nt;
                 }
-                tile = static_cast<int>(rem);
+                tile = rem;
             }
         }
         u_first = u;
@@ -248,7 +266,7 @@ struct Walker {
         if (u >= u_end) return false;
         s.keys = PREFIX ? shared : own_tiles<KT>(P, q, k);
         const int units = max(s.keys.n, 1);
-        const int take = static_cast<int>(min(static_cast<int64_t>(units - tile), u_end - u));
+        const int take = min(units - tile, u_end - u);
         const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2;
         s.row0 = k << rt_log2;
         s.nrows = min(1 << rt_log2, q.n * P.G - s.row0);
@@ -258,8 +276,8 @@ struct Walker {
         s.req = PREFIX ? -1 : i;
         s.tile = tile;
         s.ntile = min(take, s.keys.n);
-        s.pmin = PREFIX ? pmin : max(s.base + s.row0 / P.G, 0);
-        s.pmax = PREFIX ? pmax : s.base + (s.row0 + s.nrows - 1) / P.G;
+        s.pmin = PREFIX ? pmin : max(s.base + (k == 0 ? 0 : s.row0 / P.G), 0);
+        s.pmax = PREFIX ? pmax : s.keys.hi - 1;
         const bool whole = take == units;
         if (P.shared_len > 0) {
             // along a class's units either the item or the worker grows from one part to the next, so
@@ -322,6 +340,17 @@ __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int l
         scan(P.shared_table, 0, min(sinks, L));
     }
     return __any_sync(0xffffffffu, bad) ? SPEC_REQ_BAD_BLOCKS : SPEC_REQ_OK;
+}
+
+// What a kernel of own items leaves to the joining kernel, by one warp of each CTA: the requests' status,
+// and (the last CTA) the units before each request.
+template <int KT>
+__device__ __forceinline__ void keep_books(const AttendParams &P, int lane) {
+    if (blockIdx.x == gridDim.x - 1) record_units<KT>(P, lane);
+    for (int i = blockIdx.x; i < P.B; i += gridDim.x) {
+        const int st = attend_status(P, i, lane);
+        if (lane == 0 && SPEC_IN(i, P.B, DBG_ATTEND)) P.status[i] = st;
+    }
 }
 
 }  // namespace spec

@@ -1,5 +1,5 @@
 // Fifth-generation tensor cores on sm_103a: tensor memory, matrix instructions on bf16 operands with fp32
-// accumulators, and the row-gathering tensor copies that feed them.
+// accumulators, and the tensor copies that feed them.
 #pragma once
 
 #include <cstdint>
@@ -57,18 +57,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 // ---------------------------------------------------------------- matrix instructions
 
 // Shared-memory operand in the 128-byte swizzle: rows of 128 bytes (64 bf16), the eight 16-byte pieces
-// of row r at positions (piece ^ (r % 8)), groups of eight rows 1024 bytes apart.
-// Operands that run along K in memory (queries, keys): step = 1024, block unused.
-// Operands that run along M or N (values: rows are the K index): groups of eight rows step = 1024
-// apart, blocks of 64 columns `block` bytes apart.
+// of row r at positions (piece ^ (r % 8)), groups of eight rows 1024 bytes apart. It runs along K in
+// memory (queries, keys: a row is an index of M or N; block unused), or along M or N (values,
+// weights: a row is an index of K; columns 64.. lie `block` bytes on).
 __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t block) {
     return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (static_cast<uint64_t>(block >> 4) << 16) |
            (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// bf16 x bf16 -> fp32, M = 128 rows, N columns; b_cols: B runs along N in memory.
-__device__ __forceinline__ uint32_t mma_shape(int n, bool b_cols) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_cols ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-           ((128u >> 4) << 24);
+// The same in the 64-byte swizzle: rows of 64 bytes, four pieces at (piece ^ (r / 2 % 4)).
+__device__ __forceinline__ uint64_t smem_operand64(uint32_t addr) {
+    return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (1ull << 16) | (static_cast<uint64_t>(512u >> 4) << 32) |
+           (1ull << 46) | (4ull << 61);
+}
+// bf16 x bf16 -> fp32, M = 128 rows, N columns; a_cols, b_cols: the operand runs along M or N in memory.
+__device__ __forceinline__ uint32_t mma_shape(int n, bool a_cols, bool b_cols) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_cols ? 1u << 15 : 0u) | (b_cols ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 // D (tensor memory) = A (shared) B (shared) + (add ? D : 0), 16 deep. One thread issues.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
@@ -92,7 +96,16 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
                  : "memory");
 }
 
-// ---------------------------------------------------------------- gathering copies
+// ---------------------------------------------------------------- tensor copies
+
+// A box of a two-dimensional tensor map, from column x and row y, to shared memory.
+__device__ __forceinline__ void copy_box(void *dst, const void *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
 
 // Rows r0..r3 of a two-dimensional tensor map (box one row of 64 bf16, 128-byte swizzle), columns x ..
 // x + 63, to four consecutive 128-byte rows of shared memory; 512 bytes complete on `bar`.
@@ -107,7 +120,14 @@ __device__ __forceinline__ void prefetch_map(const void *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// ---------------------------------------------------------------- pairs of fp32
+// ---------------------------------------------------------------- fp32
+
+// The warp's maximum; a NaN gives way to a number.
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
