@@ -34,12 +34,14 @@ struct Shared {
     uint32_t tmem;
 };
 
+// An accumulator's queries, and its output on the way out: two blocks.
+constexpr int kQBytes = 2 * kBlock;
 __host__ constexpr int stages(int D) {
-    const int n = (227 * 1024 - 1024 - static_cast<int>(sizeof(Shared)) - 2 * tile_bytes(D)) / tile_bytes(D);
+    const int n = (227 * 1024 - 1024 - static_cast<int>(sizeof(Shared)) - 2 * kQBytes) / tile_bytes(D);
     return n < kMaxStages ? n : kMaxStages;
 }
 __host__ constexpr int smem_bytes(int D) {
-    return 1024 + (2 + stages(D)) * tile_bytes(D) + static_cast<int>(sizeof(Shared));
+    return 1024 + 2 * kQBytes + stages(D) * tile_bytes(D) + static_cast<int>(sizeof(Shared));
 }
 
 // ---------------------------------------------------------------- matrix instructions (one thread)
@@ -177,14 +179,18 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
         float m = -INFINITY, l = 0.0f;  // reference (scores, unscaled) and sum
         bool dead = true;               // no position, or no keys at all
         if (mine > 0 && nt > 0) {
-            // its query into the swizzled tile
-            if (have && SPEC_IN(t, P.T, DBG_ATTEND)) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) +
-                                                                   t * P.q_stride + static_cast<int64_t>(h) * P.D);
+            // the warp's queries into the swizzled tile, some rows at a time: lanes side by side along a row
+            // (a request of one sector per row and lane would take four times the time)
+            const int per = P.D / 8, at_once = kWarp / per, piece = lane % per;
+            const int64_t src = t * P.q_stride + static_cast<int64_t>(h) * P.D;
 #pragma unroll 4
-                for (int c = 0; c < P.D / 8; ++c)
-                    *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * kBlock + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
-                        src[c];
+            for (int r0 = 0; r0 < kWarp; r0 += at_once) {
+                const int r = r0 + lane / per;
+                const int64_t row = __shfl_sync(0xffffffffu, src, r & 31);
+                const int at = warp * kWarp + r;
+                if (lane < at_once * per && r < kWarp && at < mine && SPEC_IN(row + 8 * piece, P.T * P.q_stride, DBG_ATTEND))
+                    *reinterpret_cast<uint4 *>(q_tile + (piece >> 3) * kBlock + at * 128 + (((piece & 7) ^ (at & 7)) << 4)) =
+                        reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + row)[piece];
             }
             fence_proxy_async_smem();
             mbar_arrive(&sh.q_full[w]);
@@ -235,25 +241,31 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 s_phase ^= 1u;
                 tc_fence_after();
                 if (warp_has) {
-                    float z[kKT];
+                    // S is read twice, for the maximum and for the weights: 128 scores would not stay in the
+                    // thread's registers beside the rest, and tensor memory reads them faster than a spill
+                    auto see = [&](float (&z)[32], int c) {
+                        tmem_wait_ld();
+                        if (edge) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c * 32 < n) tmem_ld32(z + 32 * c, s_addr + 32 * c);
-                    tmem_wait_ld();
-                    if (edge) {
+                            for (int e = 0; e < 32; ++e) {
+                                const int x = x0 + c + e;
+                                if (!(x >= s.keys.from && x <= lim && (x >= wlo || x < P.n_sink))) z[e] = -INFINITY;
+                            }
+                        }
+                    };
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = 0; c < n; c += 32) {
+                        float z[32];
+                        tmem_ld32(z, s_addr + c);
+                        see(z, c);
 #pragma unroll
-                        for (int e = 0; e < kKT; ++e) {
-                            const int x = x0 + e;
-                            if (!(x >= s.keys.from && x <= lim && (x >= wlo || x < P.n_sink))) z[e] = -INFINITY;
+                        for (int e = 0; e < 32; e += 4) {
+                            mx[0] = fmaxf(mx[0], fmaxf(z[e], z[e + 1]));
+                            mx[1] = fmaxf(mx[1], fmaxf(z[e + 2], z[e + 3]));
                         }
                     }
-                    float mx[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-                    for (int e = 4; e < kKT; e += 8)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a)
-                            mx[a] = e + 4 + a < kKT ? fmaxf(mx[a], fmaxf(z[e + a], z[e + 4 + a])) : fmaxf(mx[a], z[e + a]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float top = fmaxf(mx[0], mx[1]);
                     // a new reference when the old one is too low (or there was none)
                     const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack);
                     if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
@@ -277,20 +289,21 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                     const float2 sc = make_float2(P.scale_log2, P.scale_log2);
                     const float2 rf = make_float2(-ref * P.scale_log2, -ref * P.scale_log2);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+                    for (int c = 0; c < n; c += 32) {
+                        float z[32];
+                        uint32_t pw[16];
+                        tmem_ld32(z, s_addr + c);
+                        see(z, c);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c * 32 < n) {
-                            uint32_t pw[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float2 y = fma2(make_float2(z[32 * c + 2 * e], z[32 * c + 2 * e + 1]), sc, rf);
-                                y.x = ex2(y.x);
-                                y.y = ex2(y.y);
-                                sum[e & 1] = add2(sum[e & 1], y);
-                                pw[e] = pack_bf16(y.x, y.y);
-                            }
-                            tmem_st16(s_addr + 16 * c, pw);
+                        for (int e = 0; e < 16; ++e) {
+                            float2 y = fma2(make_float2(z[2 * e], z[2 * e + 1]), sc, rf);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum[e & 1] = add2(sum[e & 1], y);
+                            pw[e] = pack_bf16(y.x, y.y);
                         }
+                        tmem_st16(s_addr + c / 2, pw);  // over columns that have been read
                     }
                     sum[0] = add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
@@ -318,30 +331,57 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
         const bool none = l == 0.0f;
         const float inv = s.part >= 0 ? 1.0f : 1.0f / l;
         if (warp_has) {
+            // O leaves through a quarter of the query memory (every product with it is done), 8 KB: rows of
+            // 256 bytes, the 16-byte pieces of row r at (piece ^ (r % 8)); out of it the lanes go side by side
+            // along the rows (see the queries)
+            unsigned char *mem = q_tile + warp * (kQBytes / 4);
+            const bool part = s.part >= 0;
+            const int span = part ? 64 : 128;  // columns at a time
+            const int64_t row_out = part ? (s.part + off + tid) * static_cast<int64_t>(P.D)
+                                         : t * P.out_stride + static_cast<int64_t>(h) * P.D;
 #pragma unroll 1
-            for (int d = 0; d < P.D; d += 16) {
-                float o[16];
+            for (int d0 = 0; d0 < P.D; d0 += span) {
+                const int width = min(span, P.D - d0);
                 __syncwarp();
-                if (nt > 0) {
-                    tmem_ld16(o, o_addr + d);
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * inv;
-                if (!have) continue;
-                if (s.part >= 0) {
-                    if (SPEC_IN(s.part + off + tid, P.part_rows, DBG_ATTEND)) {
-                        float4 *dst = reinterpret_cast<float4 *>(P.part_o + (s.part + off + tid) * P.D + d);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+#pragma unroll 1
+                for (int d = 0; d < width; d += 16) {
+                    float o[16];
+                    if (nt > 0) {
+                        tmem_ld16(o, o_addr + d0 + d);
+                        tmem_wait_ld();
                     }
-                } else if (SPEC_IN(t, P.T, DBG_ATTEND)) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.out) + t * P.out_stride +
-                                                           static_cast<int64_t>(h) * P.D + d);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                            pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                    for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * inv;
+                    unsigned char *row = mem + lane * 256;
+                    const int p0 = part ? d >> 2 : d >> 3;
+                    if (part) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4 *>(row + (((p0 + e) ^ (lane & 7)) << 4)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<uint4 *>(row + (((p0 + e) ^ (lane & 7)) << 4)) =
+                                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                    }
+                }
+                __syncwarp();
+                const int per = part ? width / 4 : width / 8, at_once = kWarp / per, piece = lane % per;
+#pragma unroll 4
+                for (int r0 = 0; r0 < kWarp; r0 += at_once) {
+                    const int r = r0 + lane / per;
+                    const int64_t dst = __shfl_sync(0xffffffffu, row_out, r & 31);
+                    if (lane < at_once * per && r < kWarp && warp * kWarp + r < mine) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(mem + r * 256 + ((piece ^ (r & 7)) << 4));
+                        if (part) {
+                            if (SPEC_IN(dst + d0 + 4 * piece, P.part_rows * P.D, DBG_ATTEND))
+                                *reinterpret_cast<uint4 *>(P.part_o + dst + d0 + 4 * piece) = v;
+                        } else if (SPEC_IN(dst + d0 + 8 * piece, P.T * P.out_stride, DBG_ATTEND)) {
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.out) + dst + d0 + 8 * piece) = v;
+                        }
+                    }
                 }
             }
             if (have) {
@@ -357,7 +397,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             }
         }
         tc_fence_before();  // O may be written again once the next segment's P is ready
+        // the query memory may be written again once all four warps are through
         __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.agree[w]);
+        if (!wait_warp(ab, &sh.agree[w], agree_phase)) return;
+        agree_phase ^= 1u;
         if (lane == 0) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
         desc.step();
     }
@@ -372,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ unsigned char raw[];
     unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const int tb = tile_bytes(P.D);
-    unsigned char *ring_mem = base + 2 * tb;
+    unsigned char *ring_mem = base + 2 * kQBytes;
     Shared &sh = *reinterpret_cast<Shared *>(ring_mem + n_stages * tb);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
@@ -405,18 +449,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
 
     if (warp < 8) {
-        softmax_role<PREFIX>(P, sh, base + (warp / 4) * tb, ring_mem, warp / 4, n_stages);
-    } else if (warp == 8) {
-        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
-    } else if (warp == 9) {
-        if constexpr (!PREFIX) keep_books<kKT>(P, lane);
-    } else if (lane == 0) {
-        const int w = warp - 10;
-        mma_role(P, sh, base + w * tb, ring_mem, w, n_stages);
-        // nothing this thread issued is in flight when the CTA ends
-        mma_commit(&sh.drain[w]);
+        softmax_role<PREFIX>(P, sh, base + (warp / 4) * kQBytes, ring_mem, warp / 4, n_stages);
+    } else {
+        if (warp == 8) {
+            load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
+        } else if (warp == 9) {
+            if constexpr (!PREFIX) keep_books<kKT>(P, lane);
+        } else if (lane == 0) {
+            const int w = warp - 10;
+            mma_role(P, sh, base + w * kQBytes, ring_mem, w, n_stages);
+            // nothing this thread issued is in flight when the CTA ends
+            mma_commit(&sh.drain[w]);
 #pragma unroll 1
-        for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain[w], 0, kHintNs); ++t) {
+            for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain[w], 0, kHintNs); ++t) {
+            }
         }
     }
     __syncwarp();

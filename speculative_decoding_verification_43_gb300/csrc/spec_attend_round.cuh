@@ -207,7 +207,6 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
     Scratch<RT> &scratch = *reinterpret_cast<Scratch<RT> *>(p_tile);
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
     uint32_t s_phases = 0, o_phase = 0, a_phase = 0, word = 0;
-    constexpr int kChunks = RT / 16;
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -276,33 +275,40 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             if (!wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u)) return;
             s_phases ^= 1u << b;
             tc_fence_after();
-            float z[RT];
+            // this position's scores with 16 rows from row e on (read anew where they are needed: tensor
+            // memory gives them back sooner than all the rows' scores would fit in registers)
+            auto scores = [&](float (&z)[16], int e) {
+                tmem_ld16(z, s_addr + b * RT + e);
+                tmem_wait_ld();
+                if (edge) {
+                    const bool in = x >= s.keys.from && x < s.keys.hi, sink = x < P.n_sink;
+                    const int back = P.window > 0 ? P.window : INT_MAX;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                if (c * 16 < nrows) tmem_ld16(z + 16 * c, s_addr + b * RT + 16 * c);
-            tmem_wait_ld();
-            if (edge) {
-                const bool in = x >= s.keys.from && x < s.keys.hi;
-                const int back = P.window > 0 ? P.window : INT_MAX;
-                const bool sink = x < P.n_sink;
-#pragma unroll
-                for (int e = 0; e < RT; ++e)
-                    if ((e & ~15) < nrows) {
-                        const int p = sh.pos[e];
-                        if (!(in && x <= p && (sink || p - x < back))) z[e] = -INFINITY;
+                    for (int y = 0; y < 16; ++y) {
+                        const int p = sh.pos[e + y];
+                        if (!(in && x <= p && (sink || p - x < back))) z[y] = -INFINITY;
                     }
-            }
-            // the scores against the references
+                }
+            };
             const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+            // four scores against their references
+            auto against = [&](const float *z, int e, float2 &a, float2 &c) {
+                const float4 rf = *reinterpret_cast<const float4 *>(sh.nref + e);
+                a = fma2(make_float2(z[0], z[1]), sc, make_float2(rf.x, rf.y));
+                c = fma2(make_float2(z[2], z[3]), sc, make_float2(rf.z, rf.w));
+            };
             float top = -INFINITY;
+#pragma unroll 1
+            for (int e = 0; e < nrows; e += 16) {
+                float z[16];
+                scores(z, e);
 #pragma unroll
-            for (int e = 0; e < RT; e += 4)
-                if ((e & ~15) < nrows) {
-                    const float4 rf = *reinterpret_cast<const float4 *>(sh.nref + e);
-                    const float2 a = fma2(make_float2(z[e], z[e + 1]), sc, make_float2(rf.x, rf.y));
-                    const float2 c = fma2(make_float2(z[e + 2], z[e + 3]), sc, make_float2(rf.z, rf.w));
+                for (int y = 0; y < 16; y += 4) {
+                    float2 a, c;
+                    against(z + y, e + y, a, c);
                     top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
                 }
+            }
             mine |= __any_sync(0xffffffffu, top > kSlack) ? 1u : 0u;
             if (!agree(sh, a_phase, warp, lane, mine, word)) return;
             if (i > 0) {  // the product before this tile: the weights' memory is free, O at rest
@@ -312,12 +318,16 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             }
             if (word & 1u) {
                 // new references: the rows' maxima over the tile, where they are larger
+#pragma unroll 1
+                for (int e = 0; e < nrows; e += 16) {
+                    float z[16];
+                    scores(z, e);
 #pragma unroll
-                for (int e = 0; e < RT; ++e)
-                    if ((e & ~15) < nrows) {
-                        const float v = redux_max(z[e]);
-                        if (lane == 0) scratch.warp[warp][e] = v;
+                    for (int y = 0; y < 16; ++y) {
+                        const float v = redux_max(z[y]);
+                        if (lane == 0) scratch.warp[warp][e + y] = v;
                     }
+                }
                 if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
                 if (tid < n16) {
                     const float v = fmaxf(fmaxf(scratch.warp[0][tid], scratch.warp[1][tid]),
@@ -355,25 +365,29 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             const bool skip = (word & 2u) != 0;
             unsigned char *prow = p_tile + tid * (RT * 2);
 #pragma unroll
-            for (int e = 0; e < RT; e += 8)
-                if ((e & ~15) < nrows) {
-                    uint32_t pw[4];
+            for (int e = 0; e < RT; e += 16)
+                if (e < nrows) {
+                    float z[16];
+                    scores(z, e);
 #pragma unroll
-                    for (int y = 0; y < 8; y += 4) {
-                        const float4 rf = *reinterpret_cast<const float4 *>(sh.nref + e + y);
-                        float2 a = fma2(make_float2(z[e + y], z[e + y + 1]), sc, make_float2(rf.x, rf.y));
-                        float2 c = fma2(make_float2(z[e + y + 2], z[e + y + 3]), sc, make_float2(rf.z, rf.w));
-                        a.x = ex2(a.x);
-                        a.y = ex2(a.y);
-                        c.x = ex2(c.x);
-                        c.y = ex2(c.y);
-                        l[(e + y) / 2] = add2(l[(e + y) / 2], a);
-                        l[(e + y) / 2 + 1] = add2(l[(e + y) / 2 + 1], c);
-                        pw[y / 2] = pack_bf16(a.x, a.y);
-                        pw[y / 2 + 1] = pack_bf16(c.x, c.y);
+                    for (int y = 0; y < 16; y += 8) {
+                        uint32_t pw[4];
+#pragma unroll
+                        for (int u = y; u < y + 8; u += 4) {
+                            float2 a, c;
+                            against(z + u, e + u, a, c);
+                            a.x = ex2(a.x);
+                            a.y = ex2(a.y);
+                            c.x = ex2(c.x);
+                            c.y = ex2(c.y);
+                            l[(e + u) / 2] = add2(l[(e + u) / 2], a);
+                            l[(e + u) / 2 + 1] = add2(l[(e + u) / 2 + 1], c);
+                            pw[(u - y) / 2] = pack_bf16(a.x, a.y);
+                            pw[(u - y) / 2 + 1] = pack_bf16(c.x, c.y);
+                        }
+                        const int piece = RT == 64 ? ((e + y) >> 3) ^ (tid & 7) : ((e + y) >> 3) ^ ((tid >> 1) & 3);
+                        *reinterpret_cast<uint4 *>(prow + piece * 16) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
                     }
-                    const int piece = RT == 64 ? (e >> 3) ^ (tid & 7) : (e >> 3) ^ ((tid >> 1) & 3);
-                    *reinterpret_cast<uint4 *>(prow + piece * 16) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
                 }
             if (skip) {
                 if (!agree(sh, a_phase, warp, lane, 0u, word)) return;  // all weights are there

@@ -119,7 +119,7 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
     Ring ring = {0, stages, 0}, desc = {0, 2, 0};
     Walker<kKT, PREFIX> walk;
     walk.start(P, worker, lane);
-    Segment s;
+    Segment s = {};
     bool ok = true;
     int used = 0;
     auto copy_tile = [&](const CUtensorMap *map, const TilePlan &t) {
