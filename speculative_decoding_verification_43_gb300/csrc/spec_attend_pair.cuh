@@ -51,16 +51,21 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
     const int tb = tile_bytes(P.D);
     int32_t *ab = &sh.pipe.abort;
     const uint32_t s_col = sh.tmem + w * 256, o_col = s_col + 128, p_col = s_col;
-    const uint32_t q_addr = smem_addr(q_tile), t_addr = smem_addr(ring_mem);
+    // One thread's instructions set the pace: 64 cycles of products each leave room for little more than
+    // an addition, so the operands are prepared and the steps unrolled.
+    const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
+                   v_op = smem_operand(smem_addr(ring_mem), kBlock);
+    const int steps = P.D / 16;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
     uint32_t q_phase = 0, p_phase = 0;
     const uint32_t pv_shape = mma_shape(P.D, false, true);
     auto score = [&](int n) {  // S = Q K^T
-        const uint32_t k_addr = t_addr + ring.slot * tb;
+        const uint64_t k = operand_at(k_op, ring.slot * tb);
         const uint32_t shape = mma_shape(n, false, false);
-        for (int d = 0; d < P.D; d += 16) {
-            const uint32_t at = (d >> 6) * kBlock + (d & 63) * 2;
-            mma_ss(s_col, smem_operand(q_addr + at, 16), smem_operand(k_addr + at, 16), shape, d > 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = (i >> 2) * kBlock + (i & 3) * 32;
+            if (i < steps) mma_ss(s_col, operand_at(q_op, at), operand_at(k, at), shape, i > 0);
         }
         mma_commit(&sh.s_full[w]);
         mma_commit(&sh.pipe.empty[ring.slot]);
@@ -90,9 +95,10 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                 p_phase ^= 1u;
                 tc_fence_after();
                 if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w])) {  // O += P V
-                    const uint32_t v_addr = t_addr + ring.slot * tb;
-                    for (int k = 0; k < n; k += 16)
-                        mma_ts(o_col, p_col + k / 2, smem_operand(v_addr + k * 128, kBlock), pv_shape, t > 0 || k > 0);
+                    const uint64_t v = operand_at(v_op, ring.slot * tb);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i * 16 < n) mma_ts(o_col, p_col + 8 * i, operand_at(v, i * 2048), pv_shape, t > 0 || i > 0);
                 }
                 mma_commit(&sh.pipe.empty[ring.slot]);
                 ring.step();
@@ -214,7 +220,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 }
             }
             dead = p < 0;
-            const int lim = min(p, s.keys.hi - 1), wlo = P.window > 0 ? p - P.window + 1 : 0;
+            const int lim = min(p, s.keys.hi - 1), wlo = P.window > 0 ? p - P.window + 1 : 0, from = s.keys.from;
+            if (!have) m = 0.0f;  // lanes without a row never ask for another reference
             for (int i = 0; i < nt; ++i) {
                 const int x0 = tile_begin<kKT>(s.keys, s.tile + i), n = tile_keys(s.keys, x0);
                 const bool edge = edge_tile(P, s, x0);
@@ -241,60 +248,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 s_phase ^= 1u;
                 tc_fence_after();
                 if (warp_has) {
-                    // S is read twice, for the maximum and for the weights: 128 scores would not stay in the
-                    // thread's registers beside the rest, and tensor memory reads them faster than a spill
-                    auto see = [&](float (&z)[32], int c) {
-                        tmem_wait_ld();
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int x = x0 + c + e;
-                                if (!(x >= s.keys.from && x <= lim && (x >= wlo || x < P.n_sink))) z[e] = -INFINITY;
-                            }
-                        }
-                    };
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < n; c += 32) {
-                        float z[32];
-                        tmem_ld32(z, s_addr + c);
-                        see(z, c);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            mx[0] = fmaxf(mx[0], fmaxf(z[e], z[e + 1]));
-                            mx[1] = fmaxf(mx[1], fmaxf(z[e + 2], z[e + 3]));
-                        }
-                    }
-                    const float top = fmaxf(mx[0], mx[1]);
-                    // a new reference when the old one is too low (or there was none)
-                    const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack);
-                    if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                        const float a = grow && m != -INFINITY ? ex2((m - top) * P.scale_log2) : 1.0f;
-                        l *= a;
-                        // S is complete, and with it the product of the tile before: O is at rest
-#pragma unroll 1
-                        for (int d = 0; d < P.D; d += 16) {
-                            float o[16];
-                            uint32_t ow[16];
-                            tmem_ld16(o, o_addr + d);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * a);
-                            tmem_st16(o_addr + d, ow);
-                        }
-                        tmem_wait_st();
-                    }
-                    if (grow) m = top;
-                    const float ref = m == -INFINITY ? 0.0f : m;
                     const float2 sc = make_float2(P.scale_log2, P.scale_log2);
-                    const float2 rf = make_float2(-ref * P.scale_log2, -ref * P.scale_log2);
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-                    for (int c = 0; c < n; c += 32) {
-                        float z[32];
-                        uint32_t pw[16];
-                        tmem_ld32(z, s_addr + c);
-                        see(z, c);
+                    // weights of 32 scores, packed; their sum and maximum
+                    float2 sum[2];
+                    auto weigh = [&](const float *z, uint32_t *pw, const float2 &rf) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float2 y = fma2(make_float2(z[2 * e], z[2 * e + 1]), sc, rf);
@@ -303,14 +260,101 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                             sum[e & 1] = add2(sum[e & 1], y);
                             pw[e] = pack_bf16(y.x, y.y);
                         }
-                        tmem_st16(s_addr + c / 2, pw);  // over columns that have been read
+                    };
+                    auto greatest = [&](const float *z, float mx) {
+                        float a = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            mx = fmaxf(mx, fmaxf(z[e], z[e + 1]));
+                            a = fmaxf(a, fmaxf(z[e + 2], z[e + 3]));
+                        }
+                        return fmaxf(mx, a);
+                    };
+                    // A tile that all rows see whole, with the reference there is: one pass, the weights kept
+                    // back until it is certain that the reference serves (P would cover scores of S).
+                    bool done = false;
+                    if (!edge && __all_sync(0xffffffffu, m != -INFINITY)) {
+                        const float2 rf = make_float2(-m * P.scale_log2, -m * P.scale_log2);
+                        float za[32], zb[32];
+                        uint32_t pw[64];
+                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                        tmem_ld32(za, s_addr);
+                        tmem_wait_ld32(za);
+                        tmem_ld32(zb, s_addr + 32);
+                        float top = greatest(za, -INFINITY);
+                        weigh(za, pw, rf);
+                        tmem_wait_ld32(zb);
+                        tmem_ld32(za, s_addr + 64);
+                        top = greatest(zb, top);
+                        weigh(zb, pw + 16, rf);
+                        tmem_wait_ld32(za);
+                        tmem_ld32(zb, s_addr + 96);
+                        top = greatest(za, top);
+                        weigh(za, pw + 32, rf);
+                        tmem_wait_ld32(zb);
+                        top = greatest(zb, top);
+                        weigh(zb, pw + 48, rf);
+                        done = !__any_sync(0xffffffffu, have && (top - m) * P.scale_log2 > kSlack);
+                        if (done)
+#pragma unroll
+                            for (int c = 0; c < 64; c += 16) tmem_st16(s_addr + c, pw + c);
+                    }
+                    if (!done) {
+                        // the maximum first, then the weights; S is read twice
+                        auto see = [&](float (&z)[32], int c) {
+                            tmem_ld32(z, s_addr + c);
+                            tmem_wait_ld32(z);
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const int x = x0 + c + e;
+                                    if (!(x >= from && x <= lim && (x >= wlo || x < P.n_sink))) z[e] = -INFINITY;
+                                }
+                            }
+                        };
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < n; c += 32) {
+                            float z[32];
+                            see(z, c);
+                            top = greatest(z, top);
+                        }
+                        // a new reference when the old one is too low (or there was none)
+                        const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack);
+                        if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                            const float a = grow && m != -INFINITY ? ex2((m - top) * P.scale_log2) : 1.0f;
+                            l *= a;
+                            // S is complete, and with it the product of the tile before: O is at rest
+#pragma unroll 1
+                            for (int d = 0; d < P.D; d += 16) {
+                                float o[16];
+                                uint32_t ow[16];
+                                tmem_ld16(o, o_addr + d);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * a);
+                                tmem_st16(o_addr + d, ow);
+                            }
+                            tmem_wait_st();
+                        }
+                        if (grow) m = top;
+                        const float ref = m == -INFINITY ? 0.0f : m;
+                        const float2 rf = make_float2(-ref * P.scale_log2, -ref * P.scale_log2);
+                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+                        for (int c = 0; c < n; c += 32) {
+                            float z[32];
+                            uint32_t pw[16];
+                            see(z, c);
+                            weigh(z, pw, rf);
+                            tmem_st16(s_addr + c / 2, pw);  // over columns that have been read
+                        }
                     }
                     sum[0] = add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                     tmem_wait_st();
                     if (skip)
-                        mixed_tile(P.D, s_addr, o_addr, ring_mem + v_slot * tb, x0, n, s.keys.from, lim, wlo, P.n_sink,
-                                   i == 0);
+                        mixed_tile(P.D, s_addr, o_addr, ring_mem + v_slot * tb, x0, n, from, lim, wlo, P.n_sink, i == 0);
                 }
                 if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
                 tc_fence_before();

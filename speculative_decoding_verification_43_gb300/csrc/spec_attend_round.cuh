@@ -72,11 +72,13 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
     const int tb = tile_bytes(P.D);
     int32_t *ab = &sh.pipe.abort;
     const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * RT;
-    const uint32_t q_addr = smem_addr(q_tile), p_addr = smem_addr(p_tile), t_addr = smem_addr(ring_mem);
+    // with up to 64 columns the output's lanes 64.. repeat the first 64 (unused)
+    const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
+                   v_op = smem_operand(smem_addr(ring_mem), blocks(P.D) == 2 ? kBlock : 0),
+                   p_op = RT == 64 ? smem_operand(smem_addr(p_tile), 16) : smem_operand64(smem_addr(p_tile));
+    const int steps = P.D / 16;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
     uint32_t q_phase = 0, p_phase = 0;
-    // with up to 64 columns the output's lanes 64.. repeat the first 64 (unused)
-    const uint32_t v_block = blocks(P.D) == 2 ? kBlock : 0u;
     for (;;) {
         if (!wait_one(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -86,12 +88,13 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
             const int n16 = (nrows + 15) & ~15;
             const uint32_t qk_shape = mma_shape(n16, false, false), pv_shape = mma_shape(n16, true, true);
             auto score = [&](int b) {  // S^T = K Q^T
-                const uint32_t k_addr = t_addr + ring.slot * tb;
-#pragma unroll 2
-                for (int d = 0; d < P.D; d += 16) {
-                    const uint32_t in = (d & 63) * 2;
-                    mma_ss(s_col + b * RT, smem_operand(k_addr + (d >> 6) * kBlock + in, 16),
-                           smem_operand(q_addr + (d >> 6) * (RT * 128) + in, 16), qk_shape, d > 0);
+                const uint64_t k = operand_at(k_op, ring.slot * tb);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t in = (i & 3) * 32;
+                    if (i < steps)
+                        mma_ss(s_col + b * RT, operand_at(k, (i >> 2) * kBlock + in),
+                               operand_at(q_op, (i >> 2) * (RT * 128) + in), qk_shape, i > 0);
                 }
                 mma_commit(&sh.s_full[b]);
                 mma_commit(&sh.pipe.empty[ring.slot]);
@@ -117,13 +120,13 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
                 p_phase ^= 1u;
                 tc_fence_after();
                 if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip)) {  // O^T += V^T P^T
-                    const uint32_t v_addr = t_addr + v.slot * tb;
+                    const uint64_t values = operand_at(v_op, v.slot * tb);
                     const int n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile + t));
-#pragma unroll 2
-                    for (int k = 0; k < n; k += 16)
-                        mma_ss(o_col, smem_operand(v_addr + k * 128, v_block),
-                               RT == 64 ? smem_operand(p_addr + k * 128, 16) : smem_operand64(p_addr + k * 64), pv_shape,
-                               t > 0 || k > 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i * 16 < n)
+                            mma_ss(o_col, operand_at(values, i * 2048), operand_at(p_op, i * 16 * RT * 2), pv_shape,
+                                   t > 0 || i > 0);
                 }
                 mma_commit(&sh.o_done);
                 mma_commit(&sh.pipe.empty[v.slot]);
@@ -275,9 +278,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             if (!wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u)) return;
             s_phases ^= 1u << b;
             tc_fence_after();
-            // this position's scores with 16 rows from row e on (read anew where they are needed: tensor
-            // memory gives them back sooner than all the rows' scores would fit in registers)
-            auto scores = [&](float (&z)[16], int e) {
+            // this position's scores with 16 rows from row e on
+            auto read = [&](float *z, int e) {
                 tmem_ld16(z, s_addr + b * RT + e);
                 tmem_wait_ld();
                 if (edge) {
@@ -290,6 +292,19 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     }
                 }
             };
+            // 32 rows' scores stay in registers; 64 rows' would not, beside their sums, and are read anew
+            constexpr bool kHeld = RT == 32;
+            float held[kHeld ? RT : 16];
+            if constexpr (kHeld) {
+#pragma unroll
+                for (int e = 0; e < RT; e += 16)
+                    if (e < nrows) read(held + e, e);
+            }
+            auto scores = [&](int e) -> float * {
+                if constexpr (kHeld) return held + e;
+                read(held, e);
+                return held;
+            };
             const float2 sc = make_float2(P.scale_log2, P.scale_log2);
             // four scores against their references
             auto against = [&](const float *z, int e, float2 &a, float2 &c) {
@@ -298,17 +313,17 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                 c = fma2(make_float2(z[2], z[3]), sc, make_float2(rf.z, rf.w));
             };
             float top = -INFINITY;
-#pragma unroll 1
-            for (int e = 0; e < nrows; e += 16) {
-                float z[16];
-                scores(z, e);
 #pragma unroll
-                for (int y = 0; y < 16; y += 4) {
-                    float2 a, c;
-                    against(z + y, e + y, a, c);
-                    top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
+            for (int e = 0; e < RT; e += 16)
+                if (e < nrows) {
+                    const float *z = scores(e);
+#pragma unroll
+                    for (int y = 0; y < 16; y += 4) {
+                        float2 a, c;
+                        against(z + y, e + y, a, c);
+                        top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
+                    }
                 }
-            }
             mine |= __any_sync(0xffffffffu, top > kSlack) ? 1u : 0u;
             if (!agree(sh, a_phase, warp, lane, mine, word)) return;
             if (i > 0) {  // the product before this tile: the weights' memory is free, O at rest
@@ -318,16 +333,16 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             }
             if (word & 1u) {
                 // new references: the rows' maxima over the tile, where they are larger
-#pragma unroll 1
-                for (int e = 0; e < nrows; e += 16) {
-                    float z[16];
-                    scores(z, e);
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const float v = redux_max(z[y]);
-                        if (lane == 0) scratch.warp[warp][e + y] = v;
+                for (int e = 0; e < RT; e += 16)
+                    if (e < nrows) {
+                        const float *z = scores(e);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const float v = redux_max(z[y]);
+                            if (lane == 0) scratch.warp[warp][e + y] = v;
+                        }
                     }
-                }
                 if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
                 if (tid < n16) {
                     const float v = fmaxf(fmaxf(scratch.warp[0][tid], scratch.warp[1][tid]),
@@ -367,8 +382,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
 #pragma unroll
             for (int e = 0; e < RT; e += 16)
                 if (e < nrows) {
-                    float z[16];
-                    scores(z, e);
+                    const float *z = scores(e);
 #pragma unroll
                     for (int y = 0; y < 16; y += 8) {
                         uint32_t pw[4];

@@ -45,6 +45,14 @@ __device__ __forceinline__ void tmem_ld16(float *r, uint32_t addr) {
           "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(addr));
 }
+// Waits for this thread's loads, of which the 32 registers are the last: what uses them stays behind.
+__device__ __forceinline__ void tmem_wait_ld32(float *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                   "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                   "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -64,7 +72,15 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t block) 
     return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (static_cast<uint64_t>(block >> 4) << 16) |
            (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// The same in the 64-byte swizzle: rows of 64 bytes, four pieces at (piece ^ (r / 2 % 4)).
+// The operand `bytes` further on (within the 14 bits of its address).
+__device__ __forceinline__ uint64_t operand_at(uint64_t operand, uint32_t bytes) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(operand));
+    lo += bytes >> 4;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(operand) : "r"(lo), "r"(hi));
+    return operand;
+}
+// An operand in the 64-byte swizzle: rows of 64 bytes, four pieces at (piece ^ (r / 2 % 4)).
 __device__ __forceinline__ uint64_t smem_operand64(uint32_t addr) {
     return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (1ull << 16) | (static_cast<uint64_t>(512u >> 4) << 32) |
            (1ull << 46) | (4ull << 61);
