@@ -1,12 +1,16 @@
 // Attention of many rows on the tensor cores (bf16, head sizes that are multiples of 16 up to 128): long
 // prompts, and the shared prefix, whose rows are those of the whole batch.
 //
-// One CTA per SM, an item of 256 packed rows in two accumulators of 128 that use the same tiles. Per
-// tile of 128 keys and accumulator:
+// One CTA per SM, an item of 256 packed rows in two accumulators of 128 that use the same tiles. Per half
+// tile of 64 keys and accumulator:
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, S (fp32) in tensor memory
 //   P = 2^(S - m)  a warpgroup, one row per thread; P (bf16) goes back over S's columns
 //   O += P V       tcgen05.mma, P read from tensor memory, V from shared memory
-// One accumulator's products run while the other's softmax does.
+// Tensor memory holds O (128 columns) and S of two halves (64 each) per accumulator: the scores of the
+// next half are there when a half's weights are done, and the products' latency (some 1500 cycles from a
+// finished P to the next S) is hidden. With S of whole tiles, one each, a tile took 4500 cycles, of which the
+// warpgroups waited 2150. The halves cost the first product a third of its rate (64 columns do not make
+// up for reading 128 rows of queries again).
 // A row's m is a reference, not the running maximum: O and the sum are rescaled only when the maximum
 // has grown by more than 2^8 beyond it (P then stays below 2^8, whose bf16 rounding is relative all the
 // same), so the output hardly ever leaves tensor memory before the end.
@@ -23,14 +27,15 @@ namespace pair {
 using namespace tiles;
 
 constexpr int kRTLog2 = 8, kRows = 128;  // rows of an item, of an accumulator
+constexpr int kHalf = kKT / 2;           // positions whose scores are taken at a time
 constexpr int kThreads = 384;
 constexpr float kSlack = 8.0f;           // log2 growth of the maximum that O and the sum absorb
 
 struct Shared {
     Pipe<kMaxStages> pipe;
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], agree[2], drain[2];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], agree[2], drain[2];
     uint32_t bad[2][2][4];  // per warp: its quarter of the values holds one that is not finite
-    uint32_t skip[2];       // the warpgroup has done this tile's second product itself
+    uint32_t skip[2][2];    // the warpgroup has done this half's second product itself
     uint32_t tmem;
 };
 
@@ -50,32 +55,32 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                                          int w, int n_stages) {
     const int tb = tile_bytes(P.D);
     int32_t *ab = &sh.pipe.abort;
-    const uint32_t s_col = sh.tmem + w * 256, o_col = s_col + 128, p_col = s_col;
+    const uint32_t s_col = sh.tmem + w * 256, o_col = s_col + 128;
     // One thread's instructions set the pace: 64 cycles of products each leave room for little more than
     // an addition, so the operands are prepared and the steps unrolled.
     const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
                    v_op = smem_operand(smem_addr(ring_mem), kBlock);
     const int steps = P.D / 16;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
-    uint32_t q_phase = 0, p_phase = 0;
+    uint32_t q_phase = 0, p_phase = 0, products = 0;
     const uint32_t pv_shape = mma_shape(P.D, false, true);
-    auto score = [&](int n) {  // S = Q K^T
-        const uint64_t k = operand_at(k_op, ring.slot * tb);
+    // S of half u of the tile in slot: n of its positions are used
+    auto score = [&](const Ring &at, int u, int n) {
+        const uint64_t k = operand_at(k_op, at.slot * tb + u * (kHalf * 128));
         const uint32_t shape = mma_shape(n, false, false);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t at = (i >> 2) * kBlock + (i & 3) * 32;
-            if (i < steps) mma_ss(s_col, operand_at(q_op, at), operand_at(k, at), shape, i > 0);
+            const uint32_t in = (i >> 2) * kBlock + (i & 3) * 32;
+            if (i < steps) mma_ss(s_col + u * kHalf, operand_at(q_op, in), operand_at(k, in), shape, i > 0);
         }
-        mma_commit(&sh.s_full[w]);
-        mma_commit(&sh.pipe.empty[ring.slot]);
-        ring.step();
+        mma_commit(&sh.s_full[w][u]);
     };
     for (;;) {
         if (!wait_one(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
         if (s.nrows == 0) return;
-        const int nt = s.ntile;
+        const int nt = s.ntile, first = s.tile;
+        const KeyTiles keys = s.keys;
         if (nt > 0 && s.nrows <= w * kRows) {
             for (int t = 0; t < 2 * nt; ++t) {  // no rows for this accumulator: let the tiles go by
                 if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
@@ -87,31 +92,49 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
             q_phase ^= 1u;
             if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
             tc_fence_after();
-            int n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile));
-            score(n);
+            int n = tile_keys(keys, tile_begin<kKT>(keys, first));
+            score(ring, 0, min(n, kHalf));
+            if (n > kHalf) score(ring, 1, n - kHalf);
+            mma_commit(&sh.pipe.empty[ring.slot]);
+            ring.step();
             for (int t = 0; t < nt; ++t) {
-                if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-                if (!wait_one(ab, &sh.p_full[w], p_phase)) return;
-                p_phase ^= 1u;
-                tc_fence_after();
-                if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w])) {  // O += P V
-                    const uint64_t v = operand_at(v_op, ring.slot * tb);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i * 16 < n) mma_ts(o_col, p_col + 8 * i, operand_at(v, i * 2048), pv_shape, t > 0 || i > 0);
-                }
-                mma_commit(&sh.pipe.empty[ring.slot]);
+                const Ring v = ring;  // this tile's values; the next tile's keys follow them
                 ring.step();
-                if (t + 1 < nt) {
-                    if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-                    tc_fence_after();
-                    // S and P share columns: matrix instructions of one thread run in the order of
-                    // their issue, so this one follows the product that reads P
-                    n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile + t + 1));
-                    score(n);
-                } else {
-                    mma_commit(&sh.o_full[w]);
+                const bool more = t + 1 < nt;
+                const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int here = n - u * kHalf;
+                    if (here > 0) {
+                        if (u == 0 && !wait_one(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                        if (!wait_one(ab, &sh.p_full[w][u], p_phase >> u & 1u)) return;
+                        p_phase ^= 1u << u;
+                        tc_fence_after();
+                        if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w][u])) {  // O += P V
+                            const uint64_t values = operand_at(v_op, v.slot * tb + u * (kHalf * 128));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i * 16 < here)
+                                    mma_ts(o_col, s_col + u * kHalf + 8 * i, operand_at(values, i * 2048), pv_shape,
+                                           t > 0 || u > 0 || i > 0);
+                        }
+                        mma_commit(&sh.o_done[w][products & 1u]);
+                        ++products;
+                    }
+                    // S and P share columns: matrix instructions of one thread run in the order of their
+                    // issue, so the next scores follow the product that reads P
+                    if (u == 0 && more && !wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                    if (next > u * kHalf) {
+                        tc_fence_after();
+                        score(ring, u, min(next - u * kHalf, kHalf));
+                    }
                 }
+                mma_commit(&sh.pipe.empty[v.slot]);
+                if (more) {
+                    mma_commit(&sh.pipe.empty[ring.slot]);
+                    ring.step();
+                }
+                n = next;
             }
         }
         mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
@@ -123,7 +146,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
 
 // The second product of a tile with values that are not finite, on the fp32 units: the row's weights
 // are in tensor memory already, O is complete up to the tile before. first: O holds nothing yet.
-__device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr, const unsigned char *v_tile, int x0, int n,
+__device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr, const unsigned char *v_tile, int k0, int x0, int n,
                                         int from, int lim, int wlo, int sinks, bool first) {
 #pragma unroll 1
     for (int d = 0; d < D; d += 16) {
@@ -147,7 +170,7 @@ __device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr,
                     const uint32_t pw = __float_as_uint(p[e / 2]);
                     const float w = __uint_as_float(e % 2 ? pw & 0xffff0000u : pw << 16);
 #pragma unroll 4
-                    for (int i = 0; i < 16; ++i) o[i] = fmaf(w, tile_value(v_tile, k + e, d + i), o[i]);
+                    for (int i = 0; i < 16; ++i) o[i] = fmaf(w, tile_value(v_tile, k0 + k + e, d + i), o[i]);
                 }
             }
         }
@@ -169,7 +192,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_addr = sh.tmem + w * 256 + lanes, o_addr = s_addr + 128;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
-    uint32_t s_phase = 0, o_phase = 0, agree_phase = 0;
+    uint32_t s_phase = 0, agree_phase = 0, products = 0;
+    // Products take two barriers in turn: when a half's scores are there, the product two before it is done
+    // (the scores were issued behind it), so that on either barrier only one phase can be meant.
+    auto product_done = [&](uint32_t x) { return wait_warp(ab, &sh.o_done[w][x & 1u], x >> 1 & 1u); };
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -222,16 +248,20 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             dead = p < 0;
             const int lim = min(p, s.keys.hi - 1), wlo = P.window > 0 ? p - P.window + 1 : 0, from = s.keys.from;
             if (!have) m = 0.0f;  // lanes without a row never ask for another reference
+            const KeyTiles keys = s.keys;
+            const int first = s.tile;
+            // a tile is seen whole by all rows from x0 = from on to here, when no window cuts it off
+            const int whole = min(s.pmin, keys.hi - 1) - (kKT - 1), cut = P.window > 0 ? s.pmax - P.window : -1;
+            const float2 sc = make_float2(P.scale_log2, P.scale_log2);
             for (int i = 0; i < nt; ++i) {
-                const int x0 = tile_begin<kKT>(s.keys, s.tile + i), n = tile_keys(s.keys, x0);
-                const bool edge = edge_tile(P, s, x0);
-                const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
-                const uint32_t v_phase = ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase;
+                const int x0 = tile_begin<kKT>(keys, first + i), n = tile_keys(keys, x0);
+                const bool edge = x0 > whole || x0 < from || (x0 <= cut && x0 + kKT > P.n_sink);
+                unsigned char *v_tile = ring_mem + (ring.slot + 1 == ring.n ? 0 : ring.slot + 1) * tb;
                 bool skip = false;
                 if (edge) {
-                    if (!wait_warp(ab, &sh.pipe.full[v_slot], v_phase)) return;
-                    const bool bad =
-                        __any_sync(0xffffffffu, clean_values(P, s.keys, ring_mem + v_slot * tb, x0, n, tid));
+                    const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
+                    if (!wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase)) return;
+                    const bool bad = __any_sync(0xffffffffu, clean_values(P, keys, v_tile, x0, n, tid));
                     fence_proxy_async_smem();
                     // the four warps' findings (two sets, used in turn)
                     volatile uint32_t *found = sh.bad[w][agree_phase];
@@ -244,126 +274,99 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                     agree_phase ^= 1u;
                     skip = (found[0] | found[1] | found[2] | found[3]) != 0;
                 }
-                if (!wait_warp(ab, &sh.s_full[w], s_phase)) return;
-                s_phase ^= 1u;
-                tc_fence_after();
-                if (warp_has) {
-                    const float2 sc = make_float2(P.scale_log2, P.scale_log2);
-                    // weights of 32 scores, packed; their sum and maximum
-                    float2 sum[2];
-                    auto weigh = [&](const float *z, uint32_t *pw, const float2 &rf) {
+#pragma unroll 1
+                for (int u = 0; u * kHalf < n; ++u) {
+                    const int xu = x0 + u * kHalf, nu = min(n - u * kHalf, kHalf);
+                    const uint32_t s_at = s_addr + u * kHalf;
+                    if (!wait_warp(ab, &sh.s_full[w][u], s_phase >> u & 1u)) return;
+                    s_phase ^= 1u << u;
+                    tc_fence_after();
+                    if (warp_has) {
+                        float za[32], zb[32];
+                        uint32_t pw[32];
+                        tmem_ld32(za, s_at);
+                        if (nu > 32) tmem_ld32(zb, s_at + 32);
+                        tmem_wait_ld32(za);
+                        tmem_wait_ld32(zb);
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int xa = xu + e, xb = xu + 32 + e;
+                                if (!(xa >= from && xa <= lim && (xa >= wlo || xa < P.n_sink))) za[e] = -INFINITY;
+                                if (!(xb >= from && xb <= lim && (xb >= wlo || xb < P.n_sink))) zb[e] = -INFINITY;
+                            }
+                        }
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            mx[0] = fmaxf(mx[0], fmaxf(za[e], za[e + 1]));
+                            mx[1] = fmaxf(mx[1], fmaxf(za[e + 2], za[e + 3]));
+                            mx[2] = fmaxf(mx[2], fmaxf(zb[e], zb[e + 1]));
+                            mx[3] = fmaxf(mx[3], fmaxf(zb[e + 2], zb[e + 3]));
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        // a new reference when the old one is too low (or there was none)
+                        const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack) && have;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                                // the product before this half's is the last that was begun
+                                if (!product_done(products - 1)) return;
+                                tc_fence_after();
+                                const float a = grow && m != -INFINITY ? ex2((m - top) * P.scale_log2) : 1.0f;
+                                l *= a;
+#pragma unroll 1
+                                for (int d = 0; d < P.D; d += 16) {
+                                    float o[16];
+                                    uint32_t ow[16];
+                                    tmem_ld16(o, o_addr + d);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * a);
+                                    tmem_st16(o_addr + d, ow);
+                                }
+                                tmem_wait_st();
+                            }
+                            if (grow) m = top;
+                        }
+                        const float ref = m == -INFINITY ? 0.0f : -m * P.scale_log2;
+                        const float2 rf = make_float2(ref, ref);
+                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float2 y = fma2(make_float2(z[2 * e], z[2 * e + 1]), sc, rf);
+                            float2 y = fma2(make_float2(za[2 * e], za[2 * e + 1]), sc, rf);
                             y.x = ex2(y.x);
                             y.y = ex2(y.y);
                             sum[e & 1] = add2(sum[e & 1], y);
                             pw[e] = pack_bf16(y.x, y.y);
                         }
-                    };
-                    auto greatest = [&](const float *z, float mx) {
-                        float a = -INFINITY;
+                        tmem_st16(s_at, pw);  // over columns that have been read
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            mx = fmaxf(mx, fmaxf(z[e], z[e + 1]));
-                            a = fmaxf(a, fmaxf(z[e + 2], z[e + 3]));
+                        for (int e = 0; e < 16; ++e) {
+                            float2 y = fma2(make_float2(zb[2 * e], zb[2 * e + 1]), sc, rf);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum[e & 1] = add2(sum[e & 1], y);
+                            pw[16 + e] = pack_bf16(y.x, y.y);
                         }
-                        return fmaxf(mx, a);
-                    };
-                    // A tile that all rows see whole, with the reference there is: one pass, the weights kept
-                    // back until it is certain that the reference serves (P would cover scores of S).
-                    bool done = false;
-                    if (!edge && __all_sync(0xffffffffu, m != -INFINITY)) {
-                        const float2 rf = make_float2(-m * P.scale_log2, -m * P.scale_log2);
-                        float za[32], zb[32];
-                        uint32_t pw[64];
-                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                        tmem_ld32(za, s_addr);
-                        tmem_wait_ld32(za);
-                        tmem_ld32(zb, s_addr + 32);
-                        float top = greatest(za, -INFINITY);
-                        weigh(za, pw, rf);
-                        tmem_wait_ld32(zb);
-                        tmem_ld32(za, s_addr + 64);
-                        top = greatest(zb, top);
-                        weigh(zb, pw + 16, rf);
-                        tmem_wait_ld32(za);
-                        tmem_ld32(zb, s_addr + 96);
-                        top = greatest(za, top);
-                        weigh(za, pw + 32, rf);
-                        tmem_wait_ld32(zb);
-                        top = greatest(zb, top);
-                        weigh(zb, pw + 48, rf);
-                        done = !__any_sync(0xffffffffu, have && (top - m) * P.scale_log2 > kSlack);
-                        if (done)
-#pragma unroll
-                            for (int c = 0; c < 64; c += 16) tmem_st16(s_addr + c, pw + c);
-                    }
-                    if (!done) {
-                        // the maximum first, then the weights; S is read twice
-                        auto see = [&](float (&z)[32], int c) {
-                            tmem_ld32(z, s_addr + c);
-                            tmem_wait_ld32(z);
-                            if (edge) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const int x = x0 + c + e;
-                                    if (!(x >= from && x <= lim && (x >= wlo || x < P.n_sink))) z[e] = -INFINITY;
-                                }
-                            }
-                        };
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < n; c += 32) {
-                            float z[32];
-                            see(z, c);
-                            top = greatest(z, top);
-                        }
-                        // a new reference when the old one is too low (or there was none)
-                        const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack);
-                        if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                            const float a = grow && m != -INFINITY ? ex2((m - top) * P.scale_log2) : 1.0f;
-                            l *= a;
-                            // S is complete, and with it the product of the tile before: O is at rest
-#pragma unroll 1
-                            for (int d = 0; d < P.D; d += 16) {
-                                float o[16];
-                                uint32_t ow[16];
-                                tmem_ld16(o, o_addr + d);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * a);
-                                tmem_st16(o_addr + d, ow);
-                            }
-                            tmem_wait_st();
-                        }
-                        if (grow) m = top;
-                        const float ref = m == -INFINITY ? 0.0f : m;
-                        const float2 rf = make_float2(-ref * P.scale_log2, -ref * P.scale_log2);
-                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-                        for (int c = 0; c < n; c += 32) {
-                            float z[32];
-                            uint32_t pw[16];
-                            see(z, c);
-                            weigh(z, pw, rf);
-                            tmem_st16(s_addr + c / 2, pw);  // over columns that have been read
+                        tmem_st16(s_at + 16, pw + 16);
+                        sum[0] = add2(sum[0], sum[1]);
+                        l += sum[0].x + sum[0].y;
+                        tmem_wait_st();
+                        if (skip) {
+                            if (i + u > 0 && !product_done(products - 1)) return;
+                            tc_fence_after();
+                            mixed_tile(P.D, s_at, o_addr, v_tile, u * kHalf, xu, nu, from, lim, wlo, P.n_sink, i + u == 0);
                         }
                     }
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
-                    tmem_wait_st();
-                    if (skip)
-                        mixed_tile(P.D, s_addr, o_addr, ring_mem + v_slot * tb, x0, n, from, lim, wlo, P.n_sink, i == 0);
+                    if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w][u]) = skip;
+                    tc_fence_before();
+                    mbar_arrive(&sh.p_full[w][u]);
+                    ++products;
                 }
-                if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
-                tc_fence_before();
-                mbar_arrive(&sh.p_full[w]);
                 ring.step();
                 ring.step();
             }
-            if (!wait_warp(ab, &sh.o_full[w], o_phase)) return;
-            o_phase ^= 1u;
+            if (!product_done(products - 1)) return;
             tc_fence_after();
         } else {
             for (int i = 0; i < 2 * nt; ++i) ring.step();
@@ -475,12 +478,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.pipe.desc_full[i], 1);
             mbar_init(&sh.pipe.desc_empty[i], 10);  // eight softmax warps and two issuing threads
             mbar_init(&sh.q_full[i], 128);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 128);
-            mbar_init(&sh.o_full[i], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&sh.s_full[i][u], 1);
+                mbar_init(&sh.p_full[i][u], 128);
+                mbar_init(&sh.o_done[i][u], 1);
+                sh.skip[i][u] = 0;
+            }
             mbar_init(&sh.agree[i], 4);
             mbar_init(&sh.drain[i], 1);
-            sh.skip[i] = 0;
         }
         sh.pipe.abort = 0;
         fence_mbar_init();
