@@ -1,22 +1,22 @@
 // Attention of many rows on the tensor cores (bf16, head sizes that are multiples of 16 up to 128): long
 // prompts, and the shared prefix, whose rows are those of the whole batch.
 //
-// One CTA per SM, an item of 256 packed rows in two accumulators of 128 that use the same tiles. Per half
-// tile of 64 keys and accumulator:
+// One CTA per SM, an item of 256 packed rows in two accumulators of 128 that use the same tiles. Per
+// tile of 128 keys and accumulator:
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, S (fp32) in tensor memory
-//   P = 2^(S - m)  a warpgroup, one row per thread; P (bf16) goes back over S's columns
+//   P = 2^(S - m)  a warpgroup, one row per thread; P (bf16) goes back over S's columns, in two halves
 //   O += P V       tcgen05.mma, P read from tensor memory, V from shared memory
-// Tensor memory holds O (128 columns) and S of two halves (64 each) per accumulator: the scores of the
-// next half are there when a half's weights are done, and the products' latency (some 1500 cycles from a
-// finished P to the next S) is hidden. With S of whole tiles, one each, a tile took 4500 cycles, of which the
-// warpgroups waited 2150. The halves cost the first product a third of its rate (64 columns do not make
-// up for reading 128 rows of queries again).
+// One warp issues the products of both accumulators in turn, so that one's run while the other's softmax
+// does: a product of 128 x 128 x 128 takes 512 cycles of the tensor cores, four of them a tile. Issued
+// by a warp each, both would wait for the tensor cores at the same time and then for the softmax.
+// (S of half tiles in two buffers hides the products' latency altogether, but 64 columns of keys take
+// as long as 128: the queries' 128 rows are read again. It took 4000 cycles a tile.)
 // A row's m is a reference, not the running maximum: O and the sum are rescaled only when the maximum
 // has grown by more than 2^8 beyond it (P then stays below 2^8, whose bf16 rounding is relative all the
 // same), so the output hardly ever leaves tensor memory before the end.
 //
-// Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 keeps the books (the requests' status), 10 and
-// 11 issue matrix instructions (for accumulator 0 and 1).
+// Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 keeps the books (the requests' status), 10
+// issues matrix instructions.
 #pragma once
 
 #include "spec_attend_tiles.cuh"
@@ -28,14 +28,14 @@ using namespace tiles;
 
 constexpr int kRTLog2 = 8, kRows = 128;  // rows of an item, of an accumulator
 constexpr int kHalf = kKT / 2;           // positions whose scores are taken at a time
-constexpr int kThreads = 384;
+constexpr int kThreads = 352;
 constexpr float kSlack = 8.0f;           // log2 growth of the maximum that O and the sum absorb
 
 struct Shared {
     Pipe<kMaxStages> pipe;
-    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], agree[2], drain[2];
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_half[2], o_full[2], agree[2], drain;
     uint32_t bad[2][2][4];  // per warp: its quarter of the values holds one that is not finite
-    uint32_t skip[2][2];    // the warpgroup has done this half's second product itself
+    uint32_t skip[2];       // the warpgroup does this tile's second product itself
     uint32_t tmem;
 };
 
@@ -49,95 +49,102 @@ __host__ constexpr int smem_bytes(int D) {
     return 1024 + 2 * kQBytes + stages(D) * tile_bytes(D) + static_cast<int>(sizeof(Shared));
 }
 
-// ---------------------------------------------------------------- matrix instructions (one thread)
+// ---------------------------------------------------------------- matrix instructions (one warp)
 
-__device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsigned char *q_tile, unsigned char *ring_mem,
-                                         int w, int n_stages) {
+__device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsigned char *q_mem, unsigned char *ring_mem,
+                                         int n_stages) {
     const int tb = tile_bytes(P.D);
     int32_t *ab = &sh.pipe.abort;
-    const uint32_t s_col = sh.tmem + w * 256, o_col = s_col + 128;
-    // One thread's instructions set the pace: 64 cycles of products each leave room for little more than
-    // an addition, so the operands are prepared and the steps unrolled.
-    const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
+    const uint32_t tmem = sh.tmem, pv_shape = mma_shape(P.D, false, true);
+    const uint64_t q_op = smem_operand(smem_addr(q_mem), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
                    v_op = smem_operand(smem_addr(ring_mem), kBlock);
     const int steps = P.D / 16;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
-    uint32_t q_phase = 0, p_phase = 0, products = 0;
-    const uint32_t pv_shape = mma_shape(P.D, false, true);
-    // S of half u of the tile in slot: n of its positions are used
-    auto score = [&](const Ring &at, int u, int n) {
-        const uint64_t k = operand_at(k_op, at.slot * tb + u * (kHalf * 128));
+    uint32_t q_phases = 0, p_phases = 0;
+    // S = Q K^T of accumulator w; n positions of the tile are used
+    auto score = [&](int w, const Ring &at, int n) {
+        const uint64_t k = operand_at(k_op, at.slot * tb), q = operand_at(q_op, w * kQBytes);
         const uint32_t shape = mma_shape(n, false, false);
+        if (elect_lane()) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t in = (i >> 2) * kBlock + (i & 3) * 32;
-            if (i < steps) mma_ss(s_col + u * kHalf, operand_at(q_op, in), operand_at(k, in), shape, i > 0);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t in = (i >> 2) * kBlock + (i & 3) * 32;
+                if (i < steps) mma_ss(tmem + w * 256, operand_at(q, in), operand_at(k, in), shape, i > 0);
+            }
+            mma_commit(&sh.s_full[w]);
         }
-        mma_commit(&sh.s_full[w][u]);
+        __syncwarp();
+    };
+    // O += P V of accumulator w and half u; n positions of the half are used
+    auto weigh = [&](int w, int u, const Ring &at, int n, bool add) {
+        const uint64_t v = operand_at(v_op, at.slot * tb + u * (kHalf * 128));
+        const uint32_t p = tmem + w * 256 + u * kHalf, o = tmem + w * 256 + 128;
+        if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) && elect_lane()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i * 16 < n) mma_ts(o, p + 8 * i, operand_at(v, i * 2048), pv_shape, add || i > 0);
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t *bar) {
+        if (elect_lane()) mma_commit(bar);
+        __syncwarp();
     };
     for (;;) {
-        if (!wait_one(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
+        if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
         if (s.nrows == 0) return;
-        const int nt = s.ntile, first = s.tile;
+        const int nt = s.ntile, first = s.tile, accs = s.nrows > kRows ? 2 : 1;
         const KeyTiles keys = s.keys;
-        if (nt > 0 && s.nrows <= w * kRows) {
-            for (int t = 0; t < 2 * nt; ++t) {  // no rows for this accumulator: let the tiles go by
-                if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-                mbar_arrive(&sh.pipe.empty[ring.slot]);
-                ring.step();
-            }
-        } else if (nt > 0) {
-            if (!wait_one(ab, &sh.q_full[w], q_phase)) return;
-            q_phase ^= 1u;
-            if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-            tc_fence_after();
+        if (nt > 0) {
             int n = tile_keys(keys, tile_begin<kKT>(keys, first));
-            score(ring, 0, min(n, kHalf));
-            if (n > kHalf) score(ring, 1, n - kHalf);
-            mma_commit(&sh.pipe.empty[ring.slot]);
+            if (!wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+            for (int w = 0; w < accs; ++w) {
+                if (!wait_warp(ab, &sh.q_full[w], q_phases >> w & 1u)) return;
+                q_phases ^= 1u << w;
+                tc_fence_after();
+                score(w, ring, n);
+            }
+            commit(&sh.pipe.empty[ring.slot]);
             ring.step();
             for (int t = 0; t < nt; ++t) {
                 const Ring v = ring;  // this tile's values; the next tile's keys follow them
                 ring.step();
                 const bool more = t + 1 < nt;
                 const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int here = n - u * kHalf;
-                    if (here > 0) {
-                        if (u == 0 && !wait_one(ab, &sh.pipe.full[v.slot], v.phase)) return;
-                        if (!wait_one(ab, &sh.p_full[w][u], p_phase >> u & 1u)) return;
-                        p_phase ^= 1u << u;
+                if (!wait_warp(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                for (int w = 0; w < accs; ++w) {
+                    if (!wait_warp(ab, &sh.p_full[w][0], p_phases >> w & 1u)) return;
+                    tc_fence_after();
+                    weigh(w, 0, v, min(n, kHalf), t > 0);
+                    if (n > kHalf) {
+                        commit(&sh.o_half[w]);
+                        if (!wait_warp(ab, &sh.p_full[w][1], p_phases >> (2 + w) & 1u)) return;
+                        p_phases ^= 4u << w;
                         tc_fence_after();
-                        if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w][u])) {  // O += P V
-                            const uint64_t values = operand_at(v_op, v.slot * tb + u * (kHalf * 128));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (i * 16 < here)
-                                    mma_ts(o_col, s_col + u * kHalf + 8 * i, operand_at(values, i * 2048), pv_shape,
-                                           t > 0 || u > 0 || i > 0);
-                        }
-                        mma_commit(&sh.o_done[w][products & 1u]);
-                        ++products;
+                        weigh(w, 1, v, n - kHalf, true);
                     }
-                    // S and P share columns: matrix instructions of one thread run in the order of their
-                    // issue, so the next scores follow the product that reads P
-                    if (u == 0 && more && !wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-                    if (next > u * kHalf) {
+                    p_phases ^= 1u << w;
+                    if (more) {
+                        if (w == 0 && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
                         tc_fence_after();
-                        score(ring, u, min(next - u * kHalf, kHalf));
+                        // S and P share columns: matrix instructions of one thread run in the order of
+                        // their issue, so this one follows the product that reads P
+                        score(w, ring, next);
+                    } else {
+                        commit(&sh.o_full[w]);
                     }
                 }
-                mma_commit(&sh.pipe.empty[v.slot]);
+                commit(&sh.pipe.empty[v.slot]);
                 if (more) {
-                    mma_commit(&sh.pipe.empty[ring.slot]);
+                    commit(&sh.pipe.empty[ring.slot]);
                     ring.step();
                 }
                 n = next;
             }
         }
-        mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        if (elect_lane()) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        __syncwarp();
         desc.step();
     }
 }
@@ -192,10 +199,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_addr = sh.tmem + w * 256 + lanes, o_addr = s_addr + 128;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
-    uint32_t s_phase = 0, agree_phase = 0, products = 0;
-    // Products take two barriers in turn: when a half's scores are there, the product two before it is done
-    // (the scores were issued behind it), so that on either barrier only one phase can be meant.
-    auto product_done = [&](uint32_t x) { return wait_warp(ab, &sh.o_done[w][x & 1u], x >> 1 & 1u); };
+    uint32_t s_phase = 0, o_phase = 0, half_phase = 0, agree_phase = 0;
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -274,13 +278,15 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                     agree_phase ^= 1u;
                     skip = (found[0] | found[1] | found[2] | found[3]) != 0;
                 }
+                if (!wait_warp(ab, &sh.s_full[w], s_phase)) return;
+                s_phase ^= 1u;
+                tc_fence_after();
+                // (the tile before has been read out of this word: its products were issued before S)
+                if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
 #pragma unroll 1
                 for (int u = 0; u * kHalf < n; ++u) {
                     const int xu = x0 + u * kHalf, nu = min(n - u * kHalf, kHalf);
                     const uint32_t s_at = s_addr + u * kHalf;
-                    if (!wait_warp(ab, &sh.s_full[w][u], s_phase >> u & 1u)) return;
-                    s_phase ^= 1u << u;
-                    tc_fence_after();
                     if (warp_has) {
                         float za[32], zb[32];
                         uint32_t pw[32];
@@ -309,8 +315,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         const bool grow = top > m && !((top - m) * P.scale_log2 <= kSlack) && have;
                         if (__any_sync(0xffffffffu, grow)) {
                             if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                                // the product before this half's is the last that was begun
-                                if (!product_done(products - 1)) return;
+                                // O is at rest: with S came the end of the tiles before, and the first half's
+                                // product has a barrier of its own
+                                if (u > 0 && !wait_warp(ab, &sh.o_half[w], half_phase)) return;
                                 tc_fence_after();
                                 const float a = grow && m != -INFINITY ? ex2((m - top) * P.scale_log2) : 1.0f;
                                 l *= a;
@@ -353,20 +360,20 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         l += sum[0].x + sum[0].y;
                         tmem_wait_st();
                         if (skip) {
-                            if (i + u > 0 && !product_done(products - 1)) return;
+                            if (u > 0 && !wait_warp(ab, &sh.o_half[w], half_phase)) return;
                             tc_fence_after();
                             mixed_tile(P.D, s_at, o_addr, v_tile, u * kHalf, xu, nu, from, lim, wlo, P.n_sink, i + u == 0);
                         }
                     }
-                    if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w][u]) = skip;
                     tc_fence_before();
                     mbar_arrive(&sh.p_full[w][u]);
-                    ++products;
                 }
+                if (n > kHalf) half_phase ^= 1u;
                 ring.step();
                 ring.step();
             }
-            if (!product_done(products - 1)) return;
+            if (!wait_warp(ab, &sh.o_full[w], o_phase)) return;
+            o_phase ^= 1u;
             tc_fence_after();
         } else {
             for (int i = 0; i < 2 * nt; ++i) ring.step();
@@ -472,21 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < n_stages; ++i) {
             mbar_init(&sh.pipe.full[i], 1);
-            mbar_init(&sh.pipe.empty[i], 2);  // both accumulators
+            mbar_init(&sh.pipe.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.pipe.desc_full[i], 1);
-            mbar_init(&sh.pipe.desc_empty[i], 10);  // eight softmax warps and two issuing threads
+            mbar_init(&sh.pipe.desc_empty[i], 9);  // eight softmax warps and the issuing one
             mbar_init(&sh.q_full[i], 128);
-            for (int u = 0; u < 2; ++u) {
-                mbar_init(&sh.s_full[i][u], 1);
-                mbar_init(&sh.p_full[i][u], 128);
-                mbar_init(&sh.o_done[i][u], 1);
-                sh.skip[i][u] = 0;
-            }
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i][0], 128);
+            mbar_init(&sh.p_full[i][1], 128);
+            mbar_init(&sh.o_half[i], 1);
+            mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.agree[i], 4);
-            mbar_init(&sh.drain[i], 1);
+            sh.skip[i] = 0;
         }
+        mbar_init(&sh.drain, 1);
         sh.pipe.abort = 0;
         fence_mbar_init();
         prefetch_map(&kmap);
@@ -504,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
         } else if (warp == 9) {
             if constexpr (!PREFIX) keep_books<kKT>(P, lane);
-        } else if (lane == 0) {
-            const int w = warp - 10;
-            mma_role(P, sh, base + w * kQBytes, ring_mem, w, n_stages);
-            // nothing this thread issued is in flight when the CTA ends
-            mma_commit(&sh.drain[w]);
+        } else {
+            mma_role(P, sh, base, ring_mem, n_stages);
+            // nothing this warp issued is in flight when the CTA ends
+            if (elect_lane()) mma_commit(&sh.drain);
+            __syncwarp();
 #pragma unroll 1
-            for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain[w], 0, kHintNs); ++t) {
+            for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain, 0, kHintNs); ++t) {
             }
         }
     }

@@ -90,7 +90,14 @@ __device__ __forceinline__ uint32_t mma_shape(int n, bool a_cols, bool b_cols) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_cols ? 1u << 15 : 0u) | (b_cols ? 1u << 16 : 0u) |
            (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// D (tensor memory) = A (shared) B (shared) + (add ? D : 0), 16 deep. One thread issues.
+// True in one lane of a converged warp, the same one every time. Around matrix instructions a warp that
+// stays together keeps their operands in uniform registers, where they are taken from.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// D (tensor memory) = A (shared) B (shared) + (add ? D : 0), 16 deep. One lane issues.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
