@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const At
         for (int r = first + warp; r < min(first + kJoinRows, rows); r += kJoinWarps) {
             own.later = static_cast<int64_t>(2 * own.w0) * P.own_pitch + r;
             own.base = own.later + (before < start ? P.own_pitch : 0);
-            const int j = (r0 + r) / P.G, g = r0 + r - j * P.G;
+            const int j = P.by_group(r0 + r), g = r0 + r - j * P.G;
             join_row<E>(P, own, pre, q.r0 + j, head * P.G + g, lane);
         }
         return;
@@ -266,9 +266,8 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
     P.G = a->n_q_heads / a->n_kv_heads;
     P.D = a->head_dim;
     P.page_size = a->page_size;
-    P.page_shift = -1;
-    for (int s = 0; s < 31; ++s)
-        if (a->page_size == 1 << s) P.page_shift = s;
+    P.by_page = FastDiv(a->page_size);
+    P.by_group = FastDiv(P.G);
     P.max_blocks = a->max_blocks;
     P.n_pages = a->n_pages;
     P.window = a->window;

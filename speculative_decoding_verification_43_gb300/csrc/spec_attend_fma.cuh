@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
         __syncthreads();  // the last segment's queries and tiles have been used
         for (int c = threadIdx.x; c < s.nrows * per; c += kThreads) {
             const int r = c / per, d = (c - r * per) * V;
-            const int j = (s.row0 + r) / P.G, g = s.row0 + r - j * P.G;
+            const int j = P.by_group(s.row0 + r), g = s.row0 + r - j * P.G;
             if (SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
                 bring(sQ + r * D + d, static_cast<const E *>(P.q) + (s.t0 + j) * P.q_stride +
                                           static_cast<int64_t>(s.head * P.G + g) * D + d);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
 #pragma unroll
             for (int c = 0; c < NC; ++c) R.o[r][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r < nr) {
-                const int j = (s.row0 + r * kWarps + warp) / P.G;
+                const int j = P.by_group(s.row0 + r * kWarps + warp);
                 if constexpr (PREFIX) {
                     const ReqRows q = load_request(P, find_request(P.row_off, P.B, j, lane));
                     R.pos[r] = j >= q.r0 && j < q.r0 + q.n ? q.kv - q.n + (j - q.r0) : -1;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
                 // a sum that is not a number must reach the joined row, whatever the other parts' maxima
                 if (lane == 0) P.part_ml[s.part + row] = make_float2(isnan(R.l[r]) ? INFINITY : R.m[r], R.l[r]);
             } else {
-                const int j = (s.row0 + row) / P.G, g = s.row0 + row - j * P.G;
+                const int j = P.by_group(s.row0 + row), g = s.row0 + row - j * P.G;
                 const int t = s.t0 + j, h = s.head * P.G + g;
                 if (!SPEC_IN(t, P.T, DBG_ATTEND)) continue;
                 const float inv = R.l[r] == 0.0f ? 0.0f : 1.0f / R.l[r];

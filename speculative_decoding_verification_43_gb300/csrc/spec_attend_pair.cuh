@@ -107,6 +107,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
             }
             commit(&sh.pipe.empty[ring.slot]);
             ring.step();
+#pragma unroll 1
             for (int t = 0; t < nt; ++t) {
                 const Ring v = ring;  // this tile's values; the next tile's keys follow them
                 ring.step();
@@ -210,7 +211,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
         const bool warp_has = warp * kWarp < mine;
         const int nt = s.ntile;
         // this thread's row
-        const int pr = s.row0 + off + tid, j = pr / P.G, g = pr - j * P.G;
+        const int pr = s.row0 + off + tid, j = P.by_group(pr), g = pr - j * P.G;
         const int t = s.t0 + j, h = s.head * P.G + g;
         float m = -INFINITY, l = 0.0f;  // reference (scores, unscaled) and sum
         bool dead = true;               // no position, or no keys at all
@@ -234,6 +235,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             if (have) {
                 if constexpr (PREFIX) {
                     int lo = 0, n = P.B;  // the row's request
+#pragma unroll 1
                     while (n > 1) {
                         const int half = n / 2;
                         if (P.row_off[lo + half] <= t) {
@@ -257,6 +259,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             // a tile is seen whole by all rows from x0 = from on to here, when no window cuts it off
             const int whole = min(s.pmin, keys.hi - 1) - (kKT - 1), cut = P.window > 0 ? s.pmax - P.window : -1;
             const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+#pragma unroll 1
             for (int i = 0; i < nt; ++i) {
                 const int x0 = tile_begin<kKT>(keys, first + i), n = tile_keys(keys, x0);
                 const bool edge = x0 > whole || x0 < from || (x0 <= cut && x0 + kKT > P.n_sink);

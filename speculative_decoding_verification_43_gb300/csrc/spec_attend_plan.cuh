@@ -25,7 +25,8 @@ namespace spec {
 
 struct AttendParams {
     int32_t B, T, Hq, Hkv, G, D;
-    int32_t page_size, page_shift;  // page_shift >= 0: page_size is 1 << page_shift
+    int32_t page_size;
+    FastDiv by_page, by_group;      // by page_size and G
     int32_t box_log2;               // slots copied as one box (a divisor of page_size), as a power of two
     int32_t max_blocks, n_pages, window, n_sink, shared_len;
     float scale_log2;  // scale * log2(e): the softmax is taken in base 2
@@ -63,7 +64,7 @@ __device__ __forceinline__ ReqRows load_request(const AttendParams &P, int i) {
 
 // Element offset of position x's slot (head 0), or -1 when it has no page.
 __device__ __forceinline__ int64_t slot_offset(const AttendParams &P, const int32_t *table, int x) {
-    const int b = P.page_shift >= 0 ? x >> P.page_shift : x / P.page_size;
+    const int b = P.by_page(x);
     const int page = table[b];
     if (page < 0 || page >= P.n_pages) return -1;
     return page * P.page_stride + (x - b * P.page_size) * P.slot_stride;
@@ -107,7 +108,7 @@ __device__ __forceinline__ bool item_sees(const AttendParams &P, const KeyTiles 
 template <int KT>
 __device__ __forceinline__ KeyTiles own_tiles(const AttendParams &P, const ReqRows &q, int k) {
     const int base = q.kv - q.n, r0 = k << P.own_rt_log2, r1 = r0 + (1 << P.own_rt_log2), end = q.n * P.G;
-    const int j0 = k == 0 ? 0 : r0 / P.G, j1 = r1 >= end ? q.n - 1 : (r1 - 1) / P.G;
+    const int j0 = P.by_group(r0), j1 = P.by_group(min(r1, end) - 1);
     return key_tiles<KT>(P, P.shared_len, base + j1 + 1, max(base + j0, 0));
 }
 // Row tiles of n rows of G query heads.
@@ -117,6 +118,7 @@ template <int KT>
 __device__ __forceinline__ int own_units(const AttendParams &P, const ReqRows &q) {
     int u = 0;
     const int tiles = row_tiles(q.n * P.G, P.own_rt_log2);
+#pragma unroll 1
     for (int k = 0; k < tiles; ++k) u += max(own_tiles<KT>(P, q, k).n, 1);
     return u;
 }
@@ -151,6 +153,7 @@ template <int KT>
 __device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane) {
     Totals t = {0, 0, (P.B + kWarp - 1) / kWarp, INT_MAX, -1};
     int mine = 0;
+#pragma unroll 1
     for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
         const ReqRows q = load_request(P, i);
         if (q.n > 0 && q.kv > 0) {
@@ -176,6 +179,7 @@ template <int KT>
 __device__ __forceinline__ void record_units(const AttendParams &P, int lane) {
     const Totals t = batch_totals<KT>(P, lane);
     int u = t.before;
+#pragma unroll 1
     for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
         if (SPEC_IN(i, P.B, DBG_ATTEND)) P.unit_prefix[i] = u;
         u += P.Hkv * own_units<KT>(P, load_request(P, i));
@@ -241,6 +245,7 @@ struct Walker {
                 // the lane whose requests have unit u (the last one with no more before it), then the request
                 const int l = __popc(__ballot_sync(0xffffffffu, t.before <= u)) - 1;
                 int rem = u - __shfl_sync(0xffffffffu, t.before, l), per_head;
+#pragma unroll 1
                 for (i = l * t.per;; ++i) {
                     q = load_request(P, i);
                     per_head = own_units<KT>(P, q);
@@ -250,6 +255,7 @@ struct Walker {
                 head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
                 head = rem / per_head;
                 rem -= head * per_head;
+#pragma unroll 1
                 for (; k + 1 < head_tiles; ++k) {
                     const int nt = max(own_tiles<KT>(P, q, k).n, 1);
                     if (rem < nt) break;
@@ -276,7 +282,7 @@ struct Walker {
         s.req = PREFIX ? -1 : i;
         s.tile = tile;
         s.ntile = min(take, s.keys.n);
-        s.pmin = PREFIX ? pmin : max(s.base + (k == 0 ? 0 : s.row0 / P.G), 0);
+        s.pmin = PREFIX ? pmin : max(s.base + P.by_group(s.row0), 0);
         s.pmax = PREFIX ? pmax : s.keys.hi - 1;
         const bool whole = take == units;
         if (P.shared_len > 0) {
@@ -299,6 +305,7 @@ struct Walker {
                 if (++head >= P.Hkv) {
                     head = 0;
                     if (!PREFIX && u < u_end) {
+#pragma unroll 1
                         do {
                             q = load_request(P, ++i);
                         } while (q.n == 0 && i + 1 < P.B);
@@ -320,24 +327,23 @@ __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int l
     if (r0 < 0 || r1 < r0 || r1 > P.T || kv < 0) return SPEC_REQ_BAD_SHAPE;
     if (r1 == r0 || kv == 0) return SPEC_REQ_OK;
     if (kv > static_cast<int64_t>(P.max_blocks) * P.page_size) return SPEC_REQ_BAD_BLOCKS;
-    bool bad = false;
-    // positions [a, b) through a table
-    auto scan = [&](const int32_t *table, int a, int b) {
-        if (a >= b) return;
-        for (int x = a / P.page_size + lane; x <= (b - 1) / P.page_size; x += kWarp) {
-            const int page = table[x];
-            bad |= page < 0 || page >= P.n_pages;
-        }
-    };
     const int32_t *table = P.block_table + static_cast<int64_t>(i) * P.max_blocks;
     const int win = P.window > 0 ? max(max(kv - (r1 - r0), 0) - P.window + 1, 0) : 0;
     const int sinks = min(min(P.n_sink, win), kv);
     const int L = P.shared_len;
-    scan(table, max(win, L), kv);
-    scan(table, L, sinks);
-    if (L > 0) {
-        scan(P.shared_table, win, min(L, kv));
-        scan(P.shared_table, 0, min(sinks, L));
+    bool bad = false;
+    // the positions seen: window and sinks, of the request's own part and of the shared prefix
+#pragma unroll 1
+    for (int part = 0; part < (L > 0 ? 4 : 2); ++part) {
+        const int a = part == 0 ? max(win, L) : part == 1 ? L : part == 2 ? win : 0;
+        const int b = part == 0 ? kv : part == 1 ? sinks : part == 2 ? min(L, kv) : min(sinks, L);
+        if (a >= b) continue;
+        const int32_t *pages = part < 2 ? table : P.shared_table;
+#pragma unroll 1
+        for (int x = P.by_page(a) + lane; x <= P.by_page(b - 1); x += kWarp) {
+            const int page = pages[x];
+            bad |= page < 0 || page >= P.n_pages;
+        }
     }
     return __any_sync(0xffffffffu, bad) ? SPEC_REQ_BAD_BLOCKS : SPEC_REQ_OK;
 }
@@ -347,6 +353,7 @@ __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int l
 template <int KT>
 __device__ __forceinline__ void keep_books(const AttendParams &P, int lane) {
     if (blockIdx.x == gridDim.x - 1) record_units<KT>(P, lane);
+#pragma unroll 1
     for (int i = blockIdx.x; i < P.B; i += gridDim.x) {
         const int st = attend_status(P, i, lane);
         if (lane == 0 && SPEC_IN(i, P.B, DBG_ATTEND)) P.status[i] = st;

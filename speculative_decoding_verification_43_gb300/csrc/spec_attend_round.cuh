@@ -87,54 +87,52 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
         if (nt > 0) {
             const int n16 = (nrows + 15) & ~15;
             const uint32_t qk_shape = mma_shape(n16, false, false), pv_shape = mma_shape(n16, true, true);
-            auto score = [&](int b) {  // S^T = K Q^T
-                const uint64_t k = operand_at(k_op, ring.slot * tb);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t in = (i & 3) * 32;
-                    if (i < steps)
-                        mma_ss(s_col + b * RT, operand_at(k, (i >> 2) * kBlock + in),
-                               operand_at(q_op, (i >> 2) * (RT * 128) + in), qk_shape, i > 0);
-                }
-                mma_commit(&sh.s_full[b]);
-                mma_commit(&sh.pipe.empty[ring.slot]);
-                ring.step();
-            };
             if (!wait_one(ab, &sh.q_full, q_phase)) return;
             q_phase ^= 1u;
-            if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-            tc_fence_after();
-            score(0);
+            // step t: tile t's product, and tile t + 1's scores (step -1: the first scores alone). The scores
+            // go first if their keys are there.
 #pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
+            for (int t = -1; t < nt; ++t) {
+                const bool more = t + 1 < nt;
                 const Ring v = ring;  // this tile's values; the next tile's keys follow them
-                ring.step();
-                // the next scores first if their keys are there, else this tile's product
-                bool ahead = t + 1 < nt && mbar_try_wait(&sh.pipe.full[ring.slot], ring.phase);
-                if (ahead) {
-                    tc_fence_after();
-                    score((t + 1) & 1);
-                }
-                if (!wait_one(ab, &sh.pipe.full[v.slot], v.phase)) return;
-                if (!wait_one(ab, &sh.p_full, p_phase)) return;
-                p_phase ^= 1u;
-                tc_fence_after();
-                if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip)) {  // O^T += V^T P^T
-                    const uint64_t values = operand_at(v_op, v.slot * tb);
-                    const int n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile + t));
+                if (t >= 0) ring.step();
+                const bool ahead = more && mbar_try_wait(&sh.pipe.full[ring.slot], ring.phase);
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    if (part == (ahead ? 0 : 1)) {
+                        if (!more) continue;
+                        if (!ahead && !wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                        tc_fence_after();
+                        const int b = (t + 1) & 1;  // S^T = K Q^T
+                        const uint64_t k = operand_at(k_op, ring.slot * tb);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i * 16 < n)
-                            mma_ss(o_col, operand_at(values, i * 2048), operand_at(p_op, i * 16 * RT * 2), pv_shape,
-                                   t > 0 || i > 0);
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t in = (i & 3) * 32;
+                            if (i < steps)
+                                mma_ss(s_col + b * RT, operand_at(k, (i >> 2) * kBlock + in),
+                                       operand_at(q_op, (i >> 2) * (RT * 128) + in), qk_shape, i > 0);
+                        }
+                        mma_commit(&sh.s_full[b]);
+                        mma_commit(&sh.pipe.empty[ring.slot]);
+                    } else if (t >= 0) {
+                        if (!wait_one(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                        if (!wait_one(ab, &sh.p_full, p_phase)) return;
+                        p_phase ^= 1u;
+                        tc_fence_after();
+                        if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip)) {  // O^T += V^T P^T
+                            const uint64_t values = operand_at(v_op, v.slot * tb);
+                            const int n = tile_keys(s.keys, tile_begin<kKT>(s.keys, s.tile + t));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (i * 16 < n)
+                                    mma_ss(o_col, operand_at(values, i * 2048), operand_at(p_op, i * 16 * RT * 2), pv_shape,
+                                           t > 0 || i > 0);
+                        }
+                        mma_commit(&sh.o_done);
+                        mma_commit(&sh.pipe.empty[v.slot]);
+                    }
                 }
-                mma_commit(&sh.o_done);
-                mma_commit(&sh.pipe.empty[v.slot]);
-                if (t + 1 < nt && !ahead) {
-                    if (!wait_one(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-                    tc_fence_after();
-                    score((t + 1) & 1);
-                }
+                if (more) ring.step();
             }
         }
         mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
@@ -144,19 +142,29 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
 
 // ---------------------------------------------------------------- softmax (one position per thread)
 
-// The four warps meet; each leaves a word, and all get the words' union. Bounded, like every wait.
-template <int RT>
-__device__ __forceinline__ bool agree(Shared<RT> &sh, uint32_t &phase, int warp, int lane, uint32_t mine, uint32_t &all) {
-    volatile uint32_t *found = sh.found[phase];
+// The four warps meet; each leaves a word, and all get the words' union (-1: a wait gave up).
+__device__ __forceinline__ int meet(int32_t *abort, uint64_t *bar, uint32_t (*found)[4], uint32_t phase, uint32_t mine) {
+    const int warp = threadIdx.x / kWarp;
+    volatile uint32_t *words = found[phase];
     __syncwarp();
-    if (lane == 0) {
-        found[warp] = mine;
-        mbar_arrive(&sh.agree);
+    if (threadIdx.x % kWarp == 0) {
+        words[warp] = mine;
+        mbar_arrive(bar);
     }
-    if (!wait_warp(&sh.pipe.abort, &sh.agree, phase)) return false;
+    if (!wait_warp(abort, bar, phase)) return -1;
+    return static_cast<int>(words[0] | words[1] | words[2] | words[3]);
+}
+// Out of line for the meetings that come once per item.
+__device__ __noinline__ int meet_far(int32_t *abort, uint64_t *bar, uint32_t (*found)[4], uint32_t phase, uint32_t mine) {
+    return meet(abort, bar, found, phase, mine);
+}
+template <int RT, bool FAR = true>
+__device__ __forceinline__ bool agree(Shared<RT> &sh, uint32_t &phase, uint32_t mine, uint32_t &all) {
+    const int r = FAR ? meet_far(&sh.pipe.abort, &sh.agree, sh.found, phase, mine)
+                      : meet(&sh.pipe.abort, &sh.agree, sh.found, phase, mine);
     phase ^= 1u;
-    all = found[0] | found[1] | found[2] | found[3];
-    return true;
+    all = static_cast<uint32_t>(r);
+    return r >= 0;
 }
 
 // The second product of a tile with values that are not finite, on the fp32 units: thread d has output
@@ -219,13 +227,13 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
         {
             // 128 / RT threads bring each row's query (rows up to n16: zeros) and note whose row it is
             constexpr int kPer = 128 / RT;
-            const int r = tid / kPer, pr = s.row0 + r, j = pr / P.G, g = pr - j * P.G;
+            const int r = tid / kPer, pr = s.row0 + r, j = P.by_group(pr), g = pr - j * P.G;
             const int t = s.t0 + j, h = s.head * P.G + g;
             if (r < n16) {
                 const bool have = r < nrows && SPEC_IN(t, P.T, DBG_ATTEND);
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) +
                                                                    t * P.q_stride + static_cast<int64_t>(h) * P.D);
-#pragma unroll 4
+#pragma unroll 2
                 for (int c = tid % kPer; c < P.D / 8; c += kPer)
                     *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * (RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                         have ? src[c] : make_uint4(0u, 0u, 0u, 0u);
@@ -234,6 +242,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     if (have) {
                         if constexpr (PREFIX) {
                             int lo = 0, n = P.B;  // the row's request
+#pragma unroll 1
                             while (n > 1) {
                                 const int half = n / 2;
                                 if (P.row_off[lo + half] <= t) {
@@ -258,7 +267,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             fence_proxy_async_smem();
             mbar_arrive(&sh.q_full);
         }
-        if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
+        if (!agree(sh, a_phase, 0u, word)) return;
 
         float2 l[RT / 2];  // this thread's share of the rows' sums
 #pragma unroll
@@ -325,7 +334,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     }
                 }
             mine |= __any_sync(0xffffffffu, top > kSlack) ? 1u : 0u;
-            if (!agree(sh, a_phase, warp, lane, mine, word)) return;
+            if (!agree<RT, false>(sh, a_phase, mine, word)) return;
             if (i > 0) {  // the product before this tile: the weights' memory is free, O at rest
                 if (!wait_warp(ab, &sh.o_done, o_phase)) return;
                 o_phase ^= 1u;
@@ -343,7 +352,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                             if (lane == 0) scratch.warp[warp][e + y] = v;
                         }
                     }
-                if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
+                if (!agree(sh, a_phase, 0u, word)) return;
                 if (tid < n16) {
                     const float v = fmaxf(fmaxf(scratch.warp[0][tid], scratch.warp[1][tid]),
                                           fmaxf(scratch.warp[2][tid], scratch.warp[3][tid]));
@@ -353,7 +362,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     scratch.row[tid] = grow && old != kNoRef ? ex2(nw - old) : 1.0f;
                     if (grow) sh.nref[tid] = nw;
                 }
-                if (!agree(sh, a_phase, warp, lane, mine & 2u, word)) return;
+                if (!agree(sh, a_phase, mine & 2u, word)) return;
 #pragma unroll
                 for (int e = 0; e < RT; e += 2)
                     if ((e & ~15) < nrows) {
@@ -374,7 +383,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     tmem_wait_st();
                 }
                 const uint32_t keep = word;
-                if (!agree(sh, a_phase, warp, lane, 0u, word)) return;  // the scratch has been read
+                if (!agree(sh, a_phase, 0u, word)) return;  // the scratch has been read
                 word = keep;
             }
             const bool skip = (word & 2u) != 0;
@@ -404,7 +413,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     }
                 }
             if (skip) {
-                if (!agree(sh, a_phase, warp, lane, 0u, word)) return;  // all weights are there
+                if (!agree(sh, a_phase, 0u, word)) return;  // all weights are there
                 mixed_tile<RT>(P, sh, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
             }
             if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip) = skip;
@@ -440,7 +449,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             }
             scratch.warp[warp][c + lane] = v[0];
         }
-        if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
+        if (!agree(sh, a_phase, 0u, word)) return;
         if (tid < nrows) {
             float sum = scratch.warp[0][tid] + scratch.warp[1][tid] + scratch.warp[2][tid] + scratch.warp[3][tid];
             if (sh.pos[tid] < 0) sum = 0.0f;  // padding
@@ -458,26 +467,25 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                 scratch.row[tid] = none ? 0.0f : 1.0f / sum;
             }
         }
-        if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
+        if (!agree(sh, a_phase, 0u, word)) return;
 #pragma unroll 1
-        for (int r0 = 0; r0 < nrows; r0 += 16) {
-            float o[16];
+        for (int r0 = 0; r0 < nrows; r0 += 4) {
+            float o[4];
             __syncwarp();
             if (nt > 0) {
-                tmem_ld16(o, o_addr + r0);
+                tmem_ld4(o, o_addr + r0);
                 tmem_wait_ld();
             }
             if (tid < P.D) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     const int r = r0 + e;
                     if (r >= nrows) break;
                     const float a = scratch.row[r], y = a == 0.0f ? 0.0f : o[e] * a;
                     if (s.part >= 0) {
                         if (SPEC_IN(s.part + r, P.part_rows, DBG_ATTEND)) P.part_o[(s.part + r) * P.D + tid] = y;
                     } else if (SPEC_IN(sh.tok[r], P.T, DBG_ATTEND)) {
-                        static_cast<__nv_bfloat16 *>(P.out)[sh.tok[r] * P.out_stride +
-                                                            static_cast<int64_t>(sh.qhead[r]) * P.D + tid] =
+                        static_cast<__nv_bfloat16 *>(P.out)[sh.tok[r] * P.out_stride + sh.qhead[r] * P.D + tid] =
                             __float2bfloat16_rn(y);
                     }
                 }
@@ -485,7 +493,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
         }
         tc_fence_before();
         // the rows' notes and the scratch may be written again
-        if (!agree(sh, a_phase, warp, lane, 0u, word)) return;
+        if (!agree(sh, a_phase, 0u, word)) return;
         if (lane == 0) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
         desc.step();
     }
