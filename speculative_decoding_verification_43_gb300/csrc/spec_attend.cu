@@ -27,66 +27,69 @@ constexpr int kSMs = 152;
 
 // ---------------------------------------------------------------- joining the parts
 
-constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * kWarp, kJoinRows = 16;
+constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * kWarp;
 
-// Parts of one row: part x < n comes from worker w0 + x.
+// Parts of one row: part x < n lies `pitch` rows after part x - 1 (part 1 after `later`, where the first
+// worker's slot differs from the others').
 struct PartRun {
-    int w0, n;
-    int64_t base;  // part 0's row in the workspace, the first and the later workers' parts apart
-    int64_t later;
-    int pitch;
-
-    __device__ __forceinline__ int64_t row(int x) const {
-        return (x == 0 ? base : later) + static_cast<int64_t>(x) * pitch;
-    }
+    int n, pitch;
+    int64_t base, later;
+    __device__ __forceinline__ int64_t row(int x) const { return x == 0 ? base : later + static_cast<int64_t>(x) * pitch; }
 };
 
-// Joins the parts of one row and writes it; a warp per row.
+// Joins the parts of one row and writes it; a warp per row. The parts' outputs are asked for together with
+// their maxima, four at a time, and weighed when both are there.
 template <typename E>
 __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a, const PartRun &b, int t, int h,
                                          int lane) {
     const int n = a.n + b.n;
-    float M = -INFINITY;
-    for (int x = lane; x < n; x += kWarp) {
-        const int64_t r = x < a.n ? a.row(x) : b.row(x - a.n);
-        if (SPEC_IN(r, P.part_rows, DBG_ATTEND)) M = fmaxf(M, P.part_ml[r].x);
-    }
-    M = warp_max(M);
+    float M = -INFINITY, L = 0.0f;
     float4 o[2] = {};
-    float L = 0.0f;
-    if (M != -INFINITY) {
-        for (int x0 = 0; x0 < n; x0 += kWarp) {
-            const int x = x0 + lane;
-            int64_t r = 0;
-            float w = 0.0f;
-            if (x < n) {
-                r = x < a.n ? a.row(x) : b.row(x - a.n);
-                if (SPEC_IN(r, P.part_rows, DBG_ATTEND)) {
-                    const float2 ml = P.part_ml[r];
-                    w = ex2(ml.x - M);
-                    L += w * ml.y;
-                }
-            }
-            const int cnt = min(kWarp, n - x0);
-#pragma unroll 4
-            for (int j = 0; j < cnt; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-                const int64_t rj = __shfl_sync(0xffffffffu, r, j);
-                if (wj == 0.0f) continue;  // holds nothing
-                const float *src = P.part_o + rj * P.D;
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += kWarp) {
+        const int x = x0 + lane;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (x < n) {
+            const int64_t r = x < a.n ? a.row(x) : b.row(x - a.n);
+            if (SPEC_IN(r, P.part_rows, DBG_ATTEND)) ml = P.part_ml[r];
+        }
+        const float top = fmaxf(M, warp_max(ml.x));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        // weights of these parts, and of what has been joined so far
+        const float w = ex2(ml.x - ref), keep = M == -INFINITY ? 0.0f : ex2(M - ref);
+        L = L * keep + warp_sum(w == 0.0f ? 0.0f : w * ml.y);
+        M = top;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) o[c] = make_float4(o[c].x * keep, o[c].y * keep, o[c].z * keep, o[c].w * keep);
+        const int cnt = min(kWarp, n - x0);
+#pragma unroll 1
+        for (int j0 = 0; j0 < cnt; j0 += 4) {
+            float4 v[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int y = x0 + min(j0 + j, cnt - 1);
+                const int64_t r = y < a.n ? a.row(y) : b.row(y - a.n);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int d = c * 128 + 4 * lane;
-                    if (d >= P.D) continue;
-                    const float4 v = *reinterpret_cast<const float4 *>(src + d);
-                    o[c].x = fmaf(wj, v.x, o[c].x);
-                    o[c].y = fmaf(wj, v.y, o[c].y);
-                    o[c].z = fmaf(wj, v.z, o[c].z);
-                    o[c].w = fmaf(wj, v.w, o[c].w);
+                    v[j][c] = d < P.D && SPEC_IN(r, P.part_rows, DBG_ATTEND)
+                                  ? *reinterpret_cast<const float4 *>(P.part_o + r * P.D + d)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float wj = j0 + j < cnt ? __shfl_sync(0xffffffffu, w, (j0 + j) & 31) : 0.0f;
+                if (wj == 0.0f) continue;  // holds nothing
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    o[c].x = fmaf(wj, v[j][c].x, o[c].x);
+                    o[c].y = fmaf(wj, v[j][c].y, o[c].y);
+                    o[c].z = fmaf(wj, v[j][c].z, o[c].z);
+                    o[c].w = fmaf(wj, v[j][c].w, o[c].w);
                 }
             }
         }
-        L = warp_sum(L);
     }
     if (!SPEC_IN(t, P.T, DBG_ATTEND)) return;
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -100,125 +103,106 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
         P.lse[static_cast<int64_t>(t) * P.Hq + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// Blocks [0, B): request i's status goes out, and the rows of a request in error become 0 / -inf.
-// Then, without a shared prefix, kJoinRows rows a block for every border between two workers that is the
-// first to cut an item; with one, kJoinRows rows (of all query heads) a block.
-template <typename E, int KT>
+// Request i's status goes out, and the rows of a request in error become 0 / -inf (a block).
+template <typename E>
+__device__ __forceinline__ void finish_request(const AttendParams &P, int i) {
+    int bad = 0;
+#pragma unroll 1
+    for (int w = threadIdx.x; w < P.own_workers + P.prefix_workers; w += kJoinThreads) bad |= P.err[w];
+    const int st = P.status[i] | (__syncthreads_or(bad) ? SPEC_REQ_TIMEOUT : 0);
+    if (threadIdx.x == 0 && P.req_status) P.req_status[i] = st;
+    if (st == SPEC_REQ_OK) return;
+    const ReqRows q = load_request(P, i);
+#pragma unroll 1
+    for (int j = 0; j < q.n; ++j) {
+        E *o = static_cast<E *>(P.out) + (q.r0 + j) * P.out_stride;
+#pragma unroll 1
+        for (int d = 4 * threadIdx.x; d < P.Hq * P.D; d += 4 * kJoinThreads)
+            fma::store4(o + d, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        if (P.lse)
+#pragma unroll 1
+            for (int h = threadIdx.x; h < P.Hq; h += kJoinThreads)
+                P.lse[static_cast<int64_t>(q.r0 + j) * P.Hq + h] = -INFINITY;
+    }
+}
+
+// Calls without a shared prefix: a warp for each row that an item begun by a worker may have (worker x,
+// rows 4 y ..), after the requests' blocks. Its first read says what there is to join; two round trips to
+// memory in all.
+template <typename E>
 __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(const AttendParams P) {
     griddep_launch_dependents();
     griddep_wait();
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    if (blockIdx.x < static_cast<unsigned>(P.B)) {
-        const int i = blockIdx.x;
-        int bad = 0;
-        for (int w = threadIdx.x; w < P.own_workers + P.prefix_workers; w += kJoinThreads) bad |= P.err[w];
-        const int st = P.status[i] | (__syncthreads_or(bad) ? SPEC_REQ_TIMEOUT : 0);
-        if (threadIdx.x == 0 && P.req_status) P.req_status[i] = st;
-        if (st == SPEC_REQ_OK) return;
-        const ReqRows q = load_request(P, i);
-        const int per = P.Hq * P.D;
-        for (int j = 0; j < q.n; ++j) {
-            E *o = static_cast<E *>(P.out) + (q.r0 + j) * P.out_stride;
-            for (int d = 4 * threadIdx.x; d < per; d += 4 * kJoinThreads)
-                fma::store4(o + d, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-            if (P.lse)
-                for (int h = threadIdx.x; h < P.Hq; h += kJoinThreads)
-                    P.lse[static_cast<int64_t>(q.r0 + j) * P.Hq + h] = -INFINITY;
-        }
-        return;
-    }
-    const int blk = blockIdx.x - P.B;
-    const int total = P.unit_prefix[P.B];
-    PartRun own = {}, pre = {};
-    if (P.shared_len == 0) {
-        if (total == 0) return;
-        const int per = (P.own_pitch + kJoinRows - 1) / kJoinRows;
-        const int c = blk / per + 1;  // the border between workers c - 1 and c
-        const Shares share(total, P.own_workers);
-        if (c >= share.workers) return;
-        const int u = share.first(c);
-        // the item with unit u
-        int lo = 0, n = P.B;
-        while (n > 1) {
-            const int half = n / 2;
-            if (P.unit_prefix[lo + half] <= u) {
-                lo += half;
-                n -= half;
-            } else {
-                n = half;
-            }
-        }
-        const ReqRows q = load_request(P, lo);
-        const int per_head = own_units<KT>(P, q);
-        const int head = (u - P.unit_prefix[lo]) / per_head;
-        int start = P.unit_prefix[lo] + head * per_head;
-        int k = 0, units = 0;
-        for (;; ++k) {
-            units = max(own_tiles<KT>(P, q, k).n, 1);
-            if (u < start + units) break;
-            start += units;
-        }
-        // nothing is cut here, or an earlier border has the item
-        const int before = share.first(c - 1);
-        if (start == u || before > start) return;
-        if (P.status[lo] != SPEC_REQ_OK) return;
-        // the item begins in worker c - 1: in its first segment (slot 0) when that starts with it, else in its
-        // last (slot 1); the others begin with it
-        own.w0 = c - 1;
-        own.n = share.owner(start + units - 1) - own.w0 + 1;
-        own.pitch = 2 * P.own_pitch;
-        const int first = (blk % per) * kJoinRows;
-        const int r0 = k << P.own_rt_log2, rows = min(1 << P.own_rt_log2, q.n * P.G - r0);
-        for (int r = first + warp; r < min(first + kJoinRows, rows); r += kJoinWarps) {
-            own.later = static_cast<int64_t>(2 * own.w0) * P.own_pitch + r;
-            own.base = own.later + (before < start ? P.own_pitch : 0);
-            const int j = P.by_group(r0 + r), g = r0 + r - j * P.G;
-            join_row<E>(P, own, pre, q.r0 + j, head * P.G + g, lane);
-        }
-        return;
-    }
-    const Totals t = batch_totals<KT>(P, lane);
-    const int pre_units = max(prefix_tiles<KT>(P, t).n, 1);
-    const int tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
-    const Shares share(total, P.own_workers);
-    const Shares pre_share(P.Hkv * tiles * pre_units, P.prefix_workers);
-    for (int x = 0; x < kJoinRows / kJoinWarps; ++x) {
-        const int64_t row = static_cast<int64_t>(blk) * kJoinRows + x * kJoinWarps + warp;
-        if (row >= static_cast<int64_t>(P.T) * P.Hq) return;
-        const int tok = static_cast<int>(row / P.Hq), h = static_cast<int>(row - static_cast<int64_t>(tok) * P.Hq);
-        const int head = h / P.G, g = h - head * P.G;
-        const int i = find_request(P.row_off, P.B, tok, lane);
-        const ReqRows q = load_request(P, i);
-        if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) continue;
-        {
-            const int pr = tok * P.G + g, k = pr >> P.prefix_rt_log2;
-            const int start = (head * tiles + k) * pre_units;
-            pre.w0 = pre_share.owner(start);
-            pre.n = pre_share.owner(start + pre_units - 1) - pre.w0 + 1;
+    if (blockIdx.x < static_cast<unsigned>(P.B)) return finish_request<E>(P, blockIdx.x);
+    const int blk = blockIdx.x - P.B, per = (P.own_pitch + kJoinWarps - 1) / kJoinWarps;
+    const int w = blk / per, r = (blk - w * per) * kJoinWarps + threadIdx.x / kWarp;
+    const CutItem c = P.cut[w];
+    if (r >= c.nrows || P.status[c.req] != SPEC_REQ_OK) return;
+    PartRun run, none = {};
+    run.n = c.parts;
+    run.pitch = 2 * P.own_pitch;
+    run.later = static_cast<int64_t>(2 * w) * P.own_pitch + r;
+    run.base = run.later + c.slot * P.own_pitch;
+    const int j = P.by_group(c.row0 + r), g = c.row0 + r - j * P.G;
+    join_row<E>(P, run, none, c.t0 + j, c.head * P.G + g, threadIdx.x % kWarp);
+}
+
+// Calls with a shared prefix: every row has parts of both classes. A warp for the rows of one token that
+// share a key/value head.
+template <typename E, int KT>
+__global__ void __launch_bounds__(kJoinThreads) spec_attend_join_shared_kernel(const AttendParams P) {
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x < static_cast<unsigned>(P.B)) return finish_request<E>(P, blockIdx.x);
+    const int lane = threadIdx.x % kWarp;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - P.B) * kJoinWarps + threadIdx.x / kWarp;
+    if (unit >= static_cast<int64_t>(P.T) * P.Hkv) return;
+    const int tok = static_cast<int>(unit / P.Hkv), head = static_cast<int>(unit - static_cast<int64_t>(tok) * P.Hkv);
+    const int i = find_request(P.row_off, P.B, tok, lane);
+    const ReqRows q = load_request(P, i);
+    if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) return;
+    const int pre_units = *P.prefix_units, tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
+    const Shares share(P.unit_prefix[P.B], P.own_workers), pre_share(P.Hkv * tiles * pre_units, P.prefix_workers);
+    // items of the row tiles before this row's: they are walked through with it
+    int start = P.unit_prefix[i] + head * own_units<KT>(P, q), k = 0, units = max(own_tiles<KT>(P, q, 0).n, 1);
+    const int64_t pre_rows = static_cast<int64_t>(head) * P.T * P.G;
+    const int64_t own_rows = static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
+                             (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G;
+    PartRun pre = {}, own = {};
+    int pre_k = -1, own_k = -1;
+#pragma unroll 1
+    for (int g = 0; g < P.G; ++g) {
+        const int pr = tok * P.G + g, ow = (tok - q.r0) * P.G + g;
+        if (pr >> P.prefix_rt_log2 != pre_k) {
+            pre_k = pr >> P.prefix_rt_log2;
+            const int first = (head * tiles + pre_k) * pre_units, w0 = pre_share.owner(first);
+            pre.n = pre_share.owner(first + pre_units - 1) - w0 + 1;
             pre.pitch = P.prefix_pitch;
-            pre.base = pre.later =
-                static_cast<int64_t>(head) * P.T * P.G + pr + static_cast<int64_t>(pre.w0) * P.prefix_pitch;
+            pre.base = pre.later = pre_rows + static_cast<int64_t>(w0) * P.prefix_pitch;
         }
-        {
-            const int pr = (tok - q.r0) * P.G + g, k = pr >> P.own_rt_log2;
-            int start = P.unit_prefix[i] + head * own_units<KT>(P, q);
-            for (int y = 0; y < k; ++y) start += max(own_tiles<KT>(P, q, y).n, 1);
-            own.w0 = share.owner(start);
-            own.n = share.owner(start + max(own_tiles<KT>(P, q, k).n, 1) - 1) - own.w0 + 1;
+        if (ow >> P.own_rt_log2 != own_k) {
+            own_k = ow >> P.own_rt_log2;
+#pragma unroll 1
+            for (; k < own_k; ++k) {
+                start += units;
+                units = max(own_tiles<KT>(P, q, k + 1).n, 1);
+            }
+            const int w0 = share.owner(start);
+            own.n = share.owner(start + units - 1) - w0 + 1;
             own.pitch = P.own_pitch;
-            own.base = own.later = static_cast<int64_t>(P.T) * P.Hq +
-                                   static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
-                                   (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + pr +
-                                   static_cast<int64_t>(own.w0) * P.own_pitch;
+            own.base = own.later = own_rows + static_cast<int64_t>(w0) * P.own_pitch;
         }
-        join_row<E>(P, pre, own, tok, h, lane);
+        PartRun a = pre, b = own;
+        a.base = a.later += pr;
+        b.base = b.later += ow;
+        join_row<E>(P, a, b, tok, head * P.G + g, lane);
     }
 }
 
 // ---------------------------------------------------------------- host side
 
 struct AttendLayout {
-    size_t status, unit_prefix, err, ml, o, total;
+    size_t status, unit_prefix, cut, prefix_units, err, ml, o, total;
 };
 
 static AttendLayout attend_layout(const AttendParams &P) {
@@ -231,6 +215,8 @@ static AttendLayout attend_layout(const AttendParams &P) {
     };
     L.status = take(static_cast<size_t>(P.B) * 4);
     L.unit_prefix = take((static_cast<size_t>(P.B) + 1) * 4);
+    L.cut = take(static_cast<size_t>(P.own_workers) * sizeof(CutItem));
+    L.prefix_units = take(4);
     L.err = take(static_cast<size_t>(P.own_workers + P.prefix_workers) * 4);
     L.ml = take(static_cast<size_t>(P.part_rows) * 8);
     L.o = take(static_cast<size_t>(P.part_rows) * P.D * 4);
@@ -408,12 +394,11 @@ static cudaError_t launch_fma(const AttendParams &P, cudaStream_t stream) {
 
 template <typename E, int KT>
 static cudaError_t launch_join(const AttendParams &P, cudaStream_t stream) {
-    const int64_t blocks =
-        P.shared_len > 0
-            ? (static_cast<int64_t>(P.T) * P.Hq + kJoinRows - 1) / kJoinRows
-            : static_cast<int64_t>(P.own_workers - 1) * ((P.own_pitch + kJoinRows - 1) / kJoinRows);
-    return launch_after(spec_attend_join_kernel<E, KT>, dim3(static_cast<unsigned>(P.B + blocks)),
-                        dim3(kJoinThreads), 0, stream, P);
+    const bool shared = P.shared_len > 0;
+    const int64_t blocks = shared ? (static_cast<int64_t>(P.T) * P.Hkv + kJoinWarps - 1) / kJoinWarps
+                                  : static_cast<int64_t>(P.own_workers) * ((P.own_pitch + kJoinWarps - 1) / kJoinWarps);
+    return launch_after(shared ? spec_attend_join_shared_kernel<E, KT> : spec_attend_join_kernel<E>,
+                        dim3(static_cast<unsigned>(P.B + blocks)), dim3(kJoinThreads), 0, stream, P);
 }
 
 static cudaError_t enqueue_tensor(const AttendParams &P, const CacheMaps &M, cudaStream_t stream) {
@@ -500,6 +485,8 @@ extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, s
     P.req_status = a->req_status;
     P.status = reinterpret_cast<int32_t *>(ws + L.status);
     P.unit_prefix = reinterpret_cast<int32_t *>(ws + L.unit_prefix);
+    P.cut = reinterpret_cast<CutItem *>(ws + L.cut);
+    P.prefix_units = reinterpret_cast<int32_t *>(ws + L.prefix_units);
     P.err = reinterpret_cast<int32_t *>(ws + L.err);
     P.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     P.part_o = reinterpret_cast<float *>(ws + L.o);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
     Walker<kKT, PREFIX> walk;
     walk.start(P, blockIdx.x, lane);
     Segment s;
-    while (walk.next(P, s)) {
+    while (walk.next(P, s, lane)) {
         constexpr int V = 16 / sizeof(E);
         const int per = D / V;
         __syncthreads();  // the last segment's queries and tiles have been used

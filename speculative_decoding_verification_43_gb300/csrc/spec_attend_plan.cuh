@@ -23,6 +23,15 @@
 
 namespace spec {
 
+// An item that several workers share, as the joining kernel needs it: written by the worker that begins it
+// (calls without a shared prefix; nrows = 0: this worker begins none).
+struct CutItem {
+    int req, t0, row0, nrows, head;
+    int parts;      // workers, this one first
+    int slot;       // this worker's slot of two; the others have their first
+    int pad;
+};
+
 struct AttendParams {
     int32_t B, T, Hq, Hkv, G, D;
     int32_t page_size;
@@ -40,6 +49,8 @@ struct AttendParams {
     // workspace
     int32_t *status;       // [B]
     int32_t *unit_prefix;  // [B+1] units of the own items before each request
+    CutItem *cut;          // [own workers]
+    int32_t *prefix_units; // units of a prefix item
     float2 *part_ml;       // [part rows] maximum (base 2, scaled) and sum
     float *part_o;         // [part rows][D] unnormalised output
     int32_t *err;          // [workers of both classes] 1: a bounded wait gave up
@@ -174,7 +185,8 @@ __device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane) 
     t.pmax = __reduce_max_sync(0xffffffffu, t.pmax);
     return t;
 }
-// Leaves the units before each request, and those of all, to the joining kernel (one warp).
+// Leaves the units before each request, and those of all, to the joining kernel of a call with a shared
+// prefix (one warp).
 template <int KT>
 __device__ __forceinline__ void record_units(const AttendParams &P, int lane) {
     const Totals t = batch_totals<KT>(P, lane);
@@ -215,6 +227,7 @@ struct Walker {
     ReqRows q;
     KeyTiles shared;       // prefix items: all alike
     int pmin, pmax;
+    Shares share = Shares(0, 1);
 
     __device__ __forceinline__ void start(const AttendParams &P, int w, int lane) {
         worker = w;
@@ -228,7 +241,8 @@ struct Walker {
             q.n = P.T;
             head_tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
             const int per = max(shared.n, 1);
-            const Shares share(P.Hkv * head_tiles * per, P.prefix_workers);
+            share = Shares(P.Hkv * head_tiles * per, P.prefix_workers);
+            if (w == 0 && lane == 0) *P.prefix_units = per;
             u = share.first(w);
             u_end = share.first(w + 1);
             if (u < u_end) {
@@ -238,7 +252,7 @@ struct Walker {
                 k = item - head * head_tiles;
             }
         } else {
-            const Shares share(t.units, P.own_workers);
+            share = Shares(t.units, P.own_workers);
             u = share.first(w);
             u_end = share.first(w + 1);
             if (u < u_end) {
@@ -265,10 +279,11 @@ struct Walker {
             }
         }
         u_first = u;
+        if (!PREFIX && P.shared_len == 0 && lane == 0) P.cut[w].nrows = 0;
     }
 
     // The next segment, or false at the end of the worker's units.
-    __device__ __forceinline__ bool next(const AttendParams &P, Segment &s) {
+    __device__ __forceinline__ bool next(const AttendParams &P, Segment &s, int lane) {
         if (u >= u_end) return false;
         s.keys = PREFIX ? shared : own_tiles<KT>(P, q, k);
         const int units = max(s.keys.n, 1);
@@ -294,7 +309,10 @@ struct Walker {
                 s.part += static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch;
         } else {
             // only a worker's first and last segment can be part of an item
-            s.part = whole ? -1 : static_cast<int64_t>(2 * worker + (u == u_first ? 0 : 1)) * P.own_pitch;
+            const int slot = u == u_first ? 0 : 1;
+            s.part = whole ? -1 : static_cast<int64_t>(2 * worker + slot) * P.own_pitch;
+            if (!whole && tile == 0 && lane == 0)
+                P.cut[worker] = {i, q.r0, s.row0, s.nrows, head, share.owner(u + units - 1) - worker + 1, slot, 0};
         }
         u += take;
         tile += take;
@@ -349,10 +367,10 @@ __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int l
 }
 
 // What a kernel of own items leaves to the joining kernel, by one warp of each CTA: the requests' status,
-// and (the last CTA) the units before each request.
+// and (with a shared prefix, the last CTA) the units before each request.
 template <int KT>
 __device__ __forceinline__ void keep_books(const AttendParams &P, int lane) {
-    if (blockIdx.x == gridDim.x - 1) record_units<KT>(P, lane);
+    if (P.shared_len > 0 && blockIdx.x == gridDim.x - 1) record_units<KT>(P, lane);
 #pragma unroll 1
     for (int i = blockIdx.x; i < P.B; i += gridDim.x) {
         const int st = attend_status(P, i, lane);

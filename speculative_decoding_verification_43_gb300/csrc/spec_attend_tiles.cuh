@@ -137,7 +137,7 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
     Segment s = {};
     bool ok = true;
     int used = 0;
-    while (ok && walk.next(P, s)) {
+    while (ok && walk.next(P, s, lane)) {
         ok = wait_warp(&pipe.abort, &pipe.desc_empty[desc.slot], desc.phase ^ 1u);
         if (!ok) break;
         if (lane == 0) {
