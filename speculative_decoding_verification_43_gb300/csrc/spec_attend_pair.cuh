@@ -268,7 +268,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 if (edge) {
                     const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
                     if (!wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase)) return;
-                    const bool bad = __any_sync(0xffffffffu, clean_values(P, keys, v_tile, x0, n, tid));
+                    const bool bad = __any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid));
                     fence_proxy_async_smem();
                     // the four warps' findings (two sets, used in turn)
                     volatile uint32_t *found = sh.bad[w][agree_phase];

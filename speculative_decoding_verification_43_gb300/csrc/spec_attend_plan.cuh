@@ -218,6 +218,10 @@ struct Segment {
 };
 
 // Walks a worker's segments. Used by whole warps; every lane holds the same state.
+// Own items in order. Prefix items are all alike and as long as a worker's share, roughly: a worker begins
+// with its last item, whose tiles start with the prefix, and goes on with the first, which it takes up where
+// the worker before has left it; so all workers are near the same position of the prefix at any time,
+// and what one head's row tiles read of it comes from L2.
 template <int KT, bool PREFIX>
 struct Walker {
     int u, u_end, u_first;
@@ -245,12 +249,7 @@ struct Walker {
             if (w == 0 && lane == 0) *P.prefix_units = per;
             u = share.first(w);
             u_end = share.first(w + 1);
-            if (u < u_end) {
-                const int item = u / per;
-                tile = u - item * per;
-                head = item / head_tiles;
-                k = item - head * head_tiles;
-            }
+            i = 0;  // segments so far
         } else {
             share = Shares(t.units, P.own_workers);
             u = share.first(w);
@@ -284,10 +283,21 @@ struct Walker {
 
     // The next segment, or false at the end of the worker's units.
     __device__ __forceinline__ bool next(const AttendParams &P, Segment &s, int lane) {
-        if (u >= u_end) return false;
         s.keys = PREFIX ? shared : own_tiles<KT>(P, q, k);
         const int units = max(s.keys.n, 1);
-        const int take = min(units - tile, u_end - u);
+        int take;
+        if constexpr (PREFIX) {
+            const int first = u / units, last = (u_end - 1) / units, item = i == 0 ? last : first + i - 1;
+            if (u >= u_end || (i > 0 && item >= last)) return false;
+            tile = item == first ? u - first * units : 0;
+            take = (item == last ? u_end - last * units : units) - tile;
+            head = item / head_tiles;
+            k = item - head * head_tiles;
+            ++i;
+        } else {
+            if (u >= u_end) return false;
+            take = min(units - tile, u_end - u);
+        }
         const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2;
         s.row0 = k << rt_log2;
         s.nrows = min(1 << rt_log2, q.n * P.G - s.row0);
@@ -314,6 +324,7 @@ struct Walker {
             if (!whole && tile == 0 && lane == 0)
                 P.cut[worker] = {i, q.r0, s.row0, s.nrows, head, share.owner(u + units - 1) - worker + 1, slot, 0};
         }
+        if (PREFIX) return true;
         u += take;
         tile += take;
         if (tile >= units) {
@@ -322,7 +333,7 @@ struct Walker {
                 k = 0;
                 if (++head >= P.Hkv) {
                     head = 0;
-                    if (!PREFIX && u < u_end) {
+                    if (u < u_end) {
 #pragma unroll 1
                         do {
                             q = load_request(P, ++i);

@@ -12,7 +12,8 @@
 // tile's scores are there when this tile's weights are done.
 // A row's maximum is a reference shared by the 128 threads: set from the item's first tile, and anew when
 // some score lies more than 2^8 above it (the threads agree on that each tile); else no maximum is
-// taken at all. Each thread sums its own weights, and the sums meet at the end.
+// taken at all. Each thread sums its own weights, and the sums meet at the end. The next segment's queries
+// are brought in, and their first scores taken, while a segment ends.
 //
 // Two CTAs per SM, each a worker: while one begins or ends an item the other keeps copies in flight.
 // Warps: 0-3 softmax, 4 loads tiles, 5 keeps the books, then issues the matrix instructions.
@@ -35,9 +36,9 @@ struct Shared {
     uint32_t found[2][4];  // per warp: a score beyond the reference (1), a value that is not finite (2)
     uint32_t skip;         // the warpgroup has done this tile's second product itself
     uint32_t tmem;
-    int pos[RT];           // positions of the rows (-1: none)
-    int tok[RT], qhead[RT];
-    alignas(16) float nref[RT];  // minus the reference, scaled; kNoRef before there is one (read four at a time)
+    // of this segment's rows and the next one's, in turn
+    int pos[2][RT];                 // positions (-1: none)
+    alignas(16) float nref[2][RT];  // minus the reference, scaled; kNoRef before there is one (read four at a time)
 };
 // What the row operations of a warpgroup need now and then, in the weights' memory while that is unused.
 template <int RT>
@@ -170,7 +171,7 @@ __device__ __forceinline__ bool agree(Shared<RT> &sh, uint32_t &phase, uint32_t 
 // The second product of a tile with values that are not finite, on the fp32 units: thread d has output
 // column d, the weights lie in shared memory, O is complete up to the tile before.
 template <int RT>
-__device__ __noinline__ void mixed_tile(const AttendParams &P, const Shared<RT> &sh, uint32_t o_addr,
+__device__ __noinline__ void mixed_tile(const AttendParams &P, const int *pos, uint32_t o_addr,
                                         const unsigned char *v_tile, const unsigned char *p_tile, const KeyTiles &keys,
                                         int x0, int n, int nrows, int d, bool first) {
 #pragma unroll 1
@@ -189,7 +190,7 @@ __device__ __noinline__ void mixed_tile(const AttendParams &P, const Shared<RT> 
             const float v = d < P.D ? tile_value(v_tile, k, d) : 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int r = r0 + e, p = r < nrows ? sh.pos[r] : -1;
+                const int r = r0 + e, p = r < nrows ? pos[r] : -1;
                 if (x <= p && (P.window == 0 || x > p - P.window || x < P.n_sink)) {
                     const int piece = RT == 64 ? (r >> 3) ^ (k & 7) : (r >> 3) ^ ((k >> 1) & 3);
                     const float w = __bfloat162float(
@@ -218,56 +219,64 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
     Scratch<RT> &scratch = *reinterpret_cast<Scratch<RT> *>(p_tile);
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
     uint32_t s_phases = 0, o_phase = 0, a_phase = 0, word = 0;
-    for (;;) {
-        if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
-        const Segment &s = sh.pipe.desc[desc.slot];
-        const int nrows = s.nrows, nt = s.ntile;
-        if (nrows == 0) return;
-        const int n16 = (nrows + 15) & ~15;
-        {
-            // 128 / RT threads bring each row's query (rows up to n16: zeros) and note whose row it is
-            constexpr int kPer = 128 / RT;
-            const int r = tid / kPer, pr = s.row0 + r, j = P.by_group(pr), g = pr - j * P.G;
-            const int t = s.t0 + j, h = s.head * P.G + g;
-            if (r < n16) {
-                const bool have = r < nrows && SPEC_IN(t, P.T, DBG_ATTEND);
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) +
-                                                                   t * P.q_stride + static_cast<int64_t>(h) * P.D);
-#pragma unroll 2
-                for (int c = tid % kPer; c < P.D / 8; c += kPer)
-                    *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * (RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                        have ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                if (tid % kPer == 0) {
-                    int p = -1;
-                    if (have) {
-                        if constexpr (PREFIX) {
-                            int lo = 0, n = P.B;  // the row's request
+    int buf = 0;
+    // Brings a segment's queries: 128 / RT threads each row's (rows up to a multiple of 16: zeros), and its
+    // position.
+    auto bring = [&](const Segment &s, int to) {
+        constexpr int kPer = 128 / RT;
+        const int r = tid / kPer, pr = s.row0 + r, j = P.by_group(pr), g = pr - j * P.G;
+        const int t = s.t0 + j, h = s.head * P.G + g;
+        if (r < ((s.nrows + 15) & ~15)) {
+            const bool have = r < s.nrows && SPEC_IN(t, P.T, DBG_ATTEND);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + t * P.q_stride +
+                                                               static_cast<int64_t>(h) * P.D);
+#pragma unroll 4
+            for (int c = tid % kPer; c < P.D / 8; c += kPer)
+                *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * (RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                    have ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            if (tid % kPer == 0) {
+                int p = -1;
+                if (have) {
+                    if constexpr (PREFIX) {
+                        int lo = 0, n = P.B;  // the row's request
 #pragma unroll 1
-                            while (n > 1) {
-                                const int half = n / 2;
-                                if (P.row_off[lo + half] <= t) {
-                                    lo += half;
-                                    n -= half;
-                                } else {
-                                    n = half;
-                                }
+                        while (n > 1) {
+                            const int half = n / 2;
+                            if (P.row_off[lo + half] <= t) {
+                                lo += half;
+                                n -= half;
+                            } else {
+                                n = half;
                             }
-                            const ReqRows q = load_request(P, lo);
-                            if (t >= q.r0 && t < q.r0 + q.n) p = q.kv - q.n + (t - q.r0);
-                        } else {
-                            p = s.base + j;
                         }
+                        const ReqRows q = load_request(P, lo);
+                        if (t >= q.r0 && t < q.r0 + q.n) p = q.kv - q.n + (t - q.r0);
+                    } else {
+                        p = s.base + j;
                     }
-                    sh.pos[r] = p;
-                    sh.tok[r] = t;
-                    sh.qhead[r] = h;
-                    sh.nref[r] = kNoRef;
                 }
+                sh.pos[to][r] = p;
+                sh.nref[to][r] = kNoRef;
             }
+        }
+        if (s.ntile > 0) {
             fence_proxy_async_smem();
             mbar_arrive(&sh.q_full);
         }
-        if (!agree(sh, a_phase, 0u, word)) return;
+    };
+    bool first_segment = true;
+    for (;;) {
+        const Segment &s = sh.pipe.desc[desc.slot];
+        if (first_segment) {
+            if (!wait_warp(ab, &sh.pipe.desc_full[0], 0)) return;
+            if (s.nrows == 0) return;
+            bring(s, 0);
+            if (!agree(sh, a_phase, 0u, word)) return;
+            first_segment = false;
+        }
+        const int nrows = s.nrows, nt = s.ntile, n16 = (nrows + 15) & ~15;
+        const int *pos = sh.pos[buf];
+        float *nref = sh.nref[buf];
 
         float2 l[RT / 2];  // this thread's share of the rows' sums
 #pragma unroll
@@ -282,7 +291,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             uint32_t mine = 0u;
             if (edge) {
                 if (!wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase)) return;
-                if (__any_sync(0xffffffffu, clean_values(P, s.keys, v_tile, x0, n, tid))) mine = 2u;
+                if (__any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid))) mine = 2u;
+                fence_proxy_async_smem();
             }
             if (!wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u)) return;
             s_phases ^= 1u << b;
@@ -296,7 +306,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     const int back = P.window > 0 ? P.window : INT_MAX;
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
-                        const int p = sh.pos[e + y];
+                        const int p = pos[e + y];
                         if (!(in && x <= p && (sink || p - x < back))) z[y] = -INFINITY;
                     }
                 }
@@ -317,24 +327,28 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             const float2 sc = make_float2(P.scale_log2, P.scale_log2);
             // four scores against their references
             auto against = [&](const float *z, int e, float2 &a, float2 &c) {
-                const float4 rf = *reinterpret_cast<const float4 *>(sh.nref + e);
+                const float4 rf = *reinterpret_cast<const float4 *>(nref + e);
                 a = fma2(make_float2(z[0], z[1]), sc, make_float2(rf.x, rf.y));
                 c = fma2(make_float2(z[2], z[3]), sc, make_float2(rf.z, rf.w));
             };
-            float top = -INFINITY;
+            if (i > 0) {
+                float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < RT; e += 16)
-                if (e < nrows) {
-                    const float *z = scores(e);
+                for (int e = 0; e < RT; e += 16)
+                    if (e < nrows) {
+                        const float *z = scores(e);
 #pragma unroll
-                    for (int y = 0; y < 16; y += 4) {
-                        float2 a, c;
-                        against(z + y, e + y, a, c);
-                        top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
+                        for (int y = 0; y < 16; y += 4) {
+                            float2 a, c;
+                            against(z + y, e + y, a, c);
+                            top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
+                        }
                     }
-                }
-            mine |= __any_sync(0xffffffffu, top > kSlack) ? 1u : 0u;
-            if (!agree<RT, false>(sh, a_phase, mine, word)) return;
+                mine |= __any_sync(0xffffffffu, top > kSlack) ? 1u : 0u;
+                if (!agree<RT, false>(sh, a_phase, mine, word)) return;
+            } else {
+                word = 1u;  // the first references (the values' flag comes with their meetings)
+            }
             if (i > 0) {  // the product before this tile: the weights' memory is free, O at rest
                 if (!wait_warp(ab, &sh.o_done, o_phase)) return;
                 o_phase ^= 1u;
@@ -356,20 +370,20 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                 if (tid < n16) {
                     const float v = fmaxf(fmaxf(scratch.warp[0][tid], scratch.warp[1][tid]),
                                           fmaxf(scratch.warp[2][tid], scratch.warp[3][tid]));
-                    const float old = sh.nref[tid], nw = -v * P.scale_log2;
+                    const float old = nref[tid], nw = -v * P.scale_log2;
                     const bool grow = v != -INFINITY && (old == kNoRef || nw < old);
                     // a row without weights so far has nothing to rescale
                     scratch.row[tid] = grow && old != kNoRef ? ex2(nw - old) : 1.0f;
-                    if (grow) sh.nref[tid] = nw;
+                    if (grow) nref[tid] = nw;
                 }
                 if (!agree(sh, a_phase, mine & 2u, word)) return;
-#pragma unroll
-                for (int e = 0; e < RT; e += 2)
-                    if ((e & ~15) < nrows) {
-                        l[e / 2].x *= scratch.row[e];
-                        l[e / 2].y *= scratch.row[e + 1];
-                    }
                 if (i > 0) {
+#pragma unroll
+                    for (int e = 0; e < RT; e += 2)
+                        if ((e & ~15) < nrows) {
+                            l[e / 2].x *= scratch.row[e];
+                            l[e / 2].y *= scratch.row[e + 1];
+                        }
 #pragma unroll 1
                     for (int r0 = 0; r0 < nrows; r0 += 16) {
                         float o[16];
@@ -381,10 +395,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                         tmem_st16(o_addr + r0, ow);
                     }
                     tmem_wait_st();
+                    const uint32_t keep = word;
+                    if (!agree(sh, a_phase, 0u, word)) return;  // the scratch has been read
+                    word = keep;
                 }
-                const uint32_t keep = word;
-                if (!agree(sh, a_phase, 0u, word)) return;  // the scratch has been read
-                word = keep;
             }
             const bool skip = (word & 2u) != 0;
             unsigned char *prow = p_tile + tid * (RT * 2);
@@ -414,7 +428,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                 }
             if (skip) {
                 if (!agree(sh, a_phase, 0u, word)) return;  // all weights are there
-                mixed_tile<RT>(P, sh, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
+                mixed_tile<RT>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
             }
             if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip) = skip;
             fence_proxy_async_smem();
@@ -423,6 +437,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             ring.step();
             ring.step();
         }
+        // the next segment's queries; this one's scores have all been taken
+        Ring then = desc;
+        then.step();
+        if (!wait_warp(ab, &sh.pipe.desc_full[then.slot], then.phase)) return;
+        const bool more = sh.pipe.desc[then.slot].nrows > 0;
+        if (more) bring(sh.pipe.desc[then.slot], buf ^ 1);
         if (nt > 0) {
             if (!wait_warp(ab, &sh.o_done, o_phase)) return;
             o_phase ^= 1u;
@@ -452,17 +472,18 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
         if (!agree(sh, a_phase, 0u, word)) return;
         if (tid < nrows) {
             float sum = scratch.warp[0][tid] + scratch.warp[1][tid] + scratch.warp[2][tid] + scratch.warp[3][tid];
-            if (sh.pos[tid] < 0) sum = 0.0f;  // padding
+            if (pos[tid] < 0) sum = 0.0f;  // padding
             const bool none = sum == 0.0f;
-            const float m = none ? -INFINITY : -sh.nref[tid];
+            const float m = none ? -INFINITY : -nref[tid];
             if (s.part >= 0) {
                 // a sum that is not a number must reach the joined row, whatever the other parts' maxima
                 if (SPEC_IN(s.part + tid, P.part_rows, DBG_ATTEND))
                     P.part_ml[s.part + tid] = make_float2(isnan(sum) ? INFINITY : m, sum);
                 scratch.row[tid] = none ? 0.0f : 1.0f;
             } else {
-                if (P.lse && SPEC_IN(sh.tok[tid], P.T, DBG_ATTEND))
-                    P.lse[static_cast<int64_t>(sh.tok[tid]) * P.Hq + sh.qhead[tid]] =
+                const int j = P.by_group(s.row0 + tid), g = s.row0 + tid - j * P.G;
+                if (P.lse && SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
+                    P.lse[static_cast<int64_t>(s.t0 + j) * P.Hq + s.head * P.G + g] =
                         none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
                 scratch.row[tid] = none ? 0.0f : 1.0f / sum;
             }
@@ -484,18 +505,22 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     const float a = scratch.row[r], y = a == 0.0f ? 0.0f : o[e] * a;
                     if (s.part >= 0) {
                         if (SPEC_IN(s.part + r, P.part_rows, DBG_ATTEND)) P.part_o[(s.part + r) * P.D + tid] = y;
-                    } else if (SPEC_IN(sh.tok[r], P.T, DBG_ATTEND)) {
-                        static_cast<__nv_bfloat16 *>(P.out)[sh.tok[r] * P.out_stride + sh.qhead[r] * P.D + tid] =
-                            __float2bfloat16_rn(y);
+                    } else {
+                        const int j = P.by_group(s.row0 + r), g = s.row0 + r - j * P.G;
+                        if (SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
+                            static_cast<__nv_bfloat16 *>(P.out)[(s.t0 + j) * P.out_stride + (s.head * P.G + g) * P.D + tid] =
+                                __float2bfloat16_rn(y);
                     }
                 }
             }
         }
+        // (the next segment meets at least once before it writes where slower warps may still read)
         tc_fence_before();
-        // the rows' notes and the scratch may be written again
-        if (!agree(sh, a_phase, 0u, word)) return;
+        __syncwarp();
         if (lane == 0) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
-        desc.step();
+        if (!more) return;
+        desc = then;
+        buf ^= 1;
     }
 }
 

@@ -40,14 +40,14 @@ struct Pipe {
 
 // A wait by one thread that gives up, and that ends when another thread of the CTA has.
 __device__ __forceinline__ bool wait_one(int32_t *abort, uint64_t *bar, uint32_t phase) {
+    if (mbar_try_wait_sleep(bar, phase, kHintNs)) return true;
 #pragma unroll 1
-    for (int t = 0; !mbar_try_wait_sleep(bar, phase, kHintNs); ++t) {
-        if (t >= kTries || *reinterpret_cast<volatile int32_t *>(abort)) {
-            *reinterpret_cast<volatile int32_t *>(abort) = 1;
-            return false;
-        }
+    for (int t = 0; t < kTries; ++t) {
+        if (mbar_try_wait_sleep(bar, phase, kHintNs)) return true;
+        if (*reinterpret_cast<volatile int32_t *>(abort)) return false;
     }
-    return true;
+    *reinterpret_cast<volatile int32_t *>(abort) = 1;
+    return false;
 }
 // The same by a whole warp, with one answer.
 __device__ __forceinline__ bool wait_warp(int32_t *abort, uint64_t *bar, uint32_t phase) {
@@ -84,45 +84,30 @@ __device__ __forceinline__ bool edge_tile(const AttendParams &P, const Segment &
 // Boxes that no row of the item sees are not copied (their pages may be gone).
 
 struct TilePlan {
-    // boxes: page id as the table has it (looked at when it is needed) and the box's slot in the page;
-    // gathering: row[] of four positions
-    int row[4];
+    int row[4];  // box: its first row; gathering: four rows
     bool on;
 };
-
-// The map's row of slot `slot` of a page; where a position has no page (its request is in error) any will do.
-__device__ __forceinline__ int map_row(const AttendParams &P, const CacheMap &M, int head, int page, int slot) {
-    return (page < 0 || page >= P.n_pages ? 0 : page) * M.page_rows + head * M.head_rows + slot;
-}
 
 __device__ __forceinline__ TilePlan plan_tile(const AttendParams &P, const CacheMap &M, const Segment &s,
                                               const int32_t *table, int x0, int n, int lane) {
     TilePlan t = {};
+    // the map's row of position x; where it has no page (its request is in error) any will do
+    auto row_of = [&](int x) {
+        const int b = P.by_page(x);
+        int page = table[b];
+        if (page < 0 || page >= P.n_pages) page = 0;
+        return page * M.page_rows + s.head * M.head_rows + (x - b * P.page_size);
+    };
     if (P.box_log2 > 0) {
-        const int x = x0 + ((lane & ((kKT >> P.box_log2) - 1)) << P.box_log2);
-        t.on = (lane >> (7 - P.box_log2)) < blocks(P.D) && x - x0 < n && item_sees(P, s.keys, x, 1 << P.box_log2);
-        if (t.on) {
-            const int b = P.by_page(x);
-            t.row[0] = table[b];
-            t.row[1] = x - b * P.page_size;
-        }
-        return t;
-    }
-    // lane l finds the rows of positions l, 32 + l, .. and hands them to the lanes that copy them
-    t.on = 4 * lane < n;
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-        const int x = x0 + 32 * j + lane;
-        int r = 0;
-        if (item_sees(P, s.keys, x)) {
-            const int b = P.by_page(x);
-            r = map_row(P, M, s.head, table[b], x - b * P.page_size);
-        }
+        const int box = lane & ((kKT >> P.box_log2) - 1), half = lane >> (7 - P.box_log2);
+        const int x = x0 + (box << P.box_log2);
+        t.on = half < blocks(P.D) && x - x0 < n && item_sees(P, s.keys, x, 1 << P.box_log2);
+        if (t.on) t.row[0] = row_of(x);
+    } else {
+        t.on = 4 * lane < n;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = __shfl_sync(0xffffffffu, r, (4 * lane + i) & 31);
-            if (lane >> 3 == j) t.row[i] = v;
-        }
+        for (int j = 0; j < 4; ++j)
+            if (t.on && item_sees(P, s.keys, x0 + 4 * lane + j)) t.row[j] = row_of(x0 + 4 * lane + j);
     }
     return t;
 }
@@ -137,6 +122,30 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
     Segment s = {};
     bool ok = true;
     int used = 0;
+    auto copy_tile = [&](const CUtensorMap *map, const TilePlan &t) {
+        uint64_t *full = &pipe.full[ring.slot];
+        ok = wait_warp(&pipe.abort, &pipe.empty[ring.slot], ring.phase ^ 1u);
+        if (!ok) return;
+        const int lanes = __popc(__ballot_sync(0xffffffffu, t.on));
+        if (lane == 0)
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>(P.box_log2 > 0 ? lanes * (128 << P.box_log2)
+                                                                             : lanes * 512 * blocks(P.D)));
+        __syncwarp();
+        unsigned char *dst = ring_mem + ring.slot * tile_bytes(P.D);
+        if (t.on) {
+            const int x = s.head * M.head_cols;
+            if (P.box_log2 > 0) {
+                const int box = lane & ((kKT >> P.box_log2) - 1), half = lane >> (7 - P.box_log2);
+                copy_box(dst + half * kBlock + (box << (P.box_log2 + 7)), map, x + 64 * half, t.row[0], full);
+            } else {
+                gather4(dst + lane * 512, map, x, t.row[0], t.row[1], t.row[2], t.row[3], full);
+                if (blocks(P.D) == 2)
+                    gather4(dst + lane * 512 + kBlock, map, x + 64, t.row[0], t.row[1], t.row[2], t.row[3], full);
+            }
+        }
+        ring.step();
+        ++used;
+    };
     while (ok && walk.next(P, s, lane)) {
         ok = wait_warp(&pipe.abort, &pipe.desc_empty[desc.slot], desc.phase ^ 1u);
         if (!ok) break;
@@ -147,47 +156,19 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
         __syncwarp();
         desc.step();
         const int32_t *table = PREFIX ? P.shared_table : P.block_table + static_cast<int64_t>(s.req) * P.max_blocks;
-        // step 2t copies tile t's keys, 2t + 1 its values; between them the next tile is planned, whose page
-        // ids arrive while the values' slot is awaited
-        TilePlan now, next;
-#pragma unroll 1
-        for (int step = -1; step < 2 * s.ntile; ++step) {
-            if (step >= 0) {
-                uint64_t *full = &pipe.full[ring.slot];
-                ok = wait_warp(&pipe.abort, &pipe.empty[ring.slot], ring.phase ^ 1u);
-                if (!ok) break;
-                const int lanes = __popc(__ballot_sync(0xffffffffu, now.on));
-                if (lane == 0)
-                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(P.box_log2 > 0 ? lanes * (128 << P.box_log2)
-                                                                                     : lanes * 512 * blocks(P.D)));
-                __syncwarp();
-                const CUtensorMap *map = step & 1 ? vmap : kmap;
-                unsigned char *dst = ring_mem + ring.slot * tile_bytes(P.D);
-                const int x = s.head * M.head_cols;
-                if (now.on && P.box_log2 > 0) {
-                    const int box = lane & ((kKT >> P.box_log2) - 1), half = lane >> (7 - P.box_log2);
-                    copy_box(dst + half * kBlock + (box << (P.box_log2 + 7)), map, x + 64 * half,
-                             map_row(P, M, s.head, now.row[0], now.row[1]), full);
-                } else if (now.on) {
-#pragma unroll 1
-                    for (int half = 0; half < blocks(P.D); ++half)
-                        gather4(dst + lane * 512 + half * kBlock, map, x + 64 * half, now.row[0], now.row[1], now.row[2],
-                                now.row[3], full);
-                }
-                __syncwarp();
-                ring.step();
-                ++used;
-            }
-            if (step & 1) {
-                now = next;
-                if (step >= 0) continue;
-            }
-            const int t = (step >> 1) + 1;  // after step -1: tile 0; after 2t: tile t + 1
-            if (t < s.ntile) {
-                const int x0 = tile_begin<kKT>(s.keys, s.tile + t);
-                next = plan_tile(P, M, s, table, x0, tile_keys(s.keys, x0), lane);
-                if (step < 0) now = next;
-            }
+        auto plan = [&](int t) {
+            const int x0 = tile_begin<kKT>(s.keys, s.tile + t);
+            return plan_tile(P, M, s, table, x0, tile_keys(s.keys, x0), lane);
+        };
+        TilePlan now;
+        if (s.ntile > 0) now = plan(0);
+        for (int t = 0; ok && t < s.ntile; ++t) {
+            copy_tile(kmap, now);
+            if (!ok) break;
+            TilePlan next;
+            if (t + 1 < s.ntile) next = plan(t + 1);  // its page ids arrive while this tile's slot is awaited
+            copy_tile(vmap, now);
+            now = next;
         }
     }
     // the end of the stream
@@ -216,27 +197,35 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
 //
 // A position that a row does not see has weight 0 for it, but 0 * inf is not 0. In an edge tile the
 // values of positions that no row of the item sees (behind the window, past the end, not copied) are
-// therefore set to 0, and those that some row sees are searched for one that is not finite. If there
-// is one, the tile's second product is taken on the fp32 units, each row with the positions it sees.
+// therefore set to 0, and those that some rows see and others do not (the rows' own positions, the
+// window's edge) are searched for one that is not finite. If there is one, the tile's second product is
+// taken on the fp32 units, each row with the positions it sees.
 
-// Thread `tid` of 128 takes position x0 + tid; true when its values are not all finite.
-__device__ __forceinline__ bool clean_values(const AttendParams &P, const KeyTiles &k, unsigned char *v_tile, int x0, int n,
+// By 128 threads: the first part a thread a position, the second 16 threads a position. True when this
+// thread has found a value that is not finite.
+__device__ __forceinline__ bool clean_values(const AttendParams &P, const Segment &s, unsigned char *v_tile, int x0, int n,
                                              int tid) {
-    if (tid >= n) return false;
-    unsigned char *row = v_tile + tid * 128;
-    if (!item_sees(P, k, x0 + tid)) {
+    const KeyTiles &k = s.keys;
+    if (tid < n && !item_sees(P, k, x0 + tid)) {
+        unsigned char *row = v_tile + tid * 128;
 #pragma unroll 1
         for (int c = 0; c < 8 * blocks(P.D); ++c)
             *reinterpret_cast<uint4 *>(row + (c >> 3) * kBlock + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        return false;
     }
+    // positions after the first row's, and positions that leave the window between the first row and the last
+    const int end = min(x0 + n, k.hi), a0 = max(x0, s.pmin + 1), a = max(min(end, s.pmax + 1) - a0, 0);
+    const int b0 = max(x0, s.pmin - P.window + 1), b = P.window > 0 ? max(min(end, s.pmax - P.window + 1) - b0, 0) : 0;
+    const int c = tid & 15;
     uint32_t top = 0u;  // the greatest magnitude as bit patterns, by halves
-#pragma unroll 2
-    for (int c = 0; c < P.D / 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(row + (c >> 3) * kBlock + (((c & 7) ^ (tid & 7)) << 4));
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-    }
+    if (c < P.D / 8)
+#pragma unroll 1
+        for (int y = tid >> 4; y < a + b; y += 8) {
+            const int x = y < a ? a0 + y : b0 + y - a, r = x - x0;
+            if (!item_sees(P, k, x)) continue;
+            const uint4 v = *reinterpret_cast<const uint4 *>(v_tile + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
     return (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
 }
 
