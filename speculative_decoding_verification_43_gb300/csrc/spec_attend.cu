@@ -162,9 +162,10 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_shared_kernel(c
     const ReqRows q = load_request(P, i);
     if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) return;
     const int pre_units = *P.prefix_units, tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
-    const Shares share(P.unit_prefix[P.B], P.own_workers), pre_share(P.Hkv * tiles * pre_units, P.prefix_workers);
+    const int pre_len = pre_units + P.prefix_extra;
+    const Shares share(P.unit_prefix[P.B], P.own_workers), pre_share(P.Hkv * tiles * pre_len, P.prefix_workers);
     // items of the row tiles before this row's: they are walked through with it
-    int start = P.unit_prefix[i] + head * own_units<KT>(P, q), k = 0, units = max(own_tiles<KT>(P, q, 0).n, 1);
+    int start = P.unit_prefix[i] + head * own_units<KT>(P, q), k = 0, units = item_tiles(own_tiles<KT>(P, q, 0));
     const int64_t pre_rows = static_cast<int64_t>(head) * P.T * P.G;
     const int64_t own_rows = static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch +
                              (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_shared_kernel(c
         const int pr = tok * P.G + g, ow = (tok - q.r0) * P.G + g;
         if (pr >> P.prefix_rt_log2 != pre_k) {
             pre_k = pr >> P.prefix_rt_log2;
-            const int first = (head * tiles + pre_k) * pre_units, w0 = pre_share.owner(first);
+            const int first = (head * tiles + pre_k) * pre_len + P.prefix_extra, w0 = pre_share.owner(first);
             pre.n = pre_share.owner(first + pre_units - 1) - w0 + 1;
             pre.pitch = P.prefix_pitch;
             pre.base = pre.later = pre_rows + static_cast<int64_t>(w0) * P.prefix_pitch;
@@ -184,11 +185,11 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_shared_kernel(c
             own_k = ow >> P.own_rt_log2;
 #pragma unroll 1
             for (; k < own_k; ++k) {
-                start += units;
-                units = max(own_tiles<KT>(P, q, k + 1).n, 1);
+                start += units + P.own_extra;
+                units = item_tiles(own_tiles<KT>(P, q, k + 1));
             }
-            const int w0 = share.owner(start);
-            own.n = share.owner(start + units - 1) - w0 + 1;
+            const int w0 = share.owner(start + P.own_extra);
+            own.n = share.owner(start + P.own_extra + units - 1) - w0 + 1;
             own.pitch = P.own_pitch;
             own.base = own.later = own_rows + static_cast<int64_t>(w0) * P.own_pitch;
         }
@@ -241,7 +242,7 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
         a->n_q_heads > 65536)
         return SPEC_ERR_UNSUPPORTED;
     // and so are the units of work, at their most with the smallest items and tiles (16 rows, 32 positions)
-    const int64_t most_tiles = std::max<int64_t>(static_cast<int64_t>(a->max_blocks) * a->page_size, a->shared_len) / 32 + 2;
+    const int64_t most_tiles = std::max<int64_t>(static_cast<int64_t>(a->max_blocks) * a->page_size, a->shared_len) / 32 + 8;
     const int64_t head_tiles =
         static_cast<int64_t>(a->total_rows) * (a->n_q_heads / a->n_kv_heads) / fma::kRT + a->B + 1;
     if (head_tiles * a->n_kv_heads > INT_MAX / most_tiles) return SPEC_ERR_UNSUPPORTED;
@@ -272,12 +273,18 @@ static void tensor_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t
     workers = rt_log2 == pair::kRTLog2 ? kSMs : kSMs * round_::kPerSM;
 }
 
+// Time of an item beside its tiles, in tiles.
+static int own_extra_units(int rt_log2) { return rt_log2 == pair::kRTLog2 ? 4 : 3; }
+
 // Workers and parts of the kernels that serve the call.
 static void attend_work(AttendParams &P, bool tensor) {
     const int64_t head_rows = static_cast<int64_t>(P.T) * P.G;
     if (tensor) {
         tensor_class(head_rows, P.B, P.own_rt_log2, P.own_workers);
         tensor_class(head_rows, 1, P.prefix_rt_log2, P.prefix_workers);
+        // an item's beginning and end take the time of some tiles
+        P.own_extra = own_extra_units(P.own_rt_log2);
+        P.prefix_extra = own_extra_units(P.prefix_rt_log2);
         // boxes of slots: the largest power of two that divides the page, from 8 to a tile
         P.box_log2 = 0;
         for (int b = 3; b <= 7; ++b)
@@ -286,6 +293,7 @@ static void attend_work(AttendParams &P, bool tensor) {
         P.own_rt_log2 = P.prefix_rt_log2 = fma::kRTLog2;
         P.own_workers = P.prefix_workers = kSMs * fma::ctas_per_sm(P.D);
         P.box_log2 = 0;
+        P.own_extra = P.prefix_extra = 2;
     }
     if (P.shared_len == 0) P.prefix_workers = 0;
     P.own_pitch = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(1 << P.own_rt_log2, head_rows)));

@@ -3,8 +3,9 @@
 //
 // Rows that share a key/value head are packed: row r of a request's head is (row j, query head g of
 // the group) = (r / G, r % G). An item is up to RT packed rows of one head; its keys, in tiles of KT
-// positions, are its units. Units are numbered item after item, and worker w of NW takes its
-// share of consecutive units: every worker gets the same number of tiles, give or take one, whatever the
+// positions, are its units, behind some that stand for the time an item takes whatever its keys are (its
+// queries, its first references, its way out). Units are numbered item after item, and worker w of NW takes its
+// share of consecutive units: every worker gets the same amount of work, give or take a tile, whatever the
 // lengths are, a long context is split over many workers, and the cut depends on the inputs alone. An item
 // that falls to several workers leaves a part (output, maximum, sum) per worker, and the joining
 // kernel adds the parts in the order of the workers.
@@ -57,6 +58,7 @@ struct AttendParams {
     int32_t own_workers, prefix_workers;
     int32_t own_rt_log2, prefix_rt_log2;  // packed rows of an item (RT), as a power of two
     int32_t own_pitch, prefix_pitch;      // rows of a worker's part
+    int32_t own_extra, prefix_extra;      // units of an item beside its tiles
     int64_t part_rows;
 };
 
@@ -124,13 +126,15 @@ __device__ __forceinline__ KeyTiles own_tiles(const AttendParams &P, const ReqRo
 }
 // Row tiles of n rows of G query heads.
 __device__ __forceinline__ int row_tiles(int rows, int rt_log2) { return (rows + (1 << rt_log2) - 1) >> rt_log2; }
-// Units of one head of a request (an item without keys is one unit: its rows are written too).
+// Tiles of an item, one at least (an item without keys has rows to write too).
+__device__ __forceinline__ int item_tiles(const KeyTiles &t) { return max(t.n, 1); }
+// Units of one head of a request.
 template <int KT>
 __device__ __forceinline__ int own_units(const AttendParams &P, const ReqRows &q) {
     int u = 0;
     const int tiles = row_tiles(q.n * P.G, P.own_rt_log2);
 #pragma unroll 1
-    for (int k = 0; k < tiles; ++k) u += max(own_tiles<KT>(P, q, k).n, 1);
+    for (int k = 0; k < tiles; ++k) u += item_tiles(own_tiles<KT>(P, q, k)) + P.own_extra;
     return u;
 }
 
@@ -224,9 +228,9 @@ struct Segment {
 // and what one head's row tiles read of it comes from L2.
 template <int KT, bool PREFIX>
 struct Walker {
-    int u, u_end, u_first;
+    int u, u_end, emitted;
     int worker;
-    int i, head, k, tile;  // request, head, row tile, tile within the item
+    int i, head, k, tile;  // request, head, row tile, unit within the item
     int head_tiles;        // row tiles of a head
     ReqRows q;
     KeyTiles shared;       // prefix items: all alike
@@ -244,9 +248,8 @@ struct Walker {
             pmax = t.pmax;
             q.n = P.T;
             head_tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
-            const int per = max(shared.n, 1);
-            share = Shares(P.Hkv * head_tiles * per, P.prefix_workers);
-            if (w == 0 && lane == 0) *P.prefix_units = per;
+            share = Shares(P.Hkv * head_tiles * (item_tiles(shared) + P.prefix_extra), P.prefix_workers);
+            if (w == 0 && lane == 0) *P.prefix_units = item_tiles(shared);
             u = share.first(w);
             u_end = share.first(w + 1);
             i = 0;  // segments so far
@@ -270,80 +273,89 @@ struct Walker {
                 rem -= head * per_head;
 #pragma unroll 1
                 for (; k + 1 < head_tiles; ++k) {
-                    const int nt = max(own_tiles<KT>(P, q, k).n, 1);
-                    if (rem < nt) break;
-                    rem -= nt;
+                    const int len = item_tiles(own_tiles<KT>(P, q, k)) + P.own_extra;
+                    if (rem < len) break;
+                    rem -= len;
                 }
                 tile = rem;
             }
         }
-        u_first = u;
+        emitted = 0;
         if (!PREFIX && P.shared_len == 0 && lane == 0) P.cut[w].nrows = 0;
     }
 
     // The next segment, or false at the end of the worker's units.
     __device__ __forceinline__ bool next(const AttendParams &P, Segment &s, int lane) {
-        s.keys = PREFIX ? shared : own_tiles<KT>(P, q, k);
-        const int units = max(s.keys.n, 1);
-        int take;
-        if constexpr (PREFIX) {
-            const int first = u / units, last = (u_end - 1) / units, item = i == 0 ? last : first + i - 1;
-            if (u >= u_end || (i > 0 && item >= last)) return false;
-            tile = item == first ? u - first * units : 0;
-            take = (item == last ? u_end - last * units : units) - tile;
-            head = item / head_tiles;
-            k = item - head * head_tiles;
-            ++i;
-        } else {
-            if (u >= u_end) return false;
-            take = min(units - tile, u_end - u);
-        }
-        const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2;
-        s.row0 = k << rt_log2;
-        s.nrows = min(1 << rt_log2, q.n * P.G - s.row0);
-        s.t0 = q.r0;
-        s.base = q.kv - q.n;
-        s.head = head;
-        s.req = PREFIX ? -1 : i;
-        s.tile = tile;
-        s.ntile = min(take, s.keys.n);
-        s.pmin = PREFIX ? pmin : max(s.base + P.by_group(s.row0), 0);
-        s.pmax = PREFIX ? pmax : s.keys.hi - 1;
-        const bool whole = take == units;
-        if (P.shared_len > 0) {
-            // along a class's units either the item or the worker grows from one part to the next, so
-            // (rows of the items before) + worker * pitch gives every part rows of its own
-            const int64_t rows = (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + s.row0;
-            s.part = rows + static_cast<int64_t>(worker) * (PREFIX ? P.prefix_pitch : P.own_pitch);
-            if (!PREFIX)
-                s.part += static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch;
-        } else {
-            // only a worker's first and last segment can be part of an item
-            const int slot = u == u_first ? 0 : 1;
-            s.part = whole ? -1 : static_cast<int64_t>(2 * worker + slot) * P.own_pitch;
-            if (!whole && tile == 0 && lane == 0)
-                P.cut[worker] = {i, q.r0, s.row0, s.nrows, head, share.owner(u + units - 1) - worker + 1, slot, 0};
-        }
-        if (PREFIX) return true;
-        u += take;
-        tile += take;
-        if (tile >= units) {
-            tile = 0;
-            if (++k >= head_tiles) {
-                k = 0;
-                if (++head >= P.Hkv) {
-                    head = 0;
-                    if (u < u_end) {
 #pragma unroll 1
-                        do {
-                            q = load_request(P, ++i);
-                        } while (q.n == 0 && i + 1 < P.B);
-                        head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
+        for (;;) {
+            s.keys = PREFIX ? shared : own_tiles<KT>(P, q, k);
+            const int extra = PREFIX ? P.prefix_extra : P.own_extra, tiles = item_tiles(s.keys), len = tiles + extra;
+            int take;
+            if constexpr (PREFIX) {
+                const int first = u / len, last = (u_end - 1) / len, item = i == 0 ? last : first + i - 1;
+                if (u >= u_end || (i > 0 && item >= last)) return false;
+                tile = item == first ? u - first * len : 0;
+                take = (item == last ? u_end - last * len : len) - tile;
+                head = item / head_tiles;
+                k = item - head * head_tiles;
+                ++i;
+            } else {
+                if (u >= u_end) return false;
+                take = min(len - tile, u_end - u);
+            }
+            const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2;
+            // the tiles among these units
+            const int a = max(tile - extra, 0), b = max(tile + take - extra, 0), begin = u - tile;
+            s.row0 = k << rt_log2;
+            s.nrows = min(1 << rt_log2, q.n * P.G - s.row0);
+            s.t0 = q.r0;
+            s.base = q.kv - q.n;
+            s.head = head;
+            s.req = PREFIX ? -1 : i;
+            s.tile = a;
+            s.ntile = s.keys.n > 0 ? b - a : 0;
+            s.pmin = PREFIX ? pmin : max(s.base + P.by_group(s.row0), 0);
+            s.pmax = PREFIX ? pmax : s.keys.hi - 1;
+            const bool whole = a == 0 && b == tiles;
+            if (P.shared_len > 0) {
+                // along a class's units either the item or the worker grows from one part to the next, so
+                // (rows of the items before) + worker * pitch gives every part rows of its own
+                const int64_t rows = (static_cast<int64_t>(q.r0) * P.Hkv + static_cast<int64_t>(head) * q.n) * P.G + s.row0;
+                s.part = rows + static_cast<int64_t>(worker) * (PREFIX ? P.prefix_pitch : P.own_pitch);
+                if (!PREFIX)
+                    s.part += static_cast<int64_t>(P.T) * P.Hq + static_cast<int64_t>(P.prefix_workers) * P.prefix_pitch;
+            } else {
+                // only a worker's first and last segment can be part of an item
+                const int slot = emitted > 0 ? 1 : 0;
+                s.part = whole ? -1 : static_cast<int64_t>(2 * worker + slot) * P.own_pitch;
+                if (!whole && a == 0 && b > 0 && lane == 0)
+                    P.cut[worker] = {i, q.r0, s.row0, s.nrows, head, share.owner(begin + len - 1) - worker + 1, slot, 0};
+            }
+            if constexpr (!PREFIX) {
+                u += take;
+                tile += take;
+                if (tile >= len) {
+                    tile = 0;
+                    if (++k >= head_tiles) {
+                        k = 0;
+                        if (++head >= P.Hkv) {
+                            head = 0;
+                            if (u < u_end) {
+#pragma unroll 1
+                                do {
+                                    q = load_request(P, ++i);
+                                } while (q.n == 0 && i + 1 < P.B);
+                                head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
+                            }
+                        }
                     }
                 }
             }
+            if (b > a) {
+                ++emitted;
+                return true;
+            }
         }
-        return true;
     }
 };
 
