@@ -163,8 +163,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
     const int D = P.D;
     float *sK = sQ + kRT * D, *sV = sK + 2 * kKT * (D + 4), *sP = sV + 2 * kKT * D;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    griddep_launch_dependents();
-    griddep_wait();
+    begin_kernel<PREFIX>(P);
 
     Walker<kKT, PREFIX> walk;
     walk.start(P, blockIdx.x, lane);
@@ -252,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
         }
     }
     if (!PREFIX && warp == kWarps - 1) keep_books<kKT>(P, lane);
+    end_kernel<PREFIX>(P);
     if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = 0;
 }
 

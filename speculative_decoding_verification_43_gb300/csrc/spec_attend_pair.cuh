@@ -477,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Shared &sh = *reinterpret_cast<Shared *>(ring_mem + n_stages * tb);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
-    griddep_launch_dependents();
     if (warp == 10) tmem_alloc(&sh.tmem, 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < n_stages; ++i) {
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_wait();
+    begin_kernel<PREFIX>(P);
 
     if (warp < 8) {
         softmax_role<PREFIX>(P, sh, base + (warp / 4) * kQBytes, ring_mem, warp / 4, n_stages);
@@ -529,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 10) tmem_free(sh.tmem, 512);
+    end_kernel<PREFIX>(P);
     if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = sh.pipe.abort;
 }
 

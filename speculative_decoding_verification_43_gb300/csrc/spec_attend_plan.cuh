@@ -389,6 +389,20 @@ __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int l
     return __any_sync(0xffffffffu, bad) ? SPEC_REQ_BAD_BLOCKS : SPEC_REQ_OK;
 }
 
+// The kernels of a call and those around it overlap. The first one waits for what came before it in the
+// stream and only then lets the next be launched; so the kernel of own items behind one of prefix items may
+// read the call's inputs at once, and works on the SMs that the prefix kernel leaves. It waits for it at
+// its own end, for the joining kernel's sake, which waits for this one alone.
+template <bool PREFIX>
+__device__ __forceinline__ void begin_kernel(const AttendParams &P) {
+    if (PREFIX || P.shared_len == 0) griddep_wait();
+    griddep_launch_dependents();
+}
+template <bool PREFIX>
+__device__ __forceinline__ void end_kernel(const AttendParams &P) {
+    if (!PREFIX && P.shared_len > 0) griddep_wait();
+}
+
 // What a kernel of own items leaves to the joining kernel, by one warp of each CTA: the requests' status,
 // and (with a shared prefix, the last CTA) the units before each request.
 template <int KT>

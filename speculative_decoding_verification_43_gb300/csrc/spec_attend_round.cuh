@@ -538,7 +538,6 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     constexpr int kColumns = RT == 64 ? 256 : 128;  // 3 RT, as a power of two
 
-    griddep_launch_dependents();
     if (warp == 5) tmem_alloc(&sh.tmem, kColumns);
     if (threadIdx.x == 0) {
         for (int i = 0; i < n_stages; ++i) {
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_wait();
+    begin_kernel<PREFIX>(P);
 
     if (warp < 4) {
         softmax_role<RT, PREFIX>(P, sh, ring_mem, q_tile, p_tile, n_stages);
@@ -586,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_free(sh.tmem, kColumns);
+    end_kernel<PREFIX>(P);
     if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = sh.pipe.abort;
 }
 
