@@ -389,14 +389,16 @@ __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int l
     return __any_sync(0xffffffffu, bad) ? SPEC_REQ_BAD_BLOCKS : SPEC_REQ_OK;
 }
 
-// The kernels of a call and those around it overlap. The first one waits for what came before it in the
-// stream and only then lets the next be launched; so the kernel of own items behind one of prefix items may
-// read the call's inputs at once, and works on the SMs that the prefix kernel leaves. It waits for it at
-// its own end, for the joining kernel's sake, which waits for this one alone.
+// How the kernels of a call overlap. The prefix kernel waits for what came before it in the stream and only
+// then lets the next be launched; so the kernel of own items behind it may read the call's inputs at once,
+// and works on the SMs that the prefix kernel leaves. It waits for it at its own end, for the joining
+// kernel's sake, which waits for this one alone. The joining kernel is not launched early: its blocks,
+// waiting beside the workers, kept the next call's workers from filling the SMs (three workers an SM: 408
+// instead of 267 us for 256 fp32 requests, call after call).
 template <bool PREFIX>
 __device__ __forceinline__ void begin_kernel(const AttendParams &P) {
     if (PREFIX || P.shared_len == 0) griddep_wait();
-    griddep_launch_dependents();
+    if (PREFIX) griddep_launch_dependents();
 }
 template <bool PREFIX>
 __device__ __forceinline__ void end_kernel(const AttendParams &P) {
