@@ -32,54 +32,86 @@ struct AppendParams {
     int32_t copy_blocks;  // blocks along x that move rows; one more after them checks the requests
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / kWarp, kAppendPerSM = 4;
 
-// N consecutive elements of E moved as one access (N * sizeof(E) a power of two up to 16 bytes).
-template <typename E, int N>
-struct alignas(sizeof(E) * N) Pack {
-    E e[N];
+// V consecutive elements of E as they lie in memory: 16 bytes, or one element.
+template <typename E, int V>
+struct Piece {
+    uint4 w;
 };
-
 template <typename E>
-__device__ __forceinline__ float to_f32(E x);
-template <>
-__device__ __forceinline__ float to_f32(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename E>
-__device__ __forceinline__ E from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
+struct Piece<E, 1> {
+    E w;
+};
+__device__ __forceinline__ void unpack(const Piece<__nv_bfloat16, 8> &p, float (&f)[8]) {
+    const uint32_t w[4] = {p.w.x, p.w.y, p.w.z, p.w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const Piece<float, 4> &p, float (&f)[4]) {
+    f[0] = __uint_as_float(p.w.x);
+    f[1] = __uint_as_float(p.w.y);
+    f[2] = __uint_as_float(p.w.z);
+    f[3] = __uint_as_float(p.w.w);
+}
+__device__ __forceinline__ void unpack(const Piece<__nv_bfloat16, 1> &p, float (&f)[1]) { f[0] = __bfloat162float(p.w); }
+__device__ __forceinline__ void unpack(const Piece<float, 1> &p, float (&f)[1]) { f[0] = p.w; }
+__device__ __forceinline__ void pack(Piece<__nv_bfloat16, 8> &p, const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    p.w = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack(Piece<float, 4> &p, const float (&f)[4]) {
+    p.w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ void pack(Piece<__nv_bfloat16, 1> &p, const float (&f)[1]) { p.w = __float2bfloat16_rn(f[0]); }
+__device__ __forceinline__ void pack(Piece<float, 1> &p, const float (&f)[1]) { p.w = f[0]; }
 
 // Floats of the cos_sin table, as wide as their alignment allows.
 template <int N>
 __device__ __forceinline__ void load_floats(float (&out)[N], const float *p) {
-    constexpr int W = N % 4 == 0 ? 4 : (N % 2 == 0 ? 2 : 1);
 #pragma unroll
-    for (int i = 0; i < N; i += W) {
-        const Pack<float, W> x = *reinterpret_cast<const Pack<float, W> *>(p + i);
-#pragma unroll
-        for (int j = 0; j < W; ++j) out[i + j] = x.e[j];
+    for (int i = 0; i < N; i += (N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1)) {
+        if constexpr (N % 4 == 0) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + i);
+            out[i] = x.x;
+            out[i + 1] = x.y;
+            out[i + 2] = x.z;
+            out[i + 3] = x.w;
+        } else if constexpr (N % 2 == 0) {
+            const float2 x = *reinterpret_cast<const float2 *>(p + i);
+            out[i] = x.x;
+            out[i + 1] = x.y;
+        } else {
+            out[i] = p[i];
+        }
     }
 }
 
-// One thread moves the same piece of a row (its task) for every row of its column of blocks: a pair
-// of packs c and c + rot/2 that turn together, a pack of interleaved pairs, or a pack that is
-// copied. V: elements per pack (16 bytes, or 1 when something is not on 16-byte boundaries).
+// One thread moves the same part of a row (its task) for every row of its column of blocks: a pair
+// of pieces c and c + rot/2 that turn together, a piece of interleaved pairs, or a piece that is
+// copied. V: elements per piece (16 bytes, or 1 when something is not on 16-byte boundaries).
 //
 // Bound by latency when there are few rows (offsets -> length -> page -> store is a chain of
-// dependent loads; the row's own values are requested before it), by DRAM when there are many.
+// dependent loads; a row's own values are requested before it): 2.5 us for 5 rows, 4.5 us for 290 rows of
+// 32 + 2 x 8 heads of 128 in bf16. By DRAM when there are many: 12935 rows of 48 heads of 64, 153 MB, in 28.9
+// us, 0.79 of the measured copy rate. Four blocks an SM leave a thread 64 registers; six (40) spilled, and
+// finding every row's slot in turn, without the next row's values under way, took 39 us.
 template <typename E, int V, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) spec_append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kernel(const AppendParams P) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % kWarp;
     if (blockIdx.x == static_cast<unsigned>(P.copy_blocks)) {
         // the requests' status, a warp each
-        constexpr int kWarps = kAppendThreads / kWarp;
-        for (int i = blockIdx.y * kWarps + threadIdx.x / kWarp; i < P.B; i += gridDim.y * kWarps) {
+        for (int i = blockIdx.y * kAppendWarps + threadIdx.x / kWarp; i < P.B; i += gridDim.y * kAppendWarps) {
             const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
             int st = 0;
             if (r0 < 0 || r1 < r0 || r1 > P.T || kv < 0) {
@@ -135,53 +167,87 @@ __global__ void __launch_bounds__(kAppendThreads) spec_append_kernel(const Appen
     const int64_t src_stride = what == Q ? P.q_stride : what == K ? P.k_stride : P.v_stride;
     src += static_cast<int64_t>(head) * P.D;
     E *cache = static_cast<E *>(what == K ? P.k_cache : P.v_cache);
-    using Vec = Pack<E, V>;
+    using Vec = Piece<E, V>;
 
-    for (int r = blockIdx.y; r < P.T; r += gridDim.y) {
+    // Rows in batches of as many as there are warps: each warp finds one row's position and slot (a chain of
+    // dependent reads: offsets, length, page), then all threads move the rows, the next row's values under
+    // way while one is turned and stored. A block with a single row has every warp find it, without meeting.
+    __shared__ int64_t slot_of[kAppendWarps];  // element offset of the row's slot, -1: not written
+    __shared__ int pos_of[kAppendWarps];
+    const int step = gridDim.y, warp = threadIdx.x / kWarp;
+    const bool single = step >= P.T;
+    for (int first = blockIdx.y; first < P.T; first += kAppendWarps * step) {
         Vec a = {}, b = {};
-        if (have) {
+        auto fetch = [&](int r) {
+            if (!have || r >= P.T) return;
             a = *reinterpret_cast<const Vec *>(src + r * src_stride + d0);
             if (two) b = *reinterpret_cast<const Vec *>(src + r * src_stride + d1);
-        }
-        const int i = find_request(P.row_off, P.B, r, lane);
-        const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
-        if (!have || r0 < 0 || r < r0 || r >= r1 || r1 > P.T || kv < 0) continue;
-        const int pos = kv - (r1 - r0) + (r - r0);
-        if (pos < 0 || pos >= P.n_pos) continue;
-        const int blk = pos / P.page_size;
-        if (blk >= P.max_blocks) continue;
-        const int page = P.block_table[static_cast<int64_t>(i) * P.max_blocks + blk];
-        if (page < 0 || page >= P.n_pages) continue;
-        if (rotates) {
-            constexpr int NC = kPairs ? V : (V + 1) / 2;
-            float c[NC], s[NC];
-            const float *cs = P.cos_sin + static_cast<int64_t>(pos) * P.rot + c0;
-            load_floats(c, cs);
-            load_floats(s, cs + P.rot / 2);
-            if constexpr (kPairs) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float x = to_f32(a.e[e]), y = to_f32(b.e[e]);
-                    a.e[e] = from_f32<E>(x * c[e] - y * s[e]);
-                    b.e[e] = from_f32<E>(y * c[e] + x * s[e]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < NC; ++e) {
-                    const float x = to_f32(a.e[2 * e]), y = to_f32(a.e[2 * e + 1]);
-                    a.e[2 * e] = from_f32<E>(x * c[e] - y * s[e]);
-                    a.e[2 * e + 1] = from_f32<E>(y * c[e] + x * s[e]);
+        };
+        fetch(first);
+        const int mine = single ? first : first + warp * step;
+        int64_t my_slot = -1;
+        int my_pos = 0;
+        if (mine < P.T) {
+            const int i = find_request(P.row_off, P.B, mine, lane);
+            const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
+            const int pos = kv - (r1 - r0) + (mine - r0);
+            if (r0 >= 0 && mine >= r0 && mine < r1 && r1 <= P.T && kv >= 0 && pos >= 0 && pos < P.n_pos) {
+                const int blk = pos / P.page_size;
+                if (blk < P.max_blocks) {
+                    const int page = P.block_table[static_cast<int64_t>(i) * P.max_blocks + blk];
+                    if (page >= 0 && page < P.n_pages && SPEC_IN(page, P.n_pages, DBG_CACHE))
+                        my_slot = page * P.page_stride + (pos - blk * P.page_size) * P.slot_stride;
                 }
             }
+            my_pos = pos;
+            if (lane == 0 && !single) {
+                slot_of[warp] = my_slot;
+                pos_of[warp] = my_pos;
+            }
         }
-        E *dst;
-        if (what == Q)
-            dst = static_cast<E *>(P.q_out) + r * P.q_out_stride + static_cast<int64_t>(head) * P.D;
-        else
-            dst = cache + page * P.page_stride + (pos - blk * P.page_size) * P.slot_stride + head * P.head_stride;
-        if (!SPEC_IN(page, P.n_pages, DBG_CACHE) || !SPEC_IN(d0 + V - 1, P.D, DBG_CACHE)) continue;
-        *reinterpret_cast<Vec *>(dst + d0) = a;
-        if (two && SPEC_IN(d1 + V - 1, P.D, DBG_CACHE)) *reinterpret_cast<Vec *>(dst + d1) = b;
+        if (!single) __syncthreads();
+#pragma unroll 1
+        for (int j = 0; j < kAppendWarps; ++j) {
+            const int r = first + j * step;
+            if (r >= P.T) break;
+            Vec x = a, y = b;
+            if (j + 1 < kAppendWarps) fetch(r + step);
+            const int64_t slot = single ? my_slot : slot_of[j];
+            if (!have || slot < 0) continue;
+            if (rotates) {
+                constexpr int NC = kPairs ? V : (V + 1) / 2;
+                float c[NC], s[NC];
+                const float *cs = P.cos_sin + static_cast<int64_t>(single ? my_pos : pos_of[j]) * P.rot + c0;
+                load_floats(c, cs);
+                load_floats(s, cs + P.rot / 2);
+                float u[V];
+                unpack(x, u);
+                if constexpr (kPairs) {
+                    float w[V];
+                    unpack(y, w);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float t = u[e];
+                        u[e] = t * c[e] - w[e] * s[e];
+                        w[e] = w[e] * c[e] + t * s[e];
+                    }
+                    pack(y, w);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) {
+                        const float t = u[2 * e];
+                        u[2 * e] = t * c[e] - u[2 * e + 1] * s[e];
+                        u[2 * e + 1] = u[2 * e + 1] * c[e] + t * s[e];
+                    }
+                }
+                pack(x, u);
+            }
+            E *dst = what == Q ? static_cast<E *>(P.q_out) + r * P.q_out_stride + static_cast<int64_t>(head) * P.D
+                               : cache + slot + head * P.head_stride;
+            if (SPEC_IN(d0 + V - 1, P.D, DBG_CACHE)) *reinterpret_cast<Vec *>(dst + d0) = x;
+            if (two && SPEC_IN(d1 + V - 1, P.D, DBG_CACHE)) *reinterpret_cast<Vec *>(dst + d1) = y;
+        }
+        if (!single) __syncthreads();  // the batch's slots have been read
     }
 }
 
@@ -191,9 +257,9 @@ static spec_status launch_append(AppendParams &P, cudaStream_t stream) {
     const int turn = kPairs ? P.rot / 2 / V : P.rot / V;
     const int tasks = (P.Hq + P.Hkv) * (turn + (P.D - P.rot) / V) + P.Hkv * (P.D / V);
     P.copy_blocks = (tasks + kAppendThreads - 1) / kAppendThreads;
-    // a block a row until the device is full (8 blocks of 256 threads on each of 152 SMs), then
-    // blocks walk rows: the task's decoding is paid once
-    const int rows = std::max(1, std::min(P.T, 152 * 8 / P.copy_blocks));
+    // a block a row until the device is full (152 SMs), then blocks walk rows, all about as many
+    const int most = std::max(1, 152 * kAppendPerSM / P.copy_blocks), turns = std::max(1, (P.T + most - 1) / most);
+    const int rows = std::max(1, (P.T + turns - 1) / turns);
     const dim3 grid(static_cast<unsigned>(P.copy_blocks) + (P.req_status ? 1u : 0u), static_cast<unsigned>(rows));
     return launch_after(spec_append_kernel<E, V, INTER>, grid, dim3(kAppendThreads), 0, stream, P) == cudaSuccess
                ? SPEC_OK
