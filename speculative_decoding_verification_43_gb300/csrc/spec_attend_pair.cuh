@@ -61,34 +61,24 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
     const int steps = P.D / 16;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
     uint32_t q_phases = 0, p_phases = 0;
-    // S = Q K^T of accumulator w; n positions of the tile are used
+    // (by the elected lane) S = Q K^T of accumulator w; n positions of the tile are used
     auto score = [&](int w, const Ring &at, int n) {
         const uint64_t k = operand_at(k_op, at.slot * tb), q = operand_at(q_op, w * kQBytes);
         const uint32_t shape = mma_shape(n, false, false);
-        if (elect_lane()) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t in = (i >> 2) * kBlock + (i & 3) * 32;
-                if (i < steps) mma_ss(tmem + w * 256, operand_at(q, in), operand_at(k, in), shape, i > 0);
-            }
-            mma_commit(&sh.s_full[w]);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t in = (i >> 2) * kBlock + (i & 3) * 32;
+            if (i < steps) mma_ss(tmem + w * 256, operand_at(q, in), operand_at(k, in), shape, i > 0);
         }
-        __syncwarp();
+        mma_commit(&sh.s_full[w]);
     };
-    // O += P V of accumulator w and half u; n positions of the half are used
+    // (by the elected lane) O += P V of accumulator w and half u; n positions of the half are used
     auto weigh = [&](int w, int u, const Ring &at, int n, bool add) {
         const uint64_t v = operand_at(v_op, at.slot * tb + u * (kHalf * 128));
         const uint32_t p = tmem + w * 256 + u * kHalf, o = tmem + w * 256 + 128;
-        if (!*reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) && elect_lane()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i * 16 < n) mma_ts(o, p + 8 * i, operand_at(v, i * 2048), pv_shape, add || i > 0);
-        }
-        __syncwarp();
-    };
-    auto commit = [&](uint64_t *bar) {
-        if (elect_lane()) mma_commit(bar);
-        __syncwarp();
+        for (int i = 0; i < 4; ++i)
+            if (i * 16 < n) mma_ts(o, p + 8 * i, operand_at(v, i * 2048), pv_shape, add || i > 0);
     };
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
@@ -103,10 +93,15 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                 if (!wait_warp(ab, &sh.q_full[w], q_phases >> w & 1u)) return;
                 q_phases ^= 1u << w;
                 tc_fence_after();
-                score(w, ring, n);
+                if (elect_lane()) {
+                    score(w, ring, n);
+                    if (w == accs - 1) mma_commit(&sh.pipe.empty[ring.slot]);
+                }
+                __syncwarp();
             }
-            commit(&sh.pipe.empty[ring.slot]);
             ring.step();
+            // Between the waits only one stretch of instructions by the elected lane: what this warp does
+            // beside issuing, the tensor cores wait for.
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
                 const Ring v = ring;  // this tile's values; the next tile's keys follow them
@@ -114,33 +109,39 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                 const bool more = t + 1 < nt;
                 const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
                 if (!wait_warp(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                if (more && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+#pragma unroll 1
                 for (int w = 0; w < accs; ++w) {
                     if (!wait_warp(ab, &sh.p_full[w][0], p_phases >> w & 1u)) return;
+                    p_phases ^= 1u << w;
                     tc_fence_after();
-                    weigh(w, 0, v, min(n, kHalf), t > 0);
+                    const bool take = !*reinterpret_cast<volatile uint32_t *>(&sh.skip[w]);
                     if (n > kHalf) {
-                        commit(&sh.o_half[w]);
+                        if (elect_lane()) {
+                            if (take) weigh(w, 0, v, kHalf, t > 0);
+                            mma_commit(&sh.o_half[w]);
+                        }
+                        __syncwarp();
                         if (!wait_warp(ab, &sh.p_full[w][1], p_phases >> (2 + w) & 1u)) return;
                         p_phases ^= 4u << w;
                         tc_fence_after();
-                        weigh(w, 1, v, n - kHalf, true);
                     }
-                    p_phases ^= 1u << w;
-                    if (more) {
-                        if (w == 0 && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
-                        tc_fence_after();
+                    if (elect_lane()) {
+                        if (take) weigh(w, n > kHalf ? 1 : 0, v, n > kHalf ? n - kHalf : n, t > 0 || n > kHalf);
                         // S and P share columns: matrix instructions of one thread run in the order of
-                        // their issue, so this one follows the product that reads P
-                        score(w, ring, next);
-                    } else {
-                        commit(&sh.o_full[w]);
+                        // their issue, so the next scores follow the product that reads P
+                        if (more)
+                            score(w, ring, next);
+                        else
+                            mma_commit(&sh.o_full[w]);
+                        if (w == accs - 1) {
+                            mma_commit(&sh.pipe.empty[v.slot]);
+                            if (more) mma_commit(&sh.pipe.empty[ring.slot]);
+                        }
                     }
+                    __syncwarp();
                 }
-                commit(&sh.pipe.empty[v.slot]);
-                if (more) {
-                    commit(&sh.pipe.empty[ring.slot]);
-                    ring.step();
-                }
+                if (more) ring.step();
                 n = next;
             }
         }
