@@ -274,7 +274,7 @@ static void tensor_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t
 }
 
 // Time of an item beside its tiles, in tiles.
-static int own_extra_units(int rt_log2) { return rt_log2 == pair::kRTLog2 ? 4 : 3; }
+static int own_extra_units(int rt_log2) { return rt_log2 == pair::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.
 static void attend_work(AttendParams &P, bool tensor) {
