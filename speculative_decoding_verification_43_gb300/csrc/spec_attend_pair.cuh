@@ -15,6 +15,11 @@
 // has grown by more than 2^8 beyond it (P then stays below 2^8, whose bf16 rounding is relative all the
 // same), so the output hardly ever leaves tensor memory before the end.
 //
+// Measured: 372 GFLOP of prompts (4 requests, 32 query and 8 key heads of 128) 369 us, 0.51 of the measured
+// bf16 rate; 550 GFLOP of a 32768-position prefix under 896 rows 440 us, 0.64. A pair of tiles takes some
+// 3500 cycles, 2048 of them products: what is left is the chain from a warpgroup's weights over the issuing
+// warp's waits to the next scores, and an item's queries and way out (six tiles' time).
+//
 // Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 keeps the books (the requests' status), 10
 // issues matrix instructions.
 #pragma once
