@@ -266,14 +266,20 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
 }
 
 // Rows of an item (as a power of two) and workers for `rows` packed rows of a head over `groups` requests
-// on the tensor cores: the round kernel's items of 32 or 64 rows while that holds an average request,
-// give or take, else the pair kernel's of 256.
+// on the tensor cores: the round kernel's items of 32 or 64 rows while they hold most requests, else the pair
+// kernel's of 256. In us, 64 requests of 2000 to 4000 positions, all with this many rows:
+//     rows      16   24   32   40   48   64   80
+//     32       139  145  148  263  265  272  391
+//     64       146  154  159  175  184  208  316
+//     256      176  183  191  191  192  193  194
+// The first limit is below 32 because the average is what is known here, and requests above it read twice.
 static void tensor_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
-    rt_log2 = rows <= 24 * groups ? 5 : rows <= 96 * groups ? 6 : pair::kRTLog2;
+    rt_log2 = rows <= 24 * groups ? 5 : rows <= 48 * groups ? 6 : pair::kRTLog2;
     workers = rt_log2 == pair::kRTLog2 ? kSMs : kSMs * round_::kPerSM;
 }
 
-// Time of an item beside its tiles, in tiles.
+// Time of an item beside its tiles, in tiles: what makes the workers end together. Pair kernel, 64 prompts, at
+// 4, 6, 8: 390, 369, 378 us; round kernel, 256 windowed requests, at 2, 3, 4, 5: 84, 81, 81, 80 us.
 static int own_extra_units(int rt_log2) { return rt_log2 == pair::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.
