@@ -278,8 +278,8 @@ static void tensor_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t
     workers = rt_log2 == pair::kRTLog2 ? kSMs : kSMs * round_::kPerSM;
 }
 
-// Time of an item beside its tiles, in tiles: what makes the workers end together. Pair kernel, 64 prompts, at
-// 4, 6, 8: 390, 369, 378 us; round kernel, 256 windowed requests, at 2, 3, 4, 5: 84, 81, 81, 80 us.
+// Time of an item beside its tiles, in tiles: what makes the workers end together. Pair kernel, 4 prompts, at
+// 4, 6, 8: 390, 369, 378 us; round kernel, 64 windowed requests, at 2, 3, 4, 5: 84, 81, 81, 80 us.
 static int own_extra_units(int rt_log2) { return rt_log2 == pair::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.

@@ -16,7 +16,7 @@
 // same), so the output hardly ever leaves tensor memory before the end.
 //
 // Measured: 372 GFLOP of prompts (4 requests, 32 query and 8 key heads of 128) 369 us, 0.51 of the measured
-// bf16 rate; 550 GFLOP of a 32768-position prefix under 896 rows 440 us, 0.64. A pair of tiles takes some
+// bf16 rate; 550 GFLOP of a 32768-position prefix under 1031 rows 441 us, 0.64. A pair of tiles takes some
 // 3500 cycles, 2048 of them products: what is left is the chain from a warpgroup's weights over the issuing
 // warp's waits to the next scores, and an item's queries and way out (six tiles' time).
 //
