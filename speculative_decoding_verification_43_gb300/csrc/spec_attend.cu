@@ -79,8 +79,9 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float wj = j0 + j < cnt ? __shfl_sync(0xffffffffu, w, (j0 + j) & 31) : 0.0f;
-                if (wj == 0.0f) continue;  // holds nothing
+                if (j0 + j >= cnt) break;
+                // (a part whose weight vanishes takes part all the same: what is not finite in it has been seen)
+                const float wj = __shfl_sync(0xffffffffu, w, j0 + j);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     o[c].x = fmaf(wj, v[j][c].x, o[c].x);

@@ -1,6 +1,6 @@
 """GPU: spec_attend on batches of other shapes, against float64 (tests/attend_ref.py): more requests than a
 CTA's warps walk at once, prompts and single tokens in one batch, values that are not finite inside and behind a
-shared prefix."""
+shared prefix and in parts whose weight vanishes when they are joined."""
 import pytest
 import torch
 
@@ -84,3 +84,23 @@ def test_not_finite_behind_a_shared_prefix(dtype, back):
     assert ((out[~sees] - ref[0][~sees]).abs() <= tol[~sees]).all()
     assert (~torch.isfinite(out[sees][..., 5])).all()
     assert ((out[sees] - ref[0][sees]).abs() <= tol[sees])[..., rest].all()
+
+
+@TYPES
+@pytest.mark.parametrize("shared", [0, 4000])
+@pytest.mark.parametrize("rows", [2, 12, 200])
+def test_not_finite_in_a_part_of_vanishing_weight(dtype, rows, shared):
+    """The first half of the text scores 2^184 times less than the second, so that parts taken over it count for
+    nothing in 32 bits. A value there that is not a number reaches its column all the same, as 0 times it does in
+    a text that is not cut; the other columns are the formula's."""
+    n = 9000
+    b = Batch([rows], [n], 4, 1, 64, dtype, 16, shared=shared, seed=21)
+    b.keys[0] = torch.where(torch.arange(n) < n // 2, -8.0, 8.0)[:, None, None].expand(n, 1, 64).to(dtype).contiguous()
+    b.pk = b.keys[0][:shared]
+    b.q = torch.ones_like(b.q)
+    ref = b.reference()
+    (b.pv if shared else b.vals[0])[100, :, 3] = float("nan")
+    got = _run(b.place())
+    out, rest = got.out.cpu().double(), [d for d in range(64) if d != 3]
+    assert torch.isnan(out[..., 3]).all()
+    assert ((out - ref[0]).abs() <= _tol(b, ref))[..., rest].all()
