@@ -27,6 +27,32 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _run_stream(obj, stream):
+    """Handle of the stream a prepared call runs on (None: the current one). The caching allocator takes a tensor
+    to be in use on the stream it was allocated on; where the call's outputs and workspace are used on another, it
+    is told, once for each stream, so that it gives their memory to nobody while the kernels are at work."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    handle = stream.cuda_stream
+    if handle not in obj._streams:
+        for t in (*vars(obj.out).values(), getattr(obj, "workspace", None)):
+            if t is not None:
+                t.record_stream(stream)
+        obj._streams.add(handle)
+    return ctypes.c_void_p(handle)
+
+
+def _hand_over(out, stream):
+    """Outputs that were allocated and written on `stream` (None: the current one), for the current stream."""
+    if stream is not None:
+        here = torch.cuda.current_stream()
+        if here.cuda_stream != stream.cuda_stream:
+            for t in vars(out).values():
+                if t is not None:
+                    t.record_stream(here)
+    return out
+
+
 def _i32(t):
     assert t.dtype == torch.int32 and t.is_contiguous() and t.is_cuda, "int32 CUDA tensor expected"
     return t
@@ -332,6 +358,7 @@ class KvAppender:
         self.B, self.T, self.Hq, self.Hkv, self.D, self.dtype = B, total_rows, Hq, Hkv, D, dtype
         self.out = AppendOutputs(q=torch.empty(total_rows, Hq, D, dtype=dtype, device=device),
                                  req_status=torch.empty(B, dtype=torch.int32, device=device))
+        self._streams = set()
         self.args = SpecKvAppendArgs()
         a = self.args
         a.B, a.total_rows, a.n_q_heads, a.n_kv_heads, a.head_dim = B, total_rows, Hq, Hkv, D
@@ -361,18 +388,21 @@ class KvAppender:
         return self
 
     def run(self, stream=None) -> AppendOutputs:
-        check(lib.spec_kv_append(ctypes.byref(self.args), _stream_handle(stream)), "spec_kv_append")
+        check(lib.spec_kv_append(ctypes.byref(self.args), _run_stream(self, stream)), "spec_kv_append")
         return self.out
 
 
 def kv_append(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, *, rot_dim: int | None = None,
               interleaved: bool = False, q_out=None, stream=None) -> AppendOutputs:
-    """Appends a round's rows to the paged cache (see include/spec_attend.h)."""
+    """Appends a round's rows to the paged cache (see include/spec_attend.h). With a stream, the outputs are
+    allocated and written there; who uses them elsewhere waits for it first."""
     T, Hkv, D = k.shape
-    c = KvAppender(row_off.numel() - 1, T, q.shape[1] if q is not None else 0, Hkv, D, k.dtype, rot_dim=rot_dim,
-                   interleaved=interleaved, device=k.device)
-    c.bind(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, q_out=q_out)
-    return c.run(stream)
+    with torch.cuda.stream(stream):
+        c = KvAppender(row_off.numel() - 1, T, q.shape[1] if q is not None else 0, Hkv, D, k.dtype, rot_dim=rot_dim,
+                       interleaved=interleaved, device=k.device)
+        c.bind(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, q_out=q_out)
+        out = c.run(stream)
+    return _hand_over(out, stream)
 
 
 @dataclass
@@ -401,7 +431,7 @@ class Attention:
         a.scale = D ** -0.5 if scale is None else scale
         a.lse, a.req_status = _ptr(self.out.lse), _ptr(self.out.req_status)
         self.workspace, self.ws_bytes = None, 0
-        self._keep = ()
+        self._streams, self._keep = set(), ()
 
     def bind(self, q, k_cache, v_cache, row_off, kv_len, block_table, *, shared_table=None, out=None):
         """q [T, Hq, D], k_cache and v_cache [n_pages, page_size, Hkv, D] of any strides, block_table
@@ -419,6 +449,7 @@ class Attention:
         self.ws_bytes = int(lib.spec_attend_workspace_size(ctypes.byref(a)))
         if self.workspace is None or self.workspace.numel() < self.ws_bytes:
             self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+            self._streams = set()
         self._keep = (q, k_cache, v_cache, row_off, kv_len, block_table, shared_table, out)
         return self
 
@@ -429,19 +460,22 @@ class Attention:
 
     def run(self, stream=None) -> AttendOutputs:
         rc = lib.spec_attend(ctypes.byref(self.args), ctypes.c_void_p(self.workspace.data_ptr()),
-                             self.workspace.numel(), _stream_handle(stream))
+                             self.workspace.numel(), _run_stream(self, stream))
         check(rc, "spec_attend")
         return self.out
 
 
 def attend(q, k_cache, v_cache, row_off, kv_len, block_table, *, window: int = 0, n_sink: int = 0,
            shared_len: int = 0, shared_table=None, scale: float | None = None, stream=None) -> AttendOutputs:
-    """Attention of a round's rows over the paged cache (see include/spec_attend.h)."""
+    """Attention of a round's rows over the paged cache (see include/spec_attend.h). With a stream, workspace and
+    outputs are allocated and written there; who uses the outputs elsewhere waits for it first."""
     T, Hq, D = q.shape
-    a = Attention(row_off.numel() - 1, T, Hq, k_cache.shape[2], D, q.dtype, window=window, n_sink=n_sink,
-                  shared_len=shared_len, scale=scale, device=q.device)
-    a.bind(q, k_cache, v_cache, row_off, kv_len, block_table, shared_table=shared_table)
-    return a.run(stream)
+    with torch.cuda.stream(stream):
+        a = Attention(row_off.numel() - 1, T, Hq, k_cache.shape[2], D, q.dtype, window=window, n_sink=n_sink,
+                      shared_len=shared_len, scale=scale, device=q.device)
+        a.bind(q, k_cache, v_cache, row_off, kv_len, block_table, shared_table=shared_table)
+        out = a.run(stream)
+    return _hand_over(out, stream)
 
 
 def gamma_objective(alpha: float, c: float, gamma: int) -> float:
