@@ -47,10 +47,17 @@ def _hand_over(out, stream):
     if stream is not None:
         here = torch.cuda.current_stream()
         if here.cuda_stream != stream.cuda_stream:
-            for t in vars(out).values():
+            for t in out if isinstance(out, tuple) else vars(out).values():
                 if t is not None:
                     t.record_stream(here)
     return out
+
+
+def _choice(dev, stream):
+    """Outputs of a gamma choice on `stream`: int32[1], float64[1]."""
+    with torch.cuda.stream(stream):
+        out = torch.empty(1, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.float64, device=dev)
+    return _hand_over(out, stream)
 
 
 def _i32(t):
@@ -128,7 +135,7 @@ class Verifier:
                      "alpha_count", "rho_rows", "resid_rows", "frontier_prob", "frontier_margin",
                      "fallback", "depth_reached", "depth_accepted"):
             setattr(a, name, _ptr(getattr(o, name)))
-        self._keep = ()
+        self._streams, self._keep = set(), ()
 
     def bind(self, target, draft, row_off, draft_tokens, uniforms, temperature=1.0, *,
              stop_token=None, max_new=None, top_k=None, top_p=None):
@@ -178,7 +185,7 @@ class Verifier:
 
     def run(self, stream=None) -> VerifyOutputs:
         rc = lib.spec_verify(ctypes.byref(self.args), ctypes.c_void_p(self.workspace.data_ptr()),
-                             self.ws_bytes, _stream_handle(stream))
+                             self.ws_bytes, _run_stream(self, stream))
         check(rc, "spec_verify")
         return self.out
 
@@ -186,13 +193,16 @@ class Verifier:
 def verify(target, draft, row_off, draft_tokens, uniforms, temperature=1.0, *, K_max: int = 64,
            stop_token=None, max_new=None, top_k=None, top_p=None, diagnostics: bool = False,
            stream=None) -> VerifyOutputs:
-    """One verifier round on device tensors (see include/spec_verify.h for the layout)."""
+    """One verifier round on device tensors (see include/spec_verify.h for the layout). With a stream, workspace
+    and outputs are allocated and written there; who uses the outputs elsewhere waits for it first."""
     T, V = target.shape
     B = row_off.numel() - 1
-    v = Verifier(B, V, T, target.dtype, K_max=K_max, device=target.device, diagnostics=diagnostics)
-    v.bind(target, draft, row_off, draft_tokens, uniforms, temperature, stop_token=stop_token,
-           max_new=max_new, top_k=top_k, top_p=top_p)
-    return v.run(stream)
+    with torch.cuda.stream(stream):
+        v = Verifier(B, V, T, target.dtype, K_max=K_max, device=target.device, diagnostics=diagnostics)
+        v.bind(target, draft, row_off, draft_tokens, uniforms, temperature, stop_token=stop_token,
+               max_new=max_new, top_k=top_k, top_p=top_p)
+        out = v.run(stream)
+    return _hand_over(out, stream)
 
 
 @dataclass
@@ -229,7 +239,7 @@ class Compactor:
         for name in ("out_off", "packed_tokens", "packed_pos", "kv_off", "kv_src", "kv_dst",
                      "new_seq_len", "new_kv_len", "new_draft_len", "compact_status"):
             setattr(a, name, _ptr(getattr(self.out, name)))
-        self._keep = ()
+        self._streams, self._keep = set(), ()
 
     def bind(self, row_off, accept_len, n_emitted, out_tokens, req_status, prefix_len, cand_kv_rows,
              block_table, page_size: int):
@@ -247,16 +257,18 @@ class Compactor:
         return self
 
     def run(self, stream=None) -> CompactOutputs:
-        check(lib.spec_compact(ctypes.byref(self.args), _stream_handle(stream)), "spec_compact")
+        check(lib.spec_compact(ctypes.byref(self.args), _run_stream(self, stream)), "spec_compact")
         return self.out
 
 
 def compact(row_off, accept_len, n_emitted, out_tokens, req_status, prefix_len, cand_kv_rows,
             block_table, page_size: int, stream=None) -> CompactOutputs:
-    c = Compactor(row_off.numel() - 1, out_tokens.numel(), device=out_tokens.device)
-    c.bind(row_off, accept_len, n_emitted, out_tokens, req_status, prefix_len, cand_kv_rows,
-           block_table, page_size)
-    return c.run(stream)
+    with torch.cuda.stream(stream):
+        c = Compactor(row_off.numel() - 1, out_tokens.numel(), device=out_tokens.device)
+        c.bind(row_off, accept_len, n_emitted, out_tokens, req_status, prefix_len, cand_kv_rows,
+               block_table, page_size)
+        out = c.run(stream)
+    return _hand_over(out, stream)
 
 
 def run_round(verifier: "Verifier", compactor: "Compactor", alpha_prev: float, c: float, gamma_min: int = 0,
@@ -266,11 +278,12 @@ def run_round(verifier: "Verifier", compactor: "Compactor", alpha_prev: float, c
     Returns (verify outputs, compaction outputs, (gamma int32[1], alpha float64[1]))."""
     dev = verifier.out.alpha_sum.device
     if out is None:
-        out = (torch.empty(1, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.float64, device=dev))
+        out = _choice(dev, stream)
     g, a = out
+    _run_stream(compactor, stream)
     rc = lib.spec_verify_round(ctypes.byref(verifier.args), ctypes.c_void_p(verifier.workspace.data_ptr()),
                                verifier.ws_bytes, ctypes.byref(compactor.args), float(alpha_prev), float(c),
-                               int(gamma_min), int(gamma_max), _ptr(g), _ptr(a), _stream_handle(stream))
+                               int(gamma_min), int(gamma_max), _ptr(g), _ptr(a), _run_stream(verifier, stream))
     check(rc, "spec_verify_round")
     return verifier.out, compactor.out, (g, a)
 
@@ -280,7 +293,7 @@ def choose_gamma(alpha_sum, alpha_count, alpha_prev: float, c: float, gamma_min:
     """Device-side gamma choice; returns (gamma int32[1], alpha float64[1]) device tensors."""
     dev = alpha_sum.device
     if out is None:
-        out = (torch.empty(1, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.float64, device=dev))
+        out = _choice(dev, stream)
     g, a = out
     rc = lib.spec_choose_gamma(_ptr(alpha_sum), _ptr(alpha_count), float(alpha_prev), float(c),
                                int(gamma_min), int(gamma_max), _ptr(g), _ptr(a), _stream_handle(stream))
@@ -297,7 +310,7 @@ def choose_gamma_depth(depth_reached, depth_accepted, alpha_prev: float, c: floa
     _i32(depth_accepted)
     assert depth_reached.numel() == depth_accepted.numel()
     if out is None:
-        out = (torch.empty(1, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.float64, device=dev))
+        out = _choice(dev, stream)
     g, ea = out
     rc = lib.spec_choose_gamma_depth(_ptr(depth_reached), _ptr(depth_accepted), int(depth_reached.numel()),
                                      float(alpha_prev), float(c), int(gamma_min), int(gamma_max), _ptr(g),

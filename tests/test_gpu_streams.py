@@ -4,7 +4,7 @@ call still uses: the call's results are right, and the fills stay as they are.""
 import pytest
 import torch
 
-from speculative_decoding_verification_43_gb300 import api
+from speculative_decoding_verification_43_gb300 import api, workloads as W
 
 from attend_ref import Batch
 import test_gpu_append as A
@@ -155,6 +155,65 @@ def test_prepared_append_dropped_while_it_runs():
     st = busy_stream()
     c.run(st)
     del c
+    f = fills(*like)
+    torch.cuda.synchronize()
+    assert untouched(f)
+
+
+def verifier_round():
+    rd = W.make_round(W.Workload("busy", B=12, V=20000, dtype=BF, temperature=0.7, logits="zipf", sigma=1.0,
+                                 draft_sigma=0.8, K="uniform:0:7"), seed=1, rnd=0, device="cuda")
+    return rd, (rd.target, rd.draft, rd.row_off, rd.draft_tokens, rd.uniforms, rd.temperature)
+
+
+@pytest.mark.parametrize("keep", [True, False], ids=["kept", "dropped"])
+def test_verify_on_a_busy_stream(keep):
+    _, args = verifier_round()
+    v = api.Verifier(args[2].numel() - 1, args[0].shape[1], args[0].shape[0], BF).bind(*args)
+    o = v.run()
+    want = [o.accept_len.clone(), o.out_tokens.clone(), o.alpha_rows.clone()]
+    like = [torch.empty_like(t) for t in (v.workspace, o.out_tokens, o.alpha_rows)]
+    torch.cuda.synchronize()
+    st = busy_stream()
+    o = api.verify(*args, stream=st)
+    if not keep:
+        del o
+    f = fills(*like)
+    torch.cuda.synchronize()
+    assert untouched(f)
+    if keep:
+        assert all(torch.equal(x, y) for x, y in zip((o.accept_len, o.out_tokens, o.alpha_rows), want))
+
+
+def test_compact_and_the_gamma_choice_on_a_busy_stream():
+    rd, args = verifier_round()
+    o = api.verify(*args)
+    ci = W.make_compaction_inputs(rd, 64, 16)
+    ins = (rd.row_off, o.accept_len, o.n_emitted, o.out_tokens, o.req_status, ci["prefix_len"], ci["cand_kv_rows"],
+           ci["block_table"], ci["page_size"])
+    want, (g, a) = api.compact(*ins), api.choose_gamma(o.alpha_sum, o.alpha_count, 0.5, 0.05)
+    like = [torch.empty_like(t) for t in vars(want).values()]
+    torch.cuda.synchronize()
+    st = busy_stream()
+    c = api.compact(*ins, stream=st)
+    g2, a2 = api.choose_gamma(o.alpha_sum, o.alpha_count, 0.5, 0.05, stream=st)
+    f = fills(*like)
+    torch.cuda.synchronize()
+    n = int(want.out_off[-1])
+    assert torch.equal(c.out_off, want.out_off) and torch.equal(c.packed_tokens[:n], want.packed_tokens[:n])
+    assert torch.equal(g2, g) and torch.equal(a2, a) and untouched(f)
+
+
+def test_a_round_dropped_while_it_runs():
+    rd, args = verifier_round()
+    ci = W.make_compaction_inputs(rd, 64, 16)
+    v = api.Verifier(rd.B, args[0].shape[1], rd.T, BF).bind(*args)
+    c = api.Compactor(rd.B, rd.T).bind(rd.row_off, v.out.accept_len, v.out.n_emitted, v.out.out_tokens, v.out.req_status,
+                                       ci["prefix_len"], ci["cand_kv_rows"], ci["block_table"], ci["page_size"])
+    like = [torch.empty_like(t) for t in (v.workspace, v.out.out_tokens, c.out.packed_tokens, c.out.out_off)]
+    st = busy_stream()
+    api.run_round(v, c, 0.5, 0.05, stream=st)
+    del v, c
     f = fills(*like)
     torch.cuda.synchronize()
     assert untouched(f)
