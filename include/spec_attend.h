@@ -10,6 +10,11 @@
  * position p = kv_len[i] - n_i + j. A row with p < 0 is padding. n_i = 0 and kv_len[i] = 0 are
  * allowed.
  *
+ * Offsets stay within [0, T] and do not decrease. Where they do otherwise, a request has its rows if
+ * 0 <= row_off[i] <= row_off[i+1] <= T and none of the offsets within [0, T] contradicts that (no
+ * earlier one is above row_off[i], no later one below row_off[i+1]), and is served like any other; the
+ * rest report SPEC_REQ_BAD_SHAPE. So an offset outside [0, T] costs the two requests beside it.
+ *
  * The cache is paged, with the pages spec_compact speaks of: position x lies in slot x % page_size
  * of page block_table[i][x / page_size]. In memory, element d of head h, slot s, page b of the keys
  * (and alike of the values) is
@@ -40,8 +45,9 @@ extern "C" {
  * bits and rounded once to the type. Elements from rot_dim on are copied.
  * A row whose position has no page (beyond max_blocks, or a page id outside [0, n_pages)) or no
  * cos_sin row is not written at all, and its request's status says so (SPEC_REQ_BAD_BLOCKS,
- * SPEC_REQ_BAD_SHAPE); the request's other rows are written. Padding rows are not written. Rows of
- * one call must not share a cache position. */
+ * SPEC_REQ_BAD_SHAPE); the request's other rows are written. Padding rows are not written, nor are
+ * rows of a request whose offsets are wrong or contradicted or whose kv_len is negative
+ * (SPEC_REQ_BAD_SHAPE). Rows of one call must not share a cache position. */
 typedef struct {
     int32_t B, total_rows;       /* requests, rows (total_rows = row_off[B])                     */
     int32_t n_q_heads, n_kv_heads, head_dim; /* head_dim <= 512; n_q_heads may be 0 (no queries)  */
@@ -87,10 +93,11 @@ spec_status spec_kv_append(const spec_kv_append_args *args, cudaStream_t stream)
  * bf16: products on the tensor cores with 32-bit accumulation, softmax weights rounded to bf16 for
  * the second product, statistics in 32 bits. fp32: 32-bit arithmetic throughout. Results do not
  * depend on the order in which CTAs run.
- * A request with status bits has out = 0 and lse = -inf on its rows: SPEC_REQ_BAD_SHAPE for
- * inconsistent row_off or a negative kv_len, SPEC_REQ_BAD_BLOCKS for a visible position without a
- * page. SPEC_REQ_TIMEOUT on every request says that a bounded wait inside the kernel gave up (an
- * internal fault); the call's outputs then mean nothing. */
+ * A request with status bits has out = 0 and lse = -inf on its rows, if it has offsets 0 <= row_off[i]
+ * <= row_off[i+1] <= T (else it has none; rows that belong to no request are not written):
+ * SPEC_REQ_BAD_SHAPE for wrong or contradicted offsets or a negative kv_len, SPEC_REQ_BAD_BLOCKS for a
+ * visible position without a page. SPEC_REQ_TIMEOUT on every request says that a bounded wait
+ * inside the kernel gave up (an internal fault); the call's outputs then mean nothing. */
 typedef struct {
     int32_t B, total_rows;
     int32_t n_q_heads, n_kv_heads, head_dim; /* n_q_heads a multiple of n_kv_heads; head_dim <= 256,

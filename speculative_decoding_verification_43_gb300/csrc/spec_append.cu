@@ -109,12 +109,32 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % kWarp;
+    // Whether some request's offsets are wrong: the first ones are asked for here and looked at where the block
+    // has other reads to wait for.
+    int off0 = 0, off1 = 0;
+    if (static_cast<int>(threadIdx.x) < P.B) {
+        off0 = P.row_off[threadIdx.x];
+        off1 = P.row_off[threadIdx.x + 1];
+    }
+    auto some_wrong = [&]() -> bool {
+        bool wrong = !offsets_right(off0, off1, P.T);
+#pragma unroll 4
+        for (int i = threadIdx.x + kAppendThreads; i < P.B; i += kAppendThreads)
+            wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
+        return __syncthreads_or(wrong) != 0;
+    };
+    // by a warp, where some are
+    auto in_doubt = [&](int i) -> bool {
+        return __any_sync(0xffffffffu, offsets_contradict(P.row_off, P.B, P.T, i, P.row_off[i], P.row_off[i + 1], lane,
+                                                          kWarp)) != 0;
+    };
     if (blockIdx.x == static_cast<unsigned>(P.copy_blocks)) {
+        const bool broken = some_wrong();
         // the requests' status, a warp each
         for (int i = blockIdx.y * kAppendWarps + threadIdx.x / kWarp; i < P.B; i += gridDim.y * kAppendWarps) {
             const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
             int st = 0;
-            if (r0 < 0 || r1 < r0 || r1 > P.T || kv < 0) {
+            if (!offsets_right(r0, r1, P.T) || kv < 0 || (broken && in_doubt(i))) {
                 st = SPEC_REQ_BAD_SHAPE;
             } else if (r1 > r0 && kv > 0) {
                 if (kv > P.n_pos) st = SPEC_REQ_BAD_SHAPE;
@@ -176,6 +196,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
     __shared__ int pos_of[kAppendWarps];
     const int step = gridDim.y, warp = threadIdx.x / kWarp;
     const bool single = step >= P.T;
+    bool broken = false;
     for (int first = blockIdx.y; first < P.T; first += kAppendWarps * step) {
         Vec a = {}, b = {};
         auto fetch = [&](int r) {
@@ -188,10 +209,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
         int64_t my_slot = -1;
         int my_pos = 0;
         if (mine < P.T) {
-            const int i = find_request(P.row_off, P.B, mine, lane);
+            const int i = find_request(P.row_off, P.B, P.T, mine, lane);
             const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
             const int pos = kv - (r1 - r0) + (mine - r0);
-            if (r0 >= 0 && mine >= r0 && mine < r1 && r1 <= P.T && kv >= 0 && pos >= 0 && pos < P.n_pos) {
+            if (offsets_right(r0, r1, P.T) && mine >= r0 && mine < r1 && kv >= 0 && pos >= 0 && pos < P.n_pos) {
                 const int blk = pos / P.page_size;
                 if (blk < P.max_blocks) {
                     const int page = P.block_table[static_cast<int64_t>(i) * P.max_blocks + blk];
@@ -205,7 +226,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
                 pos_of[warp] = my_pos;
             }
         }
-        if (!single) __syncthreads();
+        if (first == static_cast<int>(blockIdx.y))
+            broken = some_wrong();
+        else
+            __syncthreads();
+        if (broken) {
+            if (my_slot >= 0 && in_doubt(find_request(P.row_off, P.B, P.T, mine, lane))) {
+                my_slot = -1;
+                if (lane == 0) slot_of[warp] = -1;
+            }
+            __syncthreads();
+        }
 #pragma unroll 1
         for (int j = 0; j < kAppendWarps; ++j) {
             const int r = first + j * step;

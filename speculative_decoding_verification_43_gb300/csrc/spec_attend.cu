@@ -104,13 +104,21 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
         P.lse[static_cast<int64_t>(t) * P.Hq + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// Request i's status goes out, and the rows of a request in error become 0 / -inf (a block).
+// Request i's status goes out, and the rows of a request in error become 0 / -inf (a block). Rows in doubt
+// belong to requests in error only, so that no other's rows are touched.
 template <typename E>
 __device__ __forceinline__ void finish_request(const AttendParams &P, int i) {
     int bad = 0;
+    const bool broken = *P.broken;
 #pragma unroll 1
     for (int w = threadIdx.x; w < P.own_workers + P.prefix_workers; w += kJoinThreads) bad |= P.err[w];
-    const int st = P.status[i] | (__syncthreads_or(bad) ? SPEC_REQ_TIMEOUT : 0);
+    int st = P.status[i] | (__syncthreads_or(bad) ? SPEC_REQ_TIMEOUT : 0);
+    if (broken) {
+        const int r0 = P.row_off[i], r1 = P.row_off[i + 1];
+        if (offsets_right(r0, r1, P.T) &&
+            __syncthreads_or(offsets_contradict(P.row_off, P.B, P.T, i, r0, r1, threadIdx.x, kJoinThreads)))
+            st |= SPEC_REQ_BAD_SHAPE;
+    }
     if (threadIdx.x == 0 && P.req_status) P.req_status[i] = st;
     if (st == SPEC_REQ_OK) return;
     const ReqRows q = load_request(P, i);
@@ -156,12 +164,15 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_shared_kernel(c
     griddep_wait();
     if (blockIdx.x < static_cast<unsigned>(P.B)) return finish_request<E>(P, blockIdx.x);
     const int lane = threadIdx.x % kWarp;
+    const bool broken = *P.broken;
     const int64_t unit = static_cast<int64_t>(blockIdx.x - P.B) * kJoinWarps + threadIdx.x / kWarp;
     if (unit >= static_cast<int64_t>(P.T) * P.Hkv) return;
     const int tok = static_cast<int>(unit / P.Hkv), head = static_cast<int>(unit - static_cast<int64_t>(tok) * P.Hkv);
-    const int i = find_request(P.row_off, P.B, tok, lane);
+    const int i = find_request(P.row_off, P.B, P.T, tok, lane);
     const ReqRows q = load_request(P, i);
     if (tok < q.r0 || tok >= q.r0 + q.n || P.status[i] != SPEC_REQ_OK) return;
+    if (broken && __any_sync(0xffffffffu, offsets_contradict(P.row_off, P.B, P.T, i, q.r0, q.r0 + q.n, lane, kWarp)))
+        return;
     const int pre_units = *P.prefix_units, tiles = row_tiles(P.T * P.G, P.prefix_rt_log2);
     const int pre_len = pre_units + P.prefix_extra;
     const Shares share(P.unit_prefix[P.B], P.own_workers), pre_share(P.Hkv * tiles * pre_len, P.prefix_workers);
@@ -204,7 +215,7 @@ __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_shared_kernel(c
 // ---------------------------------------------------------------- host side
 
 struct AttendLayout {
-    size_t status, unit_prefix, cut, prefix_units, err, ml, o, total;
+    size_t status, unit_prefix, cut, prefix_units, broken, err, ml, o, total;
 };
 
 static AttendLayout attend_layout(const AttendParams &P) {
@@ -219,6 +230,7 @@ static AttendLayout attend_layout(const AttendParams &P) {
     L.unit_prefix = take((static_cast<size_t>(P.B) + 1) * 4);
     L.cut = take(static_cast<size_t>(P.own_workers) * sizeof(CutItem));
     L.prefix_units = take(4);
+    L.broken = take(4);
     L.err = take(static_cast<size_t>(P.own_workers + P.prefix_workers) * 4);
     L.ml = take(static_cast<size_t>(P.part_rows) * 8);
     L.o = take(static_cast<size_t>(P.part_rows) * P.D * 4);
@@ -502,6 +514,7 @@ extern "C" spec_status spec_attend(const spec_attend_args *a, void *workspace, s
     P.unit_prefix = reinterpret_cast<int32_t *>(ws + L.unit_prefix);
     P.cut = reinterpret_cast<CutItem *>(ws + L.cut);
     P.prefix_units = reinterpret_cast<int32_t *>(ws + L.prefix_units);
+    P.broken = reinterpret_cast<int32_t *>(ws + L.broken);
     P.err = reinterpret_cast<int32_t *>(ws + L.err);
     P.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     P.part_o = reinterpret_cast<float *>(ws + L.o);

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
             if (r < nr) {
                 const int j = P.by_group(s.row0 + r * kWarps + warp);
                 if constexpr (PREFIX) {
-                    const ReqRows q = load_request(P, find_request(P.row_off, P.B, j, lane));
+                    const ReqRows q = load_request(P, find_request(P.row_off, P.B, P.T, j, lane));
                     R.pos[r] = j >= q.r0 && j < q.r0 + q.n ? q.kv - q.n + (j - q.r0) : -1;
                 } else {
                     R.pos[r] = s.base + j;

@@ -240,18 +240,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             int p = -1;
             if (have) {
                 if constexpr (PREFIX) {
-                    int lo = 0, n = P.B;  // the row's request
-#pragma unroll 1
-                    while (n > 1) {
-                        const int half = n / 2;
-                        if (P.row_off[lo + half] <= t) {
-                            lo += half;
-                            n -= half;
-                        } else {
-                            n = half;
-                        }
-                    }
-                    const ReqRows q = load_request(P, lo);
+                    const ReqRows q = load_request(P, find_request(P.row_off, P.B, P.T, t));
                     if (t >= q.r0 && t < q.r0 + q.n) p = q.kv - q.n + (t - q.r0);
                 } else {
                     p = s.base + j;

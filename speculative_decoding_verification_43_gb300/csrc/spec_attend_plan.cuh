@@ -52,6 +52,7 @@ struct AttendParams {
     int32_t *unit_prefix;  // [B+1] units of the own items before each request
     CutItem *cut;          // [own workers]
     int32_t *prefix_units; // units of a prefix item
+    int32_t *broken;       // 1: some request's offsets are wrong
     float2 *part_ml;       // [part rows] maximum (base 2, scaled) and sum
     float *part_o;         // [part rows][D] unnormalised output
     int32_t *err;          // [workers of both classes] 1: a bounded wait gave up
@@ -70,9 +71,17 @@ struct ReqRows {
 __device__ __forceinline__ ReqRows load_request(const AttendParams &P, int i) {
     const int r0 = P.row_off[i], r1 = P.row_off[i + 1];
     int kv = P.kv_len[i];
-    if (r0 < 0 || r1 < r0 || r1 > P.T) return {0, 0, 0};
+    if (!offsets_right(r0, r1, P.T)) return {0, 0, 0};
     if (kv < 0 || kv > static_cast<int64_t>(P.max_blocks) * P.page_size) kv = 0;
     return {r0, r1 - r0, kv};
+}
+
+// The same without rows that other offsets leave in doubt, which are looked for where some request's offsets
+// are wrong (broken).
+__device__ __forceinline__ ReqRows held_request(const AttendParams &P, int i, bool broken) {
+    const ReqRows q = load_request(P, i);
+    if (broken && q.n > 0 && offsets_contradict(P.row_off, P.B, P.T, i, q.r0, q.r0 + q.n, 0, 1)) return {0, 0, 0};
+    return q;
 }
 
 // Element offset of position x's slot (head 0), or -1 when it has no page.
@@ -160,22 +169,33 @@ struct Shares {
 };
 
 // The batch as a whole, by one warp: units of the own items, least and greatest position of the rows
-// (padding aside). Lane l has requests [l * per, (l + 1) * per), and `before` units lie before them.
+// (padding aside), and whether some request's offsets are wrong (then a second pass leaves out the rows in
+// doubt: with them the units need not stay within the host's bound). Lane l has requests [l * per, (l + 1) * per),
+// and `before` units lie before them.
 struct Totals {
     int units, before, per, pmin, pmax;
+    bool broken;
 };
 template <int KT>
 __device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane) {
-    Totals t = {0, 0, (P.B + kWarp - 1) / kWarp, INT_MAX, -1};
-    int mine = 0;
+    Totals t = {0, 0, (P.B + kWarp - 1) / kWarp, INT_MAX, -1, false};
+    int mine;
 #pragma unroll 1
-    for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
-        const ReqRows q = load_request(P, i);
-        if (q.n > 0 && q.kv > 0) {
-            t.pmin = min(t.pmin, max(q.kv - q.n, 0));
-            t.pmax = max(t.pmax, q.kv - 1);
+    for (;;) {
+        bool wrong = false;
+        mine = 0;
+#pragma unroll 1
+        for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
+            const ReqRows q = held_request(P, i, t.broken);
+            if (q.n > 0 && q.kv > 0) {
+                t.pmin = min(t.pmin, max(q.kv - q.n, 0));
+                t.pmax = max(t.pmax, q.kv - 1);
+            }
+            mine += P.Hkv * own_units<KT>(P, q);
+            wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
         }
-        mine += P.Hkv * own_units<KT>(P, q);
+        if (t.broken || !__any_sync(0xffffffffu, wrong)) break;
+        t.broken = true;
     }
     int incl = mine;
 #pragma unroll
@@ -198,7 +218,7 @@ __device__ __forceinline__ void record_units(const AttendParams &P, int lane) {
 #pragma unroll 1
     for (int i = lane * t.per; i < min(P.B, (lane + 1) * t.per); ++i) {
         if (SPEC_IN(i, P.B, DBG_ATTEND)) P.unit_prefix[i] = u;
-        u += P.Hkv * own_units<KT>(P, load_request(P, i));
+        u += P.Hkv * own_units<KT>(P, held_request(P, i, t.broken));
     }
     if (lane == 0) P.unit_prefix[P.B] = t.units;
 }
@@ -232,6 +252,7 @@ struct Walker {
     int worker;
     int i, head, k, tile;  // request, head, row tile, unit within the item
     int head_tiles;        // row tiles of a head
+    bool broken;           // some request's offsets are wrong
     ReqRows q;
     KeyTiles shared;       // prefix items: all alike
     int pmin, pmax;
@@ -240,6 +261,7 @@ struct Walker {
     __device__ __forceinline__ void start(const AttendParams &P, int w, int lane) {
         worker = w;
         const Totals t = batch_totals<KT>(P, lane);
+        broken = t.broken;
         head = k = tile = i = head_tiles = 0;
         q = {0, 0, 0};
         if constexpr (PREFIX) {
@@ -263,7 +285,7 @@ struct Walker {
                 int rem = u - __shfl_sync(0xffffffffu, t.before, l), per_head;
 #pragma unroll 1
                 for (i = l * t.per;; ++i) {
-                    q = load_request(P, i);
+                    q = held_request(P, i, broken);
                     per_head = own_units<KT>(P, q);
                     if (rem < P.Hkv * per_head || i + 1 >= P.B) break;
                     rem -= P.Hkv * per_head;
@@ -282,6 +304,7 @@ struct Walker {
         }
         emitted = 0;
         if (!PREFIX && P.shared_len == 0 && lane == 0) P.cut[w].nrows = 0;
+        if (!PREFIX && w == 0 && lane == 0) *P.broken = broken;
     }
 
     // The next segment, or false at the end of the worker's units.
@@ -343,7 +366,7 @@ struct Walker {
                             if (u < u_end) {
 #pragma unroll 1
                                 do {
-                                    q = load_request(P, ++i);
+                                    q = held_request(P, ++i, broken);
                                 } while (q.n == 0 && i + 1 < P.B);
                                 head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
                             }
@@ -361,11 +384,11 @@ struct Walker {
 
 // ---------------------------------------------------------------- requests' status
 
-// Status of request i, by one warp: consistent offsets and lengths, and a page for every position
-// that a row sees.
+// Status of request i, by one warp: offsets and length that are right by themselves, and a page for every
+// position that a row sees. (Rows that other requests' offsets leave in doubt: the joining kernel.)
 __device__ __forceinline__ int attend_status(const AttendParams &P, int i, int lane) {
     const int r0 = P.row_off[i], r1 = P.row_off[i + 1], kv = P.kv_len[i];
-    if (r0 < 0 || r1 < r0 || r1 > P.T || kv < 0) return SPEC_REQ_BAD_SHAPE;
+    if (!offsets_right(r0, r1, P.T) || kv < 0) return SPEC_REQ_BAD_SHAPE;
     if (r1 == r0 || kv == 0) return SPEC_REQ_OK;
     if (kv > static_cast<int64_t>(P.max_blocks) * P.page_size) return SPEC_REQ_BAD_BLOCKS;
     const int32_t *table = P.block_table + static_cast<int64_t>(i) * P.max_blocks;
