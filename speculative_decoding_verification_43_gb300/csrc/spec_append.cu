@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
                 const int blk = pos / P.page_size;
                 if (blk < P.max_blocks) {
                     const int page = P.block_table[static_cast<int64_t>(i) * P.max_blocks + blk];
-                    if (page >= 0 && page < P.n_pages && SPEC_IN(page, P.n_pages, DBG_CACHE))
+                    if (page >= 0 && page < P.n_pages)
                         my_slot = page * P.page_stride + (pos - blk * P.page_size) * P.slot_stride;
                 }
             }
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
             if (j + 1 < kAppendWarps) fetch(r + step);
             const int64_t slot = single ? my_slot : slot_of[j];
             if (!have || slot < 0) continue;
-            if (rotates) {
+            if (rotates && SPEC_IN(single ? my_pos : pos_of[j], P.n_pos, DBG_CACHE)) {
                 constexpr int NC = kPairs ? V : (V + 1) / 2;
                 float c[NC], s[NC];
                 const float *cs = P.cos_sin + static_cast<int64_t>(single ? my_pos : pos_of[j]) * P.rot + c0;
@@ -273,10 +273,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSM) spec_append_kern
                 }
                 pack(x, u);
             }
-            E *dst = what == Q ? static_cast<E *>(P.q_out) + r * P.q_out_stride + static_cast<int64_t>(head) * P.D
-                               : cache + slot + head * P.head_stride;
-            if (SPEC_IN(d0 + V - 1, P.D, DBG_CACHE)) *reinterpret_cast<Vec *>(dst + d0) = x;
-            if (two && SPEC_IN(d1 + V - 1, P.D, DBG_CACHE)) *reinterpret_cast<Vec *>(dst + d1) = y;
+            E *base = what == Q ? static_cast<E *>(P.q_out) : cache;
+            const int64_t at =
+                what == Q ? r * P.q_out_stride + static_cast<int64_t>(head) * P.D : slot + head * P.head_stride;
+            auto inside = [&](int d) -> bool {
+                return SPEC_IN(d + V - 1, P.D, DBG_CACHE) &&
+                       (what == Q ? SPEC_IN(r, P.T, DBG_OUT_ROWS) && SPEC_IN(head, P.Hq, DBG_OUT_ROWS)
+                                  : SPEC_IN(at, cache_extent(P), DBG_CACHE) &&
+                                        SPEC_IN(at + d + V - 1, cache_extent(P), DBG_CACHE));
+            };
+            if (inside(d0)) *reinterpret_cast<Vec *>(base + at + d0) = x;
+            if (two && inside(d1)) *reinterpret_cast<Vec *>(base + at + d1) = y;
         }
         if (!single) __syncthreads();  // the batch's slots have been read
     }

@@ -155,6 +155,7 @@ __device__ __forceinline__ void load_tile(const AttendParams &P, const Segment &
         if (o < 0) continue;  // seen by no row (or its request is in error): never used
         const int key = warp * 8 + j;
         for (int c = lane; c < per; c += kWarp) {
+            if (!SPEC_IN(o + c * V + V - 1, cache_extent(P), DBG_CACHE)) continue;
             bring(sK + key * (D + 4) + c * V, kc + o + c * V);
             bring(sV + key * D + c * V, vc + o + c * V);
         }

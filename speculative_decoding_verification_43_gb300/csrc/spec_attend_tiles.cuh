@@ -98,16 +98,24 @@ __device__ __forceinline__ TilePlan plan_tile(const AttendParams &P, const Cache
         if (page < 0 || page >= P.n_pages) page = 0;
         return page * M.page_rows + s.head * M.head_rows + (x - b * P.page_size);
     };
+    // (the debug build's check) slots row .. row + n - 1 of the map are the cache's
+    auto inside = [&](int row, int n) -> bool {
+        return SPEC_IN(row, (P.n_pages - 1) * M.page_rows + (P.Hkv - 1) * M.head_rows + P.page_size - n + 1, DBG_CACHE);
+    };
     if (P.box_log2 > 0) {
         const int box = lane & ((kKT >> P.box_log2) - 1), half = lane >> (7 - P.box_log2);
         const int x = x0 + (box << P.box_log2);
         t.on = half < blocks(P.D) && x - x0 < n && item_sees(P, s.keys, x, 1 << P.box_log2);
         if (t.on) t.row[0] = row_of(x);
+        t.on = t.on && inside(t.row[0], 1 << P.box_log2);
     } else {
         t.on = 4 * lane < n;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (t.on && item_sees(P, s.keys, x0 + 4 * lane + j)) t.row[j] = row_of(x0 + 4 * lane + j);
+            if (t.on && item_sees(P, s.keys, x0 + 4 * lane + j)) {
+                const int row = row_of(x0 + 4 * lane + j);
+                if (inside(row, 1)) t.row[j] = row;
+            }
     }
     return t;
 }

@@ -26,6 +26,12 @@ struct FastDiv {
     }
 };
 
+// Elements from a cache's first one to its last (for the debug build's checks).
+template <typename Params>
+__device__ __forceinline__ int64_t cache_extent(const Params &P) {
+    return (P.n_pages - 1) * P.page_stride + (P.page_size - 1) * P.slot_stride + (P.Hkv - 1) * P.head_stride + P.D;
+}
+
 // Which rows are a request's. Request i holds rows row_off[i] .. row_off[i+1]-1 when 0 <= row_off[i] <=
 // row_off[i+1] <= T and none of the offsets within [0, T] contradicts it: no earlier one is above row_off[i],
 // no later one below row_off[i+1]. So no row is held twice, the rows held are T at most, and of every row that
