@@ -104,3 +104,26 @@ def test_not_finite_in_a_part_of_vanishing_weight(dtype, rows, shared):
     out, rest = got.out.cpu().double(), [d for d in range(64) if d != 3]
     assert torch.isnan(out[..., 3]).all()
     assert ((out - ref[0]).abs() <= _tol(b, ref))[..., rest].all()
+
+
+@TYPES
+def test_every_visible_page_is_checked(dtype):
+    """One bad entry of a table with 1500 (pages of one slot), at ends and in the middle; the request next to it
+    is served. Entries behind the window and past the text may be anything."""
+    n = 1500
+    whole = Batch([2, 1], [n, 40], 2, 1, 64, dtype, 1, seed=2).place()
+    cut = Batch([2, 1], [n, 40], 2, 1, 64, dtype, 1, 300, 5, seed=2).place()
+    for b, seen in ((whole, range(n)), (cut, [*range(5), *range(n - 2 - 300 + 1, n)])):
+        a = b.attention()
+        good = a.run().out.clone()
+        assert a.out.req_status.tolist() == [0, 0]
+        for x in (0, 4, 5, 31, 32, 511, 512, 513, 543, 1023, 1024, 1197, 1198, 1199, 1230, 1498, 1499, 1500):
+            for bad in (-1, b.k_cache.shape[0]):
+                keep = b.table[0, x].item()
+                b.table[0, x] = bad
+                a.run()
+                torch.cuda.synchronize()
+                assert a.out.req_status.tolist() == [16 if x in seen else 0, 0], x
+                assert torch.equal(a.out.out[2:], good[2:])
+                assert (a.out.out[:2] == 0).all() if x in seen else torch.equal(a.out.out, good)
+                b.table[0, x] = keep
