@@ -90,9 +90,14 @@ spec_status spec_kv_append(const spec_kv_append_args *args, cudaStream_t stream)
  * if every request's block_table named these pages (block_table entries of pages wholly below
  * shared_len are not read).
  *
- * bf16: products on the tensor cores with 32-bit accumulation, softmax weights rounded to bf16 for
- * the second product, statistics in 32 bits. fp32: 32-bit arithmetic throughout. Results do not
- * depend on the order in which CTAs run.
+ * fp32: 32-bit arithmetic throughout. bf16, head_dim a multiple of 16 up to 128, and a cache whose
+ * slots make the rows of a matrix (pages a whole number of slot strides apart; a slot's heads side by
+ * side within its stride, or a whole number of slot strides apart): products on the tensor cores with
+ * 32-bit accumulation, each softmax weight rounded to bf16 for the second product; scores, statistics
+ * and the sum of the unrounded weights in 32 bits. Other bf16 calls run on the fp32 units with 32-bit
+ * weights, a good deal slower. So a bf16 call's error and speed follow its head size and layout
+ * (spec_attend_plan names the kernel): with rounded weights an output may be off by 2^-8 of
+ * sum |weight v| beside its own rounding. Results do not depend on the order in which CTAs run.
  * A request with status bits has out = 0 and lse = -inf on its rows, if it has offsets 0 <= row_off[i]
  * <= row_off[i+1] <= T (else it has none; rows that belong to no request are not written):
  * SPEC_REQ_BAD_SHAPE for wrong or contradicted offsets or a negative kv_len, SPEC_REQ_BAD_BLOCKS for a
@@ -119,6 +124,14 @@ typedef struct {
     int32_t *req_status;         /* [B] out (may be NULL)                                        */
 } spec_attend_args;
 
+/* Limits, SPEC_ERR_UNSUPPORTED beyond them: total_rows * n_q_heads and the positions a row of
+ * block_table holds (max_blocks * page_size) within 2^29 and 2^30, and so many units of work as the
+ * call could have by its sizes, whatever the lengths are, within 31 bits: with G = n_q_heads /
+ * n_kv_heads,
+ *     (total_rows * G / 16 + B + 1) * n_kv_heads * (max(max_blocks * page_size, shared_len) / 32 + 8).
+ * 65536 rows of 32 / 8 heads, for instance, fit tables of 131072 positions, and not of a million: bring
+ * fewer rows at a time or a narrower table. */
+
 /* Bytes of workspace spec_attend needs for these arguments (only the sizes are read; 0 when they are
  * invalid). 256-byte aligned; its contents need no preparation. Calls that share a workspace must
  * not overlap on the GPU. */
@@ -130,8 +143,9 @@ size_t spec_attend_workspace_size(const spec_attend_args *args);
 spec_status spec_attend(const spec_attend_args *args, void *workspace, size_t workspace_bytes,
                         cudaStream_t stream);
 
-/* The kernel that serves these arguments (a static string), or NULL when they are invalid. A
- * diagnostic: it enqueues nothing. */
+/* The kernel that serves the requests' own positions for these arguments (a static string; a shared
+ * prefix, with the rows of the whole batch, may take the one for more rows), or NULL when they are
+ * invalid. A diagnostic: it enqueues nothing. */
 const char *spec_attend_plan(const spec_attend_args *args);
 
 #ifdef __cplusplus

@@ -467,7 +467,7 @@ class Attention:
         return self
 
     def plan(self) -> str | None:
-        """The kernel that serves the bound call, or None when its sizes are invalid."""
+        """The kernel that serves the bound call's own positions, or None when its sizes are invalid."""
         name = lib.spec_attend_plan(ctypes.byref(self.args))
         return None if name is None else name.decode()
 

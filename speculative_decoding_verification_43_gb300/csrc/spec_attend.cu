@@ -285,14 +285,18 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
 //     32       139  145  148  263  265  272  391
 //     64       146  154  159  175  184  208  316
 //     256      176  183  191  191  192  193  194
-// The first limit is below 32 because the average is what is known here, and requests above it read twice.
+// The first limit is below 32 because the average is all that is known here (lengths are on the device), and a
+// request of n packed rows reads its keys once for each item, n / RT times rounded up. Batches of unlike
+// requests pay for that: 63 of 5 rows after 8000 positions with one prompt of 2000 rows take 471 us, the two
+// parts by themselves 333 and 69; 512 single tokens after 1000 with that prompt 590, by themselves 355 and 69.
 static void tensor_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
     rt_log2 = rows <= 24 * groups ? 5 : rows <= 48 * groups ? 6 : pair::kRTLog2;
     workers = rt_log2 == pair::kRTLog2 ? kSMs : kSMs * round_::kPerSM;
 }
 
 // Time of an item beside its tiles, in tiles: what makes the workers end together. Pair kernel, 4 prompts, at
-// 4, 6, 8: 390, 369, 378 us; round kernel, 64 windowed requests, at 2, 3, 4, 5: 84, 81, 81, 80 us.
+// 4, 6, 8: 390, 369, 378 us; round kernel, 64 windowed requests, at 2, 3, 4, 5: 84, 81, 81, 80 us. (One batch
+// each. The fp32 units' kernel, where 2 is taken: attend_work.)
 static int own_extra_units(int rt_log2) { return rt_log2 == pair::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.
@@ -312,6 +316,8 @@ static void attend_work(AttendParams &P, bool tensor) {
         P.own_rt_log2 = P.prefix_rt_log2 = fma::kRTLog2;
         P.own_workers = P.prefix_workers = kSMs * fma::ctas_per_sm(P.D);
         P.box_log2 = 0;
+        // at 0, 1, 2, 4, 8: 250, 248, 248, 252, 256 us (256 fp32 requests under a window), 411, 408, 412, 417, 427
+        // (64 fp32 requests of up to 8000 positions), 894, 875, 888, 912, 956 (an fp32 prompt of 2000 rows)
         P.own_extra = P.prefix_extra = 2;
     }
     if (P.shared_len == 0) P.prefix_workers = 0;

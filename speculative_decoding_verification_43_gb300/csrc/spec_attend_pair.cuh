@@ -15,10 +15,12 @@
 // has grown by more than 2^8 beyond it (P then stays below 2^8, whose bf16 rounding is relative all the
 // same), so the output hardly ever leaves tensor memory before the end.
 //
-// Measured: 372 GFLOP of prompts (4 requests, 32 query and 8 key heads of 128) 369 us, 0.51 of the measured
-// bf16 rate; 550 GFLOP of a 32768-position prefix under 1031 rows 441 us, 0.64. A pair of tiles takes some
-// 3500 cycles, 2048 of them products: what is left is the chain from a warpgroup's weights over the issuing
-// warp's waits to the next scores, and an item's queries and way out (six tiles' time).
+// Measured: 372 GFLOP of prompts (4 requests, 32 query and 8 key heads of 128) 368 us, 0.51 of the measured
+// bf16 rate; 550 GFLOP of a 32768-position prefix under 1031 rows 452 us, 0.62. A pair of tiles takes some
+// 3500 cycles by its time, 2048 of them products; on 2000 rows after 6000 positions the counters have the tensor
+// pipe active in 48 % of the cycles, instructions issued in 36 % and DRAM in 3 %, and warps waiting on loads and
+// barriers most of the rest. What is left is taken to be the chain from a warpgroup's weights over the
+// issuing warp's waits to the next scores, and an item's queries and way out (six tiles' time).
 //
 // Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 keeps the books (the requests' status), 10
 // issues matrix instructions.
