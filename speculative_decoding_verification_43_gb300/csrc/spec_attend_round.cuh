@@ -284,7 +284,21 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
             unsigned char *v_tile = ring_mem + v_slot * tb;
             uint32_t mine = 0u;
+            // A wait by parity tells this use of a slot from the one before only when that one is known to have
+            // arrived. In rings of three slots or more it is: it held keys whose scores, or values whose product,
+            // have been waited for. In a ring of two (64 rows, more than 64 columns) it held the values of the
+            // tile before, which only that tile's product says.
+            bool rested = i == 0;
+            auto rest = [&]() -> bool {
+                if (rested) return true;
+                rested = true;
+                if (!wait_warp(ab, &sh.o_done, o_phase)) return false;
+                o_phase ^= 1u;
+                tc_fence_after();
+                return true;
+            };
             if (edge) {
+                if (ring.n == 2 && !rest()) return;
                 if (!wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase)) return;
                 if (__any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid))) mine = 2u;
                 fence_proxy_async_smem();
@@ -344,11 +358,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             } else {
                 word = 1u;  // the first references (the values' flag comes with their meetings)
             }
-            if (i > 0) {  // the product before this tile: the weights' memory is free, O at rest
-                if (!wait_warp(ab, &sh.o_done, o_phase)) return;
-                o_phase ^= 1u;
-                tc_fence_after();
-            }
+            if (!rest()) return;  // the product before this tile: the weights' memory is free, O at rest
             if (word & 1u) {
                 // new references: the rows' maxima over the tile, where they are larger
 #pragma unroll
