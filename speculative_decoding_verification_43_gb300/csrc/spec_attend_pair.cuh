@@ -209,6 +209,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
     const uint32_t s_addr = sh.tmem + w * 256 + lanes, o_addr = s_addr + 128;
     Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
     uint32_t s_phase = 0, o_phase = 0, half_phase = 0, agree_phase = 0;
+    bool behind = false;  // tiles have gone by that this warpgroup has not waited for
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -261,8 +262,21 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 const int x0 = tile_begin<kKT>(keys, first + i), n = tile_keys(keys, x0);
                 const bool edge = x0 > whole || x0 < from || (x0 <= cut && x0 + kKT > P.n_sink);
                 unsigned char *v_tile = ring_mem + (ring.slot + 1 == ring.n ? 0 : ring.slot + 1) * tb;
-                bool skip = false;
+                bool skip = false, scored = false;
+                auto scores = [&]() -> bool {
+                    if (scored) return true;
+                    scored = true;
+                    if (!wait_warp(ab, &sh.s_full[w], s_phase)) return false;
+                    s_phase ^= 1u;
+                    tc_fence_after();
+                    behind = false;
+                    return true;
+                };
                 if (edge) {
+                    // A wait by parity tells this use of the slot from the one before only when that one is known to
+                    // have arrived: its scores or the next tile's, issued behind its product, have been waited for.
+                    // After items without rows for this accumulator, this item's first scores say so.
+                    if (behind && !scores()) return;
                     const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
                     if (!wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase)) return;
                     const bool bad = __any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid));
@@ -278,9 +292,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                     agree_phase ^= 1u;
                     skip = (found[0] | found[1] | found[2] | found[3]) != 0;
                 }
-                if (!wait_warp(ab, &sh.s_full[w], s_phase)) return;
-                s_phase ^= 1u;
-                tc_fence_after();
+                if (!scores()) return;
                 // (the tile before has been read out of this word: its products were issued before S)
                 if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
 #pragma unroll 1
@@ -377,6 +389,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             tc_fence_after();
         } else {
             for (int i = 0; i < 2 * nt; ++i) ring.step();
+            behind = behind || nt > 0;
         }
         if (dead) {
             m = -INFINITY;

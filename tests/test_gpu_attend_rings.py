@@ -34,14 +34,11 @@ CASES = {
 }
 
 
-@pytest.mark.parametrize("name", list(CASES))
-def test_rings_of_two(name):
-    rows, kv, Hq, Hkv, D, page, W, S, L, order = CASES[name]
-    b = Batch(rows, kv, Hq, Hkv, D, BF, page, W, S, L, seed=len(name), order=order).place()
-    a = b.attention()
-    assert a.plan() == "spec_attend_round_kernel"
+def repeat(b, kernel, times):
+    a = b.place().attention()
+    assert a.plan() == kernel
     first = None
-    for k in range(40):
+    for k in range(times):
         a.workspace.fill_(0xFF * (k % 2))
         a.out.out.fill_(7.0)
         a.run()
@@ -51,3 +48,18 @@ def test_rings_of_two(name):
             first = got
             check(b, a.out)
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1]), k
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_rings_of_two(name):
+    rows, kv, Hq, Hkv, D, page, W, S, L, order = CASES[name]
+    repeat(Batch(rows, kv, Hq, Hkv, D, BF, page, W, S, L, seed=len(name), order=order), "spec_attend_round_kernel", 40)
+
+
+@pytest.mark.parametrize("D,page,window", [(128, 3, 0), (64, 1, 0), (128, 16, 200)])
+def test_items_of_one_accumulator_before_items_of_two(D, page, window):
+    """Items of up to 128 rows, whose tiles the second accumulator's threads do not use, each followed by an item
+    of more rows over a text of less than a tile."""
+    rows = [30, 60] * 60
+    kv = [x for i in range(60) for x in (300 + 7 * (i % 40), 60 + i % 50)]
+    repeat(Batch(rows, kv, 16, 4, D, BF, page, window, 2 if window else 0, 0, seed=D), "spec_attend_pair_kernel", 20)
