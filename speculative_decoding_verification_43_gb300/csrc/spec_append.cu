@@ -101,7 +101,7 @@ __device__ __forceinline__ void load_floats(float (&out)[N], const float *p) {
 //
 // Bound by latency when there are few rows (offsets -> length -> page -> store is a chain of
 // dependent loads; a row's own values are requested before it): 2.5 us for 5 rows, 4.6 us for 290 rows of
-// 32 + 2 x 8 heads of 128 in bf16. By DRAM when there are many: 12935 rows of 48 heads of 64, 153 MB, in 29.5
+// 32 + 2 x 8 heads of 128 in bf16. By DRAM when there are many: 12935 rows of 48 heads of 64, 153 MB, in 29.7
 // us, 0.77 of the measured copy rate. One element at a time (V = 1) 288 rows of 32 + 2 x 8 heads of 80, 40
 // columns turned, take 6.1 us; 4.6 with all 80 turned, in pieces of 16 bytes. Four blocks an SM leave a thread 64 registers; six (40) spilled, and
 // finding every row's slot in turn, without the next row's values under way, took 39 us.

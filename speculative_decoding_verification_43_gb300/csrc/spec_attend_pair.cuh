@@ -15,8 +15,8 @@
 // has grown by more than 2^8 beyond it (P then stays below 2^8, whose bf16 rounding is relative all the
 // same), so the output hardly ever leaves tensor memory before the end.
 //
-// Measured: 372 GFLOP of prompts (4 requests, 32 query and 8 key heads of 128) 368 us, 0.51 of the measured
-// bf16 rate; 550 GFLOP of a 32768-position prefix under 1031 rows 452 us, 0.62. A pair of tiles takes some
+// Measured: 372 GFLOP of prompts (4 requests, 32 query and 8 key heads of 128) 371 us, 0.51 of the measured
+// bf16 rate; 550 GFLOP of a 32768-position prefix under 1031 rows 447 us, 0.63. A pair of tiles takes some
 // 3500 cycles by its time, 2048 of them products; on 2000 rows after 6000 positions the counters have the tensor
 // pipe active in 48 % of the cycles, instructions issued in 36 % and DRAM in 3 %, and warps waiting on loads and
 // barriers most of the rest. What is left is taken to be the chain from a warpgroup's weights over the

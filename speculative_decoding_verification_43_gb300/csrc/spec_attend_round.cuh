@@ -18,9 +18,9 @@
 // Two CTAs per SM, each a worker: while one begins or ends an item the other keeps copies in flight.
 // Warps: 0-3 softmax, 4 loads tiles, 5 keeps the books, then issues the matrix instructions.
 //
-// Measured: 16 requests of 4 to 65 thousand tokens (2.0 GB of keys and values) 318 us, 0.94 of the
-// measured copy rate; 64 requests of up to 16 thousand under a 1024-token window with 4 sinks (0.27 GB, items of
-// 9 tiles) 82 us, where items' beginnings and ends (some 4 us each, mostly the chain from queries to first
+// Measured: 16 requests of 4 to 65 thousand tokens (2.0 GB of keys and values) 312 to 323 us, 0.93 to 0.96
+// of the measured copy rate; 64 requests of up to 16 thousand under a 1024-token window with 4 sinks (0.27 GB,
+// items of 9 tiles) 82 us, where items' beginnings and ends (some 4 us each, mostly the chain from queries to first
 // weights and from sums to rows) are as long as their tiles. With rows along the lanes, as in the pair
 // kernel, the first took 567 us and the second 227.
 #pragma once
