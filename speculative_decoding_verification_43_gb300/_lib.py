@@ -1,5 +1,5 @@
-"""ctypes view of the C ABI in include/spec_verify.h and include/spec_attend.h (libspecverify.so,
-built in-tree).
+"""ctypes view of the C ABI in include/spec_verify.h, include/spec_attend.h, include/spec_cache8.h and
+include/spec_tables.h (libspecverify.so, built in-tree).
 
 There is no fallback: if the library is missing or fails to load, importing this module
 raises, and nothing in the package computes any part of the verifier on the CPU.
@@ -90,6 +90,23 @@ class SpecAttendArgs(ctypes.Structure):
     ]
 
 
+class SpecKvAppend8Args(ctypes.Structure):
+    _fields_ = [("append", SpecKvAppendArgs), ("k_scale", _p), ("v_scale", _p)]
+
+
+class SpecAttend8Args(ctypes.Structure):
+    _fields_ = [("attend", SpecAttendArgs), ("k_scale", _p), ("v_scale", _p)]
+
+
+class SpecBlockTablesArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", _i32), ("total_rows", _i32), ("page_size", _i32), ("max_blocks", _i32), ("n_pages", _i32),
+        ("n_shared", _i32), ("kv_len", _p), ("row_off", _p), ("shared_table", _p), ("n_blocks", _p),
+        ("block_table", _p), ("free_pages", _p), ("n_free", _p), ("slot_map", _p), ("positions", _p),
+        ("req_status", _p),
+    ]
+
+
 # every symbol include/spec_verify.h declares
 EXPORTS = ("spec_verify_workspace_size", "spec_verify", "spec_verify_noalloc", "spec_verify_plan",
            "spec_verify_round", "spec_compact",
@@ -97,6 +114,9 @@ EXPORTS = ("spec_verify_workspace_size", "spec_verify", "spec_verify_noalloc", "
            "spec_version")
 # every symbol include/spec_attend.h declares
 ATTEND_EXPORTS = ("spec_kv_append", "spec_attend_workspace_size", "spec_attend", "spec_attend_plan")
+# every symbol include/spec_cache8.h declares, and include/spec_tables.h
+CACHE8_EXPORTS = ("spec_kv_append8", "spec_attend8_workspace_size", "spec_attend8", "spec_attend8_plan")
+TABLES_EXPORTS = ("spec_block_tables_workspace_size", "spec_block_tables")
 
 
 def load_library(path: str):
@@ -139,6 +159,18 @@ def load_library(path: str):
     lib.spec_attend.restype = ctypes.c_int
     lib.spec_attend_plan.argtypes = [ctypes.POINTER(SpecAttendArgs)]
     lib.spec_attend_plan.restype = ctypes.c_char_p
+    lib.spec_kv_append8.argtypes = [ctypes.POINTER(SpecKvAppend8Args), _p]
+    lib.spec_kv_append8.restype = ctypes.c_int
+    lib.spec_attend8_workspace_size.argtypes = [ctypes.POINTER(SpecAttend8Args)]
+    lib.spec_attend8_workspace_size.restype = ctypes.c_size_t
+    lib.spec_attend8.argtypes = [ctypes.POINTER(SpecAttend8Args), _p, ctypes.c_size_t, _p]
+    lib.spec_attend8.restype = ctypes.c_int
+    lib.spec_attend8_plan.argtypes = [ctypes.POINTER(SpecAttend8Args)]
+    lib.spec_attend8_plan.restype = ctypes.c_char_p
+    lib.spec_block_tables_workspace_size.argtypes = [ctypes.POINTER(SpecBlockTablesArgs)]
+    lib.spec_block_tables_workspace_size.restype = ctypes.c_size_t
+    lib.spec_block_tables.argtypes = [ctypes.POINTER(SpecBlockTablesArgs), _p, ctypes.c_size_t, _p]
+    lib.spec_block_tables.restype = ctypes.c_int
     if hasattr(lib, "spec_debug_fetch"):  # the debug build (include/spec_debug.h)
         lib.spec_debug_fetch.argtypes = [_p]
         lib.spec_debug_fetch.restype = ctypes.c_int

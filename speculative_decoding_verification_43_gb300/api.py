@@ -12,7 +12,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import SpecAttendArgs, SpecCompactArgs, SpecKvAppendArgs, SpecVerifyArgs, check, lib
+from ._lib import (SpecAttend8Args, SpecAttendArgs, SpecBlockTablesArgs, SpecCompactArgs, SpecKvAppend8Args,
+                   SpecKvAppendArgs, SpecVerifyArgs, check, lib)
 
 _DTYPE = {torch.float32: _lib.SPEC_F32, torch.bfloat16: _lib.SPEC_BF16}
 
@@ -383,6 +384,13 @@ class KvAppender:
         """q [T, Hq, D], k and v [T, Hkv, D] (slices of one projection are fine), cos_sin
         [n_pos, rot_dim] float32 (cosines, then sines), k_cache and v_cache [n_pages, page_size, Hkv,
         D], block_table [B, max_blocks]. q_out may be q itself."""
+        self._bind_rows(q, k, v, cos_sin, q_out)
+        _bind_cache(self.args, k_cache, v_cache, self.Hkv, self.D, self.dtype)
+        _bind_requests(self.args, self.B, row_off, kv_len, block_table)
+        self._keep = (q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, q_out)
+        return self
+
+    def _bind_rows(self, q, k, v, cos_sin, q_out):
         a, T, D = self.args, self.T, self.D
         if q_out is not None:
             self.out.q = q_out
@@ -395,10 +403,6 @@ class KvAppender:
             assert cos_sin.dtype == torch.float32 and cos_sin.is_cuda and cos_sin.is_contiguous()
             assert cos_sin.dim() == 2 and cos_sin.shape[1] == a.rot_dim, (cos_sin.shape, a.rot_dim)
             a.cos_sin, a.n_pos = _ptr(cos_sin), int(cos_sin.shape[0])
-        _bind_cache(a, k_cache, v_cache, self.Hkv, D, self.dtype)
-        _bind_requests(a, self.B, row_off, kv_len, block_table)
-        self._keep = (q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, block_table, q_out)
-        return self
 
     def run(self, stream=None) -> AppendOutputs:
         check(lib.spec_kv_append(ctypes.byref(self.args), _run_stream(self, stream)), "spec_kv_append")
@@ -449,22 +453,32 @@ class Attention:
     def bind(self, q, k_cache, v_cache, row_off, kv_len, block_table, *, shared_table=None, out=None):
         """q [T, Hq, D], k_cache and v_cache [n_pages, page_size, Hkv, D] of any strides, block_table
         [B, max_blocks], shared_table [ceil(shared_len / page_size)]."""
+        self._bind_rows(q, out)
+        _bind_cache(self.args, k_cache, v_cache, self.Hkv, self.D, self.dtype)
+        self._bind_tables(row_off, kv_len, block_table, shared_table)
+        self._make_workspace(lib.spec_attend_workspace_size(ctypes.byref(self.args)))
+        self._keep = (q, k_cache, v_cache, row_off, kv_len, block_table, shared_table, out)
+        return self
+
+    def _bind_rows(self, q, out):
         a = self.args
         if out is not None:
             self.out.out = out
         a.q, a.q_stride = _rows_of(q, self.T, self.Hq, self.D, self.dtype)
         a.out, a.out_stride = _rows_of(self.out.out, self.T, self.Hq, self.D, self.dtype)
-        _bind_cache(a, k_cache, v_cache, self.Hkv, self.D, self.dtype)
+
+    def _bind_tables(self, row_off, kv_len, block_table, shared_table):
+        a = self.args
         _bind_requests(a, self.B, row_off, kv_len, block_table)
         if a.shared_len:
             assert _i32(shared_table).numel() * a.page_size >= a.shared_len
         a.shared_table = _ptr(shared_table)
-        self.ws_bytes = int(lib.spec_attend_workspace_size(ctypes.byref(a)))
+
+    def _make_workspace(self, size):
+        self.ws_bytes = int(size)
         if self.workspace is None or self.workspace.numel() < self.ws_bytes:
             self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
             self._streams = set()
-        self._keep = (q, k_cache, v_cache, row_off, kv_len, block_table, shared_table, out)
-        return self
 
     def plan(self) -> str | None:
         """The kernel that serves the bound call's own positions, or None when its sizes are invalid."""
@@ -488,6 +502,164 @@ def attend(q, k_cache, v_cache, row_off, kv_len, block_table, *, window: int = 0
                       shared_len=shared_len, scale=scale, device=q.device)
         a.bind(q, k_cache, v_cache, row_off, kv_len, block_table, shared_table=shared_table)
         out = a.run(stream)
+    return _hand_over(out, stream)
+
+
+def _bind_cache8(a, paged, k_cache, v_cache, k_scale, v_scale, Hkv: int, D: int):
+    """The paged cache in e4m3 and its scales [n_pages, Hkv]; `paged`: the struct with the cache's strides."""
+    _bind_cache(paged, k_cache, v_cache, Hkv, D, torch.float8_e4m3fn)
+    for t in (k_scale, v_scale):
+        assert t.dtype == torch.float32 and t.is_cuda and t.is_contiguous() and t.shape == (paged.n_pages, Hkv), \
+            (t.dtype, t.shape, (paged.n_pages, Hkv))
+    a.k_scale, a.v_scale = _ptr(k_scale), _ptr(v_scale)
+
+
+class KvAppender8(KvAppender):
+    """KvAppender into a cache held in e4m3 with a scale for each page and head (see include/spec_cache8.h);
+    q, k and v keep their type."""
+
+    def __init__(self, B: int, total_rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype, *,
+                 rot_dim: int | None = None, interleaved: bool = False, device=None):
+        super().__init__(B, total_rows, Hq, Hkv, D, dtype, rot_dim=rot_dim, interleaved=interleaved, device=device)
+        self.args8 = SpecKvAppend8Args()
+        self.args8.append = self.args
+        self.args = self.args8.append  # a view: what is set in it is set in args8
+
+    def bind(self, q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, k_scale, v_scale, block_table, *, q_out=None):
+        """As KvAppender.bind, with k_cache and v_cache [n_pages, page_size, Hkv, D] of float8_e4m3fn and k_scale and
+        v_scale [n_pages, Hkv] float32, which the call brings up to date."""
+        self._bind_rows(q, k, v, cos_sin, q_out)
+        _bind_cache8(self.args8, self.args, k_cache, v_cache, k_scale, v_scale, self.Hkv, self.D)
+        _bind_requests(self.args, self.B, row_off, kv_len, block_table)
+        self._keep = (q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, k_scale, v_scale, block_table, q_out)
+        return self
+
+    def run(self, stream=None) -> AppendOutputs:
+        check(lib.spec_kv_append8(ctypes.byref(self.args8), _run_stream(self, stream)), "spec_kv_append8")
+        return self.out
+
+
+def kv_append8(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, k_scale, v_scale, block_table, *,
+               rot_dim: int | None = None, interleaved: bool = False, q_out=None, stream=None) -> AppendOutputs:
+    """Appends a round's rows to the paged cache in 8 bits (see include/spec_cache8.h). With a stream, the outputs
+    are allocated and written there; who uses them elsewhere waits for it first."""
+    T, Hkv, D = k.shape
+    with torch.cuda.stream(stream):
+        c = KvAppender8(row_off.numel() - 1, T, q.shape[1] if q is not None else 0, Hkv, D, k.dtype, rot_dim=rot_dim,
+                        interleaved=interleaved, device=k.device)
+        c.bind(q, k, v, cos_sin, row_off, kv_len, k_cache, v_cache, k_scale, v_scale, block_table, q_out=q_out)
+        out = c.run(stream)
+    return _hand_over(out, stream)
+
+
+class Attention8(Attention):
+    """Attention over a cache held in e4m3 with a scale for each page and head (see include/spec_cache8.h); q and
+    the outputs keep their type."""
+
+    def __init__(self, B: int, total_rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype, *, window: int = 0,
+                 n_sink: int = 0, shared_len: int = 0, scale: float | None = None, device=None):
+        super().__init__(B, total_rows, Hq, Hkv, D, dtype, window=window, n_sink=n_sink, shared_len=shared_len,
+                         scale=scale, device=device)
+        self.args8 = SpecAttend8Args()
+        self.args8.attend = self.args
+        self.args = self.args8.attend  # a view: what is set in it is set in args8
+
+    def bind(self, q, k_cache, v_cache, k_scale, v_scale, row_off, kv_len, block_table, *, shared_table=None, out=None):
+        """As Attention.bind, with k_cache and v_cache [n_pages, page_size, Hkv, D] of float8_e4m3fn and k_scale and
+        v_scale [n_pages, Hkv] float32."""
+        self._bind_rows(q, out)
+        _bind_cache8(self.args8, self.args, k_cache, v_cache, k_scale, v_scale, self.Hkv, self.D)
+        self._bind_tables(row_off, kv_len, block_table, shared_table)
+        self._make_workspace(lib.spec_attend8_workspace_size(ctypes.byref(self.args8)))
+        self._keep = (q, k_cache, v_cache, k_scale, v_scale, row_off, kv_len, block_table, shared_table, out)
+        return self
+
+    def plan(self) -> str | None:
+        """The kernel that serves the bound call's own positions, or None when its sizes are invalid."""
+        name = lib.spec_attend8_plan(ctypes.byref(self.args8))
+        return None if name is None else name.decode()
+
+    def run(self, stream=None) -> AttendOutputs:
+        rc = lib.spec_attend8(ctypes.byref(self.args8), ctypes.c_void_p(self.workspace.data_ptr()),
+                              self.workspace.numel(), _run_stream(self, stream))
+        check(rc, "spec_attend8")
+        return self.out
+
+
+def attend8(q, k_cache, v_cache, k_scale, v_scale, row_off, kv_len, block_table, *, window: int = 0, n_sink: int = 0,
+            shared_len: int = 0, shared_table=None, scale: float | None = None, stream=None) -> AttendOutputs:
+    """Attention of a round's rows over the paged cache in 8 bits (see include/spec_cache8.h). With a stream,
+    workspace and outputs are allocated and written there; who uses the outputs elsewhere waits for it first."""
+    T, Hq, D = q.shape
+    with torch.cuda.stream(stream):
+        a = Attention8(row_off.numel() - 1, T, Hq, k_cache.shape[2], D, q.dtype, window=window, n_sink=n_sink,
+                       shared_len=shared_len, scale=scale, device=q.device)
+        a.bind(q, k_cache, v_cache, k_scale, v_scale, row_off, kv_len, block_table, shared_table=shared_table)
+        out = a.run(stream)
+    return _hand_over(out, stream)
+
+
+@dataclass
+class TableOutputs:
+    slot_map: torch.Tensor    # [T] physical row of each row's position, -1: none
+    positions: torch.Tensor   # [T]
+    req_status: torch.Tensor
+
+
+class BlockTables:
+    """A prepared spec_block_tables call for one batch shape: block tables brought to the requests' lengths, and
+    the slots of the rows (see include/spec_tables.h). total_rows 0: tables only."""
+
+    def __init__(self, B: int, total_rows: int, page_size: int, n_pages: int, device=None):
+        self.device = torch.device(device or "cuda")
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.B, self.T = B, total_rows
+        self.out = TableOutputs(slot_map=torch.empty(total_rows, **i32), positions=torch.empty(total_rows, **i32),
+                                req_status=torch.empty(B, **i32))
+        self.args = SpecBlockTablesArgs()
+        a = self.args
+        a.B, a.total_rows, a.page_size, a.n_pages = B, total_rows, page_size, n_pages
+        a.slot_map, a.positions, a.req_status = (_ptr(t) for t in vars(self.out).values())
+        self.workspace = None
+        self._streams, self._keep = set(), ()
+
+    def bind(self, kv_len, n_blocks, block_table, free_pages, n_free, *, row_off=None, shared_table=None):
+        """kv_len and n_blocks [B], block_table [B, max_blocks], free_pages [n_pages], n_free [1], row_off [B + 1]
+        (with rows), shared_table [n_shared]; n_blocks, block_table, free_pages and n_free are brought up to date."""
+        a = self.args
+        assert _i32(kv_len).shape == (self.B,) and _i32(n_blocks).shape == (self.B,)
+        assert _i32(block_table).dim() == 2 and block_table.shape[0] == self.B
+        assert _i32(free_pages).numel() == a.n_pages and _i32(n_free).numel() == 1
+        if self.T:
+            assert _i32(row_off).shape == (self.B + 1,)
+        a.max_blocks = int(block_table.shape[1])
+        a.n_shared = 0 if shared_table is None else int(_i32(shared_table).numel())
+        a.kv_len, a.n_blocks, a.block_table = _ptr(kv_len), _ptr(n_blocks), _ptr(block_table)
+        a.free_pages, a.n_free = _ptr(free_pages), _ptr(n_free)
+        a.row_off, a.shared_table = _ptr(row_off), _ptr(shared_table)
+        if self.workspace is None:
+            ws = int(lib.spec_block_tables_workspace_size(ctypes.byref(a)))
+            self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
+            self._streams = set()
+        self._keep = (kv_len, n_blocks, block_table, free_pages, n_free, row_off, shared_table)
+        return self
+
+    def run(self, stream=None) -> TableOutputs:
+        rc = lib.spec_block_tables(ctypes.byref(self.args), ctypes.c_void_p(self.workspace.data_ptr()),
+                                   self.workspace.numel(), _run_stream(self, stream))
+        check(rc, "spec_block_tables")
+        return self.out
+
+
+def block_tables(kv_len, n_blocks, block_table, free_pages, n_free, page_size: int, *, row_off=None, total_rows: int = 0,
+                 shared_table=None, stream=None) -> TableOutputs:
+    """Brings the block tables to the requests' lengths (see include/spec_tables.h); total_rows rows get their
+    slots. With a stream, workspace and outputs are allocated and written there; who uses the outputs elsewhere
+    waits for it first."""
+    with torch.cuda.stream(stream):
+        t = BlockTables(kv_len.numel(), total_rows, page_size, free_pages.numel(), device=kv_len.device)
+        t.bind(kv_len, n_blocks, block_table, free_pages, n_free, row_off=row_off, shared_table=shared_table)
+        out = t.run(stream)
     return _hand_over(out, stream)
 
 

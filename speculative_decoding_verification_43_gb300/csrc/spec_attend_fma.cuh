@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "spec_attend_plan.cuh"
+#include "spec_fp8.cuh"
 
 namespace spec {
 namespace fma {
@@ -55,6 +56,17 @@ __device__ __forceinline__ void bring(float *dst, const __nv_bfloat16 *src) {
     for (int j = 0; j < 4; ++j)
         *reinterpret_cast<float2 *>(dst + 2 * j) =
             make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+}
+
+// The same of a cache in 8 bits (16 elements), by their scale.
+__device__ __forceinline__ void bring(float *dst, const __nv_fp8_e4m3 *src, float scale) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(src);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 f = e4m3_to_float4(w[j]);
+        *reinterpret_cast<float4 *>(dst + 4 * j) = make_float4(f.x * scale, f.y * scale, f.z * scale, f.w * scale);
+    }
 }
 
 __device__ __forceinline__ void store4(float *dst, float4 v) { *reinterpret_cast<float4 *>(dst) = v; }
@@ -141,33 +153,49 @@ __device__ __forceinline__ void tile_step(const AttendParams &P, Rows<NC> &R, co
 }
 
 // The warps' share of copying one tile in: eight keys a warp.
-template <typename E>
+template <typename C>
 __device__ __forceinline__ void load_tile(const AttendParams &P, const Segment &s, float *sK, float *sV, int x0, int warp,
                                           int lane) {
-    constexpr int V = 16 / sizeof(E);
+    constexpr int V = 16 / sizeof(C);
+    constexpr bool kScaled = sizeof(C) == 1;
     const int D = P.D, per = D / V;
     int64_t off = -1;
+    float ks = 1.0f, vs = 1.0f;
     const int x = x0 + warp * 8 + lane;
     if (lane < 8 && item_sees(P, s.keys, x)) {
         const int32_t *table = s.req < 0 ? P.shared_table : P.block_table + static_cast<int64_t>(s.req) * P.max_blocks;
         off = slot_offset(P, table, x);
-        if (off >= 0) off += static_cast<int64_t>(s.head) * P.head_stride;
+        if (off >= 0) {
+            off += static_cast<int64_t>(s.head) * P.head_stride;
+            if constexpr (kScaled) {
+                const int64_t at = static_cast<int64_t>(table[P.by_page(x)]) * P.Hkv + s.head;
+                ks = P.k_scale[at];
+                vs = P.v_scale[at];
+            }
+        }
     }
-    const E *kc = static_cast<const E *>(P.k_cache), *vc = static_cast<const E *>(P.v_cache);
+    const C *kc = static_cast<const C *>(P.k_cache), *vc = static_cast<const C *>(P.v_cache);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int64_t o = __shfl_sync(0xffffffffu, off, j);
+        const float k_by = kScaled ? __shfl_sync(0xffffffffu, ks, j) : 1.0f, v_by = kScaled ? __shfl_sync(0xffffffffu, vs, j) : 1.0f;
         if (o < 0) continue;  // seen by no row (or its request is in error): never used
         const int key = warp * 8 + j;
         for (int c = lane; c < per; c += kWarp) {
             if (!SPEC_IN(o + c * V + V - 1, cache_extent(P), DBG_CACHE)) continue;
-            bring(sK + key * (D + 4) + c * V, kc + o + c * V);
-            bring(sV + key * D + c * V, vc + o + c * V);
+            if constexpr (kScaled) {
+                bring(sK + key * (D + 4) + c * V, kc + o + c * V, k_by);
+                bring(sV + key * D + c * V, vc + o + c * V, v_by);
+            } else {
+                bring(sK + key * (D + 4) + c * V, kc + o + c * V);
+                bring(sV + key * D + c * V, vc + o + c * V);
+            }
         }
     }
 }
 
-template <typename E, int NC, bool PREFIX>
+// E: the type of the rows; C: the cache's.
+template <typename E, typename C, int NC, bool PREFIX>
 __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendParams P) {
     extern __shared__ float4 smem4[];
     float *sQ = reinterpret_cast<float *>(smem4);
@@ -210,12 +238,12 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
                 }
             }
         }
-        if (s.ntile > 0) load_tile<E>(P, s, sK, sV, tile_begin<kKT>(s.keys, s.tile), warp, lane);
+        if (s.ntile > 0) load_tile<C>(P, s, sK, sV, tile_begin<kKT>(s.keys, s.tile), warp, lane);
         copy_commit();
         for (int t = 0; t < s.ntile; ++t) {
             const int b = t & 1;
             if (t + 1 < s.ntile)
-                load_tile<E>(P, s, sK + (b ^ 1) * kKT * (D + 4), sV + (b ^ 1) * kKT * D,
+                load_tile<C>(P, s, sK + (b ^ 1) * kKT * (D + 4), sV + (b ^ 1) * kKT * D,
                              tile_begin<kKT>(s.keys, s.tile + t + 1), warp, lane);
             copy_commit();
             copy_wait<1>();

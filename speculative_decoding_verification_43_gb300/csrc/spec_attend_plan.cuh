@@ -41,6 +41,7 @@ struct AttendParams {
     int32_t max_blocks, n_pages, window, n_sink, shared_len;
     float scale_log2;  // scale * log2(e): the softmax is taken in base 2
     const void *q, *k_cache, *v_cache;
+    const float *k_scale, *v_scale;  // [n_pages][Hkv], a cache in 8 bits
     int64_t q_stride, page_stride, slot_stride, head_stride;
     const int32_t *row_off, *kv_len, *block_table, *shared_table;
     void *out;

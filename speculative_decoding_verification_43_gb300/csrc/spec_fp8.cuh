@@ -1,0 +1,40 @@
+// Values in 8 bits (e4m3: sign, four bits of exponent, three of mantissa; largest 448, least 2^-9, no infinity)
+// and the scales of a cache that holds them.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+namespace spec {
+
+constexpr float kE4m3Max = 448.0f;
+// The least scale that is set: a block of zeros has it, and so have values below 2^-52.
+constexpr int kLeastScaleLog2 = -60;
+
+// Two e4m3 (the first in the lower byte) as fp32; exact.
+__device__ __forceinline__ float2 e4m3_to_float2(uint16_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+    return __half22float2(reinterpret_cast<const __half2 &>(h));
+}
+__device__ __forceinline__ float4 e4m3_to_float4(uint32_t v) {
+    const float2 a = e4m3_to_float2(static_cast<uint16_t>(v)), b = e4m3_to_float2(static_cast<uint16_t>(v >> 16));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+// Two fp32 rounded to e4m3, `lo` in the lower byte. Beyond the largest: the largest; NaN: NaN.
+__device__ __forceinline__ uint16_t to_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The least power of two s with top <= 448 s, at least 2^kLeastScaleLog2. top is finite and not negative:
+// 448 = 1.75 * 2^8, so s = 2^(e-8) for top = f 2^e with 1 <= f <= 1.75, and 2^(e-7) for f above.
+__device__ __forceinline__ float e4m3_scale(float top) {
+    const uint32_t bits = __float_as_uint(top);
+    const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float(static_cast<uint32_t>(max(e, kLeastScaleLog2) + 127) << 23);
+}
+
+}  // namespace spec

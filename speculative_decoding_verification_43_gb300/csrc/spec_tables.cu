@@ -1,0 +1,330 @@
+// Block tables and slot maps from the requests' lengths (spec_block_tables). See include/spec_tables.h for the
+// contract.
+//
+// With B_i and P_i the pages that the requests before i give back and need, and B the pages given back in all,
+// everything has its place without a loop over the requests: block b of the `have` that request i holds goes to
+// entry n_free + (B - B_i - back_i) + (have - 1 - b) of the stack, and its new block number j is entry
+// n_free + B - 1 - P_i - j. An entry at or above n_free is itself one that comes back in this call: it is looked up
+// where it lies, so that no thread waits for another's write.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "spec_device.cuh"
+#include "spec_paged.cuh"
+#include "spec_tables.h"
+
+namespace spec {
+
+// What is known of the requests once their lengths have been added up, in shared memory or in the workspace.
+struct TableBooks {
+    int32_t *fresh, *back;  // [B+1] entries that the requests before i get, and give back
+    int32_t *take;          // [B] pages that the requests before i take
+    int32_t *held, *need;   // [B] entries before and after; both 0 for a request in error
+    int32_t *all;           // n_free before, pages given back, a request's offsets are wrong
+};
+
+struct TableParams {
+    int32_t B, T, page_size, max_blocks, n_pages, n_shared;
+    FastDiv by_page;
+    const int32_t *kv_len, *row_off, *shared_table;
+    int32_t *n_blocks, *block_table, *free_pages, *n_free;
+    int32_t *slot_map, *positions, *req_status;
+    TableBooks books;  // in the workspace (unused by the single block)
+};
+
+constexpr int kTableThreads = 1024, kTableWarps = kTableThreads / kWarp;
+constexpr int kTableOne = 1024;      // requests that one block keeps the books of in shared memory,
+constexpr int kTableOneRows = 4096;  // and rows that it goes through by itself
+constexpr int kFillThreads = 256;
+
+// A request's pages: what it holds, shall hold, takes and gives back.
+struct TableRequest {
+    int held, need, take, back, status;
+};
+__device__ __forceinline__ TableRequest table_request(const TableParams &P, int i) {
+    TableRequest r = {P.n_blocks[i], 0, 0, 0, SPEC_REQ_OK};
+    const int kv = P.kv_len[i];
+    if (kv < 0 || r.held < 0 || r.held > P.max_blocks) {
+        r.status = SPEC_REQ_BAD_SHAPE;
+    } else {
+        r.need = P.by_page(kv) + (kv % P.page_size != 0);
+        if (r.need > P.max_blocks) r.status = SPEC_REQ_BAD_BLOCKS;
+    }
+    if (r.status != SPEC_REQ_OK) {
+        r.need = r.held;
+        return r;
+    }
+    const int have = max(r.held - P.n_shared, 0), want = max(r.need - P.n_shared, 0);
+    r.take = max(want - have, 0);
+    r.back = max(have - want, 0);
+    return r;
+}
+
+// The sums of three numbers over the block's threads before each, and of all in `total`.
+__device__ __forceinline__ int3 block_sums(int3 v, int3 &total, int3 *warps) {
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    int3 s = v;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, s.x, o), y = __shfl_up_sync(0xffffffffu, s.y, o),
+                  z = __shfl_up_sync(0xffffffffu, s.z, o);
+        if (lane >= o) s = make_int3(s.x + x, s.y + y, s.z + z);
+    }
+    __syncthreads();  // the last call's sums have been read
+    if (lane == kWarp - 1) warps[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int3 w = warps[lane];
+#pragma unroll
+        for (int o = 1; o < kWarp; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o),
+                      z = __shfl_up_sync(0xffffffffu, w.z, o);
+            if (lane >= o) w = make_int3(w.x + x, w.y + y, w.z + z);
+        }
+        warps[lane] = w;
+    }
+    __syncthreads();
+    total = warps[kTableWarps - 1];
+    const int3 before = warp > 0 ? warps[warp - 1] : make_int3(0, 0, 0);
+    return make_int3(before.x + s.x - v.x, before.y + s.y - v.y, before.z + s.z - v.z);
+}
+
+// The last request i < n with sums[i] <= x (sums[0] = 0).
+__device__ __forceinline__ int find_sum(const int32_t *sums, int n, int x) {
+    int lo = 0;
+#pragma unroll 1
+    while (n > 1) {
+        const int half = n / 2;
+        if (sums[lo + half] <= x) {
+            lo += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    return lo;
+}
+
+// Page of entry b of request i after the call, for b below its need.
+__device__ __forceinline__ int table_entry(const TableParams &P, const TableBooks &K, int i, int b) {
+    const int held = K.held[i];
+    if (b < held) return P.block_table[static_cast<int64_t>(i) * P.max_blocks + b];
+    if (b < P.n_shared) return P.shared_table[b];
+    const int n_free = K.all[0], back = K.all[1];
+    const int x = n_free + back - 1 - K.take[i] - (b - max(held, P.n_shared));
+    if (!SPEC_IN(x, P.n_pages, DBG_CACHE)) return -1;
+    if (x < n_free) return P.free_pages[x];
+    // it comes back in this call: the (x - n_free)-th from the end of what the requests give back
+    const int z = back - 1 - (x - n_free), r = find_sum(K.back, P.B, z);
+    return P.block_table[static_cast<int64_t>(r) * P.max_blocks + max(K.need[r], P.n_shared) + (z - K.back[r])];
+}
+
+// The tables' new entries, the pages given back, and the rows, by threads first, first + step, ..
+__device__ __forceinline__ void table_fill(const TableParams &P, const TableBooks &K, const int32_t *row_off, int first,
+                                           int step) {
+    // rows first: theirs is the longer chain
+#pragma unroll 1
+    for (int r = first; r < P.T; r += step) {
+        const int i = find_request(row_off, P.B, P.T, r);
+        const int r0 = row_off[i], r1 = row_off[i + 1], kv = P.kv_len[i];
+        if (!offsets_right(r0, r1, P.T) || r < r0 || r >= r1) continue;
+        if (K.all[2] && offsets_contradict(row_off, P.B, P.T, i, r0, r1, 0, 1)) continue;
+        const int64_t at = static_cast<int64_t>(kv) - (r1 - r0) + (r - r0);
+        const int p = kv < 0 || at < 0 ? -1 : static_cast<int>(at), b = p < 0 ? 0 : P.by_page(p);
+        int slot = -1;
+        if (p >= 0 && b < K.need[i]) {
+            const int page = table_entry(P, K, i, b);
+            if (page >= 0 && page < P.n_pages) slot = page * P.page_size + (p - b * P.page_size);
+        }
+        if (!SPEC_IN(r, P.T, DBG_OUT_ROWS)) continue;
+        if (P.slot_map) P.slot_map[r] = slot;
+        if (P.positions) P.positions[r] = p;
+    }
+    const int fresh = K.fresh[P.B], back = K.all[1];
+#pragma unroll 1
+    for (int e = first; e < fresh; e += step) {
+        const int i = find_sum(K.fresh, P.B, e), b = K.held[i] + (e - K.fresh[i]);
+        if (b < K.need[i] && SPEC_IN(b, P.max_blocks, DBG_CACHE))
+            P.block_table[static_cast<int64_t>(i) * P.max_blocks + b] = table_entry(P, K, i, b);
+    }
+#pragma unroll 1
+    for (int z = first; z < back; z += step) {
+        const int i = find_sum(K.back, P.B, z);
+        const int x = K.all[0] + back - 1 - z;
+        if (SPEC_IN(x, P.n_pages, DBG_CACHE))
+            P.free_pages[x] = P.block_table[static_cast<int64_t>(i) * P.max_blocks + max(K.need[i], P.n_shared) +
+                                            (z - K.back[i])];
+    }
+}
+
+// One block keeps the books: sums over the requests, what the stack can serve, counts and status. ONE: it goes
+// through entries and rows too. Bound by the chain lengths -> sums -> entries -> pages -> stores.
+template <bool ONE>
+__global__ void __launch_bounds__(kTableThreads) spec_tables_kernel(const __grid_constant__ TableParams P) {
+    __shared__ int3 warps[kTableWarps];
+    __shared__ int32_t mine[ONE ? 6 * (kTableOne + 1) + 3 : 3];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x;
+    TableBooks K = P.books;
+    const int32_t *row_off = P.row_off;
+    if constexpr (ONE) {
+        constexpr int n = kTableOne + 1;
+        K = {mine, mine + n, mine + 2 * n, mine + 3 * n, mine + 4 * n, mine + 6 * n};
+        if (P.T > 0) {
+            for (int i = tid; i <= P.B; i += kTableThreads) mine[5 * n + i] = P.row_off[i];
+            row_off = mine + 5 * n;
+        }
+    }
+    const int n_free = *P.n_free;
+    // what comes back in all, and whether some offsets are wrong
+    bool wrong = false;
+    int3 carry = make_int3(0, 0, 0), total;
+#pragma unroll 1
+    for (int i0 = 0; i0 < P.B; i0 += kTableThreads) {
+        const int i = i0 + tid;
+        int3 v = make_int3(0, 0, 0);
+        if (i < P.B) {
+            v.x = table_request(P, i).back;
+            if (P.T > 0) wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
+        }
+        block_sums(v, total, warps);
+        carry.x += total.x;
+    }
+    const bool broken = __syncthreads_or(wrong) != 0;
+    const bool pool = n_free >= 0 && n_free <= P.n_pages, room = pool && carry.x <= P.n_pages - n_free;
+    const int back = room ? carry.x : 0, avail = pool ? n_free + back : 0;
+    carry = make_int3(0, 0, 0);
+    int taken = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < P.B; i0 += kTableThreads) {
+        const int i = i0 + tid;
+        TableRequest r = {};
+        if (i < P.B) {
+            r = table_request(P, i);
+            if (r.back > 0 && !room) {
+                r.status = SPEC_REQ_BAD_BLOCKS;
+                r.need = r.held;
+                r.back = 0;
+            }
+        }
+        const int3 s = block_sums(make_int3(r.take, r.back, max(r.need - r.held, 0)), total, warps);
+        if (i < P.B) {
+            const int before = carry.x + s.x;
+            K.take[i] = before;
+            K.back[i] = carry.y + s.y;
+            K.fresh[i] = carry.z + s.z;
+            if (r.take > 0) {
+                if (before + r.take > avail)
+                    r.status = SPEC_REQ_BAD_BLOCKS;
+                else
+                    taken = before + r.take;
+            }
+            K.held[i] = r.status == SPEC_REQ_OK ? r.held : 0;
+            K.need[i] = r.status == SPEC_REQ_OK ? r.need : 0;
+            if (P.T > 0 && !offsets_right(P.row_off[i], P.row_off[i + 1], P.T)) r.status |= SPEC_REQ_BAD_SHAPE;
+            if (broken && !(r.status & SPEC_REQ_BAD_SHAPE) &&
+                offsets_contradict(P.row_off, P.B, P.T, i, P.row_off[i], P.row_off[i + 1], 0, 1))
+                r.status |= SPEC_REQ_BAD_SHAPE;
+            if (P.req_status && SPEC_IN(i, P.B, DBG_OUT_REQS)) P.req_status[i] = r.status;
+        }
+        carry = make_int3(carry.x + total.x, carry.y + total.y, carry.z + total.z);
+    }
+    if (tid == 0) {
+        K.back[P.B] = carry.y;
+        K.fresh[P.B] = carry.z;
+        K.all[0] = pool ? n_free : 0;
+        K.all[1] = back;
+        K.all[2] = broken;
+    }
+    // the pages taken: up to the last request that has been served
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    __syncthreads();
+    if (tid % kWarp == 0) warps[tid / kWarp].x = taken;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll 1
+        for (int w = 0; w < kTableWarps; ++w) taken = max(taken, warps[w].x);
+        if (pool) *P.n_free = avail - taken;
+    }
+    if constexpr (ONE) table_fill(P, K, row_off, tid, kTableThreads);
+    // (a request's own count is read by its own thread, above)
+#pragma unroll 1
+    for (int i = tid; i < P.B; i += kTableThreads)
+        if (K.need[i] != K.held[i]) P.n_blocks[i] = K.need[i];
+}
+
+__global__ void __launch_bounds__(kFillThreads) spec_tables_fill_kernel(const __grid_constant__ TableParams P) {
+    griddep_launch_dependents();
+    griddep_wait();
+    table_fill(P, P.books, P.row_off, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
+}
+
+static spec_status table_sizes(const spec_block_tables_args *a) {
+    if (!a) return SPEC_ERR_INVALID_ARG;
+    if (a->B < 1 || a->total_rows < 0 || a->page_size < 1 || a->max_blocks < 1 || a->n_pages < 1 || a->n_shared < 0 ||
+        a->n_shared > a->max_blocks)
+        return SPEC_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(a->B) * a->max_blocks > INT_MAX || static_cast<int64_t>(a->n_pages) * a->page_size > INT_MAX)
+        return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+static bool one_block(const spec_block_tables_args *a) { return a->B <= kTableOne && a->total_rows <= kTableOneRows; }
+
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t spec_block_tables_workspace_size(const spec_block_tables_args *a) {
+    if (table_sizes(a) != SPEC_OK) return 0;
+    return (static_cast<size_t>(a->B) + 1) * 5 * sizeof(int32_t) + 256;
+}
+
+extern "C" spec_status spec_block_tables(const spec_block_tables_args *a, void *workspace, size_t workspace_bytes,
+                                         cudaStream_t stream) {
+    const spec_status st = table_sizes(a);
+    if (st != SPEC_OK) return st;
+    if (!a->kv_len || !a->n_blocks || !a->block_table || !a->free_pages || !a->n_free) return SPEC_ERR_INVALID_ARG;
+    if ((a->total_rows > 0 && !a->row_off) || (a->n_shared > 0 && !a->shared_table)) return SPEC_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < spec_block_tables_workspace_size(a) ||
+        reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return SPEC_ERR_WORKSPACE;
+    TableParams P = {};
+    P.B = a->B;
+    P.T = a->total_rows;
+    P.page_size = a->page_size;
+    P.max_blocks = a->max_blocks;
+    P.n_pages = a->n_pages;
+    P.n_shared = a->n_shared;
+    P.by_page = FastDiv(a->page_size);
+    P.kv_len = a->kv_len;
+    P.row_off = a->row_off;
+    P.shared_table = a->shared_table;
+    P.n_blocks = a->n_blocks;
+    P.block_table = a->block_table;
+    P.free_pages = a->free_pages;
+    P.n_free = a->n_free;
+    P.slot_map = a->slot_map;
+    P.positions = a->positions;
+    P.req_status = a->req_status;
+    int32_t *w = static_cast<int32_t *>(workspace);
+    const int n = P.B + 1;
+    P.books = {w, w + n, w + 2 * n, w + 3 * n, w + 4 * n, w + 5 * n};
+    if (one_block(a))
+        return launch_after(spec_tables_kernel<true>, dim3(1), dim3(kTableThreads), 0, stream, P) == cudaSuccess
+                   ? SPEC_OK
+                   : SPEC_ERR_CUDA;
+    cudaError_t e = launch_after(spec_tables_kernel<false>, dim3(1), dim3(kTableThreads), 0, stream, P);
+    if (e == cudaSuccess) e = launch_after(spec_tables_fill_kernel, dim3(2 * 152), dim3(kFillThreads), 0, stream, P);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+#ifdef SPEC_DEBUG
+namespace spec {
+// The debug words of this translation unit's kernels.
+cudaError_t debug_take_tables(unsigned int out[4]) { return spec_dbg_take(out); }
+}  // namespace spec
+#endif

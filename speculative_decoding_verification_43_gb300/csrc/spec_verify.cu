@@ -255,14 +255,19 @@ namespace spec {
 cudaError_t debug_take_compact(unsigned int out[4]);
 cudaError_t debug_take_append(unsigned int out[4]);
 cudaError_t debug_take_attend(unsigned int out[4]);
+cudaError_t debug_take_append8(unsigned int out[4]);
+cudaError_t debug_take_attend8(unsigned int out[4]);
+cudaError_t debug_take_tables(unsigned int out[4]);
 }
 
 extern "C" spec_status spec_debug_fetch(unsigned int *out) {
     if (!out) return SPEC_ERR_INVALID_ARG;
-    unsigned int w[4][4] = {};
+    unsigned int w[7][4] = {};
     if (cudaDeviceSynchronize() != cudaSuccess) return SPEC_ERR_CUDA;
     if (spec::spec_dbg_take(w[0]) != cudaSuccess || spec::debug_take_compact(w[1]) != cudaSuccess ||
-        spec::debug_take_append(w[2]) != cudaSuccess || spec::debug_take_attend(w[3]) != cudaSuccess)
+        spec::debug_take_append(w[2]) != cudaSuccess || spec::debug_take_attend(w[3]) != cudaSuccess ||
+        spec::debug_take_append8(w[4]) != cudaSuccess || spec::debug_take_attend8(w[5]) != cudaSuccess ||
+        spec::debug_take_tables(w[6]) != cudaSuccess)
         return SPEC_ERR_CUDA;
     for (int k = 0; k < 4; ++k) out[k] = 0u;
     for (const auto &u : w) {
