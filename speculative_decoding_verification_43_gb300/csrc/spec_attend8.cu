@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "spec_attend8_round.cuh"
+#include "spec_attend8_tiles.cuh"
 #include "spec_attend_fma.cuh"
 #include "spec_attend_host.cuh"
 #include "spec_attend_plan.cuh"
@@ -23,10 +25,109 @@ static spec_status attend8_sizes(const spec_attend8_args *a, AttendParams &P) {
     return a->attend.head_dim % 16 == 0 ? SPEC_OK : SPEC_ERR_UNSUPPORTED;
 }
 
+// Rows of an item (as a power of two) and workers for `rows` packed rows of a head over `groups` requests on the
+// tensor cores.
+static void tensor8_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
+    rt_log2 = rows <= 24 * groups ? 5 : 6;
+    workers = kSMs * round8::kPerSM;
+}
+
+// Time of an item beside its tiles, in tiles.
+static int extra8_units(int rt_log2) { return 4; }
+
 // Workers and parts of the kernels that serve the call.
 static void attend8_work(AttendParams &P, bool tensor) {
-    attend_fma_work(P);
+    const int64_t head_rows = static_cast<int64_t>(P.T) * P.G;
+    if (tensor) {
+        tensor8_class(head_rows, P.B, P.own_rt_log2, P.own_workers);
+        tensor8_class(head_rows, 1, P.prefix_rt_log2, P.prefix_workers);
+        P.own_extra = extra8_units(P.own_rt_log2);
+        P.prefix_extra = extra8_units(P.prefix_rt_log2);
+        P.box_log2 = box_log2_of(P.page_size);
+    } else {
+        attend_fma_work(P);
+    }
     attend_parts(P);
+}
+
+// Whether the tensor cores may serve a call of these sizes; strides apart.
+static bool tensor8_sizes(const spec_attend8_args *a) {
+    return a->attend.dtype == SPEC_BF16 && a->attend.head_dim <= 128 && box_log2_of(a->attend.page_size) > 0;
+}
+
+// The cache as three-dimensional tensor maps (head_dim x heads x slots), where its strides allow it: pages a whole
+// number of slots apart, heads inside a slot or a whole number of slots apart. What a tile's rows have beyond
+// head_dim comes as zeros, not as the next head's elements.
+struct CacheShape {
+    int64_t heads, head_stride, rows;
+};
+static bool cache_map8(const spec_attend8_args *args, tiles8::CacheMap &M, CacheShape &shape) {
+    const spec_attend_args *a = &args->attend;
+    if (!tensor8_sizes(args)) return false;
+    const int64_t slot = a->slot_stride, D = a->head_dim, heads = a->n_kv_heads;
+    if (slot <= 0 || (a->n_pages > 1 && a->page_stride % slot != 0)) return false;
+    const int64_t page_rows = a->n_pages > 1 ? a->page_stride / slot : 0;
+    int64_t head_rows = 0;
+    shape = {1, slot, 0};
+    M.head_step = 0;
+    if (heads > 1 && a->head_stride >= D && (heads - 1) * a->head_stride + D <= slot) {
+        shape.heads = heads;
+        shape.head_stride = a->head_stride;
+        M.head_step = 1;
+    } else if (D <= slot && (heads == 1 || (a->head_stride > 0 && a->head_stride % slot == 0))) {
+        head_rows = heads > 1 ? a->head_stride / slot : 0;
+    } else {
+        return false;
+    }
+    shape.rows = (a->n_pages - 1) * page_rows + (heads - 1) * head_rows + a->page_size;
+    if (shape.rows > INT_MAX / 2 || slot >= (1ll << 40) || shape.head_stride >= (1ll << 40)) return false;
+    M.page_rows = static_cast<int32_t>(page_rows);
+    M.head_rows = static_cast<int32_t>(head_rows);
+    return page_rows <= INT_MAX / 2 && head_rows <= INT_MAX / 2;
+}
+static bool encode_map8(CUtensorMap &map, const void *cache, const CacheShape &shape, const spec_attend_args *a, int box_rows) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a->head_dim), static_cast<cuuint64_t>(shape.heads),
+                                static_cast<cuuint64_t>(shape.rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(shape.head_stride), static_cast<cuuint64_t>(a->slot_stride)};
+    const cuuint32_t box[3] = {128, 1, static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct CacheMaps8 {
+    tiles8::CacheMap where;
+    CUtensorMap k, v;
+};
+
+template <typename Kernel>
+static cudaError_t launch_tensor8(Kernel *kernel, int ctas, int threads, int smem, int stages, const AttendParams &P,
+                                  const CacheMaps8 &M, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_after(kernel, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
+                        static_cast<size_t>(smem), stream, P, M.where, M.k, M.v, stages);
+}
+
+// One class of items on the tensor cores.
+template <bool PREFIX>
+static cudaError_t launch_class8(const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
+    const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2, workers = PREFIX ? P.prefix_workers : P.own_workers;
+    if (rt_log2 == 5)
+        return launch_tensor8(round8::spec_attend8_round_kernel<32, PREFIX>, workers, round8::kThreads,
+                              round8::smem_bytes<32>(), round8::stages<32>(), P, M, stream);
+    return launch_tensor8(round8::spec_attend8_round_kernel<64, PREFIX>, workers, round8::kThreads,
+                          round8::smem_bytes<64>(), round8::stages<64>(), P, M, stream);
+}
+
+static cudaError_t enqueue_tensor8(const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    if (P.shared_len > 0) e = launch_class8<true>(P, M, stream);
+    if (e == cudaSuccess) e = launch_class8<false>(P, M, stream);
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, tiles8::kKT>(P, stream);
+    return e;
 }
 
 template <typename E, int NC, bool PREFIX>
@@ -56,14 +157,20 @@ using namespace spec;
 extern "C" size_t spec_attend8_workspace_size(const spec_attend8_args *a) {
     AttendParams P = {};
     if (attend8_sizes(a, P) != SPEC_OK) return 0;
+    // either kernel may serve the call: which one follows from the strides
     attend8_work(P, false);
-    return attend_layout(P).total;
+    const size_t fma_bytes = attend_layout(P).total;
+    if (!tensor8_sizes(a)) return fma_bytes;
+    attend8_work(P, true);
+    return std::max(fma_bytes, attend_layout(P).total);
 }
 
 extern "C" const char *spec_attend8_plan(const spec_attend8_args *a) {
     AttendParams P = {};
     if (attend8_sizes(a, P) != SPEC_OK) return nullptr;
-    return "spec_attend_fma_kernel";
+    tiles8::CacheMap M = {};
+    CacheShape shape = {};
+    return cache_map8(a, M, shape) ? "spec_attend8_round_kernel" : "spec_attend_fma_kernel";
 }
 
 extern "C" spec_status spec_attend8(const spec_attend8_args *a, void *workspace, size_t workspace_bytes,
@@ -76,10 +183,20 @@ extern "C" spec_status spec_attend8(const spec_attend8_args *a, void *workspace,
     if (st != SPEC_OK) return st;
     P.k_scale = a->k_scale;
     P.v_scale = a->v_scale;
-    attend8_work(P, false);
+    CacheMaps8 M = {};
+    CacheShape shape = {};
+    const bool tensor = cache_map8(a, M.where, shape);
+    attend8_work(P, tensor);
     if (!workspace || workspace_bytes < spec_attend8_workspace_size(a) || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
         return SPEC_ERR_WORKSPACE;
     attend_place(P, workspace);
+    if (tensor) {
+        const int box = 1 << P.box_log2;
+        if (!encode_map8(M.k, a->attend.k_cache, shape, &a->attend, box) ||
+            !encode_map8(M.v, a->attend.v_cache, shape, &a->attend, box))
+            return SPEC_ERR_CUDA;
+        return enqueue_tensor8(P, M, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    }
     const cudaError_t e =
         a->attend.dtype == SPEC_BF16 ? enqueue_fma8<__nv_bfloat16>(P, stream) : enqueue_fma8<float>(P, stream);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

@@ -1,0 +1,636 @@
+// Attention of few rows over the cache in 8 bits on the tensor cores (bf16 rows, head sizes that are multiples of 16
+// up to 128): a verification round, single tokens. The work is laid out as in spec_attend_round.cuh: positions and
+// output columns along the lanes, the item's rows along the columns,
+//   S^T = K Q^T     K as it lies in the cache, Q in two parts (spec_attend8_tiles.cuh)
+//   O^T += V^T P^T  V as it lies in the cache, P in three parts, each with rows of RT bytes a position
+// Half the bytes of bf16 make the time between two tiles half as long, while the products take 20 instructions a
+// tile instead of 16, of 42 cycles each (a product's time follows its 128 lanes until it has 64 columns). So one
+// warp issues them together (a single thread took 126 cycles an instruction to issue them).
+//
+// Scales. A thread has one position: its key's scale is one factor of all its scores, and a row's factor (the
+// query's own scale, the softmax's and log2 e) comes from shared memory beside the row's reference. The value's
+// scale v goes into the weight, w = 2^(z + log2 v - reference), so that the weights' range follows what they
+// contribute; the row's sum takes w / v. The reference puts the first tile's largest weight at 2^11, and is renewed
+// when one passes 2^15: e5m2 holds weights from 2^15 down to 2^-16, that is 2^-27 of the reference.
+#pragma once
+
+#include "spec_attend8_tiles.cuh"
+
+namespace spec {
+namespace round8 {
+
+using namespace tiles8;
+
+constexpr int kThreads = 192, kPerSM = 2, kStages = 5;
+constexpr float kTop = 11.0f;  // log2 of the largest weight under a new reference, and of what may be reached
+constexpr float kMost = 15.0f; // before the next
+
+template <int RT>
+struct Shared {
+    Pipe<kStages> pipe;
+    uint64_t q_full, s_full[2], p_full, o_done, agree, drain;
+    uint32_t found[2][4];  // per warp: a score beyond the reference (1), a value that is not finite (2)
+    uint32_t skip;         // the warpgroup has done this tile's second product itself
+    uint32_t tmem;
+    // of this segment's rows and the next one's, in turn
+    int pos[2][RT];                 // positions (-1: none)
+    alignas(16) float nref[2][RT];  // minus the reference; kNoRef before there is one (read four at a time)
+    alignas(16) float factor[2][RT];  // of the scores
+};
+// What the row operations of a warpgroup need now and then, in the weights' memory while that is unused.
+template <int RT>
+struct Scratch {
+    float warp[4][RT];
+    float row[RT];
+};
+// A reference that every finite score exceeds and that leaves -inf alone.
+constexpr float kNoRef = 3e38f;
+
+// Queries: two parts of 128 bytes a row; weights: three parts of a byte a row and position.
+__host__ __device__ constexpr int q_part(int RT) { return RT * 128; }
+__host__ __device__ constexpr int p_part(int RT) { return kKT * RT; }
+__host__ __device__ constexpr int q_bytes(int RT) { return 2 * q_part(RT); }
+__host__ __device__ constexpr int p_bytes(int RT) { return 3 * p_part(RT); }
+template <int RT>
+__host__ constexpr int stages() {
+    // 228 KB of shared memory, 1 KB of it taken per CTA
+    constexpr int n = (228 * 1024 / kPerSM - 1024 - static_cast<int>(sizeof(Shared<RT>)) - q_bytes(RT) - p_bytes(RT)) / kTile;
+    return n < kStages ? n : kStages;
+}
+template <int RT>
+__host__ constexpr int smem_bytes() {
+    return stages<RT>() * kTile + q_bytes(RT) + p_bytes(RT) + static_cast<int>(sizeof(Shared<RT>));
+}
+// (three tiles, so that what a slot held before is always known to have arrived: see the softmax's waits)
+static_assert(stages<32>() >= 3 && stages<64>() >= 3, "a tile of keys, one of values and the next tile's keys");
+static_assert(sizeof(Scratch<64>) <= p_bytes(64) && sizeof(Scratch<32>) <= p_bytes(32), "fits the weights' memory");
+
+// ---------------------------------------------------------------- matrix instructions (one warp)
+
+template <int RT>
+__device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, unsigned char *ring_mem,
+                                         unsigned char *q_tile, unsigned char *p_tile, int n_stages) {
+    int32_t *ab = &sh.pipe.abort;
+    const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * RT;
+    const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), ring_op = smem_operand(smem_addr(ring_mem), 16),
+                   p_op = RT == 64 ? smem_operand64(smem_addr(p_tile)) : smem_operand32(smem_addr(p_tile));
+    const int steps = (P.D + 31) / 32;
+    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    uint32_t q_phase = 0, p_phase = 0;
+    for (;;) {
+        if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
+        const Segment &s = sh.pipe.desc[desc.slot];
+        const int nrows = s.nrows, nt = s.ntile, first = s.tile;
+        const KeyTiles keys = s.keys;
+        if (nrows == 0) return;
+        if (nt > 0) {
+            const int n16 = (nrows + 15) & ~15;
+            const uint32_t qk_shape = mma8_shape(n16, false, false, false, false),
+                           pv_shape = mma8_shape(n16, false, true, true, true);
+            if (!wait_warp(ab, &sh.q_full, q_phase)) return;
+            q_phase ^= 1u;
+            // step t: tile t's product, and tile t + 1's scores (step -1: the first scores alone). The scores
+            // go first if their keys are there.
+#pragma unroll 1
+            for (int t = -1; t < nt; ++t) {
+                const bool more = t + 1 < nt;
+                const Ring v = ring;  // this tile's values; the next tile's keys follow them
+                if (t >= 0) ring.step();
+                const bool ahead = more && __all_sync(0xffffffffu, mbar_try_wait(&sh.pipe.full[ring.slot], ring.phase));
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    if (part == (ahead ? 0 : 1)) {
+                        if (!more) continue;
+                        if (!ahead && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                        tc_fence_after();
+                        const int b = (t + 1) & 1;  // S^T = K Q^T
+                        const uint64_t k = operand_at(ring_op, ring.slot * kTile);
+                        if (elect_lane()) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (i < steps)
+                                        mma8_ss(s_col + b * RT, operand_at(k, i * 32), operand_at(q_op, q * q_part(RT) + i * 32),
+                                                qk_shape, q + i > 0);
+                            mma_commit(&sh.s_full[b]);
+                            mma_commit(&sh.pipe.empty[ring.slot]);
+                        }
+                        __syncwarp();
+                    } else if (t >= 0) {
+                        if (!wait_warp(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                        if (!wait_warp(ab, &sh.p_full, p_phase)) return;
+                        p_phase ^= 1u;
+                        tc_fence_after();
+                        const bool take = !*reinterpret_cast<volatile uint32_t *>(&sh.skip);
+                        const uint64_t values = operand_at(ring_op, v.slot * kTile);
+                        const int n = tile_keys(keys, tile_begin<kKT>(keys, first + t));
+                        if (elect_lane()) {
+                            if (take) {  // O^T += V^T P^T
+#pragma unroll
+                                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (i * 32 < n)
+                                            mma8_ss(o_col, operand_at(values, i * 4096),
+                                                    operand_at(p_op, p * p_part(RT) + i * 32 * RT), pv_shape, t > 0 || p + i > 0);
+                            }
+                            mma_commit(&sh.o_done);
+                            mma_commit(&sh.pipe.empty[v.slot]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (more) ring.step();
+            }
+        }
+        if (elect_lane()) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        __syncwarp();
+        desc.step();
+    }
+}
+
+// ---------------------------------------------------------------- softmax (one position per thread)
+
+// The four warps meet; each leaves a word, and all get the words' union (-1: a wait gave up).
+__device__ __forceinline__ int meet(int32_t *abort, uint64_t *bar, uint32_t (*found)[4], uint32_t phase, uint32_t mine) {
+    const int warp = threadIdx.x / kWarp;
+    volatile uint32_t *words = found[phase];
+    __syncwarp();
+    if (threadIdx.x % kWarp == 0) {
+        words[warp] = mine;
+        mbar_arrive(bar);
+    }
+    if (!wait_warp(abort, bar, phase)) return -1;
+    return static_cast<int>(words[0] | words[1] | words[2] | words[3]);
+}
+// Out of line for the meetings that come once per item.
+__device__ __noinline__ int meet_far(int32_t *abort, uint64_t *bar, uint32_t (*found)[4], uint32_t phase, uint32_t mine) {
+    return meet(abort, bar, found, phase, mine);
+}
+template <int RT, bool FAR = true>
+__device__ __forceinline__ bool agree(Shared<RT> &sh, uint32_t &phase, uint32_t mine, uint32_t &all) {
+    const int r = FAR ? meet_far(&sh.pipe.abort, &sh.agree, sh.found, phase, mine)
+                      : meet(&sh.pipe.abort, &sh.agree, sh.found, phase, mine);
+    phase ^= 1u;
+    all = static_cast<uint32_t>(r);
+    return r >= 0;
+}
+
+// The second product of a tile with values that are not finite, on the fp32 units: thread d has output
+// column d, the weights lie in shared memory, O is complete up to the tile before.
+template <int RT>
+__device__ __noinline__ void mixed_tile(const AttendParams &P, const int *pos, uint32_t o_addr,
+                                        const unsigned char *v_tile, const unsigned char *p_tile, const KeyTiles &keys,
+                                        int x0, int n, int nrows, int d, bool first) {
+#pragma unroll 1
+    for (int r0 = 0; r0 < nrows; r0 += 16) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(o, o_addr + r0);
+        tmem_wait_ld();
+        if (first)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            const int x = x0 + k;
+            if (!item_sees(P, keys, x)) continue;
+            const float v = d < P.D ? tile_value(v_tile, k, d) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = r0 + e, p = r < nrows ? pos[r] : -1;
+                if (x <= p && (P.window == 0 || x > p - P.window || x < P.n_sink)) {
+                    const int piece = RT == 64 ? (r >> 4) ^ ((k >> 1) & 3) : (r >> 4) ^ ((k >> 2) & 1);
+                    const unsigned char *at = p_tile + k * RT + piece * 16 + (r & 15);
+                    const float w = e5m2_to_float(at[0]) + e5m2_to_float(at[p_part(RT)]) + e5m2_to_float(at[2 * p_part(RT)]);
+                    o[e] = fmaf(w, v, o[e]);
+                }
+            }
+        }
+        uint32_t ow[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e]);
+        __syncwarp();
+        tmem_st16(o_addr + r0, ow);
+        tmem_wait_st();
+    }
+}
+
+template <int RT, bool PREFIX>
+__device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &sh, unsigned char *ring_mem,
+                                             unsigned char *q_tile, unsigned char *p_tile, int n_stages) {
+    const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
+    int32_t *ab = &sh.pipe.abort;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t s_addr = sh.tmem + lanes, o_addr = s_addr + 2 * RT;
+    Scratch<RT> &scratch = *reinterpret_cast<Scratch<RT> *>(p_tile);
+    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    uint32_t s_phases = 0, o_phase = 0, a_phase = 0, word = 0;
+    int buf = 0;
+    // Brings a segment's queries: 128 / RT threads each row's (rows up to a multiple of 16: zeros), and its
+    // position.
+    auto bring = [&](const Segment &s, int to) {
+        constexpr int kPer = 128 / RT, kPieces = 16 / kPer;
+        const int r = tid / kPer, pr = s.row0 + r, j = P.by_group(pr), g = pr - j * P.G;
+        const int t = s.t0 + j, h = s.head * P.G + g;
+        const bool have = r < s.nrows && SPEC_IN(t, P.T, DBG_ATTEND);
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + t * P.q_stride +
+                                                           static_cast<int64_t>(h) * P.D);
+        uint4 x[kPieces];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int c = tid % kPer + i * kPer;
+            x[i] = have && c < P.D / 8 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            top = top_bits(top, x[i]);
+        }
+#pragma unroll
+        for (int o = 1; o < kPer; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t bits = max(top & 0xffffu, top >> 16);
+        const float qs = query_scale(bits), inv = 1.0f / qs;
+        if (r < ((s.nrows + 15) & ~15)) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int c = tid % kPer + i * kPer;
+                uint2 hi, lo;
+                split_query(x[i], inv, hi, lo);
+                unsigned char *at = q_tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+                *reinterpret_cast<uint2 *>(at) = hi;
+                *reinterpret_cast<uint2 *>(at + q_part(RT)) = lo;
+            }
+            if (tid % kPer == 0) {
+                int p = -1;
+                if (have) {
+                    if constexpr (PREFIX) {
+                        const ReqRows q = load_request(P, find_request(P.row_off, P.B, P.T, t));
+                        if (t >= q.r0 && t < q.r0 + q.n) p = q.kv - q.n + (t - q.r0);
+                    } else {
+                        p = s.base + j;
+                    }
+                }
+                sh.pos[to][r] = p;
+                sh.nref[to][r] = kNoRef;
+                sh.factor[to][r] = bits < 0x7f80u ? qs * P.scale_log2 : NAN;
+            }
+        }
+        if (s.ntile > 0) {
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.q_full);
+        }
+    };
+    bool first_segment = true;
+    for (;;) {
+        const Segment &s = sh.pipe.desc[desc.slot];
+        if (first_segment) {
+            if (!wait_warp(ab, &sh.pipe.desc_full[0], 0)) return;
+            if (s.nrows == 0) return;
+            bring(s, 0);
+            if (!agree(sh, a_phase, 0u, word)) return;
+            first_segment = false;
+        }
+        const int nrows = s.nrows, nt = s.ntile, n16 = (nrows + 15) & ~15;
+        const int *pos = sh.pos[buf];
+        float *nref = sh.nref[buf];
+        const float *factor = sh.factor[buf];
+
+        float2 l[RT / 2];  // this thread's share of the rows' sums
+#pragma unroll
+        for (int e = 0; e < RT / 2; ++e) l[e] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+            const int b = i & 1;
+            const int x0 = tile_begin<kKT>(s.keys, s.tile + i), n = tile_keys(s.keys, x0), x = x0 + tid;
+            const bool edge = edge_tile(P, s, x0);
+            const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
+            unsigned char *v_tile = ring_mem + v_slot * kTile;
+            uint32_t mine = 0u;
+            bool rested = i == 0;
+            auto rest = [&]() -> bool {
+                if (rested) return true;
+                rested = true;
+                if (!wait_warp(ab, &sh.o_done, o_phase)) return false;
+                o_phase ^= 1u;
+                tc_fence_after();
+                return true;
+            };
+            // The scales come with the values. A wait by parity tells this use of a slot from the one before only when
+            // that one is known to have arrived; in a ring of three slots or more it is: it held keys whose scores, or
+            // values whose product, have been waited for.
+            auto landed = [&]() -> bool {
+                return wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase);
+            };
+            if (edge) {
+                if (!landed()) return;
+                if (__any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid))) mine = 2u;
+                fence_proxy_async_smem();
+            }
+            if (!wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u)) return;
+            s_phases ^= 1u << b;
+            if (!edge && !landed()) return;
+            tc_fence_after();
+            // this position's scales (1 where no row sees it and none were copied)
+            const bool used = !edge || item_sees(P, s.keys, x);
+            const float2 by = used ? sh.pipe.scale[v_slot][tid >> P.box_log2] : make_float2(1.0f, 1.0f);
+            const ValueScale vs = value_scale(by.y);
+            const float2 kf = make_float2(by.x, by.x), vl = make_float2(vs.log2, vs.log2), vi = make_float2(vs.inv, vs.inv);
+            // this position's scores with 16 rows from row e on
+            auto read = [&](float *z, int e) {
+                tmem_ld16(z, s_addr + b * RT + e);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 16; y += 2) {
+                    const float2 m = mul2(make_float2(z[y], z[y + 1]), kf);
+                    z[y] = m.x;
+                    z[y + 1] = m.y;
+                }
+                if (edge) {
+                    const bool in = x >= s.keys.from && x < s.keys.hi, sink = x < P.n_sink;
+                    const int back = P.window > 0 ? P.window : INT_MAX;
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        const int p = pos[e + y];
+                        if (!(in && x <= p && (sink || p - x < back))) z[y] = -INFINITY;
+                    }
+                }
+            };
+            // 32 rows' scores stay in registers; 64 rows' would not, beside their sums, and are read anew
+            constexpr bool kHeld = RT == 32;
+            float held[kHeld ? RT : 16];
+            if constexpr (kHeld) {
+#pragma unroll
+                for (int e = 0; e < RT; e += 16)
+                    if (e < nrows) read(held + e, e);
+            }
+            auto scores = [&](int e) -> float * {
+                if constexpr (kHeld) return held + e;
+                read(held, e);
+                return held;
+            };
+            // the logarithms of four weights
+            auto against = [&](const float *z, int e, float2 &a, float2 &c) {
+                const float4 rf = *reinterpret_cast<const float4 *>(nref + e), fc = *reinterpret_cast<const float4 *>(factor + e);
+                a = fma2(make_float2(z[0], z[1]), make_float2(fc.x, fc.y), add2(make_float2(rf.x, rf.y), vl));
+                c = fma2(make_float2(z[2], z[3]), make_float2(fc.z, fc.w), add2(make_float2(rf.z, rf.w), vl));
+            };
+            if (i > 0) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < RT; e += 16)
+                    if (e < nrows) {
+                        const float *z = scores(e);
+#pragma unroll
+                        for (int y = 0; y < 16; y += 4) {
+                            float2 a, c;
+                            against(z + y, e + y, a, c);
+                            top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
+                        }
+                    }
+                mine |= __any_sync(0xffffffffu, top > kMost) ? 1u : 0u;
+                if (!agree<RT, false>(sh, a_phase, mine, word)) return;
+            } else {
+                word = 1u;  // the first references (the values' flag comes with their meetings)
+            }
+            if (!rest()) return;  // the product before this tile: the weights' memory is free, O at rest
+            if (word & 1u) {
+                // new references: the rows' maxima over the tile, where they are larger
+#pragma unroll
+                for (int e = 0; e < RT; e += 16)
+                    if (e < nrows) {
+                        const float *z = scores(e);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const float v = redux_max(fmaf(z[y], factor[e + y], vs.log2));
+                            if (lane == 0) scratch.warp[warp][e + y] = v;
+                        }
+                    }
+                if (!agree(sh, a_phase, 0u, word)) return;
+                if (tid < n16) {
+                    const float v = fmaxf(fmaxf(scratch.warp[0][tid], scratch.warp[1][tid]),
+                                          fmaxf(scratch.warp[2][tid], scratch.warp[3][tid]));
+                    const float old = nref[tid], nw = kTop - v;
+                    const bool grow = v != -INFINITY && (old == kNoRef || nw < old);
+                    // a row without weights so far has nothing to rescale
+                    scratch.row[tid] = grow && old != kNoRef ? ex2(nw - old) : 1.0f;
+                    if (grow) nref[tid] = nw;
+                }
+                if (!agree(sh, a_phase, mine & 2u, word)) return;
+                if (i > 0) {
+#pragma unroll
+                    for (int e = 0; e < RT; e += 2)
+                        if ((e & ~15) < nrows) {
+                            l[e / 2].x *= scratch.row[e];
+                            l[e / 2].y *= scratch.row[e + 1];
+                        }
+#pragma unroll 1
+                    for (int r0 = 0; r0 < nrows; r0 += 16) {
+                        float o[16];
+                        uint32_t ow[16];
+                        tmem_ld16(o, o_addr + r0);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * scratch.row[r0 + e]);
+                        tmem_st16(o_addr + r0, ow);
+                    }
+                    tmem_wait_st();
+                    const uint32_t keep = word;
+                    if (!agree(sh, a_phase, 0u, word)) return;  // the scratch has been read
+                    word = keep;
+                }
+            }
+            const bool skip = (word & 2u) != 0;
+            unsigned char *prow = p_tile + tid * RT;
+#pragma unroll
+            for (int e = 0; e < RT; e += 16)
+                if (e < nrows) {
+                    const float *z = scores(e);
+                    uint32_t pw[4][3];
+#pragma unroll
+                    for (int y = 0; y < 16; y += 4) {
+                        float2 a, c;
+                        against(z + y, e + y, a, c);
+                        a.x = ex2(a.x);
+                        a.y = ex2(a.y);
+                        c.x = ex2(c.x);
+                        c.y = ex2(c.y);
+                        if (edge) {
+                            // (the logarithm of a scale that is no number must not reach rows that do not see it)
+                            a.x = z[y] == -INFINITY ? 0.0f : a.x;
+                            a.y = z[y + 1] == -INFINITY ? 0.0f : a.y;
+                            c.x = z[y + 2] == -INFINITY ? 0.0f : c.x;
+                            c.y = z[y + 3] == -INFINITY ? 0.0f : c.y;
+                        }
+                        l[(e + y) / 2] = fma2(a, vi, l[(e + y) / 2]);
+                        l[(e + y) / 2 + 1] = fma2(c, vi, l[(e + y) / 2 + 1]);
+                        split_e5m2(a.x, a.y, c.x, c.y, pw[y / 4]);
+                    }
+                    const int piece = RT == 64 ? (e >> 4) ^ ((tid >> 1) & 3) : (e >> 4) ^ ((tid >> 2) & 1);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<uint4 *>(prow + p * p_part(RT) + piece * 16) =
+                            make_uint4(pw[0][p], pw[1][p], pw[2][p], pw[3][p]);
+                }
+            if (skip) {
+                if (!agree(sh, a_phase, 0u, word)) return;  // all weights are there
+                mixed_tile<RT>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
+            }
+            if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip) = skip;
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(&sh.p_full);
+            ring.step();
+            ring.step();
+        }
+        // the next segment's queries; this one's scores have all been taken
+        Ring then = desc;
+        then.step();
+        if (!wait_warp(ab, &sh.pipe.desc_full[then.slot], then.phase)) return;
+        const bool more = sh.pipe.desc[then.slot].nrows > 0;
+        if (more) bring(sh.pipe.desc[then.slot], buf ^ 1);
+        if (nt > 0) {
+            if (!wait_warp(ab, &sh.o_done, o_phase)) return;
+            o_phase ^= 1u;
+            tc_fence_after();
+        }
+        // the sums: over the lanes, lane x ending with row x (and 32 + x) of its chunk, then over the warps
+#pragma unroll
+        for (int c = 0; c < RT; c += 32) {
+            float v[32];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                v[2 * e] = l[c / 2 + e].x;
+                v[2 * e + 1] = l[c / 2 + e].y;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < o) {
+                        const float send = up ? v[e] : v[e + o], keep = up ? v[e + o] : v[e];
+                        v[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+            }
+            scratch.warp[warp][c + lane] = v[0];
+        }
+        if (!agree(sh, a_phase, 0u, word)) return;
+        if (tid < nrows) {
+            float sum = scratch.warp[0][tid] + scratch.warp[1][tid] + scratch.warp[2][tid] + scratch.warp[3][tid];
+            if (pos[tid] < 0) sum = 0.0f;  // padding
+            const bool none = sum == 0.0f;
+            const float m = none ? -INFINITY : -nref[tid];
+            if (s.part >= 0) {
+                // a sum that is not a number must reach the joined row, whatever the other parts' maxima
+                if (SPEC_IN(s.part + tid, P.part_rows, DBG_ATTEND))
+                    P.part_ml[s.part + tid] = make_float2(isnan(sum) ? INFINITY : m, sum);
+                scratch.row[tid] = none ? 0.0f : 1.0f;
+            } else {
+                const int j = P.by_group(s.row0 + tid), g = s.row0 + tid - j * P.G;
+                if (P.lse && SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
+                    P.lse[static_cast<int64_t>(s.t0 + j) * P.Hq + s.head * P.G + g] =
+                        none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+                scratch.row[tid] = none ? 0.0f : 1.0f / sum;
+            }
+        }
+        if (!agree(sh, a_phase, 0u, word)) return;
+#pragma unroll 1
+        for (int r0 = 0; r0 < nrows; r0 += 4) {
+            float o[4];
+            __syncwarp();
+            if (nt > 0) {
+                tmem_ld4(o, o_addr + r0);
+                tmem_wait_ld();
+            }
+            if (tid < P.D) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = r0 + e;
+                    if (r >= nrows) break;
+                    const float a = scratch.row[r], y = a == 0.0f ? 0.0f : o[e] * a;
+                    if (s.part >= 0) {
+                        if (SPEC_IN(s.part + r, P.part_rows, DBG_ATTEND)) P.part_o[(s.part + r) * P.D + tid] = y;
+                    } else {
+                        const int j = P.by_group(s.row0 + r), g = s.row0 + r - j * P.G;
+                        if (SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
+                            static_cast<__nv_bfloat16 *>(P.out)[(s.t0 + j) * P.out_stride + (s.head * P.G + g) * P.D + tid] =
+                                __float2bfloat16_rn(y);
+                    }
+                }
+            }
+        }
+        // (the next segment meets at least once before it writes where slower warps may still read)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        if (!more) return;
+        desc = then;
+        buf ^= 1;
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int RT, bool PREFIX>
+__global__ void __launch_bounds__(kThreads, kPerSM)
+    spec_attend8_round_kernel(const __grid_constant__ AttendParams P, const CacheMap M,
+                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                             const int n_stages) {
+    extern __shared__ __align__(1024) unsigned char ring_mem[];  // tiles, queries, weights, the rest
+    unsigned char *q_tile = ring_mem + n_stages * kTile;
+    unsigned char *p_tile = q_tile + q_bytes(RT);
+    Shared<RT> &sh = *reinterpret_cast<Shared<RT> *>(p_tile + p_bytes(RT));
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    constexpr int kColumns = RT == 64 ? 256 : 128;  // 3 RT, as a power of two
+
+    if (warp == 5) tmem_alloc(&sh.tmem, kColumns);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < n_stages; ++i) {
+            mbar_init(&sh.pipe.full[i], 1);
+            mbar_init(&sh.pipe.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.pipe.desc_full[i], 1);
+            mbar_init(&sh.pipe.desc_empty[i], 5);  // four softmax warps and the issuing thread
+            mbar_init(&sh.s_full[i], 1);
+        }
+        mbar_init(&sh.q_full, 128);
+        mbar_init(&sh.p_full, 128);
+        mbar_init(&sh.o_done, 1);
+        mbar_init(&sh.agree, 4);
+        mbar_init(&sh.drain, 1);
+        sh.skip = 0;
+        sh.pipe.abort = 0;
+        fence_mbar_init();
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    begin_kernel<PREFIX>(P);
+
+    if (warp < 4) {
+        softmax_role<RT, PREFIX>(P, sh, ring_mem, q_tile, p_tile, n_stages);
+    } else if (warp == 4) {
+        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
+    } else {
+        if constexpr (!PREFIX) keep_books<kKT>(P, lane);
+        mma_role<RT>(P, sh, ring_mem, q_tile, p_tile, n_stages);
+        // nothing this warp issued is in flight when the CTA ends
+        if (elect_lane()) mma_commit(&sh.drain);
+        __syncwarp();
+#pragma unroll 1
+        for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain, 0, kHintNs); ++t) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_free(sh.tmem, kColumns);
+    end_kernel<PREFIX>(P);
+    if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = sh.pipe.abort;
+}
+
+}  // namespace round8
+}  // namespace spec

@@ -29,6 +29,29 @@ __device__ __forceinline__ uint16_t to_e4m3(float lo, float hi) {
     return r;
 }
 
+// Four weights (16-bit floats' range, below 61440) as sums of three e5m2 each; the words have the first weight in
+// the lowest byte. e5m2 is the upper byte of a 16-bit float, so: the weight is rounded to a 16-bit float (11
+// bits), its upper byte after rounding is the first part (three bits), what that leaves, which is a multiple of
+// the 16-bit float's last place and at most four of the first part's places off, gives the second in the same way
+// and the third. Three bits each hold it whole, down to the least e5m2, 2^-16.
+__device__ __forceinline__ void split_e5m2(float a, float b, float c, float d, uint32_t (&w)[3]) {
+    __half2 x = __floats2half2_rn(a, b), y = __floats2half2_rn(c, d);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t u = (reinterpret_cast<const uint32_t &>(x) + 0x00800080u) & 0xff00ff00u,
+                       v = (reinterpret_cast<const uint32_t &>(y) + 0x00800080u) & 0xff00ff00u;
+        w[i] = __byte_perm(u, v, 0x7531);
+        if (i < 2) {
+            x = __hsub2(x, reinterpret_cast<const __half2 &>(u));
+            y = __hsub2(y, reinterpret_cast<const __half2 &>(v));
+        }
+    }
+}
+// An e5m2 in the upper byte of the lower half of a word.
+__device__ __forceinline__ float e5m2_to_float(uint32_t byte) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 8)));
+}
+
 // The least power of two s with top <= 448 s, at least 2^kLeastScaleLog2. top is finite and not negative:
 // 448 = 1.75 * 2^8, so s = 2^(e-8) for top = f 2^e with 1 <= f <= 1.75, and 2^(e-7) for f above.
 __device__ __forceinline__ float e4m3_scale(float top) {

@@ -90,6 +90,11 @@ __device__ __forceinline__ uint64_t smem_operand64(uint32_t addr) {
     return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (1ull << 16) | (static_cast<uint64_t>(512u >> 4) << 32) |
            (1ull << 46) | (4ull << 61);
 }
+// An operand in the 32-byte swizzle: rows of 32 bytes, two pieces at (piece ^ (r / 4 % 2)).
+__device__ __forceinline__ uint64_t smem_operand32(uint32_t addr) {
+    return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (1ull << 16) | (static_cast<uint64_t>(256u >> 4) << 32) |
+           (1ull << 46) | (6ull << 61);
+}
 // bf16 x bf16 -> fp32, M = 128 rows, N columns; a_cols, b_cols: the operand runs along M or N in memory.
 __device__ __forceinline__ uint32_t mma_shape(int n, bool a_cols, bool b_cols) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_cols ? 1u << 15 : 0u) | (b_cols ? 1u << 16 : 0u) |
@@ -118,6 +123,26 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
+// Operands of 8 bits, 32 deep an instruction. e4m3, or e5m2 where said; M = 128 rows, N columns.
+__device__ __forceinline__ uint32_t mma8_shape(int n, bool a_e5m2, bool b_e5m2, bool a_cols, bool b_cols) {
+    return (1u << 4) | (a_e5m2 ? 1u << 7 : 0u) | (b_e5m2 ? 1u << 10 : 0u) | (a_cols ? 1u << 15 : 0u) |
+           (b_cols ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// The same with A in tensor memory: lane = row, four values along K per column.
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
 // One arrival on `bar` when every matrix instruction this thread has issued so far is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -133,6 +158,23 @@ __device__ __forceinline__ void copy_box(void *dst, const void *map, int x, int 
             smem_addr(dst)),
         "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
+}
+
+// A box of a three-dimensional tensor map, from column x, row y and plane z.
+__device__ __forceinline__ void copy_box3(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+// Four bytes to shared memory, and an arrival on `bar`, beside those it expects, when this thread's copies of this
+// kind have landed. The barrier's phase must not be able to end before the second is issued.
+__device__ __forceinline__ void copy_word(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_words_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Rows r0..r3 of a two-dimensional tensor map (box one row of 64 bf16, 128-byte swizzle), columns x ..
@@ -163,6 +205,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "=l"(reinterpret_cast<uint64_t &>(d))
         : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
           "l"(reinterpret_cast<const uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
     return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

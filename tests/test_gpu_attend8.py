@@ -132,7 +132,7 @@ def test_no_number_where_only_later_rows_see_it(dtype, rows, what):
         assert torch.isnan(out[last].float()).all() and torch.isnan(lse[last]).all()
 
 
-@pytest.mark.parametrize("rows", [[5], [150]], ids=str)
+@pytest.mark.parametrize("rows", [[5], [13], [150], [400]], ids=str)
 def test_scale_that_is_no_number_spoils_those_who_see_it(rows):
     """The page of the last positions: rows before them are as if it did not exist."""
     n = rows[0]
