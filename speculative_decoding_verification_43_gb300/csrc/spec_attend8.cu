@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "spec_attend8_pair.cuh"
 #include "spec_attend8_round.cuh"
 #include "spec_attend8_tiles.cuh"
 #include "spec_attend_fma.cuh"
@@ -28,12 +29,12 @@ static spec_status attend8_sizes(const spec_attend8_args *a, AttendParams &P) {
 // Rows of an item (as a power of two) and workers for `rows` packed rows of a head over `groups` requests on the
 // tensor cores.
 static void tensor8_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
-    rt_log2 = rows <= 24 * groups ? 5 : 6;
-    workers = kSMs * round8::kPerSM;
+    rt_log2 = rows <= 24 * groups ? 5 : rows <= 48 * groups ? 6 : pair8::kRTLog2;
+    workers = rt_log2 == pair8::kRTLog2 ? kSMs : kSMs * round8::kPerSM;
 }
 
 // Time of an item beside its tiles, in tiles.
-static int extra8_units(int rt_log2) { return 4; }
+static int extra8_units(int rt_log2) { return rt_log2 == pair8::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.
 static void attend8_work(AttendParams &P, bool tensor) {
@@ -118,8 +119,11 @@ static cudaError_t launch_class8(const AttendParams &P, const CacheMaps8 &M, cud
     if (rt_log2 == 5)
         return launch_tensor8(round8::spec_attend8_round_kernel<32, PREFIX>, workers, round8::kThreads,
                               round8::smem_bytes<32>(), round8::stages<32>(), P, M, stream);
-    return launch_tensor8(round8::spec_attend8_round_kernel<64, PREFIX>, workers, round8::kThreads,
-                          round8::smem_bytes<64>(), round8::stages<64>(), P, M, stream);
+    if (rt_log2 == 6)
+        return launch_tensor8(round8::spec_attend8_round_kernel<64, PREFIX>, workers, round8::kThreads,
+                              round8::smem_bytes<64>(), round8::stages<64>(), P, M, stream);
+    return launch_tensor8(pair8::spec_attend8_pair_kernel<PREFIX>, workers, pair8::kThreads, pair8::smem_bytes(),
+                          pair8::stages(), P, M, stream);
 }
 
 static cudaError_t enqueue_tensor8(const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
@@ -170,7 +174,9 @@ extern "C" const char *spec_attend8_plan(const spec_attend8_args *a) {
     if (attend8_sizes(a, P) != SPEC_OK) return nullptr;
     tiles8::CacheMap M = {};
     CacheShape shape = {};
-    return cache_map8(a, M, shape) ? "spec_attend8_round_kernel" : "spec_attend_fma_kernel";
+    if (!cache_map8(a, M, shape)) return "spec_attend_fma_kernel";
+    attend8_work(P, true);
+    return P.own_rt_log2 == pair8::kRTLog2 ? "spec_attend8_pair_kernel" : "spec_attend8_round_kernel";
 }
 
 extern "C" spec_status spec_attend8(const spec_attend8_args *a, void *workspace, size_t workspace_bytes,
