@@ -93,8 +93,11 @@ static bool encode_map8(CUtensorMap &map, const void *cache, const CacheShape &s
                                 static_cast<cuuint64_t>(shape.rows)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(shape.head_stride), static_cast<cuuint64_t>(a->slot_stride)};
     const cuuint32_t box[3] = {128, 1, static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
+    // no more than the head's own bytes: promoted to 256, a read brought the next head's too, 1.4 times the bytes
+    const CUtensorMapL2promotion promotion =
+        a->head_dim > 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -103,13 +106,13 @@ struct CacheMaps8 {
     CUtensorMap k, v;
 };
 
-template <typename Kernel>
-static cudaError_t launch_tensor8(Kernel *kernel, int ctas, int threads, int smem, int stages, const AttendParams &P,
-                                  const CacheMaps8 &M, cudaStream_t stream) {
+template <typename Kernel, typename... More>
+static cudaError_t launch_tensor8(Kernel *kernel, int ctas, int threads, int smem, const AttendParams &P, const CacheMaps8 &M,
+                                  cudaStream_t stream, More... more) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
-                        static_cast<size_t>(smem), stream, P, M.where, M.k, M.v, stages);
+                        static_cast<size_t>(smem), stream, P, M.where, M.k, M.v, more...);
 }
 
 // One class of items on the tensor cores.
@@ -118,12 +121,11 @@ static cudaError_t launch_class8(const AttendParams &P, const CacheMaps8 &M, cud
     const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2, workers = PREFIX ? P.prefix_workers : P.own_workers;
     if (rt_log2 == 5)
         return launch_tensor8(round8::spec_attend8_round_kernel<32, PREFIX>, workers, round8::kThreads,
-                              round8::smem_bytes<32>(), round8::stages<32>(), P, M, stream);
+                              round8::smem_bytes<32>(), P, M, stream, round8::stages<32>());
     if (rt_log2 == 6)
         return launch_tensor8(round8::spec_attend8_round_kernel<64, PREFIX>, workers, round8::kThreads,
-                              round8::smem_bytes<64>(), round8::stages<64>(), P, M, stream);
-    return launch_tensor8(pair8::spec_attend8_pair_kernel<PREFIX>, workers, pair8::kThreads, pair8::smem_bytes(),
-                          pair8::stages(), P, M, stream);
+                              round8::smem_bytes<64>(), P, M, stream, round8::stages<64>());
+    return launch_tensor8(pair8::spec_attend8_pair_kernel<PREFIX>, workers, pair8::kThreads, pair8::kSmem, P, M, stream);
 }
 
 static cudaError_t enqueue_tensor8(const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {

@@ -1,14 +1,20 @@
 // Attention of many rows over the cache in 8 bits on the tensor cores (bf16 rows, head sizes that are multiples of
 // 16 up to 128): long prompts, and the shared prefix. The work is laid out as in spec_attend_pair.cuh: an item of
 // 256 packed rows in two accumulators of 128 that use the same tiles, a row a thread, one warp issuing the
-// products of both in turn.
-//   S = Q K^T      Q in two parts, K as it lies in the cache (spec_attend8_tiles.cuh)
-//   O += P V       P in three parts of 8 bits, over S's columns in tensor memory; V as it lies in the cache
-// That is 8 + 12 instructions of 65 cycles a tile and accumulator (128 x 128 x 32; bf16: 8 + 8 of the same time).
+// products of both in turn. Per tile of 128 keys and accumulator:
+//   S = Q K^T      Q in two e4m3 parts (spec_attend8_tiles.cuh), K as it lies in the cache
+//   P = 2^(S - m)  a warpgroup, one row per thread; P (16-bit floats) goes back over S's columns, in two halves
+//   O += P V       V as 16-bit floats, to which two warps bring each tile once for all 256 rows
+// Taking V as it is would need P in three parts of 8 bits: 12 instructions instead of 8 and five operations a weight
+// on top of four (prompts: 866 us against TIME), while converting V is one for two values, and exact. 16-bit floats
+// hold weights from 2^15 down to 2^-25 to 11 bits, so a row's reference m may stay 2^8 behind its maximum.
 //
-// A column of S has its position's scales: of the key (a factor of the score) and of the value (which goes into
-// the weight as its logarithm, and out of it again in the row's sum, as in spec_attend8_round.cuh). They are the
-// same for a box of at least eight columns.
+// Scales: a column of S has its position's scales, of the key (a factor of the score) and of the value (its
+// logarithm goes into the weight, and its reciprocal into the row's sum, as in spec_attend8_round.cuh). The
+// converting warps leave both per box of slots, and set the values of positions that no row sees to 0.
+//
+// Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 issues matrix instructions, 10 and 11 convert values
+// (11 keeps the books first: the requests' status).
 #pragma once
 
 #include "spec_attend8_tiles.cuh"
@@ -20,39 +26,40 @@ using namespace tiles8;
 
 constexpr int kRTLog2 = 8, kRows = 128;  // rows of an item, of an accumulator
 constexpr int kHalf = kKT / 2;           // positions whose scores are taken at a time
-constexpr int kPart = kHalf / 4;         // columns of tensor memory of a part of a half's weights
-constexpr int kThreads = 352;
-constexpr float kTop = 11.0f;            // log2 of the largest weight under a new reference, and of what may be
+constexpr int kThreads = 384;
+// Keys lie in the even slots of the ring and values in the odd ones, so that each of their readers waits for every use
+// of the slots it reads, and a wait by parity cannot take one use for another.
+constexpr int kStages = 4;
+constexpr int kBlock = kKT * 128, kValues = 2 * kBlock;  // values as 16-bit floats: two blocks of 64 columns
+constexpr float kTop = 7.0f;             // log2 of the largest weight under a new reference, and of what may be
 constexpr float kMost = 15.0f;           // reached before the next
 
 struct Shared {
-    Pipe<kMaxStages> pipe;
+    Pipe<kStages> pipe;
     uint64_t q_full[2], s_full[2], p_full[2][2], o_half[2], o_full[2], agree[2], drain;
-    uint32_t bad[2][2][4];  // per warp: its quarter of the values holds one that is not finite
-    uint32_t skip[2];       // the warpgroup does this tile's second product itself
-    float factor[2][kRows]; // of the rows' scores
+    uint64_t v_full[2], v_empty[2];     // converted values
+    uint32_t skip[2];                   // the warpgroup does this tile's second product itself
+    uint32_t no_number[2][2];           // per slot of values and converting warp: it has found a NaN
     uint32_t tmem;
+    alignas(16) float4 by[2][kBoxes];   // per slot of values and box: key scale, log2 of the value scale, its reciprocal
+    float factor[2][kRows];             // of the rows' scores
 };
 
 // An accumulator's queries in two parts, and its output on the way out.
 constexpr int kQPart = kRows * 128, kQBytes = 2 * kQPart;
-__host__ constexpr int stages() {
-    constexpr int n = (227 * 1024 - 1024 - static_cast<int>(sizeof(Shared)) - 2 * kQBytes) / kTile;
-    return n < kMaxStages ? n : kMaxStages;
-}
-__host__ constexpr int smem_bytes() {
-    return 1024 + 2 * kQBytes + stages() * kTile + static_cast<int>(sizeof(Shared));
-}
+constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kValues + kStages * kTile + static_cast<int>(sizeof(Shared));
+static_assert(kSmem <= 227 * 1024, "fits");
 
 // ---------------------------------------------------------------- matrix instructions (one warp)
 
-__device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsigned char *q_mem, unsigned char *ring_mem,
-                                         int n_stages) {
+__device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsigned char *q_mem, unsigned char *v_mem,
+                                         unsigned char *ring_mem) {
     int32_t *ab = &sh.pipe.abort;
-    const uint32_t tmem = sh.tmem, pv_shape = mma8_shape(P.D, true, false, false, true);
-    const uint64_t q_op = smem_operand(smem_addr(q_mem), 16), ring_op = smem_operand(smem_addr(ring_mem), 16);
+    const uint32_t tmem = sh.tmem, pv_shape = mma_shape_f16(P.D, false, true);
+    const uint64_t q_op = smem_operand(smem_addr(q_mem), 16), ring_op = smem_operand(smem_addr(ring_mem), 16),
+                   v_op = smem_operand(smem_addr(v_mem), kBlock);
     const int steps = (P.D + 31) / 32;
-    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    Ring ring = {0, kStages, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
     uint32_t q_phases = 0, p_phases = 0;
     // (by the elected lane) S = Q K^T of accumulator w; n positions of the tile are used
     auto score = [&](int w, const Ring &at, int n) {
@@ -68,13 +75,11 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
     };
     // (by the elected lane) O += P V of accumulator w and half u; n positions of the half are used
     auto weigh = [&](int w, int u, const Ring &at, int n, bool add) {
-        const uint64_t v = operand_at(ring_op, at.slot * kTile + u * (kHalf * 128));
+        const uint64_t v = operand_at(v_op, at.slot * kValues + u * (kHalf * 128));
         const uint32_t p = tmem + w * 256 + u * kHalf, o = tmem + w * 256 + 128;
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (i * 32 < n) mma8_ts(o, p + part * kPart + 8 * i, operand_at(v, i * 4096), pv_shape, add || part + i > 0);
+        for (int i = 0; i < 4; ++i)
+            if (i * 16 < n) mma_ts(o, p + 8 * i, operand_at(v, i * 2048), pv_shape, add || i > 0);
     };
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
@@ -100,11 +105,10 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
             // beside issuing, the tensor cores wait for.
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
-                const Ring v = ring;  // this tile's values; the next tile's keys follow them
-                ring.step();
+                ring.step();  // past this tile's values, which are read as they have been converted
                 const bool more = t + 1 < nt;
                 const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
-                if (!wait_warp(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                if (!wait_warp(ab, &sh.v_full[values.slot], values.phase)) return;
                 if (more && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
 #pragma unroll 1
                 for (int w = 0; w < accs; ++w) {
@@ -114,7 +118,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                     const bool take = !*reinterpret_cast<volatile uint32_t *>(&sh.skip[w]);
                     if (n > kHalf) {
                         if (elect_lane()) {
-                            if (take) weigh(w, 0, v, kHalf, t > 0);
+                            if (take) weigh(w, 0, values, kHalf, t > 0);
                             mma_commit(&sh.o_half[w]);
                         }
                         __syncwarp();
@@ -123,7 +127,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                         tc_fence_after();
                     }
                     if (elect_lane()) {
-                        if (take) weigh(w, n > kHalf ? 1 : 0, v, n > kHalf ? n - kHalf : n, t > 0 || n > kHalf);
+                        if (take) weigh(w, n > kHalf ? 1 : 0, values, n > kHalf ? n - kHalf : n, t > 0 || n > kHalf);
                         // S and P share columns: matrix instructions of one thread run in the order of
                         // their issue, so the next scores follow the product that reads P
                         if (more)
@@ -131,13 +135,14 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                         else
                             mma_commit(&sh.o_full[w]);
                         if (w == accs - 1) {
-                            mma_commit(&sh.pipe.empty[v.slot]);
+                            mma_commit(&sh.v_empty[values.slot]);
                             if (more) mma_commit(&sh.pipe.empty[ring.slot]);
                         }
                     }
                     __syncwarp();
                 }
                 if (more) ring.step();
+                values.step();
                 n = next;
             }
         }
@@ -147,11 +152,78 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
     }
 }
 
+// ---------------------------------------------------------------- values (two warps)
+
+__device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, unsigned char *v_mem,
+                                             const unsigned char *ring_mem, int which, int lane) {
+    int32_t *ab = &sh.pipe.abort;
+    Ring ring = {0, kStages, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
+    const int c = lane & 7, half = c >> 2;
+    for (;;) {
+        if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
+        const Segment &s = sh.pipe.desc[desc.slot];
+        if (s.nrows == 0) return;
+        const int nt = s.ntile;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+            const int x0 = tile_begin<kKT>(s.keys, s.tile + t), n = tile_keys(s.keys, x0);
+            const bool edge = edge_tile(P, s, x0);
+            ring.step();
+            if (!wait_warp(ab, &sh.v_empty[values.slot], values.phase ^ 1u)) return;
+            if (!wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+            if (which == 0 && lane < kKT >> P.box_log2) {
+                // (no scales were copied for boxes that no row sees)
+                const bool used = !edge || item_sees(P, s.keys, x0 + (lane << P.box_log2), 1 << P.box_log2);
+                const float2 by = used ? sh.pipe.scale[ring.slot][lane] : make_float2(1.0f, 1.0f);
+                const ValueScale vs = value_scale(by.y);
+                sh.by[values.slot][lane] = make_float4(by.x, vs.log2, vs.inv, 0.0f);
+            }
+            // 16 values a lane at a time, eight lanes a row: two pieces of eight 16-bit floats in the row's block, the
+            // blocks' lanes taking them in opposite order so that eight lanes write to all banks
+            const unsigned char *from = ring_mem + ring.slot * kTile;
+            unsigned char *to = v_mem + values.slot * kValues + half * kBlock;
+            uint32_t found = 0u;
+            if (c < P.D / 16) {
+#pragma unroll 4
+                for (int r = which * 4 + (lane >> 3); r < n; r += 8) {
+                    uint4 v = *reinterpret_cast<const uint4 *>(from + r * 128 + ((c ^ (r & 7)) << 4));
+                    if (edge) {
+                        if (!item_sees(P, s.keys, x0 + r)) v = make_uint4(0u, 0u, 0u, 0u);
+                        found |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                                 __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    }
+                    const uint4 lo = make_uint4(e4m3_to_half2(v.x), e4m3_to_half2(v.x >> 16), e4m3_to_half2(v.y),
+                                                e4m3_to_half2(v.y >> 16)),
+                                hi = make_uint4(e4m3_to_half2(v.z), e4m3_to_half2(v.z >> 16), e4m3_to_half2(v.w),
+                                                e4m3_to_half2(v.w >> 16));
+                    unsigned char *row = to + r * 128;
+                    const int piece = (c & 3) * 2;
+                    *reinterpret_cast<uint4 *>(row + (((piece + half) ^ (r & 7)) << 4)) = half ? hi : lo;
+                    *reinterpret_cast<uint4 *>(row + (((piece + 1 - half) ^ (r & 7)) << 4)) = half ? lo : hi;
+                }
+            }
+            found = __any_sync(0xffffffffu, found != 0u);
+            if (lane == 0) sh.no_number[values.slot][which] = found;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.v_full[values.slot]);
+                mbar_arrive(&sh.pipe.empty[ring.slot]);
+            }
+            ring.step();
+            values.step();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
+        desc.step();
+    }
+}
+
 // ---------------------------------------------------------------- softmax (one row per thread)
 
-// The second product of a tile with values that are not finite, on the fp32 units: the row's weights
-// are in tensor memory already, O is complete up to the tile before. first: O holds nothing yet.
-__device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr, const unsigned char *v_tile, int k0, int x0, int n,
+// The second product of a tile with values that are no numbers, on the fp32 units: the row's weights are in tensor
+// memory already, O is complete up to the tile before. first: O holds nothing yet.
+__device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr, const unsigned char *values, int k0, int x0, int n,
                                         int from, int lim, int wlo, int sinks, bool first) {
 #pragma unroll 1
     for (int d = 0; d < D; d += 16) {
@@ -163,22 +235,24 @@ __device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr,
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0.0f;
 #pragma unroll 1
-        for (int k = 0; k < n; k += 16) {
-            float p[3][4];
+        for (int k = 0; k < n; k += 32) {
+            float p[16];
             __syncwarp();
-#pragma unroll
-            for (int part = 0; part < 3; ++part) tmem_ld4(p[part], p_addr + part * kPart + k / 4);
+            tmem_ld16(p, p_addr + k / 2);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 32; ++e) {
                 const int x = x0 + k + e;
                 if (k + e < n && x >= from && x <= lim && (x >= wlo || x < sinks)) {
-                    float w = 0.0f;
-#pragma unroll
-                    for (int part = 0; part < 3; ++part)
-                        w += e5m2_to_float(__float_as_uint(p[part][e / 4]) >> (e % 4 * 8) & 0xffu);
+                    const uint32_t pw = __float_as_uint(p[e / 2]);
+                    const float w = __half2float(__ushort_as_half(static_cast<unsigned short>(e % 2 ? pw >> 16 : pw)));
+                    const int row = k0 + k + e;
 #pragma unroll 4
-                    for (int i = 0; i < 16; ++i) o[i] = fmaf(w, tile_value(v_tile, k0 + k + e, d + i), o[i]);
+                    for (int i = 0; i < 16; ++i) {
+                        const unsigned char *at = values + ((d + i) >> 6) * kBlock + row * 128 +
+                                                  (((((d + i) & 63) >> 3) ^ (row & 7)) << 4) + ((d + i) & 7) * 2;
+                        o[i] = fmaf(w, __half2float(*reinterpret_cast<const __half *>(at)), o[i]);
+                    }
                 }
             }
         }
@@ -193,14 +267,13 @@ __device__ __noinline__ void mixed_tile(int D, uint32_t p_addr, uint32_t o_addr,
 
 template <bool PREFIX>
 __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, unsigned char *q_tile,
-                                             unsigned char *ring_mem, int w, int n_stages) {
+                                             const unsigned char *v_mem, int w) {
     const int tid = threadIdx.x % 128, warp = tid / kWarp, lane = tid % kWarp;
     int32_t *ab = &sh.pipe.abort;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_addr = sh.tmem + w * 256 + lanes, o_addr = s_addr + 128;
-    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    Ring values = {0, 2, 0}, desc = {0, 2, 0};
     uint32_t s_phase = 0, o_phase = 0, half_phase = 0, agree_phase = 0;
-    bool behind = false;  // tiles have gone by that this warpgroup has not waited for
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -266,42 +339,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             for (int i = 0; i < nt; ++i) {
                 const int x0 = tile_begin<kKT>(keys, first + i), n = tile_keys(keys, x0);
                 const bool edge = x0 > whole || x0 < from || (x0 <= cut && x0 + kKT > P.n_sink);
-                const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
-                unsigned char *v_tile = ring_mem + v_slot * kTile;
-                bool skip = false, scored = false;
-                auto scores = [&]() -> bool {
-                    if (scored) return true;
-                    scored = true;
-                    if (!wait_warp(ab, &sh.s_full[w], s_phase)) return false;
-                    s_phase ^= 1u;
-                    tc_fence_after();
-                    behind = false;
-                    return true;
-                };
-                auto landed = [&]() -> bool {
-                    return wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase);
-                };
-                if (edge) {
-                    // A wait by parity tells this use of the slot from the one before only when that one is known to
-                    // have arrived: its scores or the next tile's, issued behind its product, have been waited for.
-                    // After items without rows for this accumulator, this item's first scores say so.
-                    if (behind && !scores()) return;
-                    if (!landed()) return;
-                    const bool bad = __any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid));
-                    fence_proxy_async_smem();
-                    // the four warps' findings (two sets, used in turn)
-                    volatile uint32_t *found = sh.bad[w][agree_phase];
-                    __syncwarp();
-                    if (lane == 0) {
-                        found[warp] = bad;
-                        mbar_arrive(&sh.agree[w]);
-                    }
-                    if (!wait_warp(ab, &sh.agree[w], agree_phase)) return;
-                    agree_phase ^= 1u;
-                    skip = (found[0] | found[1] | found[2] | found[3]) != 0;
-                }
-                if (!scores()) return;
-                if (!edge && !landed()) return;  // the scales come with the values
+                if (!wait_warp(ab, &sh.s_full[w], s_phase)) return;
+                s_phase ^= 1u;
+                // A wait by parity tells this use of a slot of values from the one before, two tiles ago, as that one is
+                // known to have arrived: its products were issued before these scores.
+                if (!wait_warp(ab, &sh.v_full[values.slot], values.phase)) return;
+                tc_fence_after();
+                const unsigned char *v_tile = v_mem + values.slot * kValues;
+                const bool skip = edge && (sh.no_number[values.slot][0] | sh.no_number[values.slot][1]) != 0;
                 // (the tile before has been read out of this word: its products were issued before S)
                 if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
 #pragma unroll 1
@@ -315,31 +360,33 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         tmem_wait_ld32(z);
                         tmem_wait_ld32(z + 32);
                         // scores in base 2, and the scales' logarithms with them: eight columns share them
-                        float2 by[8];
+                        float inv[8];
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            const int x = xu + 8 * c;
-                            float2 sk = make_float2(1.0f, 1.0f);
-                            if (!edge || item_sees(P, keys, x, 8)) sk = sh.pipe.scale[v_slot][(u * kHalf + 8 * c) >> P.box_log2];
-                            const ValueScale vs = value_scale(sk.y);
-                            by[c] = make_float2(vs.log2, vs.inv);
-                            const float kf = sk.x * factor;
+                            const float4 by = sh.by[values.slot][(u * kHalf + 8 * c) >> P.box_log2];
+                            inv[c] = by.z;
+                            const float kf = by.x * factor;
 #pragma unroll
                             for (int e = 8 * c; e < 8 * c + 8; e += 2) {
-                                const float2 y = fma2(make_float2(z[e], z[e + 1]), make_float2(kf, kf), make_float2(vs.log2, vs.log2));
+                                const float2 y = fma2(make_float2(z[e], z[e + 1]), make_float2(kf, kf), make_float2(by.y, by.y));
                                 z[e] = y.x;
                                 z[e + 1] = y.y;
                             }
-                            if (edge)
+                        }
+                        if (edge) {
 #pragma unroll
-                                for (int e = 8 * c; e < 8 * c + 8; ++e) {
-                                    const int xe = xu + e;
-                                    if (!(xe >= from && xe <= lim && (xe >= wlo || xe < P.n_sink))) z[e] = -INFINITY;
-                                }
+                            for (int e = 0; e < 64; ++e) {
+                                const int xe = xu + e;
+                                if (!(xe >= from && xe <= lim && (xe >= wlo || xe < P.n_sink))) z[e] = -INFINITY;
+                            }
+                        }
 #pragma unroll
-                            for (int e = 8 * c; e < 8 * c + 8; e += 2)
-                                mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(z[e], z[e + 1]));
+                        for (int e = 0; e < 64; e += 8) {
+                            mx[0] = fmaxf(mx[0], fmaxf(z[e], z[e + 1]));
+                            mx[1] = fmaxf(mx[1], fmaxf(z[e + 2], z[e + 3]));
+                            mx[2] = fmaxf(mx[2], fmaxf(z[e + 4], z[e + 5]));
+                            mx[3] = fmaxf(mx[3], fmaxf(z[e + 6], z[e + 7]));
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                         // a new reference when the old one is too low (or there was none): m is kTop below it
@@ -369,25 +416,17 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         const float ref = m == -INFINITY ? 0.0f : -m;
                         const float2 rf = make_float2(ref, ref);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                        uint32_t pw[3][16];
+                        uint32_t pw[32];
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            float2 a = add2(make_float2(z[e], z[e + 1]), rf), c = add2(make_float2(z[e + 2], z[e + 3]), rf);
-                            a.x = ex2(a.x);
-                            a.y = ex2(a.y);
-                            c.x = ex2(c.x);
-                            c.y = ex2(c.y);
-                            const float2 inv = make_float2(by[e >> 3].y, by[e >> 3].y);
-                            sum[0] = fma2(a, inv, sum[0]);
-                            sum[1] = fma2(c, inv, sum[1]);
-                            uint32_t parts[3];
-                            split_e5m2(a.x, a.y, c.x, c.y, parts);
-#pragma unroll
-                            for (int part = 0; part < 3; ++part) pw[part][e / 4] = parts[part];
+                        for (int e = 0; e < 64; e += 2) {
+                            float2 y = add2(make_float2(z[e], z[e + 1]), rf);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum[e / 2 & 1] = fma2(y, make_float2(inv[e >> 3], inv[e >> 3]), sum[e / 2 & 1]);
+                            pw[e / 2] = pack_f16(y.x, y.y);
+                            if (e == 30) tmem_st16(s_at, pw);  // over columns that have been read
                         }
-                        // over columns that have been read
-#pragma unroll
-                        for (int part = 0; part < 3; ++part) tmem_st16(s_at + part * kPart, pw[part]);
+                        tmem_st16(s_at + 16, pw + 16);
                         sum[0] = add2(sum[0], sum[1]);
                         l += sum[0].x + sum[0].y;
                         tmem_wait_st();
@@ -401,15 +440,13 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                     mbar_arrive(&sh.p_full[w][u]);
                 }
                 if (n > kHalf) half_phase ^= 1u;
-                ring.step();
-                ring.step();
+                values.step();
             }
             if (!wait_warp(ab, &sh.o_full[w], o_phase)) return;
             o_phase ^= 1u;
             tc_fence_after();
         } else {
-            for (int i = 0; i < 2 * nt; ++i) ring.step();
-            behind = behind || nt > 0;
+            for (int i = 0; i < nt; ++i) values.step();
         }
         if (dead) {
             m = -INFINITY;
@@ -499,22 +536,22 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
 template <bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
     spec_attend8_pair_kernel(const __grid_constant__ AttendParams P, const CacheMap M, const __grid_constant__ CUtensorMap kmap,
-                            const __grid_constant__ CUtensorMap vmap, const int n_stages) {
+                             const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ unsigned char raw[];
     unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    unsigned char *ring_mem = base + 2 * kQBytes;
-    Shared &sh = *reinterpret_cast<Shared *>(ring_mem + n_stages * kTile);
+    unsigned char *v_mem = base + 2 * kQBytes, *ring_mem = v_mem + 2 * kValues;
+    Shared &sh = *reinterpret_cast<Shared *>(ring_mem + kStages * kTile);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
-    if (warp == 10) tmem_alloc(&sh.tmem, 512);
+    if (warp == 9) tmem_alloc(&sh.tmem, 512);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < n_stages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.pipe.full[i], 1);
-            mbar_init(&sh.pipe.empty[i], 1);
+            mbar_init(&sh.pipe.empty[i], i % 2 == 0 ? 1 : 2);  // keys: the products; values: the converting warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.pipe.desc_full[i], 1);
-            mbar_init(&sh.pipe.desc_empty[i], 9);  // eight softmax warps and the issuing one
+            mbar_init(&sh.pipe.desc_empty[i], 11);  // eight softmax warps, the issuing and the converting ones
             mbar_init(&sh.q_full[i], 128);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i][0], 128);
@@ -522,6 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.o_half[i], 1);
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.agree[i], 4);
+            mbar_init(&sh.v_full[i], 2);
+            mbar_init(&sh.v_empty[i], 1);
             sh.skip[i] = 0;
         }
         mbar_init(&sh.drain, 1);
@@ -536,27 +575,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin_kernel<PREFIX>(P);
 
     if (warp < 8) {
-        softmax_role<PREFIX>(P, sh, base + (warp / 4) * kQBytes, ring_mem, warp / 4, n_stages);
-    } else {
-        if (warp == 8) {
-            load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
-        } else if (warp == 9) {
-            if constexpr (!PREFIX) keep_books<kKT>(P, lane);
-        } else {
-            mma_role(P, sh, base, ring_mem, n_stages);
-            // nothing this warp issued is in flight when the CTA ends
-            if (elect_lane()) mma_commit(&sh.drain);
-            __syncwarp();
+        softmax_role<PREFIX>(P, sh, base + (warp / 4) * kQBytes, v_mem, warp / 4);
+    } else if (warp == 8) {
+        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, kStages, blockIdx.x, lane);
+    } else if (warp == 9) {
+        mma_role(P, sh, base, v_mem, ring_mem);
+        // nothing this warp issued is in flight when the CTA ends
+        if (elect_lane()) mma_commit(&sh.drain);
+        __syncwarp();
 #pragma unroll 1
-            for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain, 0, kHintNs); ++t) {
-            }
+        for (int t = 0; t < kTries && !mbar_try_wait_sleep(&sh.drain, 0, kHintNs); ++t) {
         }
+    } else {
+        if constexpr (!PREFIX)
+            if (warp == 11) keep_books<kKT>(P, lane);
+        convert_role(P, sh, v_mem, ring_mem, warp - 10, lane);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 10) tmem_free(sh.tmem, 512);
+    if (warp == 9) tmem_free(sh.tmem, 512);
     end_kernel<PREFIX>(P);
     if (threadIdx.x == 0) P.err[(PREFIX ? P.own_workers : 0) + blockIdx.x] = sh.pipe.abort;
 }

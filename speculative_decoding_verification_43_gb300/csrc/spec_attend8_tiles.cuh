@@ -24,7 +24,6 @@ using tiles::wait_one;
 using tiles::wait_warp;
 
 constexpr int kTile = kKT * 128;  // bytes
-constexpr int kMaxStages = 10;
 constexpr int kBoxes = kKT / 8;   // of a tile, at most
 
 // Where heads and pages lie in the tensor maps (head_dim x heads x slots): slot s of page b, head h is plane

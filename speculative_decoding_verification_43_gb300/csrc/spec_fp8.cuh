@@ -12,10 +12,15 @@ constexpr float kE4m3Max = 448.0f;
 // The least scale that is set: a block of zeros has it, and so have values below 2^-52.
 constexpr int kLeastScaleLog2 = -60;
 
-// Two e4m3 (the first in the lower byte) as fp32; exact.
-__device__ __forceinline__ float2 e4m3_to_float2(uint16_t v) {
+// Two e4m3 in the lower half of a word (the first in the lower byte) as 16-bit floats; exact.
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t v) {
     uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+    return h;
+}
+// The same as fp32.
+__device__ __forceinline__ float2 e4m3_to_float2(uint16_t v) {
+    const uint32_t h = e4m3_to_half2(v);
     return __half22float2(reinterpret_cast<const __half2 &>(h));
 }
 __device__ __forceinline__ float4 e4m3_to_float4(uint32_t v) {

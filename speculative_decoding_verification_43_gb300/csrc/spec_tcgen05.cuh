@@ -100,6 +100,11 @@ __device__ __forceinline__ uint32_t mma_shape(int n, bool a_cols, bool b_cols) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_cols ? 1u << 15 : 0u) | (b_cols ? 1u << 16 : 0u) |
            (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
+// The same on 16-bit floats.
+__device__ __forceinline__ uint32_t mma_shape_f16(int n, bool a_cols, bool b_cols) {
+    return (1u << 4) | (a_cols ? 1u << 15 : 0u) | (b_cols ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
 // True in one lane of a converged warp, the same one every time. Around matrix instructions a warp that
 // stays together keeps their operands in uniform registers, where they are taken from.
 __device__ __forceinline__ bool elect_lane() {
@@ -220,6 +225,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=l"(reinterpret_cast<uint64_t &>(d))
         : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
     return d;
+}
+// Two fp32 as packed 16-bit floats, `lo` in the lower half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 // Two fp32 as packed bf16, `lo` in the lower half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
