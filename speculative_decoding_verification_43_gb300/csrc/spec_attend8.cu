@@ -106,13 +106,13 @@ struct CacheMaps8 {
     CUtensorMap k, v;
 };
 
-template <typename Kernel, typename... More>
+template <typename Kernel>
 static cudaError_t launch_tensor8(Kernel *kernel, int ctas, int threads, int smem, const AttendParams &P, const CacheMaps8 &M,
-                                  cudaStream_t stream, More... more) {
+                                  cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
-                        static_cast<size_t>(smem), stream, P, M.where, M.k, M.v, more...);
+                        static_cast<size_t>(smem), stream, P, M.where, M.k, M.v);
 }
 
 // One class of items on the tensor cores.
@@ -121,10 +121,10 @@ static cudaError_t launch_class8(const AttendParams &P, const CacheMaps8 &M, cud
     const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2, workers = PREFIX ? P.prefix_workers : P.own_workers;
     if (rt_log2 == 5)
         return launch_tensor8(round8::spec_attend8_round_kernel<32, PREFIX>, workers, round8::kThreads,
-                              round8::smem_bytes<32>(), P, M, stream, round8::stages<32>());
+                              round8::smem_bytes<32>(), P, M, stream);
     if (rt_log2 == 6)
         return launch_tensor8(round8::spec_attend8_round_kernel<64, PREFIX>, workers, round8::kThreads,
-                              round8::smem_bytes<64>(), P, M, stream, round8::stages<64>());
+                              round8::smem_bytes<64>(), P, M, stream);
     return launch_tensor8(pair8::spec_attend8_pair_kernel<PREFIX>, workers, pair8::kThreads, pair8::kSmem, P, M, stream);
 }
 

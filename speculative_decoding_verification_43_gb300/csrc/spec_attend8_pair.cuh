@@ -27,15 +27,13 @@ using namespace tiles8;
 constexpr int kRTLog2 = 8, kRows = 128;  // rows of an item, of an accumulator
 constexpr int kHalf = kKT / 2;           // positions whose scores are taken at a time
 constexpr int kThreads = 384;
-// Keys lie in the even slots of the ring and values in the odd ones, so that each of their readers waits for every use
-// of the slots it reads, and a wait by parity cannot take one use for another.
-constexpr int kStages = 4;
+constexpr int kStages = 4;               // tiles of keys and of values, two each
 constexpr int kBlock = kKT * 128, kValues = 2 * kBlock;  // values as 16-bit floats: two blocks of 64 columns
 constexpr float kTop = 7.0f;             // log2 of the largest weight under a new reference, and of what may be
 constexpr float kMost = 15.0f;           // reached before the next
 
 struct Shared {
-    Pipe<kStages> pipe;
+    Pipe<kStages / 2, kStages / 2> pipe;
     uint64_t q_full[2], s_full[2], p_full[2][2], o_half[2], o_full[2], agree[2], drain;
     uint64_t v_full[2], v_empty[2];     // converted values
     uint32_t skip[2];                   // the warpgroup does this tile's second product itself
@@ -56,14 +54,14 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                                          unsigned char *ring_mem) {
     int32_t *ab = &sh.pipe.abort;
     const uint32_t tmem = sh.tmem, pv_shape = mma_shape_f16(P.D, false, true);
-    const uint64_t q_op = smem_operand(smem_addr(q_mem), 16), ring_op = smem_operand(smem_addr(ring_mem), 16),
+    const uint64_t q_op = smem_operand(smem_addr(q_mem), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
                    v_op = smem_operand(smem_addr(v_mem), kBlock);
     const int steps = (P.D + 31) / 32;
-    Ring ring = {0, kStages, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
+    Ring ring = {0, kStages / 2, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
     uint32_t q_phases = 0, p_phases = 0;
     // (by the elected lane) S = Q K^T of accumulator w; n positions of the tile are used
     auto score = [&](int w, const Ring &at, int n) {
-        const uint64_t k = operand_at(ring_op, at.slot * kTile), q = operand_at(q_op, w * kQBytes);
+        const uint64_t k = operand_at(k_op, at.slot * kTile), q = operand_at(q_op, w * kQBytes);
         const uint32_t shape = mma8_shape(n, false, false, false, false);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -89,14 +87,14 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
         const KeyTiles keys = s.keys;
         if (nt > 0) {
             int n = tile_keys(keys, tile_begin<kKT>(keys, first));
-            if (!wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+            if (!wait_warp(ab, &sh.pipe.k_full[ring.slot], ring.phase)) return;
             for (int w = 0; w < accs; ++w) {
                 if (!wait_warp(ab, &sh.q_full[w], q_phases >> w & 1u)) return;
                 q_phases ^= 1u << w;
                 tc_fence_after();
                 if (elect_lane()) {
                     score(w, ring, n);
-                    if (w == accs - 1) mma_commit(&sh.pipe.empty[ring.slot]);
+                    if (w == accs - 1) mma_commit(&sh.pipe.k_empty[ring.slot]);
                 }
                 __syncwarp();
             }
@@ -105,11 +103,10 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
             // beside issuing, the tensor cores wait for.
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
-                ring.step();  // past this tile's values, which are read as they have been converted
                 const bool more = t + 1 < nt;
                 const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
                 if (!wait_warp(ab, &sh.v_full[values.slot], values.phase)) return;
-                if (more && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                if (more && !wait_warp(ab, &sh.pipe.k_full[ring.slot], ring.phase)) return;
 #pragma unroll 1
                 for (int w = 0; w < accs; ++w) {
                     if (!wait_warp(ab, &sh.p_full[w][0], p_phases >> w & 1u)) return;
@@ -136,7 +133,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                             mma_commit(&sh.o_full[w]);
                         if (w == accs - 1) {
                             mma_commit(&sh.v_empty[values.slot]);
-                            if (more) mma_commit(&sh.pipe.empty[ring.slot]);
+                            if (more) mma_commit(&sh.pipe.k_empty[ring.slot]);
                         }
                     }
                     __syncwarp();
@@ -157,7 +154,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
 __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, unsigned char *v_mem,
                                              const unsigned char *ring_mem, int which, int lane) {
     int32_t *ab = &sh.pipe.abort;
-    Ring ring = {0, kStages, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
+    Ring ring = {0, kStages / 2, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
     const int c = lane & 7, half = c >> 2;
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
@@ -168,9 +165,8 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
         for (int t = 0; t < nt; ++t) {
             const int x0 = tile_begin<kKT>(s.keys, s.tile + t), n = tile_keys(s.keys, x0);
             const bool edge = edge_tile(P, s, x0);
-            ring.step();
             if (!wait_warp(ab, &sh.v_empty[values.slot], values.phase ^ 1u)) return;
-            if (!wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+            if (!wait_warp(ab, &sh.pipe.v_full[ring.slot], ring.phase)) return;
             if (which == 0 && lane < kKT >> P.box_log2) {
                 // (no scales were copied for boxes that no row sees)
                 const bool used = !edge || item_sees(P, s.keys, x0 + (lane << P.box_log2), 1 << P.box_log2);
@@ -180,7 +176,7 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
             }
             // 16 values a lane at a time, eight lanes a row: two pieces of eight 16-bit floats in the row's block, the
             // blocks' lanes taking them in opposite order so that eight lanes write to all banks
-            const unsigned char *from = ring_mem + ring.slot * kTile;
+            const unsigned char *from = ring_mem + (kStages / 2 + ring.slot) * kTile;
             unsigned char *to = v_mem + values.slot * kValues + half * kBlock;
             uint32_t found = 0u;
             if (c < P.D / 16) {
@@ -208,7 +204,7 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sh.v_full[values.slot]);
-                mbar_arrive(&sh.pipe.empty[ring.slot]);
+                mbar_arrive(&sh.pipe.v_empty[ring.slot]);
             }
             ring.step();
             values.step();
@@ -545,13 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 9) tmem_alloc(&sh.tmem, 512);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.pipe.full[i], 1);
-            mbar_init(&sh.pipe.empty[i], i % 2 == 0 ? 1 : 2);  // keys: the products; values: the converting warps
-        }
+        init_pipe(sh.pipe, 2, 11);  // values: the converting warps; segments: eight softmax warps, the issuing one and these
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.pipe.desc_full[i], 1);
-            mbar_init(&sh.pipe.desc_empty[i], 11);  // eight softmax warps, the issuing and the converting ones
             mbar_init(&sh.q_full[i], 128);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i][0], 128);
@@ -564,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.skip[i] = 0;
         }
         mbar_init(&sh.drain, 1);
-        sh.pipe.abort = 0;
         fence_mbar_init();
         prefetch_map(&kmap);
         prefetch_map(&vmap);
@@ -577,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 8) {
         softmax_role<PREFIX>(P, sh, base + (warp / 4) * kQBytes, v_mem, warp / 4);
     } else if (warp == 8) {
-        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, kStages, blockIdx.x, lane);
+        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, blockIdx.x, lane);
     } else if (warp == 9) {
         mma_role(P, sh, base, v_mem, ring_mem);
         // nothing this warp issued is in flight when the CTA ends

@@ -21,15 +21,15 @@ namespace round8 {
 
 using namespace tiles8;
 
-constexpr int kThreads = 192, kPerSM = 2, kStages = 5;
+constexpr int kThreads = 192, kPerSM = 2;
 constexpr float kTop = 11.0f;  // log2 of the largest weight under a new reference, and of what may be reached
 constexpr float kMost = 15.0f; // before the next
 
 template <int RT>
 struct Shared {
-    Pipe<kStages> pipe;
-    uint64_t q_full, s_full[2], p_full, o_done, agree, drain;
-    uint32_t found[2][4];  // per warp: a score beyond the reference (1), a value that is not finite (2)
+    Pipe<2, RT == 32 ? 3 : 2> pipe;
+    uint64_t q_full, s_full[2], p_full, o_done, drain;
+    uint32_t found[4];     // per warp: what it brings to a meeting
     uint32_t skip;         // the warpgroup has done this tile's second product itself
     uint32_t tmem;
     // of this segment's rows and the next one's, in turn
@@ -52,30 +52,30 @@ __host__ __device__ constexpr int p_part(int RT) { return kKT * RT; }
 __host__ __device__ constexpr int q_bytes(int RT) { return 2 * q_part(RT); }
 __host__ __device__ constexpr int p_bytes(int RT) { return 3 * p_part(RT); }
 template <int RT>
-__host__ constexpr int stages() {
-    // 228 KB of shared memory, 1 KB of it taken per CTA
-    constexpr int n = (228 * 1024 / kPerSM - 1024 - static_cast<int>(sizeof(Shared<RT>)) - q_bytes(RT) - p_bytes(RT)) / kTile;
-    return n < kStages ? n : kStages;
+__host__ __device__ constexpr int stages() {
+    return decltype(Shared<RT>::pipe)::kKeys + decltype(Shared<RT>::pipe)::kValues;
 }
 template <int RT>
 __host__ constexpr int smem_bytes() {
     return stages<RT>() * kTile + q_bytes(RT) + p_bytes(RT) + static_cast<int>(sizeof(Shared<RT>));
 }
-// (three tiles, so that what a slot held before is always known to have arrived: see the softmax's waits)
-static_assert(stages<32>() >= 3 && stages<64>() >= 3, "a tile of keys, one of values and the next tile's keys");
+// 228 KB of shared memory, 1 KB of it taken per CTA
+static_assert(smem_bytes<32>() <= 228 * 1024 / kPerSM - 1024 && smem_bytes<64>() <= 228 * 1024 / kPerSM - 1024, "fits");
 static_assert(sizeof(Scratch<64>) <= p_bytes(64) && sizeof(Scratch<32>) <= p_bytes(32), "fits the weights' memory");
 
 // ---------------------------------------------------------------- matrix instructions (one warp)
 
 template <int RT>
 __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, unsigned char *ring_mem,
-                                         unsigned char *q_tile, unsigned char *p_tile, int n_stages) {
+                                         unsigned char *q_tile, unsigned char *p_tile) {
     int32_t *ab = &sh.pipe.abort;
+    constexpr int kKeys = decltype(Shared<RT>::pipe)::kKeys, kValues = decltype(Shared<RT>::pipe)::kValues;
     const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * RT;
-    const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), ring_op = smem_operand(smem_addr(ring_mem), 16),
+    const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
+                   v_op = smem_operand(smem_addr(ring_mem + kKeys * kTile), 16),
                    p_op = RT == 64 ? smem_operand64(smem_addr(p_tile)) : smem_operand32(smem_addr(p_tile));
     const int steps = (P.D + 31) / 32;
-    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
+    Ring next = {0, kKeys, 0}, v = {0, kValues, 0}, desc = {0, 2, 0};
     uint32_t q_phase = 0, p_phase = 0;
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
@@ -94,17 +94,15 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
 #pragma unroll 1
             for (int t = -1; t < nt; ++t) {
                 const bool more = t + 1 < nt;
-                const Ring v = ring;  // this tile's values; the next tile's keys follow them
-                if (t >= 0) ring.step();
-                const bool ahead = more && __all_sync(0xffffffffu, mbar_try_wait(&sh.pipe.full[ring.slot], ring.phase));
+                const bool ahead = more && __all_sync(0xffffffffu, mbar_try_wait(&sh.pipe.k_full[next.slot], next.phase));
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     if (part == (ahead ? 0 : 1)) {
                         if (!more) continue;
-                        if (!ahead && !wait_warp(ab, &sh.pipe.full[ring.slot], ring.phase)) return;
+                        if (!ahead && !wait_warp(ab, &sh.pipe.k_full[next.slot], next.phase)) return;
                         tc_fence_after();
                         const int b = (t + 1) & 1;  // S^T = K Q^T
-                        const uint64_t k = operand_at(ring_op, ring.slot * kTile);
+                        const uint64_t k = operand_at(k_op, next.slot * kTile);
                         if (elect_lane()) {
 #pragma unroll
                             for (int q = 0; q < 2; ++q)
@@ -114,16 +112,16 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
                                         mma8_ss(s_col + b * RT, operand_at(k, i * 32), operand_at(q_op, q * q_part(RT) + i * 32),
                                                 qk_shape, q + i > 0);
                             mma_commit(&sh.s_full[b]);
-                            mma_commit(&sh.pipe.empty[ring.slot]);
+                            mma_commit(&sh.pipe.k_empty[next.slot]);
                         }
                         __syncwarp();
                     } else if (t >= 0) {
-                        if (!wait_warp(ab, &sh.pipe.full[v.slot], v.phase)) return;
+                        if (!wait_warp(ab, &sh.pipe.v_full[v.slot], v.phase)) return;
                         if (!wait_warp(ab, &sh.p_full, p_phase)) return;
                         p_phase ^= 1u;
                         tc_fence_after();
                         const bool take = !*reinterpret_cast<volatile uint32_t *>(&sh.skip);
-                        const uint64_t values = operand_at(ring_op, v.slot * kTile);
+                        const uint64_t values = operand_at(v_op, v.slot * kTile);
                         const int n = tile_keys(keys, tile_begin<kKT>(keys, first + t));
                         if (elect_lane()) {
                             if (take) {  // O^T += V^T P^T
@@ -136,12 +134,13 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
                                                     operand_at(p_op, p * p_part(RT) + i * 32 * RT), pv_shape, t > 0 || p + i > 0);
                             }
                             mma_commit(&sh.o_done);
-                            mma_commit(&sh.pipe.empty[v.slot]);
+                            mma_commit(&sh.pipe.v_empty[v.slot]);
                         }
                         __syncwarp();
                     }
                 }
-                if (more) ring.step();
+                if (more) next.step();
+                if (t >= 0) v.step();
             }
         }
         if (elect_lane()) mbar_arrive(&sh.pipe.desc_empty[desc.slot]);
@@ -152,30 +151,21 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
 
 // ---------------------------------------------------------------- softmax (one position per thread)
 
-// The four warps meet; each leaves a word, and all get the words' union (-1: a wait gave up).
-__device__ __forceinline__ int meet(int32_t *abort, uint64_t *bar, uint32_t (*found)[4], uint32_t phase, uint32_t mine) {
-    const int warp = threadIdx.x / kWarp;
-    volatile uint32_t *words = found[phase];
-    __syncwarp();
-    if (threadIdx.x % kWarp == 0) {
-        words[warp] = mine;
-        mbar_arrive(bar);
-    }
-    if (!wait_warp(abort, bar, phase)) return -1;
-    return static_cast<int>(words[0] | words[1] | words[2] | words[3]);
+// The four warps meet at a hardware barrier: true when some thread brings a flag. A meeting has no limit of its own, so
+// all four come to every one: a warp whose bounded wait has given up goes on with what it has (`gone`), brings that
+// to the next meeting, and there they leave together. (At an mbarrier, with words in shared memory, a meeting
+// took some 1000 cycles of a tile's 4000.)
+__device__ __forceinline__ bool meet(bool flag) { return bar_any(1, 128, flag); }
+// The same with a word each, of which all get the union.
+__device__ __forceinline__ uint32_t meet_words(uint32_t *found, uint32_t mine) {
+    if (!meet(mine != 0u)) return 0u;
+    if (threadIdx.x % kWarp == 0) found[threadIdx.x / kWarp] = mine;
+    bar_sync(1, 128);
+    const uint32_t all = found[0] | found[1] | found[2] | found[3];
+    bar_sync(1, 128);
+    return all;
 }
-// Out of line for the meetings that come once per item.
-__device__ __noinline__ int meet_far(int32_t *abort, uint64_t *bar, uint32_t (*found)[4], uint32_t phase, uint32_t mine) {
-    return meet(abort, bar, found, phase, mine);
-}
-template <int RT, bool FAR = true>
-__device__ __forceinline__ bool agree(Shared<RT> &sh, uint32_t &phase, uint32_t mine, uint32_t &all) {
-    const int r = FAR ? meet_far(&sh.pipe.abort, &sh.agree, sh.found, phase, mine)
-                      : meet(&sh.pipe.abort, &sh.agree, sh.found, phase, mine);
-    phase ^= 1u;
-    all = static_cast<uint32_t>(r);
-    return r >= 0;
-}
+constexpr uint32_t kBeyond = 1, kNoNumber = 2, kGone = 4;  // a weight too large, a value that is no number, a wait given up
 
 // The second product of a tile with values that are not finite, on the fp32 units: thread d has output
 // column d, the weights lie in shared memory, O is complete up to the tile before.
@@ -219,15 +209,17 @@ __device__ __noinline__ void mixed_tile(const AttendParams &P, const int *pos, u
 
 template <int RT, bool PREFIX>
 __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &sh, unsigned char *ring_mem,
-                                             unsigned char *q_tile, unsigned char *p_tile, int n_stages) {
+                                             unsigned char *q_tile, unsigned char *p_tile) {
+    constexpr int kKeys = decltype(Shared<RT>::pipe)::kKeys, kValues = decltype(Shared<RT>::pipe)::kValues;
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     int32_t *ab = &sh.pipe.abort;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_addr = sh.tmem + lanes, o_addr = s_addr + 2 * RT;
     Scratch<RT> &scratch = *reinterpret_cast<Scratch<RT> *>(p_tile);
-    Ring ring = {0, n_stages, 0}, desc = {0, 2, 0};
-    uint32_t s_phases = 0, o_phase = 0, a_phase = 0, word = 0;
+    Ring values = {0, kValues, 0}, desc = {0, 2, 0};
+    uint32_t s_phases = 0, o_phase = 0;
     int buf = 0;
+    bool gone = false;
     // Brings a segment's queries: 128 / RT threads each row's (rows up to a multiple of 16: zeros), and its
     // position.
     auto bring = [&](const Segment &s, int to) {
@@ -283,10 +275,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
     for (;;) {
         const Segment &s = sh.pipe.desc[desc.slot];
         if (first_segment) {
-            if (!wait_warp(ab, &sh.pipe.desc_full[0], 0)) return;
+            gone = !wait_warp(ab, &sh.pipe.desc_full[0], 0);
+            if (meet(gone)) return;
             if (s.nrows == 0) return;
             bring(s, 0);
-            if (!agree(sh, a_phase, 0u, word)) return;
+            bar_sync(1, 128);
             first_segment = false;
         }
         const int nrows = s.nrows, nt = s.ntile, n16 = (nrows + 15) & ~15;
@@ -302,47 +295,44 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             const int b = i & 1;
             const int x0 = tile_begin<kKT>(s.keys, s.tile + i), n = tile_keys(s.keys, x0), x = x0 + tid;
             const bool edge = edge_tile(P, s, x0);
-            const int v_slot = ring.slot + 1 == ring.n ? 0 : ring.slot + 1;
-            unsigned char *v_tile = ring_mem + v_slot * kTile;
+            unsigned char *v_tile = ring_mem + (kKeys + values.slot) * kTile;
             uint32_t mine = 0u;
             bool rested = i == 0;
-            auto rest = [&]() -> bool {
-                if (rested) return true;
+            auto rest = [&]() {
+                if (rested) return;
                 rested = true;
-                if (!wait_warp(ab, &sh.o_done, o_phase)) return false;
+                gone |= !wait_warp(ab, &sh.o_done, o_phase);
                 o_phase ^= 1u;
                 tc_fence_after();
-                return true;
             };
-            // The scales come with the values. A wait by parity tells this use of a slot from the one before only when
-            // that one is known to have arrived; in a ring of three slots or more it is: it held keys whose scores, or
-            // values whose product, have been waited for.
-            auto landed = [&]() -> bool {
-                return wait_warp(ab, &sh.pipe.full[v_slot], ring.slot + 1 == ring.n ? ring.phase ^ 1u : ring.phase);
-            };
+            // The scales come with the values. (A wait by parity cannot take the use of the slot before for this one: that
+            // was two tiles ago or more, and the product of its values has been waited for.)
+            auto landed = [&]() { gone |= !wait_warp(ab, &sh.pipe.v_full[values.slot], values.phase); };
             if (edge) {
-                if (!landed()) return;
-                if (__any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid))) mine = 2u;
+                landed();
+                if (__any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid))) mine = kNoNumber;
                 fence_proxy_async_smem();
             }
-            if (!wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u)) return;
+            gone |= !wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u);
             s_phases ^= 1u << b;
-            if (!edge && !landed()) return;
+            if (!edge) landed();
             tc_fence_after();
             // this position's scales (1 where no row sees it and none were copied)
             const bool used = !edge || item_sees(P, s.keys, x);
-            const float2 by = used ? sh.pipe.scale[v_slot][tid >> P.box_log2] : make_float2(1.0f, 1.0f);
+            const float2 by = used ? sh.pipe.scale[values.slot][tid >> P.box_log2] : make_float2(1.0f, 1.0f);
             const ValueScale vs = value_scale(by.y);
             const float2 kf = make_float2(by.x, by.x), vl = make_float2(vs.log2, vs.log2), vi = make_float2(vs.inv, vs.inv);
-            // this position's scores with 16 rows from row e on
-            auto read = [&](float *z, int e) {
-                tmem_ld16(z, s_addr + b * RT + e);
-                tmem_wait_ld();
+            // from 16 rows' products (from row e on) to the logarithms of this position's weights, references aside
+            auto finish = [&](float *z, int e) {
 #pragma unroll
-                for (int y = 0; y < 16; y += 2) {
-                    const float2 m = mul2(make_float2(z[y], z[y + 1]), kf);
-                    z[y] = m.x;
-                    z[y + 1] = m.y;
+                for (int y = 0; y < 16; y += 4) {
+                    const float4 fc = *reinterpret_cast<const float4 *>(factor + e + y);
+                    const float2 a = fma2(mul2(make_float2(z[y], z[y + 1]), kf), make_float2(fc.x, fc.y), vl),
+                                 c = fma2(mul2(make_float2(z[y + 2], z[y + 3]), kf), make_float2(fc.z, fc.w), vl);
+                    z[y] = a.x;
+                    z[y + 1] = a.y;
+                    z[y + 2] = c.x;
+                    z[y + 3] = c.y;
                 }
                 if (edge) {
                     const bool in = x >= s.keys.from && x < s.keys.hi, sink = x < P.n_sink;
@@ -358,20 +348,27 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             constexpr bool kHeld = RT == 32;
             float held[kHeld ? RT : 16];
             if constexpr (kHeld) {
+                if (nrows > 16)
+                    tmem_ld32(held, s_addr + b * RT);
+                else
+                    tmem_ld16(held, s_addr + b * RT);
+                tmem_wait_ld32(held);
 #pragma unroll
                 for (int e = 0; e < RT; e += 16)
-                    if (e < nrows) read(held + e, e);
+                    if (e < nrows) finish(held + e, e);
             }
             auto scores = [&](int e) -> float * {
                 if constexpr (kHeld) return held + e;
-                read(held, e);
+                tmem_ld16(held, s_addr + b * RT + e);
+                tmem_wait_ld();
+                finish(held, e);
                 return held;
             };
             // the logarithms of four weights
             auto against = [&](const float *z, int e, float2 &a, float2 &c) {
-                const float4 rf = *reinterpret_cast<const float4 *>(nref + e), fc = *reinterpret_cast<const float4 *>(factor + e);
-                a = fma2(make_float2(z[0], z[1]), make_float2(fc.x, fc.y), add2(make_float2(rf.x, rf.y), vl));
-                c = fma2(make_float2(z[2], z[3]), make_float2(fc.z, fc.w), add2(make_float2(rf.z, rf.w), vl));
+                const float4 rf = *reinterpret_cast<const float4 *>(nref + e);
+                a = add2(make_float2(z[0], z[1]), make_float2(rf.x, rf.y));
+                c = add2(make_float2(z[2], z[3]), make_float2(rf.z, rf.w));
             };
             if (i > 0) {
                 float top = -INFINITY;
@@ -386,13 +383,13 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                             top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
                         }
                     }
-                mine |= __any_sync(0xffffffffu, top > kMost) ? 1u : 0u;
-                if (!agree<RT, false>(sh, a_phase, mine, word)) return;
-            } else {
-                word = 1u;  // the first references (the values' flag comes with their meetings)
+                mine |= __any_sync(0xffffffffu, top > kMost) ? kBeyond : 0u;
             }
-            if (!rest()) return;  // the product before this tile: the weights' memory is free, O at rest
-            if (word & 1u) {
+            mine |= gone ? kGone : 0u;
+            uint32_t word = meet_words(sh.found, mine);
+            if (word & kGone) return;
+            rest();  // the product before this tile: the weights' memory is free, O at rest
+            if (i == 0 || word & kBeyond) {
                 // new references: the rows' maxima over the tile, where they are larger
 #pragma unroll
                 for (int e = 0; e < RT; e += 16)
@@ -400,11 +397,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                         const float *z = scores(e);
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
-                            const float v = redux_max(fmaf(z[y], factor[e + y], vs.log2));
+                            const float v = redux_max(z[y]);
                             if (lane == 0) scratch.warp[warp][e + y] = v;
                         }
                     }
-                if (!agree(sh, a_phase, 0u, word)) return;
+                bar_sync(1, 128);
                 if (tid < n16) {
                     const float v = fmaxf(fmaxf(scratch.warp[0][tid], scratch.warp[1][tid]),
                                           fmaxf(scratch.warp[2][tid], scratch.warp[3][tid]));
@@ -414,7 +411,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                     scratch.row[tid] = grow && old != kNoRef ? ex2(nw - old) : 1.0f;
                     if (grow) nref[tid] = nw;
                 }
-                if (!agree(sh, a_phase, mine & 2u, word)) return;
+                bar_sync(1, 128);
                 if (i > 0) {
 #pragma unroll
                     for (int e = 0; e < RT; e += 2)
@@ -433,12 +430,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                         tmem_st16(o_addr + r0, ow);
                     }
                     tmem_wait_st();
-                    const uint32_t keep = word;
-                    if (!agree(sh, a_phase, 0u, word)) return;  // the scratch has been read
-                    word = keep;
+                    bar_sync(1, 128);  // the scratch has been read
                 }
             }
-            const bool skip = (word & 2u) != 0;
+            const bool skip = (word & kNoNumber) != 0;
             unsigned char *prow = p_tile + tid * RT;
 #pragma unroll
             for (int e = 0; e < RT; e += 16)
@@ -471,24 +466,24 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                             make_uint4(pw[0][p], pw[1][p], pw[2][p], pw[3][p]);
                 }
             if (skip) {
-                if (!agree(sh, a_phase, 0u, word)) return;  // all weights are there
+                bar_sync(1, 128);  // all weights are there
                 mixed_tile<RT>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
             }
             if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip) = skip;
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(&sh.p_full);
-            ring.step();
-            ring.step();
+            values.step();
         }
         // the next segment's queries; this one's scores have all been taken
         Ring then = desc;
         then.step();
-        if (!wait_warp(ab, &sh.pipe.desc_full[then.slot], then.phase)) return;
+        gone |= !wait_warp(ab, &sh.pipe.desc_full[then.slot], then.phase);
+        if (meet(gone)) return;
         const bool more = sh.pipe.desc[then.slot].nrows > 0;
         if (more) bring(sh.pipe.desc[then.slot], buf ^ 1);
         if (nt > 0) {
-            if (!wait_warp(ab, &sh.o_done, o_phase)) return;
+            gone |= !wait_warp(ab, &sh.o_done, o_phase);
             o_phase ^= 1u;
             tc_fence_after();
         }
@@ -513,7 +508,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             }
             scratch.warp[warp][c + lane] = v[0];
         }
-        if (!agree(sh, a_phase, 0u, word)) return;
+        if (meet(gone)) return;
         if (tid < nrows) {
             float sum = scratch.warp[0][tid] + scratch.warp[1][tid] + scratch.warp[2][tid] + scratch.warp[3][tid];
             if (pos[tid] < 0) sum = 0.0f;  // padding
@@ -532,7 +527,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                 scratch.row[tid] = none ? 0.0f : 1.0f / sum;
             }
         }
-        if (!agree(sh, a_phase, 0u, word)) return;
+        bar_sync(1, 128);
 #pragma unroll 1
         for (int r0 = 0; r0 < nrows; r0 += 4) {
             float o[4];
@@ -573,10 +568,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
 template <int RT, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, kPerSM)
     spec_attend8_round_kernel(const __grid_constant__ AttendParams P, const CacheMap M,
-                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                             const int n_stages) {
+                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char ring_mem[];  // tiles, queries, weights, the rest
-    unsigned char *q_tile = ring_mem + n_stages * kTile;
+    unsigned char *q_tile = ring_mem + stages<RT>() * kTile;
     unsigned char *p_tile = q_tile + q_bytes(RT);
     Shared<RT> &sh = *reinterpret_cast<Shared<RT> *>(p_tile + p_bytes(RT));
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
@@ -584,22 +578,13 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
 
     if (warp == 5) tmem_alloc(&sh.tmem, kColumns);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < n_stages; ++i) {
-            mbar_init(&sh.pipe.full[i], 1);
-            mbar_init(&sh.pipe.empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.pipe.desc_full[i], 1);
-            mbar_init(&sh.pipe.desc_empty[i], 5);  // four softmax warps and the issuing thread
-            mbar_init(&sh.s_full[i], 1);
-        }
+        init_pipe(sh.pipe, 1, 5);  // values: the products; segments: four softmax warps and the issuing one
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1);
         mbar_init(&sh.q_full, 128);
         mbar_init(&sh.p_full, 128);
         mbar_init(&sh.o_done, 1);
-        mbar_init(&sh.agree, 4);
         mbar_init(&sh.drain, 1);
         sh.skip = 0;
-        sh.pipe.abort = 0;
         fence_mbar_init();
         prefetch_map(&kmap);
         prefetch_map(&vmap);
@@ -610,12 +595,12 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
     begin_kernel<PREFIX>(P);
 
     if (warp < 4) {
-        softmax_role<RT, PREFIX>(P, sh, ring_mem, q_tile, p_tile, n_stages);
+        softmax_role<RT, PREFIX>(P, sh, ring_mem, q_tile, p_tile);
     } else if (warp == 4) {
-        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, n_stages, blockIdx.x, lane);
+        load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, blockIdx.x, lane);
     } else {
         if constexpr (!PREFIX) keep_books<kKT>(P, lane);
-        mma_role<RT>(P, sh, ring_mem, q_tile, p_tile, n_stages);
+        mma_role<RT>(P, sh, ring_mem, q_tile, p_tile);
         // nothing this warp issued is in flight when the CTA ends
         if (elect_lane()) mma_commit(&sh.drain);
         __syncwarp();

@@ -32,14 +32,17 @@ struct CacheMap {
     int32_t page_rows, head_rows, head_step;
 };
 
-// A ring of tiles, their scales (with the values' tile: of the keys and of the values), and the segments they
-// belong to: written by the loading warp.
-template <int STAGES>
+// A ring of key tiles and one of value tiles with their scales (of the keys and of the values), and the segments they
+// belong to: written by the loading warp. Two rings, because a tile's keys are let go as soon as its scores are
+// taken, a tile ahead of the softmax, and its values a tile's time later: in one ring of five slots, in order, three
+// tiles were on their way while one was worked on, in rings of two and three four are.
+template <int KEYS, int VALUES>
 struct Pipe {
-    uint64_t full[STAGES], empty[STAGES];
+    static constexpr int kKeys = KEYS, kValues = VALUES;
+    uint64_t k_full[KEYS], k_empty[KEYS], v_full[VALUES], v_empty[VALUES];
     uint64_t desc_full[2], desc_empty[2];
     Segment desc[2];
-    float2 scale[STAGES][kBoxes];
+    float2 scale[VALUES][kBoxes];
     int32_t abort;  // a wait gave up: everyone leaves
 };
 
@@ -72,34 +75,23 @@ __device__ __forceinline__ TilePlan plan_tile(const AttendParams &P, const Cache
     return t;
 }
 
-template <bool PREFIX, int STAGES>
+// ring_mem: the slots of keys, then those of values.
+template <bool PREFIX, int KEYS, int VALUES>
 __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap &M, const CUtensorMap *kmap,
-                                          const CUtensorMap *vmap, Pipe<STAGES> &pipe, unsigned char *ring_mem, int stages,
-                                          int worker, int lane) {
-    Ring ring = {0, stages, 0}, desc = {0, 2, 0};
+                                          const CUtensorMap *vmap, Pipe<KEYS, VALUES> &pipe, unsigned char *ring_mem, int worker,
+                                          int lane) {
+    Ring keys = {0, KEYS, 0}, values = {0, VALUES, 0}, desc = {0, 2, 0};
     Walker<kKT, PREFIX> walk;
     walk.start(P, worker, lane);
     Segment s = {};
     bool ok = true;
-    int used = 0;
-    auto copy_tile = [&](const CUtensorMap *map, const TilePlan &t, bool scales) {
-        uint64_t *full = &pipe.full[ring.slot];
-        ok = wait_warp(&pipe.abort, &pipe.empty[ring.slot], ring.phase ^ 1u);
-        if (!ok) return;
-        if (scales && t.on) {
-            const int64_t at = static_cast<int64_t>(t.page) * P.Hkv + s.head;
-            copy_word(&pipe.scale[ring.slot][lane].x, P.k_scale + at);
-            copy_word(&pipe.scale[ring.slot][lane].y, P.v_scale + at);
-            copy_words_arrive(full);  // (the phase waits for lane 0's arrival, below)
-        }
+    int used_keys = 0, used_values = 0;
+    auto copy_tile = [&](const CUtensorMap *map, const TilePlan &t, uint64_t *full, unsigned char *dst) {
         const int boxes = __popc(__ballot_sync(0xffffffffu, t.on));
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * (128 << P.box_log2)));
         __syncwarp();
-        if (t.on)
-            copy_box3(ring_mem + ring.slot * kTile + (lane << (P.box_log2 + 7)), map, 0, s.head * M.head_step, t.row, full);
-        ring.step();
-        ++used;
+        if (t.on) copy_box3(dst + (lane << (P.box_log2 + 7)), map, 0, s.head * M.head_step, t.row, full);
     };
     while (ok && walk.next(P, s, lane)) {
         ok = wait_warp(&pipe.abort, &pipe.desc_empty[desc.slot], desc.phase ^ 1u);
@@ -117,12 +109,27 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
         };
         TilePlan now;
         if (s.ntile > 0) now = plan(0);
-        for (int t = 0; ok && t < s.ntile; ++t) {
-            copy_tile(kmap, now, false);
+#pragma unroll 1
+        for (int t = 0; t < s.ntile; ++t) {
+            ok = wait_warp(&pipe.abort, &pipe.k_empty[keys.slot], keys.phase ^ 1u);
             if (!ok) break;
+            copy_tile(kmap, now, &pipe.k_full[keys.slot], ring_mem + keys.slot * kTile);
+            keys.step();
+            ++used_keys;
             TilePlan next;
             if (t + 1 < s.ntile) next = plan(t + 1);  // its page ids arrive while this tile's slot is awaited
-            copy_tile(vmap, now, true);
+            ok = wait_warp(&pipe.abort, &pipe.v_empty[values.slot], values.phase ^ 1u);
+            if (!ok) break;
+            uint64_t *full = &pipe.v_full[values.slot];
+            if (now.on) {
+                const int64_t at = static_cast<int64_t>(now.page) * P.Hkv + s.head;
+                copy_word(&pipe.scale[values.slot][lane].x, P.k_scale + at);
+                copy_word(&pipe.scale[values.slot][lane].y, P.v_scale + at);
+                copy_words_arrive(full);  // (the phase waits for lane 0's arrival, in copy_tile)
+            }
+            copy_tile(vmap, now, full, ring_mem + (KEYS + values.slot) * kTile);
+            values.step();
+            ++used_values;
             now = next;
         }
     }
@@ -134,18 +141,38 @@ __device__ __forceinline__ void load_role(const AttendParams &P, const CacheMap 
     }
     __syncwarp();
     // every copy has landed and every tile has been let go before the CTA may end
-    Ring back = {0, stages, 0};
+    auto drain = [&](uint64_t *full, uint64_t *empty, int n, int used) {
+        Ring back = {0, n, 0};
 #pragma unroll 1
-    for (int i = 0; i < used; ++i) {
-        if (i + stages >= used) {
+        for (int i = 0; i < used; ++i) {
+            if (i + n >= used) {
 #pragma unroll 1
-            for (int t = 0; t < kTries && !mbar_try_wait_sleep(&pipe.full[back.slot], back.phase, kHintNs); ++t) {
+                for (int t = 0; t < kTries && !mbar_try_wait_sleep(&full[back.slot], back.phase, kHintNs); ++t) {
+                }
+                if (ok) wait_one(&pipe.abort, &empty[back.slot], back.phase);
             }
-            if (ok) wait_one(&pipe.abort, &pipe.empty[back.slot], back.phase);
+            back.step();
         }
-        back.step();
-    }
+    };
+    drain(pipe.k_full, pipe.k_empty, KEYS, used_keys);
+    drain(pipe.v_full, pipe.v_empty, VALUES, used_values);
     __syncwarp();
+}
+template <int KEYS, int VALUES>
+__device__ __forceinline__ void init_pipe(Pipe<KEYS, VALUES> &pipe, int value_readers, int desc_readers) {
+    for (int i = 0; i < KEYS; ++i) {
+        mbar_init(&pipe.k_full[i], 1);
+        mbar_init(&pipe.k_empty[i], 1);
+    }
+    for (int i = 0; i < VALUES; ++i) {
+        mbar_init(&pipe.v_full[i], 1);
+        mbar_init(&pipe.v_empty[i], value_readers);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&pipe.desc_full[i], 1);
+        mbar_init(&pipe.desc_empty[i], desc_readers);
+    }
+    pipe.abort = 0;
 }
 
 // ---------------------------------------------------------------- queries

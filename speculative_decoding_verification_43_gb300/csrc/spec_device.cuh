@@ -146,6 +146,16 @@ __device__ __forceinline__ void st_async_v4(uint32_t remote_addr, uint4 v, uint3
 __device__ __forceinline__ void bar_sync(int id, int count) {
     asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// The same, with the answer whether `flag` is true in any of the threads.
+__device__ __forceinline__ bool bar_any(int id, int count, bool flag) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbarrier.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(count), "r"(static_cast<uint32_t>(flag))
+        : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void bar_arrive(int id, int count) {
     asm volatile("barrier.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
