@@ -45,6 +45,11 @@ static void attend8_work(AttendParams &P, bool tensor) {
         P.own_extra = extra8_units(P.own_rt_log2);
         P.prefix_extra = extra8_units(P.prefix_rt_log2);
         P.box_log2 = box_log2_of(P.page_size);
+        // A slot's heads lie side by side, 128 bytes each: read at different times they cost DRAM more than their
+        // bytes. So up to eight heads of the same positions are read in step, by workers that begin together.
+        if (P.shared_len == 0 && P.own_rt_log2 != pair8::kRTLog2)
+            while (P.head_step < 8 && P.Hkv % (2 * P.head_step) == 0) P.head_step *= 2;
+        P.own_workers -= P.own_workers % P.head_step;
     } else {
         attend_fma_work(P);
     }

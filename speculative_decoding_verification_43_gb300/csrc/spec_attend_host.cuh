@@ -145,7 +145,7 @@ static __global__ void __launch_bounds__(kJoinThreads) spec_attend_join_kernel(c
     if (r >= c.nrows || P.status[c.req] != SPEC_REQ_OK) return;
     PartRun run, none = {};
     run.n = c.parts;
-    run.pitch = 2 * P.own_pitch;
+    run.pitch = 2 * P.own_pitch * P.head_step;
     run.later = static_cast<int64_t>(2 * w) * P.own_pitch + r;
     run.base = run.later + c.slot * P.own_pitch;
     const int j = P.by_group(c.row0 + r), g = c.row0 + r - j * P.G;
@@ -269,6 +269,7 @@ static spec_status attend_sizes(const spec_attend_args *a, AttendParams &P) {
     P.window = a->window;
     P.n_sink = a->n_sink;
     P.shared_len = a->shared_len;
+    P.head_step = 1;
     P.scale_log2 = a->scale * 1.4426950408889634f;
 
     return SPEC_OK;

@@ -28,7 +28,7 @@ namespace spec {
 // (calls without a shared prefix; nrows = 0: this worker begins none).
 struct CutItem {
     int req, t0, row0, nrows, head;
-    int parts;      // workers, this one first
+    int parts;      // workers (every head_step-th), this one first
     int slot;       // this worker's slot of two; the others have their first
     int pad;
 };
@@ -61,6 +61,8 @@ struct AttendParams {
     int32_t own_rt_log2, prefix_rt_log2;  // packed rows of an item (RT), as a power of two
     int32_t own_pitch, prefix_pitch;      // rows of a worker's part
     int32_t own_extra, prefix_extra;      // units of an item beside its tiles
+    int32_t head_step;  // heads that workers side by side take in step (a divisor of Hkv and own_workers; 1 with a
+                        // shared prefix): they number the units of every head_step-th head alone
     int64_t part_rows;
 };
 
@@ -192,7 +194,7 @@ __device__ __forceinline__ Totals batch_totals(const AttendParams &P, int lane) 
                 t.pmin = min(t.pmin, max(q.kv - q.n, 0));
                 t.pmax = max(t.pmax, q.kv - 1);
             }
-            mine += P.Hkv * own_units<KT>(P, q);
+            mine += P.Hkv / P.head_step * own_units<KT>(P, q);
             wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
         }
         if (t.broken || !__any_sync(0xffffffffu, wrong)) break;
@@ -277,9 +279,9 @@ struct Walker {
             u_end = share.first(w + 1);
             i = 0;  // segments so far
         } else {
-            share = Shares(t.units, P.own_workers);
-            u = share.first(w);
-            u_end = share.first(w + 1);
+            share = Shares(t.units, P.own_workers / P.head_step);
+            u = share.first(w / P.head_step);
+            u_end = share.first(w / P.head_step + 1);
             if (u < u_end) {
                 // the lane whose requests have unit u (the last one with no more before it), then the request
                 const int l = __popc(__ballot_sync(0xffffffffu, t.before <= u)) - 1;
@@ -288,12 +290,13 @@ struct Walker {
                 for (i = l * t.per;; ++i) {
                     q = held_request(P, i, broken);
                     per_head = own_units<KT>(P, q);
-                    if (rem < P.Hkv * per_head || i + 1 >= P.B) break;
-                    rem -= P.Hkv * per_head;
+                    if (rem < P.Hkv / P.head_step * per_head || i + 1 >= P.B) break;
+                    rem -= P.Hkv / P.head_step * per_head;
                 }
                 head_tiles = row_tiles(q.n * P.G, P.own_rt_log2);
                 head = rem / per_head;
                 rem -= head * per_head;
+                head = head * P.head_step + w % P.head_step;
 #pragma unroll 1
                 for (; k + 1 < head_tiles; ++k) {
                     const int len = item_tiles(own_tiles<KT>(P, q, k)) + P.own_extra;
@@ -353,7 +356,7 @@ struct Walker {
                 const int slot = emitted > 0 ? 1 : 0;
                 s.part = whole ? -1 : static_cast<int64_t>(2 * worker + slot) * P.own_pitch;
                 if (!whole && a == 0 && b > 0 && lane == 0)
-                    P.cut[worker] = {i, q.r0, s.row0, s.nrows, head, share.owner(begin + len - 1) - worker + 1, slot, 0};
+                    P.cut[worker] = {i, q.r0, s.row0, s.nrows, head, share.owner(begin + len - 1) - worker / P.head_step + 1, slot, 0};
             }
             if constexpr (!PREFIX) {
                 u += take;
@@ -362,8 +365,8 @@ struct Walker {
                     tile = 0;
                     if (++k >= head_tiles) {
                         k = 0;
-                        if (++head >= P.Hkv) {
-                            head = 0;
+                        if ((head += P.head_step) >= P.Hkv) {
+                            head = worker % P.head_step;
                             if (u < u_end) {
 #pragma unroll 1
                                 do {
