@@ -9,9 +9,12 @@
 // on top of four (prompts: 866 us against TIME), while converting V is one for two values, and exact. 16-bit floats
 // hold weights from 2^15 down to 2^-25 to 11 bits, so a row's reference m may stay 2^8 behind its maximum.
 //
-// Scales: a column of S has its position's scales, of the key (a factor of the score) and of the value (its
-// logarithm goes into the weight, and its reciprocal into the row's sum, as in spec_attend8_round.cuh). The
-// converting warps leave both per box of slots, and set the values of positions that no row sees to 0.
+// Scales: a column of S has its key's scale as a factor, the same for a box of at least eight columns. The values'
+// scales are applied where the values are converted, as fractions of the tile's largest (rounded up to a power of
+// two, 2^u): a product of e4m3 and such a fraction is a 16-bit float exactly, or to 11 bits where the scales are no
+// powers of two, or to 2^-25 of 2^u. A tile's weights are 2^(S + u - m), so that what counts is what they contribute,
+// and its part of a row's sum is 2^-u times theirs. The converting warps also set the values of positions that no row
+// sees to 0.
 //
 // Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 issues matrix instructions, 10 and 11 convert values
 // (11 keeps the books first: the requests' status).
@@ -39,7 +42,8 @@ struct Shared {
     uint32_t skip[2];                   // the warpgroup does this tile's second product itself
     uint32_t no_number[2][2];           // per slot of values and converting warp: it has found a NaN
     uint32_t tmem;
-    alignas(16) float4 by[2][kBoxes];   // per slot of values and box: key scale, log2 of the value scale, its reciprocal
+    alignas(16) float key_scale[2][kBoxes];  // per slot of values and eight columns
+    float unit[2];                      // per slot of values: log2 of what they are to be taken times
     float factor[2][kRows];             // of the rows' scores
 };
 
@@ -105,8 +109,10 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
             for (int t = 0; t < nt; ++t) {
                 const bool more = t + 1 < nt;
                 const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
-                if (!wait_warp(ab, &sh.v_full[values.slot], values.phase)) return;
-                if (more && !wait_warp(ab, &sh.pipe.k_full[ring.slot], ring.phase)) return;
+                // (this warp has waited for every use of these slots before)
+                if (!(more ? wait_two(ab, &sh.v_full[values.slot], values.phase, &sh.pipe.k_full[ring.slot], ring.phase)
+                           : wait_warp(ab, &sh.v_full[values.slot], values.phase)))
+                    return;
 #pragma unroll 1
                 for (int w = 0; w < accs; ++w) {
                     if (!wait_warp(ab, &sh.p_full[w][0], p_phases >> w & 1u)) return;
@@ -155,7 +161,7 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
                                              const unsigned char *ring_mem, int which, int lane) {
     int32_t *ab = &sh.pipe.abort;
     Ring ring = {0, kStages / 2, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
-    const int c = lane & 7, half = c >> 2;
+    const int c = lane & 7;
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -167,35 +173,65 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
             const bool edge = edge_tile(P, s, x0);
             if (!wait_warp(ab, &sh.v_empty[values.slot], values.phase ^ 1u)) return;
             if (!wait_warp(ab, &sh.pipe.v_full[ring.slot], ring.phase)) return;
-            if (which == 0 && lane < kKT >> P.box_log2) {
-                // (no scales were copied for boxes that no row sees)
-                const bool used = !edge || item_sees(P, s.keys, x0 + (lane << P.box_log2), 1 << P.box_log2);
-                const float2 by = used ? sh.pipe.scale[ring.slot][lane] : make_float2(1.0f, 1.0f);
-                const ValueScale vs = value_scale(by.y);
-                sh.by[values.slot][lane] = make_float4(by.x, vs.log2, vs.inv, 0.0f);
+            // lane x < 16: eight positions (no scales were copied for boxes that no row sees)
+            const float2 *scales = sh.pipe.scale[ring.slot];
+            const int group = lane & (kBoxes - 1);
+            const bool used = !edge || item_sees(P, s.keys, x0 + 8 * group >> P.box_log2 << P.box_log2, 1 << P.box_log2);
+            const float2 by = used ? scales[8 * group >> P.box_log2] : make_float2(1.0f, 0.0f);
+            // the least power of two that is no less than any of them
+            const float most = redux_max(by.y > 0.0f && by.y < INFINITY ? by.y : 0.0f);
+            const uint32_t bits = __float_as_uint(most);
+            const int unit = most > 0.0f ? static_cast<int>(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0) : 0;
+            const float by_unit = ex2(static_cast<float>(-unit));
+            if (which == 0 && lane < kBoxes) {
+                sh.key_scale[values.slot][lane] = by.x;
+                if (lane == 0) sh.unit[values.slot] = static_cast<float>(unit);
             }
-            // 16 values a lane at a time, eight lanes a row: two pieces of eight 16-bit floats in the row's block, the
-            // blocks' lanes taking them in opposite order so that eight lanes write to all banks
+            // 16 values a lane, eight lanes a row: two pieces of eight 16-bit floats in the row's block of columns
             const unsigned char *from = ring_mem + (kStages / 2 + ring.slot) * kTile;
-            unsigned char *to = v_mem + values.slot * kValues + half * kBlock;
+            unsigned char *to = v_mem + values.slot * kValues + (c >> 2) * kBlock;
+            const int piece = (c & 3) * 2, first = which * 4 + (lane >> 3);
             uint32_t found = 0u;
+            auto fetch = [&](int r, uint4 &v, float &share) {
+                v = *reinterpret_cast<const uint4 *>(from + r * 128 + ((c ^ (r & 7)) << 4));
+                share = scales[r >> P.box_log2].y * by_unit;
+            };
+            auto put = [&](int r, const uint4 &v, float share) {
+                const __half2 times = __float2half2_rn(share);
+                auto scaled = [&](uint32_t e) -> uint32_t {
+                    const uint32_t h = e4m3_to_half2(e);
+                    const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(h), times);
+                    return reinterpret_cast<const uint32_t &>(y);
+                };
+                unsigned char *row = to + r * 128;
+                *reinterpret_cast<uint4 *>(row + ((piece ^ (r & 7)) << 4)) =
+                    make_uint4(scaled(v.x), scaled(v.x >> 16), scaled(v.y), scaled(v.y >> 16));
+                *reinterpret_cast<uint4 *>(row + (((piece + 1) ^ (r & 7)) << 4)) =
+                    make_uint4(scaled(v.z), scaled(v.z >> 16), scaled(v.w), scaled(v.w >> 16));
+            };
             if (c < P.D / 16) {
-#pragma unroll 4
-                for (int r = which * 4 + (lane >> 3); r < n; r += 8) {
-                    uint4 v = *reinterpret_cast<const uint4 *>(from + r * 128 + ((c ^ (r & 7)) << 4));
-                    if (edge) {
-                        if (!item_sees(P, s.keys, x0 + r)) v = make_uint4(0u, 0u, 0u, 0u);
+                if (!edge) {
+                    // (half of a warp's rows at a time: their loads are under way together)
+#pragma unroll 1
+                    for (int r = first; r < kKT; r += 64) {
+                        uint4 v[8];
+                        float share[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) fetch(r + 8 * i, v[i], share[i]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) put(r + 8 * i, v[i], share[i]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int r = first; r < n; r += 8) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        float share = 0.0f;
+                        if (item_sees(P, s.keys, x0 + r)) fetch(r, v, share);
+                        found |= isfinite(share) ? 0u : 1u;
                         found |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                                  __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        put(r, v, share);
                     }
-                    const uint4 lo = make_uint4(e4m3_to_half2(v.x), e4m3_to_half2(v.x >> 16), e4m3_to_half2(v.y),
-                                                e4m3_to_half2(v.y >> 16)),
-                                hi = make_uint4(e4m3_to_half2(v.z), e4m3_to_half2(v.z >> 16), e4m3_to_half2(v.w),
-                                                e4m3_to_half2(v.w >> 16));
-                    unsigned char *row = to + r * 128;
-                    const int piece = (c & 3) * 2;
-                    *reinterpret_cast<uint4 *>(row + (((piece + half) ^ (r & 7)) << 4)) = half ? hi : lo;
-                    *reinterpret_cast<uint4 *>(row + (((piece + 1 - half) ^ (r & 7)) << 4)) = half ? lo : hi;
                 }
             }
             found = __any_sync(0xffffffffu, found != 0u);
@@ -335,13 +371,15 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             for (int i = 0; i < nt; ++i) {
                 const int x0 = tile_begin<kKT>(keys, first + i), n = tile_keys(keys, x0);
                 const bool edge = x0 > whole || x0 < from || (x0 <= cut && x0 + kKT > P.n_sink);
-                if (!wait_warp(ab, &sh.s_full[w], s_phase)) return;
+                // A wait by parity tells this use of a slot of values from the one before, two tiles ago, once that one is
+                // known to have arrived: its products were issued before these scores. So what an early look at the values
+                // says counts only if the scores are there, looked at first.
+                if (!wait_two(ab, &sh.s_full[w], s_phase, &sh.v_full[values.slot], values.phase)) return;
                 s_phase ^= 1u;
-                // A wait by parity tells this use of a slot of values from the one before, two tiles ago, as that one is
-                // known to have arrived: its products were issued before these scores.
-                if (!wait_warp(ab, &sh.v_full[values.slot], values.phase)) return;
                 tc_fence_after();
                 const unsigned char *v_tile = v_mem + values.slot * kValues;
+                const float *key_scale = sh.key_scale[values.slot];
+                const float unit = sh.unit[values.slot], by_unit = ex2(-unit);
                 const bool skip = edge && (sh.no_number[values.slot][0] | sh.no_number[values.slot][1]) != 0;
                 // (the tile before has been read out of this word: its products were issued before S)
                 if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
@@ -355,17 +393,17 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         if (nu > 32) tmem_ld32(z + 32, s_at + 32);
                         tmem_wait_ld32(z);
                         tmem_wait_ld32(z + 32);
-                        // scores in base 2, and the scales' logarithms with them: eight columns share them
-                        float inv[8];
+                        // the weights' logarithms under the reference that there is; eight columns share a scale
+                        const float less = unit - (m == -INFINITY ? 0.0f : m);
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float4 by = sh.by[values.slot][(u * kHalf + 8 * c) >> P.box_log2];
-                            inv[c] = by.z;
-                            const float kf = by.x * factor;
+                        for (int c = 0; c < 8; c += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4 *>(key_scale + u * (kHalf / 8) + c);
+                            const float k[4] = {k4.x * factor, k4.y * factor, k4.z * factor, k4.w * factor};
 #pragma unroll
-                            for (int e = 8 * c; e < 8 * c + 8; e += 2) {
-                                const float2 y = fma2(make_float2(z[e], z[e + 1]), make_float2(kf, kf), make_float2(by.y, by.y));
+                            for (int e = 8 * c; e < 8 * c + 32; e += 2) {
+                                const float kf = k[e / 8 - c];
+                                const float2 y = fma2(make_float2(z[e], z[e + 1]), make_float2(kf, kf), make_float2(less, less));
                                 z[e] = y.x;
                                 z[e + 1] = y.y;
                             }
@@ -385,15 +423,15 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                             mx[3] = fmaxf(mx[3], fmaxf(z[e + 6], z[e + 7]));
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        // a new reference when the old one is too low (or there was none): m is kTop below it
-                        const bool grow = top > m && !(top - m <= kMost) && have;
+                        // a new reference when the old one is too low (or there was none): the largest weight is 2^kTop
+                        const bool grow = have && (m == -INFINITY ? top > -INFINITY : top > kMost);
                         if (__any_sync(0xffffffffu, grow)) {
                             if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
                                 // O is at rest: with S came the end of the tiles before, and the first half's
                                 // product has a barrier of its own
                                 if (u > 0 && !wait_warp(ab, &sh.o_half[w], half_phase)) return;
                                 tc_fence_after();
-                                const float a = grow && m != -INFINITY ? ex2(m - (top - kTop)) : 1.0f;
+                                const float a = grow && m != -INFINITY ? ex2(kTop - top) : 1.0f;
                                 l *= a;
 #pragma unroll 1
                                 for (int d = 0; d < P.D; d += 16) {
@@ -407,24 +445,27 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                                 }
                                 tmem_wait_st();
                             }
-                            if (grow) m = top - kTop;
+                            const float by = grow ? kTop - top : 0.0f;
+                            if (grow) m = (m == -INFINITY ? 0.0f : m) - by;
+#pragma unroll
+                            for (int e = 0; e < 64; e += 2) {
+                                const float2 y = add2(make_float2(z[e], z[e + 1]), make_float2(by, by));
+                                z[e] = y.x;
+                                z[e + 1] = y.y;
+                            }
                         }
-                        const float ref = m == -INFINITY ? 0.0f : -m;
-                        const float2 rf = make_float2(ref, ref);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                         uint32_t pw[32];
 #pragma unroll
                         for (int e = 0; e < 64; e += 2) {
-                            float2 y = add2(make_float2(z[e], z[e + 1]), rf);
-                            y.x = ex2(y.x);
-                            y.y = ex2(y.y);
-                            sum[e / 2 & 1] = fma2(y, make_float2(inv[e >> 3], inv[e >> 3]), sum[e / 2 & 1]);
+                            const float2 y = make_float2(ex2(z[e]), ex2(z[e + 1]));
+                            sum[e / 2 & 1] = add2(sum[e / 2 & 1], y);
                             pw[e / 2] = pack_f16(y.x, y.y);
                             if (e == 30) tmem_st16(s_at, pw);  // over columns that have been read
                         }
                         tmem_st16(s_at + 16, pw + 16);
                         sum[0] = add2(sum[0], sum[1]);
-                        l += sum[0].x + sum[0].y;
+                        l += (sum[0].x + sum[0].y) * by_unit;
                         tmem_wait_st();
                         if (skip) {
                             if (u > 0 && !wait_warp(ab, &sh.o_half[w], half_phase)) return;

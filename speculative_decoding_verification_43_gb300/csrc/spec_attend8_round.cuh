@@ -307,15 +307,14 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             };
             // The scales come with the values. (A wait by parity cannot take the use of the slot before for this one: that
             // was two tiles ago or more, and the product of its values has been waited for.)
-            auto landed = [&]() { gone |= !wait_warp(ab, &sh.pipe.v_full[values.slot], values.phase); };
             if (edge) {
-                landed();
+                gone |= !wait_warp(ab, &sh.pipe.v_full[values.slot], values.phase);
                 if (__any_sync(0xffffffffu, clean_values(P, s, v_tile, x0, n, tid))) mine = kNoNumber;
                 fence_proxy_async_smem();
             }
-            gone |= !wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u);
+            gone |= !(edge ? wait_warp(ab, &sh.s_full[b], s_phases >> b & 1u)
+                           : wait_two(ab, &sh.s_full[b], s_phases >> b & 1u, &sh.pipe.v_full[values.slot], values.phase));
             s_phases ^= 1u << b;
-            if (!edge) landed();
             tc_fence_after();
             // this position's scales (1 where no row sees it and none were copied)
             const bool used = !edge || item_sees(P, s.keys, x);
