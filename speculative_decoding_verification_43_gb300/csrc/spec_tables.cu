@@ -35,10 +35,11 @@ struct TableParams {
     TableBooks books;  // in the workspace (unused by the single block)
 };
 
-constexpr int kTableThreads = 1024, kTableWarps = kTableThreads / kWarp;
-constexpr int kTableOne = 1024;      // requests that one block keeps the books of in shared memory,
-constexpr int kTableOneRows = 4096;  // and rows that it goes through by itself
-constexpr int kFillThreads = 256;
+constexpr int kTableThreads = 512, kTableWarps = kTableThreads / kWarp;
+// What one block does by itself, its books in shared memory: so many requests, rows, and entries of all tables (how
+// many change is not known here). Larger calls leave entries and rows to a second kernel.
+constexpr int kTableOne = kTableThreads, kTableOneRows = 2048, kTableOneEntries = 1 << 16;
+constexpr int kFillThreads = 256, kRowsAtOnce = 4;
 
 // A request's pages: what it holds, shall hold, takes and gives back.
 struct TableRequest {
@@ -77,14 +78,14 @@ __device__ __forceinline__ int3 block_sums(int3 v, int3 &total, int3 *warps) {
     if (lane == kWarp - 1) warps[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        int3 w = warps[lane];
+        int3 w = lane < kTableWarps ? warps[lane] : make_int3(0, 0, 0);
 #pragma unroll
         for (int o = 1; o < kWarp; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o),
                       z = __shfl_up_sync(0xffffffffu, w.z, o);
             if (lane >= o) w = make_int3(w.x + x, w.y + y, w.z + z);
         }
-        warps[lane] = w;
+        if (lane < kTableWarps) warps[lane] = w;
     }
     __syncthreads();
     total = warps[kTableWarps - 1];
@@ -123,25 +124,42 @@ __device__ __forceinline__ int table_entry(const TableParams &P, const TableBook
 }
 
 // The tables' new entries, the pages given back, and the rows, by threads first, first + step, ..
+template <int AT_ONCE>
 __device__ __forceinline__ void table_fill(const TableParams &P, const TableBooks &K, const int32_t *row_off, int first,
                                            int step) {
-    // rows first: theirs is the longer chain
+    // rows first: theirs is the longer chain; a thread takes a few in a row, which mostly share request and page
 #pragma unroll 1
-    for (int r = first; r < P.T; r += step) {
-        const int i = find_request(row_off, P.B, P.T, r);
-        const int r0 = row_off[i], r1 = row_off[i + 1], kv = P.kv_len[i];
-        if (!offsets_right(r0, r1, P.T) || r < r0 || r >= r1) continue;
-        if (K.all[2] && offsets_contradict(row_off, P.B, P.T, i, r0, r1, 0, 1)) continue;
-        const int64_t at = static_cast<int64_t>(kv) - (r1 - r0) + (r - r0);
-        const int p = kv < 0 || at < 0 ? -1 : static_cast<int>(at), b = p < 0 ? 0 : P.by_page(p);
-        int slot = -1;
-        if (p >= 0 && b < K.need[i]) {
-            const int page = table_entry(P, K, i, b);
-            if (page >= 0 && page < P.n_pages) slot = page * P.page_size + (p - b * P.page_size);
+    for (int r0 = first * AT_ONCE; r0 < P.T; r0 += step * AT_ONCE) {
+        int i = -1, begin = 0, end = 0, kv = 0, need = 0, blk = -1, page = -1;
+        bool mine = false;
+#pragma unroll 1
+        for (int r = r0; r < min(r0 + AT_ONCE, P.T); ++r) {
+            if (i < 0 || r >= end) {
+                i = find_request(row_off, P.B, P.T, r);
+                begin = row_off[i];
+                end = row_off[i + 1];
+                mine = offsets_right(begin, end, P.T) && r >= begin && r < end &&
+                       !(K.all[2] && offsets_contradict(row_off, P.B, P.T, i, begin, end, 0, 1));
+                if (!mine) end = r + 1;
+                kv = P.kv_len[i];
+                need = K.need[i];
+                blk = -1;
+            }
+            if (!mine) continue;
+            const int64_t at = static_cast<int64_t>(kv) - (end - begin) + (r - begin);
+            const int p = kv < 0 || at < 0 ? -1 : static_cast<int>(at), b = p < 0 ? 0 : P.by_page(p);
+            int slot = -1;
+            if (p >= 0 && b < need) {
+                if (b != blk) {
+                    blk = b;
+                    page = table_entry(P, K, i, b);
+                }
+                if (page >= 0 && page < P.n_pages) slot = page * P.page_size + (p - b * P.page_size);
+            }
+            if (!SPEC_IN(r, P.T, DBG_OUT_ROWS)) continue;
+            if (P.slot_map) P.slot_map[r] = slot;
+            if (P.positions) P.positions[r] = p;
         }
-        if (!SPEC_IN(r, P.T, DBG_OUT_ROWS)) continue;
-        if (P.slot_map) P.slot_map[r] = slot;
-        if (P.positions) P.positions[r] = p;
     }
     const int fresh = K.fresh[P.B], back = K.all[1];
 #pragma unroll 1
@@ -180,38 +198,51 @@ __global__ void __launch_bounds__(kTableThreads) spec_tables_kernel(const __grid
         }
     }
     const int n_free = *P.n_free;
-    // what comes back in all, and whether some offsets are wrong
+    const bool pool = n_free >= 0 && n_free <= P.n_pages;
+    TableRequest own = {};  // (one block: the thread's request)
     bool wrong = false;
-    int3 carry = make_int3(0, 0, 0), total;
-#pragma unroll 1
-    for (int i0 = 0; i0 < P.B; i0 += kTableThreads) {
-        const int i = i0 + tid;
-        int3 v = make_int3(0, 0, 0);
-        if (i < P.B) {
-            v.x = table_request(P, i).back;
-            if (P.T > 0) wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
+    int3 carry = make_int3(0, 0, 0), total = make_int3(0, 0, 0), s = make_int3(0, 0, 0);
+    auto counts = [](const TableRequest &r) { return make_int3(r.take, r.back, max(r.need - r.held, 0)); };
+    // what comes back in all, and whether some offsets are wrong
+    int back;
+    if constexpr (ONE) {
+        if (tid < P.B) {
+            own = table_request(P, tid);
+            if (P.T > 0) wrong = !offsets_right(P.row_off[tid], P.row_off[tid + 1], P.T);
         }
-        block_sums(v, total, warps);
-        carry.x += total.x;
+        s = block_sums(counts(own), total, warps);
+        back = total.y;
+    } else {
+#pragma unroll 1
+        for (int i0 = 0; i0 < P.B; i0 += kTableThreads) {
+            const int i = i0 + tid;
+            int3 v = make_int3(0, 0, 0);
+            if (i < P.B) {
+                v.y = table_request(P, i).back;
+                if (P.T > 0) wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
+            }
+            block_sums(v, total, warps);
+            carry.y += total.y;
+        }
+        back = carry.y;
+        carry = make_int3(0, 0, 0);
     }
     const bool broken = __syncthreads_or(wrong) != 0;
-    const bool pool = n_free >= 0 && n_free <= P.n_pages, room = pool && carry.x <= P.n_pages - n_free;
-    const int back = room ? carry.x : 0, avail = pool ? n_free + back : 0;
-    carry = make_int3(0, 0, 0);
+    const bool room = pool && back <= P.n_pages - n_free;
+    if (!room) back = 0;
+    const int avail = pool ? n_free + back : 0;
     int taken = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < P.B; i0 += kTableThreads) {
         const int i = i0 + tid;
-        TableRequest r = {};
-        if (i < P.B) {
-            r = table_request(P, i);
-            if (r.back > 0 && !room) {
-                r.status = SPEC_REQ_BAD_BLOCKS;
-                r.need = r.held;
-                r.back = 0;
-            }
+        TableRequest r = own;
+        if (!ONE && i < P.B) r = table_request(P, i);
+        if (r.back > 0 && !room) {
+            r.status = SPEC_REQ_BAD_BLOCKS;
+            r.need = r.held;
+            r.back = 0;
         }
-        const int3 s = block_sums(make_int3(r.take, r.back, max(r.need - r.held, 0)), total, warps);
+        if (!ONE || !room) s = block_sums(counts(r), total, warps);
         if (i < P.B) {
             const int before = carry.x + s.x;
             K.take[i] = before;
@@ -250,7 +281,7 @@ __global__ void __launch_bounds__(kTableThreads) spec_tables_kernel(const __grid
         for (int w = 0; w < kTableWarps; ++w) taken = max(taken, warps[w].x);
         if (pool) *P.n_free = avail - taken;
     }
-    if constexpr (ONE) table_fill(P, K, row_off, tid, kTableThreads);
+    if constexpr (ONE) table_fill<1>(P, K, row_off, tid, kTableThreads);
     // (a request's own count is read by its own thread, above)
 #pragma unroll 1
     for (int i = tid; i < P.B; i += kTableThreads)
@@ -260,7 +291,7 @@ __global__ void __launch_bounds__(kTableThreads) spec_tables_kernel(const __grid
 __global__ void __launch_bounds__(kFillThreads) spec_tables_fill_kernel(const __grid_constant__ TableParams P) {
     griddep_launch_dependents();
     griddep_wait();
-    table_fill(P, P.books, P.row_off, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
+    table_fill<kRowsAtOnce>(P, P.books, P.row_off, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
 }
 
 static spec_status table_sizes(const spec_block_tables_args *a) {
@@ -272,7 +303,10 @@ static spec_status table_sizes(const spec_block_tables_args *a) {
         return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
 }
-static bool one_block(const spec_block_tables_args *a) { return a->B <= kTableOne && a->total_rows <= kTableOneRows; }
+static bool one_block(const spec_block_tables_args *a) {
+    return a->B <= kTableOne && a->total_rows <= kTableOneRows &&
+           static_cast<int64_t>(a->B) * a->max_blocks <= kTableOneEntries;
+}
 
 }  // namespace spec
 
