@@ -26,7 +26,7 @@ struct Append8Params : AppendParams {
     int32_t page_units, q_units;  // warps of pages and of query rows; the requests' status after them
 };
 
-constexpr int kAppend8Threads = 256, kAppend8Warps = kAppend8Threads / kWarp;
+constexpr int kAppend8Threads = 256, kAppend8Warps = kAppend8Threads / kWarp, kLookAlone = 256;
 
 // Pages that a call touches, as candidates: request i's page number k is candidate
 //     2 i + row_off[i] / page_size + k.
@@ -101,16 +101,19 @@ __device__ __forceinline__ void turn(const AppendParams &P, const Task<V, INTER>
     }
 }
 
-// V values to e4m3 at p. x + 0 x is x, and not a number where x is not finite.
+// V values to e4m3 at p. strange: there is an infinity among the unit's values, which must become NaN as well (x + 0 x
+// is x, and not a number where x is not finite).
 template <int V>
-__device__ __forceinline__ void store8(unsigned char *p, const float (&x)[V], float scale, float inv) {
+__device__ __forceinline__ void store8(unsigned char *p, const float (&x)[V], float scale, float inv, bool strange) {
     float y[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        // (a power of two: the product is the quotient)
-        const float z = inv != 0.0f ? x[e] * inv : __fdiv_rn(x[e], scale);
-        y[e] = fmaf(x[e], 0.0f, z);
-    }
+    for (int e = 0; e < V; ++e) y[e] = x[e] * inv;
+    if (inv == 0.0f)  // (no power of two: the product would not be the quotient)
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = __fdiv_rn(x[e], scale);
+    if (strange)
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = fmaf(x[e], 0.0f, y[e]);
     if constexpr (V == 1) {
         *p = static_cast<unsigned char>(to_e4m3(y[0], 0.0f));
     } else {
@@ -129,101 +132,111 @@ __device__ __forceinline__ float exact_reciprocal(float s) {
     const uint32_t b = __float_as_uint(s), e = b >> 23;
     return (b & 0x7fffffu) == 0 && e >= 1 && e <= 253 ? __uint_as_float((254u - e) << 23) : 0.0f;
 }
+// The largest magnitude, NaN aside. finite: infinities aside too.
 template <int V>
-__device__ __forceinline__ float top_of(const float (&x)[V], float top) {
+__device__ __forceinline__ float top_of(const float (&x)[V], float top, bool finite) {
+    if (!finite) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) top = isfinite(x[e]) ? fmaxf(top, fabsf(x[e])) : top;
+        for (int e = 0; e < V; ++e) top = fmaxf(top, fabsf(x[e]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) top = isfinite(x[e]) ? fmaxf(top, fabsf(x[e])) : top;
+    }
     return top;
 }
-
-// The values of one head in one page, by a warp: rows [row, row + n) at positions x0 .., `kept` earlier slots of
-// the page. KEYS: turned on the way. Up to kHold iterations' values stay in registers between the maximum and the
-// store; more are read (from L1 or L2) and turned again.
+// The values of one head in one page, by a warp: rows [row, row + n) at positions x0 .., `kept` earlier slots of the
+// page. KEYS: turned on the way. A lane has one part of the head's row (or one after the other) for every r_step-th
+// row. The first kHold rows' loads are under way together, and their values stay in registers until the scale is known;
+// more are read and turned again (from L1 or L2).
 template <typename E, int V, bool INTER, bool KEYS>
-__device__ __forceinline__ void append_page(const Append8Params &P, int head, int row, int n, int x0, int64_t slot, int kept,
-                                            int64_t page, int lane) {
+__device__ __forceinline__ void append_page(const Append8Params &P, int head, int row, int n, int x0, int kept, int page,
+                                            int lane) {
     using Vec = Piece<E, V>;
     constexpr bool kTwo = KEYS && Task<V, INTER>::kPairs;
     constexpr int kHold = V == 1 ? 4 : 32 / (kTwo ? 2 * V : V);
-    const FastDiv &by = KEYS ? P.by_k : P.by_v;
-    const int per = KEYS ? Task<V, INTER>::kPairs ? P.D / V - P.rot / 2 / V : P.D / V : P.D / V;
-    const int total = n * per;
-    const E *src = static_cast<const E *>(KEYS ? P.k : P.v) + static_cast<int64_t>(head) * P.D;
+    const int per = KEYS && Task<V, INTER>::kPairs ? P.D / V - P.rot / 2 / V : P.D / V;
+    const int cols = min(per, kWarp), r_first = lane / cols, r_step = kWarp / cols, x_first = lane - r_first * cols;
+    const int rows = r_first < r_step ? n : 0;  // (lanes that are left over have none)
     const int64_t stride = KEYS ? P.k_stride : P.v_stride;
-    unsigned char *cache = static_cast<unsigned char *>(KEYS ? P.k_cache : P.v_cache) + slot + head * P.head_stride;
-    float *scale_at = (KEYS ? P.k_scale : P.v_scale) + page * P.Hkv + head;
-    const float old = kept > 0 ? *scale_at : 0.0f;
+    const E *src = static_cast<const E *>(KEYS ? P.k : P.v) + row * stride + static_cast<int64_t>(head) * P.D;
 
-    auto fetch = [&](int idx, Vec &a, Vec &b) {
-        const int r = by(idx);
-        const Task<V, INTER> t(P, idx - r * per, KEYS);
-        const E *p = src + (row + r) * stride;
+    auto fetch = [&](const Task<V, INTER> &t, int r, Vec &a, Vec &b) {
+        const E *p = src + r * stride;
         a = *reinterpret_cast<const Vec *>(p + t.d0);
         if (kTwo && t.two) b = *reinterpret_cast<const Vec *>(p + t.d1);
     };
-    auto values = [&](int idx, const Vec &a, const Vec &b, float (&u)[V], float (&w)[V]) {
-        const int r = by(idx);
-        const Task<V, INTER> t(P, idx - r * per, KEYS);
+    auto values = [&](const Task<V, INTER> &t, int r, const Vec &a, const Vec &b, float (&u)[V], float (&w)[V]) {
         unpack(a, u);
-        if (kTwo && t.two)
-            unpack(b, w);
-        else
-#pragma unroll
-            for (int e = 0; e < V; ++e) w[e] = 0.0f;
+        if constexpr (kTwo) unpack(b, w);  // (zeros with a single piece)
         if constexpr (KEYS) turn<V, INTER>(P, t, x0 + r, u, w);
     };
-    auto put = [&](int idx, const float (&u)[V], const float (&w)[V], float scale, float inv) {
-        const int r = by(idx);
-        const Task<V, INTER> t(P, idx - r * per, KEYS);
+    Task<V, INTER> first(P, x_first, KEYS);
+    Vec a[kHold], b[kTwo ? kHold : 1];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        a[i] = {};
+        b[kTwo ? i : 0] = {};
+        if (r_first + i * r_step < rows) fetch(first, r_first + i * r_step, a[i], b[kTwo ? i : 0]);
+    }
+    if (page < 0) return;  // (its number has been on its way with the values)
+    const int64_t slot = page * P.page_stride;
+    unsigned char *cache = static_cast<unsigned char *>(KEYS ? P.k_cache : P.v_cache) + slot + head * P.head_stride;
+    float *scale_at = (KEYS ? P.k_scale : P.v_scale) + static_cast<int64_t>(page) * P.Hkv + head;
+    const float old = kept > 0 ? *scale_at : 0.0f;
+
+    float u[kHold][V], w[kTwo ? kHold : 1][V];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+        if (i * r_step < n) values(first, min(r_first + i * r_step, n - 1), a[i], b[kTwo ? i : 0], u[i], w[kTwo ? i : 0]);
+    // calls f(task, row, values) for all of the lane's
+    auto all = [&](auto &&f) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            if (r_first + i * r_step < rows) f(first, r_first + i * r_step, u[i], w[kTwo ? i : 0]);
+        if (kHold * r_step < n || per > kWarp) {
+#pragma unroll 1
+            for (int x = x_first; x < per; x += kWarp) {
+                const Task<V, INTER> t(P, x, KEYS);
+#pragma unroll 2
+                for (int r = r_first + (x == x_first ? kHold * r_step : 0); r < rows; r += r_step) {
+                    Vec c = {}, d = {};
+                    float y[V], z[V];
+                    fetch(t, r, c, d);
+                    values(t, r, c, d, y, z);
+                    f(t, r, y, z);
+                }
+            }
+        }
+    };
+    float top = 0.0f;
+    bool strange = false;
+#pragma unroll 1
+    for (;;) {  // once; twice with an infinity
+        top = 0.0f;
+        all([&](const Task<V, INTER> &t, int, const float (&y)[V], const float (&z)[V]) {
+            top = top_of<V>(y, top, strange);
+            if (kTwo && t.two) top = top_of<V>(z, top, strange);
+        });
+        top = warp_max(top);
+        if (top < INFINITY) break;
+        strange = true;
+    }
+    const float scale = fmaxf(e4m3_scale(top), old), inv = exact_reciprocal(scale);
+    if (lane == 0 && scale != old) *scale_at = scale;
+    all([&](const Task<V, INTER> &t, int r, const float (&u)[V], const float (&w)[V]) {
         unsigned char *p = cache + (kept + r) * P.slot_stride;
         auto inside = [&](int d) -> bool {
             return SPEC_IN(d + V - 1, P.D, DBG_CACHE) &&
                    SPEC_IN(slot + (kept + r) * P.slot_stride + head * P.head_stride + d + V - 1, cache_extent(P), DBG_CACHE);
         };
-        if (inside(t.d0)) store8<V>(p + t.d0, u, scale, inv);
-        if (kTwo && t.two && inside(t.d1)) store8<V>(p + t.d1, w, scale, inv);
-    };
-
-    Vec a[kHold] = {}, b[kTwo ? kHold : 1] = {};
-    float u[kHold][V], w[kTwo ? kHold : 1][V];
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-        if (i * kWarp + lane < total) fetch(i * kWarp + lane, a[i], b[kTwo ? i : 0]);
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-        if (i * kWarp + lane < total) {
-            values(i * kWarp + lane, a[i], b[kTwo ? i : 0], u[i], w[kTwo ? i : 0]);
-            top = top_of<V>(u[i], top);
-            if constexpr (kTwo) top = top_of<V>(w[i], top);
-        }
-#pragma unroll 4
-    for (int idx = kHold * kWarp + lane; idx < total; idx += kWarp) {
-        Vec c, d = {};
-        float x[V], y[V];
-        fetch(idx, c, d);
-        values(idx, c, d, x, y);
-        top = top_of<V>(x, top);
-        if constexpr (kTwo) top = top_of<V>(y, top);
-    }
-    const float scale = fmaxf(e4m3_scale(warp_max(top)), old), inv = exact_reciprocal(scale);
-    if (lane == 0 && scale != old) *scale_at = scale;
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-        if (i * kWarp + lane < total) put(i * kWarp + lane, u[i], w[kTwo ? i : 0], scale, inv);
-#pragma unroll 4
-    for (int idx = kHold * kWarp + lane; idx < total; idx += kWarp) {
-        Vec c, d = {};
-        float x[V], y[V];
-        fetch(idx, c, d);
-        values(idx, c, d, x, y);
-        put(idx, x, y, scale, inv);
-    }
+        if (inside(t.d0)) store8<V>(p + t.d0, u, scale, inv, strange);
+        if (kTwo && t.two && inside(t.d1)) store8<V>(p + t.d1, w, scale, inv, strange);
+    });
     if (kept > 0 && scale != old) {
         // the earlier tokens' values under the new scale
         const float by_old = __fdiv_rn(old, scale);
         const int pieces = P.D / V;
-#pragma unroll 4
+#pragma unroll 1
         for (int idx = lane; idx < kept * pieces; idx += kWarp) {
             const int r = P.by_v(idx), d = (idx - r * pieces) * V;
             if (!SPEC_IN(slot + r * P.slot_stride + head * P.head_stride + d + V - 1, cache_extent(P), DBG_CACHE)) continue;
@@ -243,28 +256,33 @@ __device__ __forceinline__ void append_page(const Append8Params &P, int head, in
             }
 #pragma unroll
             for (int e = 0; e < V; ++e) x[e] *= by_old;
-            store8<V>(p, x, 1.0f, 1.0f);
+            store8<V>(p, x, 1.0f, 1.0f, false);
         }
     }
 }
 
-// A warp's work is a page's keys or values of one head (a candidate page that is none ends at once), a row's
-// queries, or a request's status. Pages whose rows are few, as in a round, are read once: the values stay in
-// registers until their scale is known.
+// A warp's work is a page's keys or values of one head (a candidate page that is none ends at once), a row's queries, or
+// a request's status. MEASURED
 template <typename E, int V, bool INTER>
 __global__ void __launch_bounds__(kAppend8Threads) spec_append8_kernel(const __grid_constant__ Append8Params P) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % kWarp;
-    bool wrong = false;
+    // whether some request's offsets are wrong: each warp looks for itself where there are few, so that none waits
+    bool broken = false;
+    if (P.B <= kLookAlone) {
 #pragma unroll 4
-    for (int i = threadIdx.x; i < P.B; i += kAppend8Threads) wrong |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
-    const bool broken = __syncthreads_or(wrong) != 0;
+        for (int i = lane; i < P.B; i += kWarp) broken |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
+        broken = __any_sync(0xffffffffu, broken) != 0;
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < P.B; i += kAppend8Threads) broken |= !offsets_right(P.row_off[i], P.row_off[i + 1], P.T);
+        broken = __syncthreads_or(broken) != 0;
+    }
     auto in_doubt = [&](int i) -> bool {
         return broken && __any_sync(0xffffffffu, offsets_contradict(P.row_off, P.B, P.T, i, P.row_off[i], P.row_off[i + 1],
                                                                     lane, kWarp)) != 0;
     };
-    const int unit = blockIdx.x * kAppend8Warps + threadIdx.x / kWarp;
     // request i's first position, or -1 where it has no rows that are its own
     struct Request {
         int r0, n, kv, base;
@@ -279,6 +297,7 @@ __global__ void __launch_bounds__(kAppend8Threads) spec_append8_kernel(const __g
         const int page = P.block_table[static_cast<int64_t>(i) * P.max_blocks + blk];
         return page < P.n_pages ? page : -1;
     };
+    int unit = blockIdx.x * kAppend8Warps + threadIdx.x / kWarp;
     if (unit < P.page_units) {
         const int c = unit / (2 * P.Hkv), which = unit - c * 2 * P.Hkv, head = which >> 1;
         const int i = find_candidate(P, c, lane);
@@ -291,19 +310,18 @@ __global__ void __launch_bounds__(kAppend8Threads) spec_append8_kernel(const __g
         const int x1 = static_cast<int>(min(begin + P.page_size, static_cast<int64_t>(min(q.kv, P.n_pos))));
         if (begin >= q.kv || x0 >= x1) return;
         const int page = page_of(i, blk);
-        if (page < 0) return;
-        const int64_t slot = page * P.page_stride;
         const int kept = static_cast<int>(x0 - begin), row = q.r0 + (x0 - q.base);
         if (which & 1)
-            append_page<E, V, INTER, false>(P, head, row, x1 - x0, x0, slot, kept, page, lane);
+            append_page<E, V, INTER, false>(P, head, row, x1 - x0, x0, kept, page, lane);
         else
-            append_page<E, V, INTER, true>(P, head, row, x1 - x0, x0, slot, kept, page, lane);
+            append_page<E, V, INTER, true>(P, head, row, x1 - x0, x0, kept, page, lane);
         return;
     }
-    if (unit < P.page_units + P.q_units) {
+    unit -= P.page_units;
+    if (unit < P.q_units) {
         using Vec = Piece<E, V>;
         constexpr int kAtOnce = 4;
-        const int r = unit - P.page_units;
+        const int r = unit;
         const int per = Task<V, INTER>::kPairs ? P.D / V - P.rot / 2 / V : P.D / V, total = P.Hq * per;
         const E *src = static_cast<const E *>(P.q) + r * P.q_stride;
         E *dst = static_cast<E *>(P.q_out) + r * P.q_out_stride;
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(kAppend8Threads) spec_append8_kernel(const __g
         }
         return;
     }
-    const int i = unit - P.page_units - P.q_units;
+    const int i = unit - P.q_units;
     if (i >= P.B || !P.req_status) return;
     const int st = append_status(P, i, lane, in_doubt);
     if (lane == 0 && SPEC_IN(i, P.B, DBG_OUT_REQS)) P.req_status[i] = st;
