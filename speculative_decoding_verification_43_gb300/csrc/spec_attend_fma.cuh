@@ -58,17 +58,6 @@ __device__ __forceinline__ void bring(float *dst, const __nv_bfloat16 *src) {
             make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
 }
 
-// The same of a cache in 8 bits (16 elements), by their scale.
-__device__ __forceinline__ void bring(float *dst, const __nv_fp8_e4m3 *src, float scale) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(src);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 f = e4m3_to_float4(w[j]);
-        *reinterpret_cast<float4 *>(dst + 4 * j) = make_float4(f.x * scale, f.y * scale, f.z * scale, f.w * scale);
-    }
-}
-
 __device__ __forceinline__ void store4(float *dst, float4 v) { *reinterpret_cast<float4 *>(dst) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *dst, float4 v) {
     __nv_bfloat162 p[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
@@ -157,42 +146,86 @@ template <typename C>
 __device__ __forceinline__ void load_tile(const AttendParams &P, const Segment &s, float *sK, float *sV, int x0, int warp,
                                           int lane) {
     constexpr int V = 16 / sizeof(C);
-    constexpr bool kScaled = sizeof(C) == 1;
     const int D = P.D, per = D / V;
     int64_t off = -1;
-    float ks = 1.0f, vs = 1.0f;
     const int x = x0 + warp * 8 + lane;
     if (lane < 8 && item_sees(P, s.keys, x)) {
         const int32_t *table = s.req < 0 ? P.shared_table : P.block_table + static_cast<int64_t>(s.req) * P.max_blocks;
         off = slot_offset(P, table, x);
-        if (off >= 0) {
-            off += static_cast<int64_t>(s.head) * P.head_stride;
-            if constexpr (kScaled) {
-                const int64_t at = static_cast<int64_t>(table[P.by_page(x)]) * P.Hkv + s.head;
-                ks = P.k_scale[at];
-                vs = P.v_scale[at];
-            }
-        }
+        if (off >= 0) off += static_cast<int64_t>(s.head) * P.head_stride;
     }
     const C *kc = static_cast<const C *>(P.k_cache), *vc = static_cast<const C *>(P.v_cache);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int64_t o = __shfl_sync(0xffffffffu, off, j);
-        const float k_by = kScaled ? __shfl_sync(0xffffffffu, ks, j) : 1.0f, v_by = kScaled ? __shfl_sync(0xffffffffu, vs, j) : 1.0f;
         if (o < 0) continue;  // seen by no row (or its request is in error): never used
         const int key = warp * 8 + j;
         for (int c = lane; c < per; c += kWarp) {
             if (!SPEC_IN(o + c * V + V - 1, cache_extent(P), DBG_CACHE)) continue;
-            if constexpr (kScaled) {
-                bring(sK + key * (D + 4) + c * V, kc + o + c * V, k_by);
-                bring(sV + key * D + c * V, vc + o + c * V, v_by);
-            } else {
-                bring(sK + key * (D + 4) + c * V, kc + o + c * V);
-                bring(sV + key * D + c * V, vc + o + c * V);
-            }
+            bring(sK + key * (D + 4) + c * V, kc + o + c * V);
+            bring(sV + key * D + c * V, vc + o + c * V);
         }
     }
 }
+
+// The same of a cache in 8 bits, in two steps: the warp's eight keys' elements and scales on their way into registers
+// while the tile before is used, then into shared memory as fp32. A lane has the same 16 elements of every 32 / per-th key
+// (per = D / 16 pieces a key; lanes left over have none).
+template <int NC>
+struct Tile8 {
+    static constexpr int kPieces = 2 * NC;  // of a lane: 8 keys, 32 / per >= 4 / NC of them at a time
+    uint4 k[kPieces], v[kPieces];
+    float ks, vs;  // lane j < 8: key j's scales
+    unsigned on;   // bit j: key j is used
+
+    __device__ __forceinline__ void fetch(const AttendParams &P, const Segment &s, int x0, int warp, int lane) {
+        const int per = P.D / 16, at_once = kWarp / per, j0 = lane / per, c = lane - j0 * per;
+        const int x = x0 + warp * 8 + lane;
+        int64_t off = -1;
+        ks = vs = 1.0f;
+        if (lane < 8 && item_sees(P, s.keys, x)) {
+            const int32_t *table = s.req < 0 ? P.shared_table : P.block_table + static_cast<int64_t>(s.req) * P.max_blocks;
+            off = slot_offset(P, table, x);
+            if (off >= 0) {
+                off += static_cast<int64_t>(s.head) * P.head_stride;
+                const int64_t at = static_cast<int64_t>(table[P.by_page(x)]) * P.Hkv + s.head;
+                ks = P.k_scale[at];
+                vs = P.v_scale[at];
+            }
+        }
+        on = __ballot_sync(0xffffffffu, off >= 0);
+        const unsigned char *kc = static_cast<const unsigned char *>(P.k_cache), *vc = static_cast<const unsigned char *>(P.v_cache);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int j = j0 + i * at_once;
+            const int64_t o = __shfl_sync(0xffffffffu, off, j & 31);
+            if (j0 < at_once && j < 8 && o >= 0 && SPEC_IN(o + c * 16 + 15, cache_extent(P), DBG_CACHE)) {
+                k[i] = *reinterpret_cast<const uint4 *>(kc + o + c * 16);
+                v[i] = *reinterpret_cast<const uint4 *>(vc + o + c * 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(const AttendParams &P, float *sK, float *sV, int warp, int lane) const {
+        const int D = P.D, per = D / 16, at_once = kWarp / per, j0 = lane / per, c = lane - j0 * per;
+        auto widen = [](float *dst, const uint4 &x, float by) {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 f = e4m3_to_float4(w[e]);
+                *reinterpret_cast<float4 *>(dst + 4 * e) = make_float4(f.x * by, f.y * by, f.z * by, f.w * by);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int j = j0 + i * at_once, key = warp * 8 + j;
+            const float kb = __shfl_sync(0xffffffffu, ks, j & 31), vb = __shfl_sync(0xffffffffu, vs, j & 31);
+            if (j0 < at_once && j < 8 && (on >> j & 1u)) {  // (others are seen by no row, or their request is in error)
+                widen(sK + key * (D + 4) + c * 16, k[i], kb);
+                widen(sV + key * D + c * 16, v[i], vb);
+            }
+        }
+    }
+};
 
 // E: the type of the rows; C: the cache's.
 template <typename E, typename C, int NC, bool PREFIX>
@@ -238,16 +271,7 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
                 }
             }
         }
-        if (s.ntile > 0) load_tile<C>(P, s, sK, sV, tile_begin<kKT>(s.keys, s.tile), warp, lane);
-        copy_commit();
-        for (int t = 0; t < s.ntile; ++t) {
-            const int b = t & 1;
-            if (t + 1 < s.ntile)
-                load_tile<C>(P, s, sK + (b ^ 1) * kKT * (D + 4), sV + (b ^ 1) * kKT * D,
-                             tile_begin<kKT>(s.keys, s.tile + t + 1), warp, lane);
-            copy_commit();
-            copy_wait<1>();
-            __syncthreads();
+        auto use = [&](int t, int b) {
             const int x0 = tile_begin<kKT>(s.keys, s.tile + t);
             const float *k = sK + b * kKT * (D + 4), *v = sV + b * kKT * D;
             switch (nr) {
@@ -257,7 +281,37 @@ __global__ void __launch_bounds__(kThreads) spec_attend_fma_kernel(const AttendP
                 case 4: tile_step<4, NC>(P, R, sQ, k, v, sP, x0, s.keys, warp, lane); break;
                 default: break;
             }
-            __syncthreads();
+        };
+        if constexpr (sizeof(C) == 1) {
+            copy_commit();
+            Tile8<NC> tile;
+            if (s.ntile > 0) {
+                tile.fetch(P, s, tile_begin<kKT>(s.keys, s.tile), warp, lane);
+                tile.put(P, sK, sV, warp, lane);
+            }
+            copy_wait<0>();  // the queries
+            for (int t = 0; t < s.ntile; ++t) {
+                const int b = t & 1;
+                __syncthreads();  // the tile is there, and the one before has been used
+                const bool more = t + 1 < s.ntile;
+                if (more) tile.fetch(P, s, tile_begin<kKT>(s.keys, s.tile + t + 1), warp, lane);
+                use(t, b);
+                if (more) tile.put(P, sK + (b ^ 1) * kKT * (D + 4), sV + (b ^ 1) * kKT * D, warp, lane);
+            }
+        } else {
+            if (s.ntile > 0) load_tile<C>(P, s, sK, sV, tile_begin<kKT>(s.keys, s.tile), warp, lane);
+            copy_commit();
+            for (int t = 0; t < s.ntile; ++t) {
+                const int b = t & 1;
+                if (t + 1 < s.ntile)
+                    load_tile<C>(P, s, sK + (b ^ 1) * kKT * (D + 4), sV + (b ^ 1) * kKT * D,
+                                 tile_begin<kKT>(s.keys, s.tile + t + 1), warp, lane);
+                copy_commit();
+                copy_wait<1>();
+                __syncthreads();
+                use(t, b);
+                __syncthreads();
+            }
         }
         copy_wait<0>();
 #pragma unroll
