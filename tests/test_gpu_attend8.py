@@ -32,6 +32,45 @@ def test_against_float64(name):
     assert torch.equal(got.out, again[0]) and torch.equal(got.lse, again[1])
 
 
+# rows, kv, Hq, Hkv, D, page, window, sinks, shared, order
+MORE = {
+    "a long text cut up": ([5], [20000], 16, 8, 64, 16, 0, 0, 0, "slot"),
+    "a long text, one head": ([2], [9000], 4, 1, 128, 8, 0, 0, 0, "head"),
+    "three heads": ([3, 7], [500, 1200], 6, 3, 128, 16, 0, 0, 0, "slot"),
+    "six heads": ([3, 7], [500, 1200], 12, 6, 64, 32, 0, 0, 0, "head"),
+    "sixteen heads": ([3, 1], [300, 700], 16, 16, 64, 16, 0, 0, 0, "slot"),
+    "33 to 64 rows a head": ([12, 9, 16], [600, 1000, 300], 8, 2, 128, 16, 0, 0, 0, "slot"),
+    "33 to 64 rows, window": ([12, 9, 16], [600, 1000, 300], 8, 2, 80, 24, 130, 7, 0, "head"),
+    "rows between": ([8, 7, 6, 5, 4, 3, 2, 1], [130 * i for i in range(1, 9)], 12, 4, 96, 16, 0, 0, 0, "slot"),
+    "prompts of 1000 rows": ([1000, 300], [1100, 300], 4, 1, 128, 64, 0, 0, 0, "slot"),
+    "prompts, heads of 80": ([300, 260], [500, 260], 8, 2, 80, 24, 0, 0, 0, "head"),
+    "prompts, window and sinks": ([400, 100], [900, 100], 4, 2, 64, 16, 150, 20, 0, "slot"),
+    "prompts behind a prefix": ([170, 100], [370, 300], 4, 2, 128, 16, 0, 0, 150, "slot"),
+    "rounds behind a prefix": ([4] * 40, [1100 + 11 * i for i in range(40)], 32, 8, 128, 16, 0, 0, 1001, "slot"),
+    "pages of 128": ([4, 2], [1000, 130], 8, 2, 128, 128, 0, 0, 0, "slot"),
+    "pages of 40": ([4, 2], [1000, 130], 8, 2, 128, 40, 0, 0, 0, "slot"),
+}
+
+
+@pytest.mark.parametrize("name", list(MORE))
+def test_layouts(name):
+    rows, kv, Hq, Hkv, D, page, W, S, L, order = MORE[name]
+    b = Batch8(rows, kv, Hq, Hkv, D, BF, page, W, S, L, seed=len(name), order=order).place()
+    got = b.attention().run()
+    torch.cuda.synchronize()
+    assert (got.req_status.cpu() == 0).all()
+    check8(b, got)
+
+
+@pytest.mark.parametrize("rows,kernel", [([4], "round"), ([12], "round"), ([13], "pair"), ([100], "pair")], ids=str)
+def test_plan_names_the_kernel(rows, kernel):
+    b = Batch8(rows, [200], 8, 2, 64, BF, 16, seed=1).place()
+    assert b.attention().plan() == f"spec_attend8_{kernel}_kernel"
+    for kw in (dict(dtype=F32), dict(page=7), dict(D=144)):
+        b = Batch8(rows, [200], 8, 2, kw.get("D", 64), kw.get("dtype", BF), kw.get("page", 16), seed=1).place()
+        assert b.attention().plan() == "spec_attend_fma_kernel"
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("loud", [0.0, 12.0], ids=["alike", "apart"])
 def test_scales(dtype, loud):
@@ -54,7 +93,7 @@ def test_many_requests_and_uneven_lengths():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("rows", [[3, 2], [40, 70], [300, 1]], ids=str)
+@pytest.mark.parametrize("rows", [[3, 2], [20, 22], [40, 70], [300, 1]], ids=str)
 def test_growing_scores(dtype, rows):
     """Scores that grow along the text, far beyond a fixed reference's range, then fall; the values' scales fall
     and grow."""
@@ -103,7 +142,7 @@ def test_one_heavy_position_and_a_long_tail():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("rows", [[5, 2], [150, 40]], ids=str)
+@pytest.mark.parametrize("rows", [[5, 2], [21, 20], [150, 40]], ids=str)
 @pytest.mark.parametrize("what", ["value", "key"])
 def test_no_number_where_only_later_rows_see_it(dtype, rows, what):
     kv = [rows[0] + 135, rows[1] + 128]
