@@ -28,8 +28,8 @@ static spec_status attend8_sizes(const spec_attend8_args *a, AttendParams &P) {
 
 // Rows of an item (as a power of two) and workers for `rows` packed rows of a head over `groups` requests on the
 // tensor cores.
-static void tensor8_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
-    rt_log2 = rows <= 24 * groups ? 5 : rows <= 48 * groups ? 6 : pair8::kRTLog2;
+static void tensor8_class(bool wide, int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
+    rt_log2 = wide || rows <= 24 * groups ? 5 : rows <= 48 * groups ? 6 : pair8::kRTLog2;
     workers = rt_log2 == pair8::kRTLog2 ? kSMs : kSMs * round8::kPerSM;
 }
 
@@ -37,11 +37,11 @@ static void tensor8_class(int64_t rows, int64_t groups, int32_t &rt_log2, int32_
 static int extra8_units(int rt_log2) { return rt_log2 == pair8::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.
-static void attend8_work(AttendParams &P, bool tensor) {
+static void attend8_work(AttendParams &P, bool tensor, bool wide) {
     const int64_t head_rows = static_cast<int64_t>(P.T) * P.G;
     if (tensor) {
-        tensor8_class(head_rows, P.B, P.own_rt_log2, P.own_workers);
-        tensor8_class(head_rows, 1, P.prefix_rt_log2, P.prefix_workers);
+        tensor8_class(wide, head_rows, P.B, P.own_rt_log2, P.own_workers);
+        tensor8_class(wide, head_rows, 1, P.prefix_rt_log2, P.prefix_workers);
         P.own_extra = extra8_units(P.own_rt_log2);
         P.prefix_extra = extra8_units(P.prefix_rt_log2);
         P.box_log2 = box_log2_of(P.page_size);
@@ -58,7 +58,7 @@ static void attend8_work(AttendParams &P, bool tensor) {
 
 // Whether the tensor cores may serve a call of these sizes; strides apart.
 static bool tensor8_sizes(const spec_attend8_args *a) {
-    return a->attend.dtype == SPEC_BF16 && a->attend.head_dim <= 128 && box_log2_of(a->attend.page_size) > 0;
+    return a->attend.head_dim <= 128 && box_log2_of(a->attend.page_size) > 0;
 }
 
 // The cache as three-dimensional tensor maps (head_dim x heads x slots), where its strides allow it: pages a whole
@@ -120,24 +120,27 @@ static cudaError_t launch_tensor8(Kernel *kernel, int ctas, int threads, int sme
                         static_cast<size_t>(smem), stream, P, M.where, M.k, M.v);
 }
 
+template <int RT, bool PREFIX, bool WIDE>
+static cudaError_t launch_round8(int workers, const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
+    return launch_tensor8(round8::spec_attend8_round_kernel<RT, PREFIX, WIDE>, workers, round8::kThreads,
+                          round8::smem_bytes<RT, WIDE>(), P, M, stream);
+}
 // One class of items on the tensor cores.
 template <bool PREFIX>
-static cudaError_t launch_class8(const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
+static cudaError_t launch_class8(bool wide, const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
     const int rt_log2 = PREFIX ? P.prefix_rt_log2 : P.own_rt_log2, workers = PREFIX ? P.prefix_workers : P.own_workers;
-    if (rt_log2 == 5)
-        return launch_tensor8(round8::spec_attend8_round_kernel<32, PREFIX>, workers, round8::kThreads,
-                              round8::smem_bytes<32>(), P, M, stream);
-    if (rt_log2 == 6)
-        return launch_tensor8(round8::spec_attend8_round_kernel<64, PREFIX>, workers, round8::kThreads,
-                              round8::smem_bytes<64>(), P, M, stream);
+    if (wide) return launch_round8<32, PREFIX, true>(workers, P, M, stream);
+    if (rt_log2 == 5) return launch_round8<32, PREFIX, false>(workers, P, M, stream);
+    if (rt_log2 == 6) return launch_round8<64, PREFIX, false>(workers, P, M, stream);
     return launch_tensor8(pair8::spec_attend8_pair_kernel<PREFIX>, workers, pair8::kThreads, pair8::kSmem, P, M, stream);
 }
 
-static cudaError_t enqueue_tensor8(const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
+static cudaError_t enqueue_tensor8(bool wide, const AttendParams &P, const CacheMaps8 &M, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
-    if (P.shared_len > 0) e = launch_class8<true>(P, M, stream);
-    if (e == cudaSuccess) e = launch_class8<false>(P, M, stream);
-    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, tiles8::kKT>(P, stream);
+    if (P.shared_len > 0) e = launch_class8<true>(wide, P, M, stream);
+    if (e == cudaSuccess) e = launch_class8<false>(wide, P, M, stream);
+    if (e == cudaSuccess)
+        e = wide ? launch_join<float, tiles8::kKT>(P, stream) : launch_join<__nv_bfloat16, tiles8::kKT>(P, stream);
     return e;
 }
 
@@ -169,10 +172,11 @@ extern "C" size_t spec_attend8_workspace_size(const spec_attend8_args *a) {
     AttendParams P = {};
     if (attend8_sizes(a, P) != SPEC_OK) return 0;
     // either kernel may serve the call: which one follows from the strides
-    attend8_work(P, false);
+    const bool wide = a->attend.dtype == SPEC_F32;
+    attend8_work(P, false, wide);
     const size_t fma_bytes = attend_layout(P).total;
     if (!tensor8_sizes(a)) return fma_bytes;
-    attend8_work(P, true);
+    attend8_work(P, true, wide);
     return std::max(fma_bytes, attend_layout(P).total);
 }
 
@@ -182,7 +186,7 @@ extern "C" const char *spec_attend8_plan(const spec_attend8_args *a) {
     tiles8::CacheMap M = {};
     CacheShape shape = {};
     if (!cache_map8(a, M, shape)) return "spec_attend_fma_kernel";
-    attend8_work(P, true);
+    attend8_work(P, true, a->attend.dtype == SPEC_F32);
     return P.own_rt_log2 == pair8::kRTLog2 ? "spec_attend8_pair_kernel" : "spec_attend8_round_kernel";
 }
 
@@ -199,7 +203,8 @@ extern "C" spec_status spec_attend8(const spec_attend8_args *a, void *workspace,
     CacheMaps8 M = {};
     CacheShape shape = {};
     const bool tensor = cache_map8(a, M.where, shape);
-    attend8_work(P, tensor);
+    const bool wide = a->attend.dtype == SPEC_F32;
+    attend8_work(P, tensor, wide);
     if (!workspace || workspace_bytes < spec_attend8_workspace_size(a) || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
         return SPEC_ERR_WORKSPACE;
     attend_place(P, workspace);
@@ -208,10 +213,10 @@ extern "C" spec_status spec_attend8(const spec_attend8_args *a, void *workspace,
         if (!encode_map8(M.k, a->attend.k_cache, shape, &a->attend, box) ||
             !encode_map8(M.v, a->attend.v_cache, shape, &a->attend, box))
             return SPEC_ERR_CUDA;
-        return enqueue_tensor8(P, M, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+        return enqueue_tensor8(wide, P, M, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
     }
     const cudaError_t e =
-        a->attend.dtype == SPEC_BF16 ? enqueue_fma8<__nv_bfloat16>(P, stream) : enqueue_fma8<float>(P, stream);
+        wide ? enqueue_fma8<float>(P, stream) : enqueue_fma8<__nv_bfloat16>(P, stream);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -336,7 +336,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 uint32_t top = top_bits(0u, x);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const uint32_t bits = max(top & 0xffffu, top >> 16);
+                const uint32_t bits = max(top & 0xffffu, top >> 16) << 16;
                 const float qs = query_scale(bits);
                 if (at < mine) {
                     uint2 hi, lo;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                     unsigned char *to = q_tile + at * 128 + (((piece >> 1) ^ (at & 7)) << 4) + (piece & 1) * 8;
                     *reinterpret_cast<uint2 *>(to) = hi;
                     *reinterpret_cast<uint2 *>(to + kQPart) = lo;
-                    if (piece == 0) sh.factor[w][at] = bits < 0x7f80u ? qs * P.scale_log2 : NAN;
+                    if (piece == 0) sh.factor[w][at] = bits < 0x7f800000u ? qs * P.scale_log2 : NAN;
                 }
             }
             __syncwarp();

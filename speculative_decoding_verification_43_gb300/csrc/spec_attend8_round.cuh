@@ -25,9 +25,19 @@ constexpr int kThreads = 192, kPerSM = 2;
 constexpr float kTop = 11.0f;  // log2 of the largest weight under a new reference, and of what may be reached
 constexpr float kMost = 15.0f; // before the next
 
-template <int RT>
+// What a row's type asks for. bf16: queries in two parts, weights in three, one accumulator each. fp32: two more parts
+// of the queries and three of the weights, which hold what the first ones leave times 2^kQueryShift and 2^kWeightShift,
+// each in an accumulator of its own, so that e4m3 and e5m2 need not reach down to it: 18 and 22 bits in all, and 26
+// bits below a query's largest element.
+template <bool WIDE>
+struct Parts {
+    static constexpr int kSets = WIDE ? 2 : 1, kQ = 2, kP = 3;  // accumulators, and parts in each
+};
+constexpr int kQueryShift = 8, kWeightShift = 11;
+
+template <int RT, bool WIDE>
 struct Shared {
-    Pipe<2, RT == 32 ? 3 : 2> pipe;
+    Pipe<2, RT == 32 && !WIDE ? 3 : 2> pipe;
     uint64_t q_full, s_full[2], p_full, o_done, drain;
     uint32_t found[4];     // per warp: what it brings to a meeting
     uint32_t skip;         // the warpgroup has done this tile's second product itself
@@ -46,31 +56,40 @@ struct Scratch {
 // A reference that every finite score exceeds and that leaves -inf alone.
 constexpr float kNoRef = 3e38f;
 
-// Queries: two parts of 128 bytes a row; weights: three parts of a byte a row and position.
+// Queries: parts of 128 bytes a row; weights: parts of a byte a row and position.
 __host__ __device__ constexpr int q_part(int RT) { return RT * 128; }
 __host__ __device__ constexpr int p_part(int RT) { return kKT * RT; }
-__host__ __device__ constexpr int q_bytes(int RT) { return 2 * q_part(RT); }
-__host__ __device__ constexpr int p_bytes(int RT) { return 3 * p_part(RT); }
-template <int RT>
-__host__ __device__ constexpr int stages() {
-    return decltype(Shared<RT>::pipe)::kKeys + decltype(Shared<RT>::pipe)::kValues;
+template <bool WIDE>
+__host__ __device__ constexpr int q_bytes(int RT) {
+    return Parts<WIDE>::kSets * Parts<WIDE>::kQ * q_part(RT);
 }
-template <int RT>
+template <bool WIDE>
+__host__ __device__ constexpr int p_bytes(int RT) {
+    return Parts<WIDE>::kSets * Parts<WIDE>::kP * p_part(RT);
+}
+template <int RT, bool WIDE>
+__host__ __device__ constexpr int stages() {
+    return decltype(Shared<RT, WIDE>::pipe)::kKeys + decltype(Shared<RT, WIDE>::pipe)::kValues;
+}
+template <int RT, bool WIDE>
 __host__ constexpr int smem_bytes() {
-    return stages<RT>() * kTile + q_bytes(RT) + p_bytes(RT) + static_cast<int>(sizeof(Shared<RT>));
+    return stages<RT, WIDE>() * kTile + q_bytes<WIDE>(RT) + p_bytes<WIDE>(RT) + static_cast<int>(sizeof(Shared<RT, WIDE>));
 }
 // 228 KB of shared memory, 1 KB of it taken per CTA
-static_assert(smem_bytes<32>() <= 228 * 1024 / kPerSM - 1024 && smem_bytes<64>() <= 228 * 1024 / kPerSM - 1024, "fits");
-static_assert(sizeof(Scratch<64>) <= p_bytes(64) && sizeof(Scratch<32>) <= p_bytes(32), "fits the weights' memory");
+constexpr int kMostSmem = 228 * 1024 / kPerSM - 1024;
+static_assert(smem_bytes<32, false>() <= kMostSmem && smem_bytes<64, false>() <= kMostSmem && smem_bytes<32, true>() <= kMostSmem,
+              "fits");
+static_assert(sizeof(Scratch<64>) <= p_bytes<false>(64) && sizeof(Scratch<32>) <= p_bytes<false>(32), "fits the weights' memory");
 
 // ---------------------------------------------------------------- matrix instructions (one warp)
 
-template <int RT>
-__device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, unsigned char *ring_mem,
+template <int RT, bool WIDE>
+__device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE> &sh, unsigned char *ring_mem,
                                          unsigned char *q_tile, unsigned char *p_tile) {
     int32_t *ab = &sh.pipe.abort;
-    constexpr int kKeys = decltype(Shared<RT>::pipe)::kKeys, kValues = decltype(Shared<RT>::pipe)::kValues;
-    const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * RT;
+    constexpr int kKeys = decltype(Shared<RT, WIDE>::pipe)::kKeys, kValues = decltype(Shared<RT, WIDE>::pipe)::kValues;
+    constexpr int kSets = Parts<WIDE>::kSets, kQ = Parts<WIDE>::kQ, kP = Parts<WIDE>::kP;
+    const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kSets * RT;
     const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
                    v_op = smem_operand(smem_addr(ring_mem + kKeys * kTile), 16),
                    p_op = RT == 64 ? smem_operand64(smem_addr(p_tile)) : smem_operand32(smem_addr(p_tile));
@@ -105,12 +124,12 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
                         const uint64_t k = operand_at(k_op, next.slot * kTile);
                         if (elect_lane()) {
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
+                            for (int q = 0; q < kSets * kQ; ++q)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     if (i < steps)
-                                        mma8_ss(s_col + b * RT, operand_at(k, i * 32), operand_at(q_op, q * q_part(RT) + i * 32),
-                                                qk_shape, q + i > 0);
+                                        mma8_ss(s_col + (b * kSets + q / kQ) * RT, operand_at(k, i * 32),
+                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shape, q % kQ + i > 0);
                             mma_commit(&sh.s_full[b]);
                             mma_commit(&sh.pipe.k_empty[next.slot]);
                         }
@@ -126,12 +145,13 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT> &sh, 
                         if (elect_lane()) {
                             if (take) {  // O^T += V^T P^T
 #pragma unroll
-                                for (int p = 0; p < 3; ++p)
+                                for (int p = 0; p < kSets * kP; ++p)
 #pragma unroll
                                     for (int i = 0; i < 4; ++i)
                                         if (i * 32 < n)
-                                            mma8_ss(o_col, operand_at(values, i * 4096),
-                                                    operand_at(p_op, p * p_part(RT) + i * 32 * RT), pv_shape, t > 0 || p + i > 0);
+                                            mma8_ss(o_col + p / kP * RT, operand_at(values, i * 4096),
+                                                    operand_at(p_op, p * p_part(RT) + i * 32 * RT), pv_shape,
+                                                    t > 0 || p % kP + i > 0);
                             }
                             mma_commit(&sh.o_done);
                             mma_commit(&sh.pipe.v_empty[v.slot]);
@@ -168,8 +188,9 @@ __device__ __forceinline__ uint32_t meet_words(uint32_t *found, uint32_t mine) {
 constexpr uint32_t kBeyond = 1, kNoNumber = 2, kGone = 4;  // a weight too large, a value that is no number, a wait given up
 
 // The second product of a tile with values that are not finite, on the fp32 units: thread d has output
-// column d, the weights lie in shared memory, O is complete up to the tile before.
-template <int RT>
+// column d, the weights lie in shared memory, O is complete up to the tile before (what this adds goes to its first
+// accumulator; the others begin with 0 if the tile is the first).
+template <int RT, bool WIDE>
 __device__ __noinline__ void mixed_tile(const AttendParams &P, const int *pos, uint32_t o_addr,
                                         const unsigned char *v_tile, const unsigned char *p_tile, const KeyTiles &keys,
                                         int x0, int n, int nrows, int d, bool first) {
@@ -193,7 +214,10 @@ __device__ __noinline__ void mixed_tile(const AttendParams &P, const int *pos, u
                 if (x <= p && (P.window == 0 || x > p - P.window || x < P.n_sink)) {
                     const int piece = RT == 64 ? (r >> 4) ^ ((k >> 1) & 3) : (r >> 4) ^ ((k >> 2) & 1);
                     const unsigned char *at = p_tile + k * RT + piece * 16 + (r & 15);
-                    const float w = e5m2_to_float(at[0]) + e5m2_to_float(at[p_part(RT)]) + e5m2_to_float(at[2 * p_part(RT)]);
+                    float w = e5m2_to_float(at[0]) + e5m2_to_float(at[p_part(RT)]) + e5m2_to_float(at[2 * p_part(RT)]);
+                    if constexpr (WIDE)
+                        w += 0x1p-11f * (e5m2_to_float(at[3 * p_part(RT)]) + e5m2_to_float(at[4 * p_part(RT)]) +
+                                         e5m2_to_float(at[5 * p_part(RT)]));
                     o[e] = fmaf(w, v, o[e]);
                 }
             }
@@ -203,18 +227,24 @@ __device__ __noinline__ void mixed_tile(const AttendParams &P, const int *pos, u
         for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e]);
         __syncwarp();
         tmem_st16(o_addr + r0, ow);
+        if (WIDE && first) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ow[e] = 0u;
+            tmem_st16(o_addr + RT + r0, ow);
+        }
         tmem_wait_st();
     }
 }
 
-template <int RT, bool PREFIX>
-__device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &sh, unsigned char *ring_mem,
+template <int RT, bool PREFIX, bool WIDE>
+__device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, WIDE> &sh, unsigned char *ring_mem,
                                              unsigned char *q_tile, unsigned char *p_tile) {
-    constexpr int kKeys = decltype(Shared<RT>::pipe)::kKeys, kValues = decltype(Shared<RT>::pipe)::kValues;
+    constexpr int kKeys = decltype(Shared<RT, WIDE>::pipe)::kKeys, kValues = decltype(Shared<RT, WIDE>::pipe)::kValues;
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     int32_t *ab = &sh.pipe.abort;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t s_addr = sh.tmem + lanes, o_addr = s_addr + 2 * RT;
+    constexpr int kSets = Parts<WIDE>::kSets, kP = Parts<WIDE>::kP;
+    const uint32_t s_addr = sh.tmem + lanes, o_addr = s_addr + 2 * kSets * RT;
     Scratch<RT> &scratch = *reinterpret_cast<Scratch<RT> *>(p_tile);
     Ring values = {0, kValues, 0}, desc = {0, 2, 0};
     uint32_t s_phases = 0, o_phase = 0;
@@ -223,34 +253,71 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
     // Brings a segment's queries: 128 / RT threads each row's (rows up to a multiple of 16: zeros), and its
     // position.
     auto bring = [&](const Segment &s, int to) {
-        constexpr int kPer = 128 / RT, kPieces = 16 / kPer;
+        constexpr int kPer = 128 / RT, kPieces = 16 / kPer;  // of eight elements
         const int r = tid / kPer, pr = s.row0 + r, j = P.by_group(pr), g = pr - j * P.G;
         const int t = s.t0 + j, h = s.head * P.G + g;
         const bool have = r < s.nrows && SPEC_IN(t, P.T, DBG_ATTEND);
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + t * P.q_stride +
-                                                           static_cast<int64_t>(h) * P.D);
-        uint4 x[kPieces];
-        uint32_t top = 0u;
+        const int64_t row = t * P.q_stride + static_cast<int64_t>(h) * P.D;
+        auto whole = [&](uint32_t top) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int c = tid % kPer + i * kPer;
-            x[i] = have && c < P.D / 8 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-            top = top_bits(top, x[i]);
-        }
-#pragma unroll
-        for (int o = 1; o < kPer; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const uint32_t bits = max(top & 0xffffu, top >> 16);
-        const float qs = query_scale(bits), inv = 1.0f / qs;
-        if (r < ((s.nrows + 15) & ~15)) {
+            for (int o = 1; o < kPer; o <<= 1) top = WIDE ? max(top, __shfl_xor_sync(0xffffffffu, top, o))
+                                                          : __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            return top;
+        };
+        auto at = [&](int c) { return q_tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8; };
+        const bool taken = r < ((s.nrows + 15) & ~15);
+        float qs;
+        bool finite;
+        if constexpr (!WIDE) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + row);
+            uint4 x[kPieces];
+            uint32_t top = 0u;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int c = tid % kPer + i * kPer;
-                uint2 hi, lo;
-                split_query(x[i], inv, hi, lo);
-                unsigned char *at = q_tile + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-                *reinterpret_cast<uint2 *>(at) = hi;
-                *reinterpret_cast<uint2 *>(at + q_part(RT)) = lo;
+                x[i] = have && c < P.D / 8 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                top = top_bits(top, x[i]);
             }
+            top = whole(top);
+            const uint32_t bits = max(top & 0xffffu, top >> 16) << 16;
+            finite = bits < 0x7f800000u;
+            qs = query_scale(bits);
+            if (taken)
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int c = tid % kPer + i * kPer;
+                    uint2 hi, lo;
+                    split_query(x[i], 1.0f / qs, hi, lo);
+                    *reinterpret_cast<uint2 *>(at(c)) = hi;
+                    *reinterpret_cast<uint2 *>(at(c) + q_part(RT)) = lo;
+                }
+        } else {
+            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(P.q) + row);
+            uint32_t top = 0u;
+            auto piece = [&](int i, int half) {
+                const int c = tid % kPer + i * kPer;
+                return have && c < P.D / 8 ? src[2 * c + half] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            };
+#pragma unroll
+            for (int i = 0; i < 2 * kPieces; ++i) {
+                const float4 x = piece(i / 2, i % 2);
+                top = max(top, max(max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu),
+                                   max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu)));
+            }
+            top = whole(top);
+            finite = top < 0x7f800000u;
+            qs = query_scale(top);
+            if (taken)
+#pragma unroll 2
+                for (int i = 0; i < 2 * kPieces; ++i) {  // (read again, from L1)
+                    uint32_t parts[4];
+                    split_query_wide<kQueryShift>(piece(i / 2, i % 2), 1.0f / qs, parts);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint32_t *>(at(tid % kPer + i / 2 * kPer) + q * q_part(RT) + i % 2 * 4) = parts[q];
+                }
+        }
+        if (taken) {
             if (tid % kPer == 0) {
                 int p = -1;
                 if (have) {
@@ -263,7 +330,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                 }
                 sh.pos[to][r] = p;
                 sh.nref[to][r] = kNoRef;
-                sh.factor[to][r] = bits < 0x7f80u ? qs * P.scale_log2 : NAN;
+                sh.factor[to][r] = finite ? qs * P.scale_log2 : NAN;
             }
         }
         if (s.ntile > 0) {
@@ -347,11 +414,24 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             constexpr bool kHeld = RT == 32;
             float held[kHeld ? RT : 16];
             if constexpr (kHeld) {
+                const uint32_t from = s_addr + b * kSets * RT;
                 if (nrows > 16)
-                    tmem_ld32(held, s_addr + b * RT);
+                    tmem_ld32(held, from);
                 else
-                    tmem_ld16(held, s_addr + b * RT);
-                tmem_wait_ld32(held);
+                    tmem_ld16(held, from);
+                if constexpr (WIDE) {
+                    float rest[RT];
+                    if (nrows > 16)
+                        tmem_ld32(rest, from + RT);
+                    else
+                        tmem_ld16(rest, from + RT);
+                    tmem_wait_ld32(held);
+                    tmem_wait_ld32(rest);
+#pragma unroll
+                    for (int e = 0; e < RT; ++e) held[e] = fmaf(rest[e], 1.0f / (1 << kQueryShift), held[e]);
+                } else {
+                    tmem_wait_ld32(held);
+                }
 #pragma unroll
                 for (int e = 0; e < RT; e += 16)
                     if (e < nrows) finish(held + e, e);
@@ -419,14 +499,16 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                             l[e / 2].y *= scratch.row[e + 1];
                         }
 #pragma unroll 1
-                    for (int r0 = 0; r0 < nrows; r0 += 16) {
+                    for (int c0 = 0; c0 < kSets * RT; c0 += 16) {
+                        const int r0 = c0 % RT;
+                        if (r0 >= nrows) continue;
                         float o[16];
                         uint32_t ow[16];
-                        tmem_ld16(o, o_addr + r0);
+                        tmem_ld16(o, o_addr + c0);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * scratch.row[r0 + e]);
-                        tmem_st16(o_addr + r0, ow);
+                        tmem_st16(o_addr + c0, ow);
                     }
                     tmem_wait_st();
                     bar_sync(1, 128);  // the scratch has been read
@@ -438,7 +520,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             for (int e = 0; e < RT; e += 16)
                 if (e < nrows) {
                     const float *z = scores(e);
-                    uint32_t pw[4][3];
+                    uint32_t pw[4][kSets * kP];
 #pragma unroll
                     for (int y = 0; y < 16; y += 4) {
                         float2 a, c;
@@ -456,17 +538,20 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                         }
                         l[(e + y) / 2] = fma2(a, vi, l[(e + y) / 2]);
                         l[(e + y) / 2 + 1] = fma2(c, vi, l[(e + y) / 2 + 1]);
-                        split_e5m2(a.x, a.y, c.x, c.y, pw[y / 4]);
+                        if constexpr (WIDE)
+                            split_e5m2_wide<kWeightShift>(a.x, a.y, c.x, c.y, pw[y / 4]);
+                        else
+                            split_e5m2(a.x, a.y, c.x, c.y, pw[y / 4]);
                     }
                     const int piece = RT == 64 ? (e >> 4) ^ ((tid >> 1) & 3) : (e >> 4) ^ ((tid >> 2) & 1);
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
+                    for (int p = 0; p < kSets * kP; ++p)
                         *reinterpret_cast<uint4 *>(prow + p * p_part(RT) + piece * 16) =
                             make_uint4(pw[0][p], pw[1][p], pw[2][p], pw[3][p]);
                 }
             if (skip) {
                 bar_sync(1, 128);  // all weights are there
-                mixed_tile<RT>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
+                mixed_tile<RT, WIDE>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
             }
             if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip) = skip;
             fence_proxy_async_smem();
@@ -534,6 +619,13 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
             if (nt > 0) {
                 tmem_ld4(o, o_addr + r0);
                 tmem_wait_ld();
+                if constexpr (WIDE) {
+                    float rest[4];
+                    tmem_ld4(rest, o_addr + RT + r0);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = fmaf(rest[e], 1.0f / (1 << kWeightShift), o[e]);
+                }
             }
             if (tid < P.D) {
 #pragma unroll
@@ -545,9 +637,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
                         if (SPEC_IN(s.part + r, P.part_rows, DBG_ATTEND)) P.part_o[(s.part + r) * P.D + tid] = y;
                     } else {
                         const int j = P.by_group(s.row0 + r), g = s.row0 + r - j * P.G;
-                        if (SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
-                            static_cast<__nv_bfloat16 *>(P.out)[(s.t0 + j) * P.out_stride + (s.head * P.G + g) * P.D + tid] =
-                                __float2bfloat16_rn(y);
+                        const int64_t to = (s.t0 + j) * P.out_stride + (s.head * P.G + g) * P.D + tid;
+                        if (!SPEC_IN(s.t0 + j, P.T, DBG_ATTEND)) continue;
+                        if constexpr (WIDE)
+                            static_cast<float *>(P.out)[to] = y;
+                        else
+                            static_cast<__nv_bfloat16 *>(P.out)[to] = __float2bfloat16_rn(y);
                     }
                 }
             }
@@ -564,16 +659,16 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT> &
 
 // ---------------------------------------------------------------- the kernel
 
-template <int RT, bool PREFIX>
+template <int RT, bool PREFIX, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kPerSM)
     spec_attend8_round_kernel(const __grid_constant__ AttendParams P, const CacheMap M,
                              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char ring_mem[];  // tiles, queries, weights, the rest
-    unsigned char *q_tile = ring_mem + stages<RT>() * kTile;
-    unsigned char *p_tile = q_tile + q_bytes(RT);
-    Shared<RT> &sh = *reinterpret_cast<Shared<RT> *>(p_tile + p_bytes(RT));
+    unsigned char *q_tile = ring_mem + stages<RT, WIDE>() * kTile;
+    unsigned char *p_tile = q_tile + q_bytes<WIDE>(RT);
+    Shared<RT, WIDE> &sh = *reinterpret_cast<Shared<RT, WIDE> *>(p_tile + p_bytes<WIDE>(RT));
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    constexpr int kColumns = RT == 64 ? 256 : 128;  // 3 RT, as a power of two
+    constexpr int kColumns = RT * Parts<WIDE>::kSets == 64 ? 256 : 128;  // 3 RT a set, as a power of two
 
     if (warp == 5) tmem_alloc(&sh.tmem, kColumns);
     if (threadIdx.x == 0) {
@@ -594,12 +689,12 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
     begin_kernel<PREFIX>(P);
 
     if (warp < 4) {
-        softmax_role<RT, PREFIX>(P, sh, ring_mem, q_tile, p_tile);
+        softmax_role<RT, PREFIX, WIDE>(P, sh, ring_mem, q_tile, p_tile);
     } else if (warp == 4) {
         load_role<PREFIX>(P, M, &kmap, &vmap, sh.pipe, ring_mem, blockIdx.x, lane);
     } else {
         if constexpr (!PREFIX) keep_books<kKT>(P, lane);
-        mma_role<RT>(P, sh, ring_mem, q_tile, p_tile);
+        mma_role<RT, WIDE>(P, sh, ring_mem, q_tile, p_tile);
         // nothing this warp issued is in flight when the CTA ends
         if (elect_lane()) mma_commit(&sh.drain);
         __syncwarp();

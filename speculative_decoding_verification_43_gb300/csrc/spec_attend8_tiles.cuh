@@ -195,10 +195,10 @@ constexpr int kLeastQueryLog2 = -100;
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, const uint4 &v) {
     return __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
 }
-// s for a row whose greatest magnitude has these bits; what is not finite gives 1.
+// s for a row whose greatest magnitude has these bits (of fp32); what is not finite gives 1.
 __device__ __forceinline__ float query_scale(uint32_t bits) {
-    if (bits >= 0x7f80u) return 1.0f;
-    const int e = static_cast<int>(bits >> 7) - 127 - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0);
+    if (bits >= 0x7f800000u) return 1.0f;
+    const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
     return __uint_as_float(static_cast<uint32_t>(max(e, kLeastQueryLog2) + 127) << 23);
 }
 // Eight bf16 times inv as hi and lo.
@@ -215,6 +215,25 @@ __device__ __forceinline__ void split_query(const uint4 &v, float inv, uint2 &hi
     }
     hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+// Four fp32 times inv in four parts: two as above, and two of what they leave (at most 1/2: a part of four bits is off by
+// at most 2^4 of 448, the next by 2^-1) times 2^SHIFT.
+template <int SHIFT>
+__device__ __forceinline__ void split_query_wide(const float4 &x, float inv, uint32_t (&parts)[4]) {
+    static_assert(SHIFT <= 9, "what is left stays within e4m3");
+    float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = to_e4m3(y[0], y[1]) | static_cast<uint32_t>(to_e4m3(y[2], y[3])) << 16;
+        const float4 f = e4m3_to_float4(p);
+        parts[i] = p;
+        const float times = i == 1 ? static_cast<float>(1 << SHIFT) : 1.0f;
+        y[0] = (y[0] - f.x) * times;
+        y[1] = (y[1] - f.y) * times;
+        y[2] = (y[2] - f.z) * times;
+        y[3] = (y[3] - f.w) * times;
+    }
 }
 
 // ---------------------------------------------------------------- values that are no numbers
@@ -252,16 +271,17 @@ __device__ __forceinline__ float tile_value(const unsigned char *v_tile, int k, 
     return e4m3_to_float2(v_tile[k * 128 + (((d >> 4) ^ (k & 7)) << 4) + (d & 15)]).x;
 }
 
-// log2 of a scale and the reciprocal that goes with it: a weight times the scale, and back. The reciprocal is finite
-// whatever the scale is: rows that do not see its position add 0 times it to their sums.
+// log2 of a scale and the reciprocal that goes with it: a weight times the scale, and back (exact for powers of two).
+// The reciprocal is finite whatever the scale is: rows that do not see its position add 0 times it to their sums.
 struct ValueScale {
     float log2, inv;
 };
 __device__ __forceinline__ ValueScale value_scale(float s) {
-    ValueScale v;
-    v.log2 = __log2f(s);
-    v.inv = fabsf(v.log2) < 126.0f ? ex2(-v.log2) : 1.0f;
-    return v;
+    const uint32_t bits = __float_as_uint(s);
+    if (bits - 0x00800000u >= 0x7f000000u) return {__log2f(s), 1.0f};  // no positive normal number
+    const int e = static_cast<int>(bits >> 23) - 127;
+    const float part = __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+    return {static_cast<float>(e) + part, ex2(-part) * ex2(static_cast<float>(-e))};
 }
 
 }  // namespace tiles8

@@ -52,6 +52,26 @@ __device__ __forceinline__ void split_e5m2(float a, float b, float c, float d, u
         }
     }
 }
+// The same, and what the 16-bit float and its three parts leave of the weight, times 2^SHIFT, in three more.
+template <int SHIFT>
+__device__ __forceinline__ void split_e5m2_wide(float a, float b, float c, float d, uint32_t (&w)[6]) {
+    __half2 x = __floats2half2_rn(a, b), y = __floats2half2_rn(c, d);
+    const float2 fx = __half22float2(x), fy = __half22float2(y);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t u = (reinterpret_cast<const uint32_t &>(x) + 0x00800080u) & 0xff00ff00u,
+                       v = (reinterpret_cast<const uint32_t &>(y) + 0x00800080u) & 0xff00ff00u;
+        w[i] = __byte_perm(u, v, 0x7531);
+        x = __hsub2(x, reinterpret_cast<const __half2 &>(u));
+        y = __hsub2(y, reinterpret_cast<const __half2 &>(v));
+    }
+    const float2 gx = __half22float2(x), gy = __half22float2(y);  // (0 but for the smallest weights)
+    constexpr float times = static_cast<float>(1 << SHIFT);
+    uint32_t more[3];
+    split_e5m2((a - fx.x + gx.x) * times, (b - fx.y + gx.y) * times, (c - fy.x + gy.x) * times, (d - fy.y + gy.y) * times, more);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w[3 + i] = more[i];
+}
 // An e5m2 in the upper byte of the lower half of a word.
 __device__ __forceinline__ float e5m2_to_float(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 8)));

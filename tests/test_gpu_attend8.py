@@ -52,10 +52,11 @@ MORE = {
 }
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("name", list(MORE))
-def test_layouts(name):
+def test_layouts(name, dtype):
     rows, kv, Hq, Hkv, D, page, W, S, L, order = MORE[name]
-    b = Batch8(rows, kv, Hq, Hkv, D, BF, page, W, S, L, seed=len(name), order=order).place()
+    b = Batch8(rows, kv, Hq, Hkv, D, dtype, page, W, S, L, seed=len(name), order=order).place()
     got = b.attention().run()
     torch.cuda.synchronize()
     assert (got.req_status.cpu() == 0).all()
@@ -66,9 +67,11 @@ def test_layouts(name):
 def test_plan_names_the_kernel(rows, kernel):
     b = Batch8(rows, [200], 8, 2, 64, BF, 16, seed=1).place()
     assert b.attention().plan() == f"spec_attend8_{kernel}_kernel"
-    for kw in (dict(dtype=F32), dict(page=7), dict(D=144)):
-        b = Batch8(rows, [200], 8, 2, kw.get("D", 64), kw.get("dtype", BF), kw.get("page", 16), seed=1).place()
-        assert b.attention().plan() == "spec_attend_fma_kernel"
+    assert Batch8(rows, [200], 8, 2, 64, F32, 16, seed=1).place().attention().plan() == "spec_attend8_round_kernel"
+    for page, D in ((7, 64), (16, 144)):
+        for dtype in (BF, F32):
+            b = Batch8(rows, [200], 8, 2, D, dtype, page, seed=1).place()
+            assert b.attention().plan() == "spec_attend_fma_kernel"
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -171,11 +174,12 @@ def test_no_number_where_only_later_rows_see_it(dtype, rows, what):
         assert torch.isnan(out[last].float()).all() and torch.isnan(lse[last]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("rows", [[5], [13], [150], [400]], ids=str)
-def test_scale_that_is_no_number_spoils_those_who_see_it(rows):
+def test_scale_that_is_no_number_spoils_those_who_see_it(rows, dtype):
     """The page of the last positions: rows before them are as if it did not exist."""
     n = rows[0]
-    b = Batch8(rows, [160 + n], 4, 2, 64, BF, 16, seed=5)
+    b = Batch8(rows, [160 + n], 4, 2, 64, dtype, 16, seed=5)
     clean = b.reference()
     b.place()
     first = (160 + n - 1) // 16 * 16           # the last page's first position
@@ -189,7 +193,7 @@ def test_scale_that_is_no_number_spoils_those_who_see_it(rows):
     class Part:
         pass
     part, kept = Part(), Part()
-    part.dtype, kept.out, kept.lse = BF, got.out.cpu()[keep], got.lse.cpu()[keep]
+    part.dtype, kept.out, kept.lse = dtype, got.out.cpu()[keep], got.lse.cpu()[keep]
     check8(part, kept, [t[keep] for t in clean])
 
 
@@ -211,10 +215,11 @@ def test_window_edge_no_number():
     check8(part, kept, [t[1:] for t in clean])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("rows", [[3], [100]], ids=str)
-def test_queries_that_are_not_finite(rows):
+def test_queries_that_are_not_finite(rows, dtype):
     """A head of one row: that head's output is no number, the others are as before."""
-    b = Batch8(rows, [200], 4, 2, 64, BF, 16, seed=6)
+    b = Batch8(rows, [200], 4, 2, 64, dtype, 16, seed=6)
     ref = b.reference()
     b.place()
     b.qd[1, 2, 7] = math.inf
@@ -229,7 +234,7 @@ def test_queries_that_are_not_finite(rows):
     class Part:
         pass
     part, kept = Part(), Part()
-    part.dtype, kept.out, kept.lse = BF, out[ok], got.lse.cpu()[ok]
+    part.dtype, kept.out, kept.lse = dtype, out[ok], got.lse.cpu()[ok]
     check8(part, kept, [t[ok] if t.shape[1] == 4 else t.expand(-1, 4)[ok] for t in ref])
 
 
