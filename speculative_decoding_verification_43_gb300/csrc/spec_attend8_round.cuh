@@ -32,6 +32,11 @@ constexpr float kMost = 15.0f; // before the next
 template <bool WIDE>
 struct Parts {
     static constexpr int kSets = WIDE ? 2 : 1, kQ = 2, kP = 3;  // accumulators, and parts in each
+    // Tiles whose products are summed by the tensor cores, which cut sums off instead of rounding them: each
+    // instruction takes about 2^-23.5 off an accumulator of one sign, 12 of them a tile. bf16 rows can bear that (2^-13
+    // after a hundred tiles); fp32 rows' sums go to columns of their own every few tiles, added up in fp32, and the
+    // smaller parts are taken first, while there is little to cut.
+    static constexpr int kGroup = WIDE ? 2 : 1 << 30;
 };
 constexpr int kQueryShift = 8, kWeightShift = 11;
 
@@ -88,7 +93,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
                                          unsigned char *q_tile, unsigned char *p_tile) {
     int32_t *ab = &sh.pipe.abort;
     constexpr int kKeys = decltype(Shared<RT, WIDE>::pipe)::kKeys, kValues = decltype(Shared<RT, WIDE>::pipe)::kValues;
-    constexpr int kSets = Parts<WIDE>::kSets, kQ = Parts<WIDE>::kQ, kP = Parts<WIDE>::kP;
+    constexpr int kSets = Parts<WIDE>::kSets, kQ = Parts<WIDE>::kQ, kP = Parts<WIDE>::kP, kGroup = Parts<WIDE>::kGroup;
     const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kSets * RT;
     const uint64_t q_op = smem_operand(smem_addr(q_tile), 16), k_op = smem_operand(smem_addr(ring_mem), 16),
                    v_op = smem_operand(smem_addr(ring_mem + kKeys * kTile), 16),
@@ -124,12 +129,12 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
                         const uint64_t k = operand_at(k_op, next.slot * kTile);
                         if (elect_lane()) {
 #pragma unroll
-                            for (int q = 0; q < kSets * kQ; ++q)
+                            for (int q = kSets * kQ - 1; q >= 0; --q)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     if (i < steps)
                                         mma8_ss(s_col + (b * kSets + q / kQ) * RT, operand_at(k, i * 32),
-                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shape, q % kQ + i > 0);
+                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shape, q % kQ < kQ - 1 || i > 0);
                             mma_commit(&sh.s_full[b]);
                             mma_commit(&sh.pipe.k_empty[next.slot]);
                         }
@@ -145,13 +150,13 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
                         if (elect_lane()) {
                             if (take) {  // O^T += V^T P^T
 #pragma unroll
-                                for (int p = 0; p < kSets * kP; ++p)
+                                for (int p = kSets * kP - 1; p >= 0; --p)
 #pragma unroll
                                     for (int i = 0; i < 4; ++i)
                                         if (i * 32 < n)
                                             mma8_ss(o_col + p / kP * RT, operand_at(values, i * 4096),
                                                     operand_at(p_op, p * p_part(RT) + i * 32 * RT), pv_shape,
-                                                    t > 0 || p % kP + i > 0);
+                                                    t % kGroup > 0 || p % kP < kP - 1 || i > 0);
                             }
                             mma_commit(&sh.o_done);
                             mma_commit(&sh.pipe.v_empty[v.slot]);
@@ -243,8 +248,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     int32_t *ab = &sh.pipe.abort;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    constexpr int kSets = Parts<WIDE>::kSets, kP = Parts<WIDE>::kP;
-    const uint32_t s_addr = sh.tmem + lanes, o_addr = s_addr + 2 * kSets * RT;
+    constexpr int kSets = Parts<WIDE>::kSets, kP = Parts<WIDE>::kP, kGroup = Parts<WIDE>::kGroup;
+    const uint32_t s_addr = sh.tmem + lanes, o_addr = s_addr + 2 * kSets * RT, sum_addr = o_addr + kSets * RT;
     Scratch<RT> &scratch = *reinterpret_cast<Scratch<RT> *>(p_tile);
     Ring values = {0, kValues, 0}, desc = {0, 2, 0};
     uint32_t s_phases = 0, o_phase = 0;
@@ -468,6 +473,22 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
             uint32_t word = meet_words(sh.found, mine);
             if (word & kGone) return;
             rest();  // the product before this tile: the weights' memory is free, O at rest
+            if (WIDE && i > 0 && i % kGroup == 0) {
+#pragma unroll 1
+                for (int r0 = 0; r0 < nrows; r0 += 16) {
+                    float o[16], more[16], sum[16];
+                    uint32_t ow[16];
+                    tmem_ld16(o, o_addr + r0);
+                    tmem_ld16(more, o_addr + RT + r0);
+                    tmem_ld16(sum, sum_addr + r0);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        ow[e] = __float_as_uint((i > kGroup ? sum[e] : 0.0f) + fmaf(more[e], 1.0f / (1 << kWeightShift), o[e]));
+                    tmem_st16(sum_addr + r0, ow);
+                }
+                tmem_wait_st();
+            }
             if (i == 0 || word & kBeyond) {
                 // new references: the rows' maxima over the tile, where they are larger
 #pragma unroll
@@ -499,7 +520,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                             l[e / 2].y *= scratch.row[e + 1];
                         }
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kSets * RT; c0 += 16) {
+                    for (int c0 = 0; c0 < (WIDE ? kSets + 1 : 1) * RT; c0 += 16) {  // (and the sums)
                         const int r0 = c0 % RT;
                         if (r0 >= nrows) continue;
                         float o[16];
@@ -551,7 +572,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                 }
             if (skip) {
                 bar_sync(1, 128);  // all weights are there
-                mixed_tile<RT, WIDE>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i == 0);
+                mixed_tile<RT, WIDE>(P, pos, o_addr, v_tile, p_tile, s.keys, x0, n, nrows, tid, i % kGroup == 0);
             }
             if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip) = skip;
             fence_proxy_async_smem();
@@ -625,6 +646,12 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[e] = fmaf(rest[e], 1.0f / (1 << kWeightShift), o[e]);
+                    if (nt > kGroup) {
+                        tmem_ld4(rest, sum_addr + r0);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] += rest[e];
+                    }
                 }
             }
             if (tid < P.D) {
@@ -668,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM)
     unsigned char *p_tile = q_tile + q_bytes<WIDE>(RT);
     Shared<RT, WIDE> &sh = *reinterpret_cast<Shared<RT, WIDE> *>(p_tile + p_bytes<WIDE>(RT));
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    constexpr int kColumns = RT * Parts<WIDE>::kSets == 64 ? 256 : 128;  // 3 RT a set, as a power of two
+    constexpr int kColumns = RT == 64 || WIDE ? 256 : 128;  // 3 RT a set, and the sums' RT, as a power of two
 
     if (warp == 5) tmem_alloc(&sh.tmem, kColumns);
     if (threadIdx.x == 0) {

@@ -8,6 +8,8 @@ import torch
 from cache8_ref import Batch8, check8
 from test_gpu_attend import CASES as ATTEND_CASES
 
+from speculative_decoding_verification_43_gb300 import api
+
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
@@ -257,3 +259,28 @@ def test_errors_of_one_request_leave_the_others():
     part, kept = Part(), Part()
     part.dtype, kept.out, kept.lse = BF, got.out.cpu()[keep], got.lse.cpu()[keep]
     check8(part, kept, [t[keep] for t in ref])
+
+
+def test_long_sums_of_one_sign_in_fp32():
+    """Values of one sign and even weights over a long text, in fp32, 96 requests on the same pages, so that a worker
+    has some 70 tiles: an accumulator that cuts every sum off instead of rounding it would be off by 2^-15. The sum of
+    n weighted values in groups that are added up in turn may be off by the additions' cuts and roundings, fewer than
+    64 on the way of each value (a group's instructions, the groups' sums and the workers', whose errors go both
+    ways), 2^-24 each, and by the weights': together 2^-17."""
+    n, B, D, page = 30000, 96, 64, 16
+    g = torch.Generator().manual_seed(1)
+    pages = n // page
+    kc, vc = (torch.randint(0x28, 0x40, (pages, page, 1, D), generator=g, dtype=torch.uint8) for _ in range(2))
+    ks, vs = (torch.exp2(torch.randint(-1, 2, (pages, 1), generator=g).float()) for _ in range(2))
+    q = torch.randn(B, 2, D, generator=g) * 0.01
+    K, V = ((c.view(torch.float8_e4m3fn).float() * s[:, :, None, None]).double().view(n, D) for c, s in ((kc, ks), (vc, vs)))
+    z = q.double() @ K.T * D ** -0.5
+    want, lse = torch.softmax(z, 2) @ V, torch.logsumexp(z, 2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.arange(pages, **i32).repeat(B, 1)
+    got = api.attend8(q.cuda(), kc.cuda().view(torch.float8_e4m3fn), vc.cuda().view(torch.float8_e4m3fn), ks.cuda(), vs.cuda(),
+                      torch.arange(B + 1, **i32), torch.full((B,), n, **i32), table)
+    torch.cuda.synchronize()
+    assert (got.req_status == 0).all()
+    assert ((got.out.cpu().double() - want).abs() <= want.abs() * 2.0 ** -17).all()
+    assert ((got.lse.cpu().double() - lse).abs() <= lse.abs() * 2.0 ** -17).all()
