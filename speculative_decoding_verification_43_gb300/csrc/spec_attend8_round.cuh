@@ -56,7 +56,8 @@ struct Shared {
 template <int RT>
 struct Scratch {
     float warp[4][RT];
-    float row[RT];
+    alignas(16) float row[RT];
+    int64_t to[RT];  // where a row goes (-1: nowhere)
 };
 // A reference that every finite score exceeds and that leaves -inf alone.
 constexpr float kNoRef = 3e38f;
@@ -393,6 +394,35 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
             const float2 by = used ? sh.pipe.scale[values.slot][tid >> P.box_log2] : make_float2(1.0f, 1.0f);
             const ValueScale vs = value_scale(by.y);
             const float2 kf = make_float2(by.x, by.x), vl = make_float2(vs.log2, vs.log2), vi = make_float2(vs.inv, vs.inv);
+            // in an edge tile, the rows that see this position
+            uint32_t seen[RT / 32];
+            if (edge) {
+                const bool in = x >= s.keys.from && x < s.keys.hi, sink = x < P.n_sink;
+                if constexpr (PREFIX) {
+                    const int back = P.window > 0 ? P.window : INT_MAX;
+#pragma unroll
+                    for (int c = 0; c < RT / 32; ++c) {
+                        seen[c] = 0u;
+#pragma unroll 4
+                        for (int y = 0; y < 32; ++y) {
+                            const int p = 32 * c + y < n16 ? pos[32 * c + y] : -1;
+                            if (in && x <= p && (sink || p - x < back)) seen[c] |= 1u << y;
+                        }
+                    }
+                } else {
+                    // positions grow with the packed rows, by one every G: those from the position's own on, up to where the
+                    // window has gone by
+                    const int64_t first = in ? (static_cast<int64_t>(x) - s.base) * P.G - s.row0 : RT;
+                    const int64_t last = P.window > 0 && !sink ? first + static_cast<int64_t>(P.window) * P.G : RT;
+                    const int a = static_cast<int>(min(max(first, static_cast<int64_t>(0)), static_cast<int64_t>(RT))),
+                              z = static_cast<int>(min(max(last, static_cast<int64_t>(0)), static_cast<int64_t>(RT)));
+#pragma unroll
+                    for (int c = 0; c < RT / 32; ++c) {
+                        const int lo = min(max(a - 32 * c, 0), 32), hi = min(max(z - 32 * c, 0), 32);
+                        seen[c] = hi > lo ? 0xffffffffu >> (32 - (hi - lo)) << lo : 0u;
+                    }
+                }
+            }
             // from 16 rows' products (from row e on) to the logarithms of this position's weights, references aside
             auto finish = [&](float *z, int e) {
 #pragma unroll
@@ -406,13 +436,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                     z[y + 3] = c.y;
                 }
                 if (edge) {
-                    const bool in = x >= s.keys.from && x < s.keys.hi, sink = x < P.n_sink;
-                    const int back = P.window > 0 ? P.window : INT_MAX;
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const int p = pos[e + y];
-                        if (!(in && x <= p && (sink || p - x < back))) z[y] = -INFINITY;
-                    }
+                    for (int y = 0; y < 16; ++y)
+                        if (!(seen[(e + y) / 32] >> (e + y) % 32 & 1u)) z[y] = -INFINITY;
                 }
             };
             // 32 rows' scores stay in registers; 64 rows' would not, beside their sums, and are read anew
@@ -619,58 +645,60 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
             if (pos[tid] < 0) sum = 0.0f;  // padding
             const bool none = sum == 0.0f;
             const float m = none ? -INFINITY : -nref[tid];
+            int64_t to = -1;
             if (s.part >= 0) {
                 // a sum that is not a number must reach the joined row, whatever the other parts' maxima
-                if (SPEC_IN(s.part + tid, P.part_rows, DBG_ATTEND))
+                if (SPEC_IN(s.part + tid, P.part_rows, DBG_ATTEND)) {
                     P.part_ml[s.part + tid] = make_float2(isnan(sum) ? INFINITY : m, sum);
+                    to = (s.part + tid) * P.D;
+                }
                 scratch.row[tid] = none ? 0.0f : 1.0f;
             } else {
-                const int j = P.by_group(s.row0 + tid), g = s.row0 + tid - j * P.G;
-                if (P.lse && SPEC_IN(s.t0 + j, P.T, DBG_ATTEND))
-                    P.lse[static_cast<int64_t>(s.t0 + j) * P.Hq + s.head * P.G + g] =
-                        none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+                const int j = P.by_group(s.row0 + tid), g = s.row0 + tid - j * P.G, h = s.head * P.G + g;
+                if (SPEC_IN(s.t0 + j, P.T, DBG_ATTEND)) {
+                    if (P.lse)
+                        P.lse[static_cast<int64_t>(s.t0 + j) * P.Hq + h] =
+                            none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+                    to = (s.t0 + j) * P.out_stride + static_cast<int64_t>(h) * P.D;
+                }
                 scratch.row[tid] = none ? 0.0f : 1.0f / sum;
             }
+            scratch.to[tid] = to;
         }
         bar_sync(1, 128);
+        const bool part = s.part >= 0;
 #pragma unroll 1
-        for (int r0 = 0; r0 < nrows; r0 += 4) {
-            float o[4];
+        for (int r0 = 0; r0 < nrows; r0 += 16) {
+            float o[16];
             __syncwarp();
             if (nt > 0) {
-                tmem_ld4(o, o_addr + r0);
-                tmem_wait_ld();
+                tmem_ld16(o, o_addr + r0);
                 if constexpr (WIDE) {
-                    float rest[4];
-                    tmem_ld4(rest, o_addr + RT + r0);
+                    float rest[16], sum[16];
+                    tmem_ld16(rest, o_addr + RT + r0);
+                    tmem_ld16(sum, sum_addr + r0);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = fmaf(rest[e], 1.0f / (1 << kWeightShift), o[e]);
-                    if (nt > kGroup) {
-                        tmem_ld4(rest, sum_addr + r0);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] += rest[e];
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = fmaf(rest[e], 1.0f / (1 << kWeightShift), o[e]) + (nt > kGroup ? sum[e] : 0.0f);
+                } else {
+                    tmem_wait_ld();
                 }
             }
             if (tid < P.D) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 16; ++e) {
                     const int r = r0 + e;
                     if (r >= nrows) break;
                     const float a = scratch.row[r], y = a == 0.0f ? 0.0f : o[e] * a;
-                    if (s.part >= 0) {
-                        if (SPEC_IN(s.part + r, P.part_rows, DBG_ATTEND)) P.part_o[(s.part + r) * P.D + tid] = y;
-                    } else {
-                        const int j = P.by_group(s.row0 + r), g = s.row0 + r - j * P.G;
-                        const int64_t to = (s.t0 + j) * P.out_stride + (s.head * P.G + g) * P.D + tid;
-                        if (!SPEC_IN(s.t0 + j, P.T, DBG_ATTEND)) continue;
-                        if constexpr (WIDE)
-                            static_cast<float *>(P.out)[to] = y;
-                        else
-                            static_cast<__nv_bfloat16 *>(P.out)[to] = __float2bfloat16_rn(y);
-                    }
+                    const int64_t to = scratch.to[r];
+                    if (to < 0) continue;
+                    if (part)
+                        P.part_o[to + tid] = y;
+                    else if constexpr (WIDE)
+                        static_cast<float *>(P.out)[to + tid] = y;
+                    else
+                        static_cast<__nv_bfloat16 *>(P.out)[to + tid] = __float2bfloat16_rn(y);
                 }
             }
         }
