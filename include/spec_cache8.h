@@ -51,18 +51,26 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  * spec_attend over the 8-bit cache: the same rows see the same positions (window, sinks, shared prefix), with
  *     k_x = k_scale * element, v_x = v_scale * element.
  * attend.dtype is the type of q and out; attend.k_cache and attend.v_cache are the e4m3 arrays. Scales are
- * finite, positive and within 2^-90 .. 2^90 (they need not be powers of two); a page whose scale is not so spoils
+ * finite, positive and within 2^-60 .. 2^60 (they need not be powers of two); a page whose scale is not so spoils
  * the rows that see one of its positions, and no others. Elements that are NaN give those rows what the formulas
  * say, and no others.
  *
- * fp32 rows, head sizes above 128, pages that are no multiple of 8 slots, and caches whose heads lie neither side
- * by side in a slot nor a whole number of slots apart: the fp32 units, 32-bit arithmetic throughout (out is rounded
- * once). Other bf16 rows: products on the tensor cores straight from the e4m3 elements, with 32-bit accumulation.
- * There a query enters as the sum of two e4m3 after division by the power of two that brings its head's largest
- * element between 224 and 448: exact for elements above 2^-11 of the largest, off by at most 2^-18 of the largest
- * below. A weight (times its position's v_scale) enters as the sum of three e5m2, which holds every 16-bit float of
- * that range: off by at most 2^-11 of itself, or 2^-27 of the row's reference. Statistics, their sum and lse come
- * from the 32-bit weights. Results do not depend on the order in which CTAs run. */
+ * Head sizes above 128, pages that are no multiple of 8 slots, and caches whose heads lie neither side by side in a
+ * slot nor a whole number of slots apart: the fp32 units, 32-bit arithmetic throughout (out is rounded once).
+ * Otherwise products on the tensor cores, with 32-bit accumulation, which cuts sums off instead of rounding them; q
+ * and the weights enter as sums of 8-bit parts. Scores, statistics, the weights' sum and lse are 32-bit.
+ *   A query is divided by the power of two that brings its head's largest element between 224 and 448.
+ *   bf16: two e4m3, exact for elements above 2^-9 of the largest, off by at most 2^-17 of the largest below.
+ *   fp32: four e4m3, off by at most 2^-19 of the element, or 2^-25 of the largest.
+ *   Weights, bf16 with up to 64 packed rows (rows times n_q_heads / n_kv_heads) a request on average: three e5m2 of the
+ *   weight times its position's v_scale, off by at most 2^-11 of itself, or 2^-27 of the row's reference.
+ *   bf16 with more, and the shared prefix with more rows in all: a 16-bit float, off by 2^-11 of itself (2^-32 of the
+ *   row's reference); a value times its v_scale is a 16-bit float too, off by at most 2^-24 of the largest v_scale within
+ *   128 positions, and by 2^-11 of itself where that v_scale is no power of two.
+ *   fp32: six e5m2, off by at most 2^-22 of itself, or 2^-38 of the reference; sums leave the tensor cores every
+ *   256 positions. (Random batches: off from 64 bits by 7e-7 of the outputs' size; a plain 32-bit form 1.1e-6.)
+ * In bf16 a sum of n terms of one sign, all taken by one worker, loses about n 2^-27 of itself by being cut off.
+ * Results do not depend on the order in which CTAs run. */
 typedef struct {
     spec_attend_args attend;
     const float *k_scale, *v_scale; /* [n_pages][n_kv_heads]                                     */

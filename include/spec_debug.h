@@ -1,11 +1,12 @@
 /*
  * The index-checked debug build of the verifier library (libspecverify_debug.so: the same
- * sources compiled with -DSPEC_DEBUG). It exports everything include/spec_verify.h and
- * include/spec_attend.h declare, with the same behaviour, plus the call below. Its kernels check
- * each index of their main global accesses (logit rows and vectors, the workspace's per-chunk and
+ * sources compiled with -DSPEC_DEBUG). It exports everything include/spec_verify.h, spec_attend.h,
+ * spec_cache8.h and spec_tables.h declare, with the same behaviour, plus the call below. Its kernels
+ * check each index of their main global accesses (logit rows and vectors, the workspace's per-chunk and
  * per-row arrays, the per-row and per-request outputs, the compaction's packed outputs, the
  * truncation cuts, the paged cache's slots whether read, copied or written, the append's output and
- * angle rows, and the attention's rows, outputs and parts) against the array's length. A failed check does not trap: it records the first failure and skips the access.
+ * angle rows, the block tables' entries and stack, and the attention's rows, outputs and parts) against
+ * the array's length. A failed check does not trap: it records the first failure and skips the access.
  *
  * The pages define no such build: it is a test aid of this library, for runs where a memory
  * checker is not available.

@@ -27,13 +27,24 @@ static spec_status attend8_sizes(const spec_attend8_args *a, AttendParams &P) {
 }
 
 // Rows of an item (as a power of two) and workers for `rows` packed rows of a head over `groups` requests on the
-// tensor cores.
+// tensor cores. By the average, because lengths are known on the device alone. Measured with 64 requests of 32 / 8 heads
+// of 128 (us with items of 32, 64 and 256 rows):
+//   packed rows of each request   32            48            64            96             128
+//   up to 2000 positions          69 88 170     104 101 169   112 116 169   155 179 177    200 198 177
+//   up to 8000                    169 202 358   290 239 358   310 277 360   451 469 388    593 529 388
+//   rows that differ, average     30            34            53            66             93
+//   up to 2000                    86 97 168     87 105 169    114 138 173   132 150 175    171 189 183
+//   up to 8000                    225 243 354   240 267 355   323 357 385   379 389 385    500 510 386
+// Between 32 and 64 the 64 rows win where the requests are alike (a fifth) and lose where they are not (a tenth). fp32
+// rows need the room of 64 rows for their further parts.
 static void tensor8_class(bool wide, int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
-    rt_log2 = wide || rows <= 24 * groups ? 5 : rows <= 48 * groups ? 6 : pair8::kRTLog2;
+    rt_log2 = wide || rows <= 32 * groups ? 5 : rows <= 64 * groups ? 6 : pair8::kRTLog2;
     workers = rt_log2 == pair8::kRTLog2 ? kSMs : kSMs * round8::kPerSM;
 }
 
-// Time of an item beside its tiles, in tiles.
+// Time of an item beside its tiles, in tiles. (Flat: 64 round items of up to 4000 positions take 95 us with 0, 96 with 4,
+// 103 with 16; 4 prompts of 1000 rows take 251 with 0, 226 with 6, 220 with 12, 226 with 24, and shorter ones are best
+// with 6.)
 static int extra8_units(int rt_log2) { return rt_log2 == pair8::kRTLog2 ? 6 : 4; }
 
 // Workers and parts of the kernels that serve the call.
@@ -46,7 +57,8 @@ static void attend8_work(AttendParams &P, bool tensor, bool wide) {
         P.prefix_extra = extra8_units(P.prefix_rt_log2);
         P.box_log2 = box_log2_of(P.page_size);
         // A slot's heads lie side by side, 128 bytes each: read at different times they cost DRAM more than their
-        // bytes. So up to eight heads of the same positions are read in step, by workers that begin together.
+        // bytes. So up to eight heads of the same positions are read in step, by workers that begin together: 16 requests
+        // of up to 16000 positions take 106 us with heads apart, 98 with two, 96 with eight in step.
         if (P.shared_len == 0 && P.own_rt_log2 != pair8::kRTLog2)
             while (P.head_step < 8 && P.Hkv % (2 * P.head_step) == 0) P.head_step *= 2;
         P.own_workers -= P.own_workers % P.head_step;

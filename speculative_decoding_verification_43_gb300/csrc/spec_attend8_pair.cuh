@@ -5,9 +5,15 @@
 //   S = Q K^T      Q in two e4m3 parts (spec_attend8_tiles.cuh), K as it lies in the cache
 //   P = 2^(S - m)  a warpgroup, one row per thread; P (16-bit floats) goes back over S's columns, in two halves
 //   O += P V       V as 16-bit floats, to which two warps bring each tile once for all 256 rows
-// Taking V as it is would need P in three parts of 8 bits: 12 instructions instead of 8 and five operations a weight
-// on top of four (prompts: 866 us against TIME), while converting V is one for two values, and exact. 16-bit floats
-// hold weights from 2^15 down to 2^-25 to 11 bits, so a row's reference m may stay 2^8 behind its maximum.
+// Taking V as it is would need P in three parts of 8 bits: 12 instructions instead of 8, and five operations a weight
+// on top of four (prompts 870 us that way, 621 this way when it came, with tiles fetched without the next head's bytes);
+// converting V is one operation for two values, and exact. 16-bit floats hold weights from 2^15 down to 2^-14 to 11
+// bits, below to 2^-25, so a row's reference m may stay 2^8 behind its maximum.
+//
+// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 570-630, 0.33 of the measured rate;
+// 64 requests behind 8192 shared positions 122-133, of which the shared ones some 60. Two tiles (both accumulators) take
+// 5000 cycles, 2080 of them products: a row's softmax takes 1900-2600 (the slower in the SM's quarters that convert values
+// too), the scores' way to it 560, and an accumulator's softmax and products follow one another.
 //
 // Scales: a column of S has its key's scale as a factor, the same for a box of at least eight columns. The values'
 // scales are applied where the values are converted, as fractions of the tile's largest (rounded up to a power of

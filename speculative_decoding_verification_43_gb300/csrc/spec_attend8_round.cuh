@@ -1,11 +1,21 @@
-// Attention of few rows over the cache in 8 bits on the tensor cores (bf16 rows, head sizes that are multiples of 16
-// up to 128): a verification round, single tokens. The work is laid out as in spec_attend_round.cuh: positions and
+// Attention of few rows over the cache in 8 bits on the tensor cores (head sizes that are multiples of 16 up to 128): a
+// verification round, single tokens; fp32 rows also in larger numbers. The work is laid out as in spec_attend_round.cuh: positions and
 // output columns along the lanes, the item's rows along the columns,
 //   S^T = K Q^T     K as it lies in the cache, Q in two parts (spec_attend8_tiles.cuh)
 //   O^T += V^T P^T  V as it lies in the cache, P in three parts, each with rows of RT bytes a position
 // Half the bytes of bf16 make the time between two tiles half as long, while the products take 20 instructions a
 // tile instead of 16, of 42 cycles each (a product's time follows its 128 lanes until it has 64 columns). So one
 // warp issues them together (a single thread took 126 cycles an instruction to issue them).
+//
+// Measured (us a call, back to back; heads 32 / 8 of 128): 16 requests of 1-8 rows with texts to 65000 (1.0 GB) 188, 0.81
+// of the copy rate, and 0.90 with 4 rows each; 64 requests under a window of 1024 (137 MB) 61; 5 rows of one request 12.6.
+// A tile takes a CTA 2500-2800 cycles with 32 rows, of which the tensor cores work 840 and the softmax threads the
+// rest, two CTAs an SM in turn; the copies alone take 159-189 us for the long texts, by the order of the pages. So the long
+// ones are bound by bytes and, with rows above 16, by the weights' arithmetic (three e5m2 a weight: eight instructions);
+// the window's items of nine tiles by their ends: some 3 us for the plan, 2 for the first tile's references.
+// What brought it here: hardware barriers between the softmax warps, and keys and values in rings of their own (226 ->
+// 191), heads of the same positions read in step, an edge tile's visible rows as bits (window 74 -> 61).
+// Two softmax warpgroups of 96 registers spilled and were twice as slow; so were three CTAs an SM.
 //
 // Scales. A thread has one position: its key's scale is one factor of all its scores, and a row's factor (the
 // query's own scale, the softmax's and log2 e) comes from shared memory beside the row's reference. The value's
@@ -27,8 +37,10 @@ constexpr float kMost = 15.0f; // before the next
 
 // What a row's type asks for. bf16: queries in two parts, weights in three, one accumulator each. fp32: two more parts
 // of the queries and three of the weights, which hold what the first ones leave times 2^kQueryShift and 2^kWeightShift,
-// each in an accumulator of its own, so that e4m3 and e5m2 need not reach down to it: 18 and 22 bits in all, and 26
-// bits below a query's largest element.
+// each in an accumulator of its own, so that e4m3 and e5m2 need not reach down to it: 19 and 22 bits in all, and 25
+// bits below a query's largest element. 40 instructions a tile instead of 20, and still a fifth of the fp32 units' time:
+// 64 requests of up to 4096 positions, 12 / 4 heads (128 MB) 246 -> 56 us, 0.34 of the copy rate, bound by the softmax threads, which make
+// six parts of a weight.
 template <bool WIDE>
 struct Parts {
     static constexpr int kSets = WIDE ? 2 : 1, kQ = 2, kP = 3;  // accumulators, and parts in each

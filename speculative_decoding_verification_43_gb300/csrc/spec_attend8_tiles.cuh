@@ -186,8 +186,8 @@ __device__ __forceinline__ void init_pipe(Pipe<KEYS, VALUES> &pipe, int value_re
 // ---------------------------------------------------------------- queries
 // A row of a head is divided by the power of two s that brings its largest element between 224 and 448, and each
 // element becomes hi + lo, hi the nearest e4m3 (four bits) and lo the nearest e4m3 to what that leaves. A bf16
-// element of eight bits is hi + lo exactly while lo's last bit is 2^-9 or more, that is from 2^-2 on (1 / 1792 of
-// the largest), and off by 2^-10 at most below. Both products go to the same scores, which are then taken times s.
+// element of eight bits is hi + lo exactly while lo's last bit is 2^-9 or more, that is from 2^-2 on (between
+// 1 / 896 and 1 / 1792 of the largest), and off by 2^-10 at most below. Both products go to the same scores, which are then taken times s.
 
 constexpr int kLeastQueryLog2 = -100;
 
@@ -218,7 +218,8 @@ __device__ __forceinline__ void split_query(const uint4 &v, float inv, uint2 &hi
 }
 
 // Four fp32 times inv in four parts: two as above, and two of what they leave (at most 1/2: a part of four bits is off by
-// at most 2^4 of 448, the next by 2^-1) times 2^SHIFT.
+// at most 2^4 of 448, the next by 2^-1) times 2^SHIFT. The first part has four bits, each further one adds five (the
+// sign is one): 19 in all, down to 2^-18.
 template <int SHIFT>
 __device__ __forceinline__ void split_query_wide(const float4 &x, float inv, uint32_t (&parts)[4]) {
     static_assert(SHIFT <= 9, "what is left stays within e4m3");

@@ -1,12 +1,13 @@
-// Attention on the fp32 units: the kernel for fp32, and for the bf16 shapes the tensor-core kernel does
-// not take. One CTA of four warps per worker; a warp owns up to four of the item's 16 packed rows.
+// Attention on the fp32 units: the kernel for fp32, for the bf16 shapes the tensor-core kernel does
+// not take, and, over the cache in 8 bits, for the shapes that its tensor-core kernels do not take. One CTA of four warps per worker; a warp owns up to four of the item's 16 packed rows.
 //
 // Per tile of 32 keys: lane x forms the scores of key x with the warp's rows (keys padded by 16 bytes
 // a row in shared memory, so that eight lanes' 16-byte reads cover all banks; queries are broadcast),
 // the running maximum and sum follow by shuffles, and for the second product the lanes turn to the
 // columns of the output, four (or eight, beyond 128) each, with the weights broadcast. The next tile is
 // copied in while this one is used (fp32: by asynchronous copies; bf16 values pass through registers on their
-// way to fp32, and each lane waits for its loads).
+// way to fp32, and each lane waits for its loads; 8-bit elements wait in registers while the tile before is used: 64 fp32
+// requests of up to 4096 positions over them 246 us, 354 with loads that are waited for).
 //
 // Bound by shared memory, whose reads take twice the arithmetic's time (each warp reads every key and
 // value): 256 requests of 4 rows and 16 query heads of 128 under a 500-token window (0.55 GB) 248 us, a

@@ -8,7 +8,6 @@
 
 namespace spec {
 
-constexpr float kE4m3Max = 448.0f;
 // The least scale that is set: a block of zeros has it, and so have values below 2^-52.
 constexpr int kLeastScaleLog2 = -60;
 

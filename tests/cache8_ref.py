@@ -138,13 +138,13 @@ class Batch8(Batch):
 def check8(batch, got, ref=None):
     """The kernel's out and lse against the reference.
 
-    Bounds, beside those of attend_ref.check (`ulps`, the exponentials, the sums). bf16 rows on the tensor cores:
-    a query element is off by at most 2^-18 of its head's largest, which moves a score by at most 2^-18 * `cut`. A
+    Bounds, beside those of attend_ref.check (`ulps`, the exponentials, the sums; fp32 rows' queries have 19 bits
+    and their weights 22 on the tensor cores, which `ulps` holds as well). bf16 rows on the tensor cores: a query element is off by at most 2^-18 of its head's largest, which moves a score by at most 2^-18 * `cut`. A
     product of a position's scale and a row's factor is rounded, 2^-23 of the score (4 |z| of `ulps` has it). The
     logarithms of the v scales are off by 2^-20 at most (|log2| below 64, 2^-22 of it each way). A weight is
     rounded to 11 bits, 2^-11 of itself, or by at most 2^-27 of the row's reference, which is at most the largest
     weight * 2^5 away from it: n keys move the output by at most n 2^-22 of the largest |v|. The output is rounded
-    once, 2^-8 of itself (2^-24 in fp32, where nothing else of this holds)."""
+    once, 2^-8 of itself (2^-24 in fp32)."""
     out, lse, mag, ulps, nk, cut, vmax = ref or batch.reference()
     got_out, got_lse = got.out.cpu().double(), got.lse.cpu().double()
     weight = 2 * ulps * 2.0 ** -22 + 2.0 ** -20 + nk * 2.0 ** -23
