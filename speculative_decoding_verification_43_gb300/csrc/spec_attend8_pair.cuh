@@ -2,8 +2,8 @@
 // 16 up to 128): long prompts, and the shared prefix. The work is laid out as in spec_attend_pair.cuh: an item of
 // 256 packed rows in two accumulators of 128 that use the same tiles, a row a thread, one warp issuing the
 // products of both in turn. Per tile of 128 keys and accumulator:
-//   S = Q K^T      Q in two e4m3 parts (spec_attend8_tiles.cuh), K as it lies in the cache
-//   P = 2^(S - m)  a warpgroup, one row per thread; P (16-bit floats) goes back over S's columns, in two halves
+//   S = Q K^T      Q in two e4m3 parts (spec_attend8_tiles.cuh), K as it lies in the cache, in two halves of 64 keys
+//   P = 2^(S - m)  a warpgroup, one row per thread; P (16-bit floats) goes back over S's columns, a half at a time
 //   O += P V       V as 16-bit floats, to which two warps bring each tile once for all 256 rows
 // Taking V as it is would need P in three parts of 8 bits: 12 instructions instead of 8, and five operations a weight
 // on top of four (prompts 870 us that way, 621 this way when it came, with tiles fetched without the next head's bytes);
@@ -43,9 +43,9 @@ constexpr float kMost = 15.0f;           // reached before the next
 
 struct Shared {
     Pipe<kStages / 2, kStages / 2> pipe;
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_half[2], o_full[2], agree[2], drain;
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], agree[2], drain;  // [accumulator][half of a tile]
     uint64_t v_full[2], v_empty[2];     // converted values
-    uint32_t skip[2];                   // the warpgroup does this tile's second product itself
+    uint32_t skip[2][2];                // the warpgroup does this half's second product itself
     uint32_t no_number[2][2];           // per slot of values and converting warp: it has found a NaN
     uint32_t tmem;
     alignas(16) float key_scale[2][kBoxes];  // per slot of values and eight columns
@@ -69,17 +69,18 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
     const int steps = (P.D + 31) / 32;
     Ring ring = {0, kStages / 2, 0}, values = {0, 2, 0}, desc = {0, 2, 0};
     uint32_t q_phases = 0, p_phases = 0;
-    // (by the elected lane) S = Q K^T of accumulator w; n positions of the tile are used
-    auto score = [&](int w, const Ring &at, int n) {
-        const uint64_t k = operand_at(k_op, at.slot * kTile), q = operand_at(q_op, w * kQBytes);
-        const uint32_t shape = mma8_shape(n, false, false, false, false);
+    // (by the elected lane) S = Q K^T of accumulator w and half u; n positions of the tile are used
+    auto score = [&](int w, int u, const Ring &at, int n) {
+        const uint64_t k = operand_at(k_op, at.slot * kTile + u * (kHalf * 128)), q = operand_at(q_op, w * kQBytes);
+        const uint32_t shape = mma8_shape(min(n - u * kHalf, kHalf), false, false, false, false);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < steps)
-                    mma8_ss(tmem + w * 256, operand_at(q, p * kQPart + i * 32), operand_at(k, i * 32), shape, p + i > 0);
-        mma_commit(&sh.s_full[w]);
+                    mma8_ss(tmem + w * 256 + u * kHalf, operand_at(q, p * kQPart + i * 32), operand_at(k, i * 32), shape,
+                            p + i > 0);
+        mma_commit(&sh.s_full[w][u]);
     };
     // (by the elected lane) O += P V of accumulator w and half u; n positions of the half are used
     auto weigh = [&](int w, int u, const Ring &at, int n, bool add) {
@@ -103,7 +104,8 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                 q_phases ^= 1u << w;
                 tc_fence_after();
                 if (elect_lane()) {
-                    score(w, ring, n);
+                    score(w, 0, ring, n);
+                    if (n > kHalf) score(w, 1, ring, n);
                     if (w == accs - 1) mma_commit(&sh.pipe.k_empty[ring.slot]);
                 }
                 __syncwarp();
@@ -113,42 +115,34 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
             // beside issuing, the tensor cores wait for.
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
-                const bool more = t + 1 < nt;
+                const bool more = t + 1 < nt;  // (only a segment's last tile may be short)
                 const int next = more ? tile_keys(keys, tile_begin<kKT>(keys, first + t + 1)) : 0;
                 // (this warp has waited for every use of these slots before)
                 if (!(more ? wait_two(ab, &sh.v_full[values.slot], values.phase, &sh.pipe.k_full[ring.slot], ring.phase)
                            : wait_warp(ab, &sh.v_full[values.slot], values.phase)))
                     return;
+                const int halves = n > kHalf ? 2 : 1;
 #pragma unroll 1
-                for (int w = 0; w < accs; ++w) {
-                    if (!wait_warp(ab, &sh.p_full[w][0], p_phases >> w & 1u)) return;
-                    p_phases ^= 1u << w;
-                    tc_fence_after();
-                    const bool take = !*reinterpret_cast<volatile uint32_t *>(&sh.skip[w]);
-                    if (n > kHalf) {
+                for (int u = 0; u < halves; ++u) {
+#pragma unroll 1
+                    for (int w = 0; w < accs; ++w) {
+                        if (!wait_warp(ab, &sh.p_full[w][u], p_phases >> (2 * u + w) & 1u)) return;
+                        p_phases ^= 1u << (2 * u + w);
+                        tc_fence_after();
+                        const bool take = !*reinterpret_cast<volatile uint32_t *>(&sh.skip[w][u]);
                         if (elect_lane()) {
-                            if (take) weigh(w, 0, values, kHalf, t > 0);
-                            mma_commit(&sh.o_half[w]);
+                            if (take) weigh(w, u, values, min(n - u * kHalf, kHalf), t + u > 0);
+                            mma_commit(&sh.o_done[w][u]);
+                            // S and P share columns: matrix instructions of one thread run in the order of
+                            // their issue, so the next scores follow the product that reads P
+                            if (next > u * kHalf) score(w, u, ring, next);
+                            if (u == halves - 1 && w == accs - 1) {
+                                mma_commit(&sh.v_empty[values.slot]);
+                                if (more) mma_commit(&sh.pipe.k_empty[ring.slot]);
+                            }
                         }
                         __syncwarp();
-                        if (!wait_warp(ab, &sh.p_full[w][1], p_phases >> (2 + w) & 1u)) return;
-                        p_phases ^= 4u << w;
-                        tc_fence_after();
                     }
-                    if (elect_lane()) {
-                        if (take) weigh(w, n > kHalf ? 1 : 0, values, n > kHalf ? n - kHalf : n, t > 0 || n > kHalf);
-                        // S and P share columns: matrix instructions of one thread run in the order of
-                        // their issue, so the next scores follow the product that reads P
-                        if (more)
-                            score(w, ring, next);
-                        else
-                            mma_commit(&sh.o_full[w]);
-                        if (w == accs - 1) {
-                            mma_commit(&sh.v_empty[values.slot]);
-                            if (more) mma_commit(&sh.pipe.k_empty[ring.slot]);
-                        }
-                    }
-                    __syncwarp();
                 }
                 if (more) ring.step();
                 values.step();
@@ -311,7 +305,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_addr = sh.tmem + w * 256 + lanes, o_addr = s_addr + 128;
     Ring values = {0, 2, 0}, desc = {0, 2, 0};
-    uint32_t s_phase = 0, o_phase = 0, half_phase = 0, agree_phase = 0;
+    uint32_t s_phases = 0, o_phases = 0, agree_phase = 0;  // (a bit per half; o_phases: of the product to come)
     for (;;) {
         if (!wait_warp(ab, &sh.pipe.desc_full[desc.slot], desc.phase)) return;
         const Segment &s = sh.pipe.desc[desc.slot];
@@ -371,6 +365,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
             if (!have) m = 0.0f;  // lanes without a row never ask for another reference
             const KeyTiles keys = s.keys;
             const int first = s.tile;
+            int last = 0;  // the half that came last
             // a tile is seen whole by all rows from x0 = from on to here, when no window cuts it off
             const int whole = min(s.pmin, keys.hi - 1) - (kKT - 1), cut = P.window > 0 ? s.pmax - P.window : -1;
 #pragma unroll 1
@@ -380,19 +375,27 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 // A wait by parity tells this use of a slot of values from the one before, two tiles ago, once that one is
                 // known to have arrived: its products were issued before these scores. So what an early look at the values
                 // says counts only if the scores are there, looked at first.
-                if (!wait_two(ab, &sh.s_full[w], s_phase, &sh.v_full[values.slot], values.phase)) return;
-                s_phase ^= 1u;
-                tc_fence_after();
+                if (!wait_two(ab, &sh.s_full[w][0], s_phases & 1u, &sh.v_full[values.slot], values.phase)) return;
                 const unsigned char *v_tile = v_mem + values.slot * kValues;
                 const float *key_scale = sh.key_scale[values.slot];
                 const float unit = sh.unit[values.slot], by_unit = ex2(-unit);
                 const bool skip = edge && (sh.no_number[values.slot][0] | sh.no_number[values.slot][1]) != 0;
-                // (the tile before has been read out of this word: its products were issued before S)
-                if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w]) = skip;
 #pragma unroll 1
                 for (int u = 0; u * kHalf < n; ++u) {
                     const int xu = x0 + u * kHalf, nu = min(n - u * kHalf, kHalf);
                     const uint32_t s_at = s_addr + u * kHalf;
+                    if (u > 0 && !wait_warp(ab, &sh.s_full[w][1], s_phases >> 1 & 1u)) return;
+                    s_phases ^= 1u << u;
+                    tc_fence_after();
+                    // (what the half before left here has been read: its product was issued before these scores)
+                    if (tid == 0) *reinterpret_cast<volatile uint32_t *>(&sh.skip[w][u]) = skip;
+                    // O is at rest once the product of the half before is done; those before that one were issued
+                    // before these scores (so that a wait by parity knows it from them)
+                    auto at_rest = [&]() -> bool {
+                        if (i + u > 0 && !wait_warp(ab, &sh.o_done[w][u ^ 1], (o_phases >> (u ^ 1) & 1u) ^ 1u)) return false;
+                        tc_fence_after();
+                        return true;
+                    };
                     if (warp_has) {
                         float z[64];
                         tmem_ld32(z, s_at);
@@ -433,10 +436,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         const bool grow = have && (m == -INFINITY ? top > -INFINITY : top > kMost);
                         if (__any_sync(0xffffffffu, grow)) {
                             if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                                // O is at rest: with S came the end of the tiles before, and the first half's
-                                // product has a barrier of its own
-                                if (u > 0 && !wait_warp(ab, &sh.o_half[w], half_phase)) return;
-                                tc_fence_after();
+                                if (!at_rest()) return;
                                 const float a = grow && m != -INFINITY ? ex2(kTop - top) : 1.0f;
                                 l *= a;
 #pragma unroll 1
@@ -474,19 +474,18 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         l += (sum[0].x + sum[0].y) * by_unit;
                         tmem_wait_st();
                         if (skip) {
-                            if (u > 0 && !wait_warp(ab, &sh.o_half[w], half_phase)) return;
-                            tc_fence_after();
+                            if (!at_rest()) return;
                             mixed_tile(P.D, s_at, o_addr, v_tile, u * kHalf, xu, nu, from, lim, wlo, P.n_sink, i + u == 0);
                         }
                     }
                     tc_fence_before();
                     mbar_arrive(&sh.p_full[w][u]);
+                    o_phases ^= 1u << u;
+                    last = u;
                 }
-                if (n > kHalf) half_phase ^= 1u;
                 values.step();
             }
-            if (!wait_warp(ab, &sh.o_full[w], o_phase)) return;
-            o_phase ^= 1u;
+            if (!wait_warp(ab, &sh.o_done[w][last], (o_phases >> last & 1u) ^ 1u)) return;
             tc_fence_after();
         } else {
             for (int i = 0; i < nt; ++i) values.step();
@@ -591,15 +590,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         init_pipe(sh.pipe, 2, 11);  // values: the converting warps; segments: eight softmax warps, the issuing one and these
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 128);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i][0], 128);
-            mbar_init(&sh.p_full[i][1], 128);
-            mbar_init(&sh.o_half[i], 1);
-            mbar_init(&sh.o_full[i], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&sh.s_full[i][u], 1);
+                mbar_init(&sh.p_full[i][u], 128);
+                mbar_init(&sh.o_done[i][u], 1);
+                sh.skip[i][u] = 0;
+            }
             mbar_init(&sh.agree[i], 4);
             mbar_init(&sh.v_full[i], 2);
             mbar_init(&sh.v_empty[i], 1);
-            sh.skip[i] = 0;
         }
         mbar_init(&sh.drain, 1);
         fence_mbar_init();
