@@ -322,29 +322,42 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
         bool dead = true;               // no position, or no keys at all
         if (mine > 0 && nt > 0) {
             // the warp's queries into the swizzled tiles, two rows at a time: 16 lanes side by side along a row (a
-            // request of one sector per row and lane would take four times the time)
+            // request of one sector per row and lane would take four times the time). Sixteen rows' loads are under way
+            // together: one after the other, with the shuffles between them, they took 21000 cycles of an item.
+            constexpr int kAtOnce = 8;
             const int piece = lane % 16;
             const int64_t src = t * P.q_stride + static_cast<int64_t>(h) * P.D;
-#pragma unroll 4
-            for (int r0 = 0; r0 < kWarp; r0 += 2) {
-                const int r = r0 + lane / 16;
-                const int64_t row = __shfl_sync(0xffffffffu, src, r);
-                const int at = warp * kWarp + r;
-                const bool there = at < mine && piece < P.D / 8 && SPEC_IN(row + 8 * piece, P.T * P.q_stride, DBG_ATTEND);
-                const uint4 x = there ? reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + row)[piece]
-                                      : make_uint4(0u, 0u, 0u, 0u);
-                uint32_t top = top_bits(0u, x);
+#pragma unroll 1
+            for (int r0 = lane / 16; r0 < kWarp; r0 += 2 * kAtOnce) {
+                uint4 x[kAtOnce];
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const uint32_t bits = max(top & 0xffffu, top >> 16) << 16;
-                const float qs = query_scale(bits);
-                if (at < mine) {
+                for (int y = 0; y < kAtOnce; ++y) {
+                    const int r = r0 + 2 * y;
+                    const int64_t row = __shfl_sync(0xffffffffu, src, r);
+                    const bool there =
+                        warp * kWarp + r < mine && piece < P.D / 8 && SPEC_IN(row + 8 * piece, P.T * P.q_stride, DBG_ATTEND);
+                    x[y] = there ? reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q) + row)[piece]
+                                 : make_uint4(0u, 0u, 0u, 0u);
+                }
+                uint32_t bits[kAtOnce];
+#pragma unroll
+                for (int y = 0; y < kAtOnce; ++y) bits[y] = top_bits(0u, x[y]);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int y = 0; y < kAtOnce; ++y)
+                        bits[y] = __vmaxu2(bits[y], __shfl_xor_sync(0xffffffffu, bits[y], o));
+#pragma unroll
+                for (int y = 0; y < kAtOnce; ++y) {
+                    const int at = warp * kWarp + r0 + 2 * y;
+                    const uint32_t top = max(bits[y] & 0xffffu, bits[y] >> 16) << 16;
+                    const float qs = query_scale(top);
                     uint2 hi, lo;
-                    split_query(x, 1.0f / qs, hi, lo);
+                    split_query(x[y], power_inverse(qs), hi, lo);
                     unsigned char *to = q_tile + at * 128 + (((piece >> 1) ^ (at & 7)) << 4) + (piece & 1) * 8;
-                    *reinterpret_cast<uint2 *>(to) = hi;
+                    *reinterpret_cast<uint2 *>(to) = hi;  // (rows that are not there: zeros)
                     *reinterpret_cast<uint2 *>(to + kQPart) = lo;
-                    if (piece == 0) sh.factor[w][at] = bits < 0x7f800000u ? qs * P.scale_log2 : NAN;
+                    if (piece == 0) sh.factor[w][at] = top < 0x7f800000u ? qs * P.scale_log2 : NAN;
                 }
             }
             __syncwarp();
@@ -510,24 +523,24 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 const int width = min(span, P.D - d0);
                 __syncwarp();
 #pragma unroll 1
-                for (int d = 0; d < width; d += 16) {
-                    float o[16];
+                for (int d = 0; d < width; d += 32) {
+                    float o[32];
                     if (nt > 0) {
-                        tmem_ld16(o, o_addr + d0 + d);
-                        tmem_wait_ld();
+                        tmem_ld32(o, o_addr + d0 + d);
+                        tmem_wait_ld32(o);
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * inv;
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.0f : o[e] * inv;
                     unsigned char *row = mem + lane * 256;
-                    const int p0 = part ? d >> 2 : d >> 3;
+                    const int p0 = part ? d >> 2 : d >> 3;  // (pieces behind the width lie in the row, unused)
                     if (part) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 8; ++e)
                             *reinterpret_cast<float4 *>(row + (((p0 + e) ^ (lane & 7)) << 4)) =
                                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                        for (int e = 0; e < 4; ++e)
                             *reinterpret_cast<uint4 *>(row + (((p0 + e) ^ (lane & 7)) << 4)) =
                                 make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
                                            pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
@@ -535,17 +548,25 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 }
                 __syncwarp();
                 const int per = part ? width / 4 : width / 8, at_once = kWarp / per, piece = lane % per;
-#pragma unroll 4
-                for (int r0 = 0; r0 < kWarp; r0 += at_once) {
-                    const int r = r0 + lane / per;
-                    const int64_t dst = __shfl_sync(0xffffffffu, row_out, r & 31);
-                    if (lane < at_once * per && r < kWarp && warp * kWarp + r < mine) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(mem + r * 256 + ((piece ^ (r & 7)) << 4));
+#pragma unroll 1
+                for (int r0 = lane / per; r0 - lane / per < kWarp; r0 += 8 * at_once) {
+                    uint4 v[8];
+                    int64_t dst[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int r = (r0 + y * at_once) & 31;  // (beyond the warp's rows: not stored)
+                        dst[y] = __shfl_sync(0xffffffffu, row_out, r);
+                        v[y] = *reinterpret_cast<const uint4 *>(mem + r * 256 + ((piece ^ (r & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int r = r0 + y * at_once;
+                        if (lane >= at_once * per || r >= kWarp || warp * kWarp + r >= mine) continue;
                         if (part) {
-                            if (SPEC_IN(dst + d0 + 4 * piece, P.part_rows * P.D, DBG_ATTEND))
-                                *reinterpret_cast<uint4 *>(P.part_o + dst + d0 + 4 * piece) = v;
-                        } else if (SPEC_IN(dst + d0 + 8 * piece, P.T * P.out_stride, DBG_ATTEND)) {
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.out) + dst + d0 + 8 * piece) = v;
+                            if (SPEC_IN(dst[y] + d0 + 4 * piece, P.part_rows * P.D, DBG_ATTEND))
+                                *reinterpret_cast<uint4 *>(P.part_o + dst[y] + d0 + 4 * piece) = v[y];
+                        } else if (SPEC_IN(dst[y] + d0 + 8 * piece, P.T * P.out_stride, DBG_ATTEND)) {
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.out) + dst[y] + d0 + 8 * piece) = v[y];
                         }
                     }
                 }

@@ -305,7 +305,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                 for (int i = 0; i < kPieces; ++i) {
                     const int c = tid % kPer + i * kPer;
                     uint2 hi, lo;
-                    split_query(x[i], 1.0f / qs, hi, lo);
+                    split_query(x[i], power_inverse(qs), hi, lo);
                     *reinterpret_cast<uint2 *>(at(c)) = hi;
                     *reinterpret_cast<uint2 *>(at(c) + q_part(RT)) = lo;
                 }
@@ -329,7 +329,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
 #pragma unroll 2
                 for (int i = 0; i < 2 * kPieces; ++i) {  // (read again, from L1)
                     uint32_t parts[4];
-                    split_query_wide<kQueryShift>(piece(i / 2, i % 2), 1.0f / qs, parts);
+                    split_query_wide<kQueryShift>(piece(i / 2, i % 2), power_inverse(qs), parts);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         *reinterpret_cast<uint32_t *>(at(tid % kPer + i / 2 * kPer) + q * q_part(RT) + i % 2 * 4) = parts[q];

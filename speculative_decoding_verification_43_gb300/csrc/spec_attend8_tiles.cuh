@@ -201,6 +201,8 @@ __device__ __forceinline__ float query_scale(uint32_t bits) {
     const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
     return __uint_as_float(static_cast<uint32_t>(max(e, kLeastQueryLog2) + 127) << 23);
 }
+// 1 / s for such an s.
+__device__ __forceinline__ float power_inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
 // Eight bf16 times inv as hi and lo.
 __device__ __forceinline__ void split_query(const uint4 &v, float inv, uint2 &hi, uint2 &lo) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
