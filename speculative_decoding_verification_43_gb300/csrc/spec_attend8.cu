@@ -43,9 +43,8 @@ static void tensor8_class(bool wide, int64_t rows, int64_t groups, int32_t &rt_l
 }
 
 // Time of an item beside its tiles, in tiles. (Flat: 64 round items of up to 4000 positions take 95 us with 0, 96 with 4,
-// 103 with 16; 4 prompts of 1000 rows take 251 with 0, 226 with 6, 220 with 12, 226 with 24, and shorter ones are best
-// with 6.)
-static int extra8_units(int rt_log2) { return rt_log2 == pair8::kRTLog2 ? 6 : 4; }
+// 103 with 16; prompts of 1000-2500 rows 460 us with 3, 456 with 4, 457 with 6, 474 with 8.)
+constexpr int kExtra8 = 4;
 
 // Workers and parts of the kernels that serve the call.
 static void attend8_work(AttendParams &P, bool tensor, bool wide) {
@@ -53,8 +52,7 @@ static void attend8_work(AttendParams &P, bool tensor, bool wide) {
     if (tensor) {
         tensor8_class(wide, head_rows, P.B, P.own_rt_log2, P.own_workers);
         tensor8_class(wide, head_rows, 1, P.prefix_rt_log2, P.prefix_workers);
-        P.own_extra = extra8_units(P.own_rt_log2);
-        P.prefix_extra = extra8_units(P.prefix_rt_log2);
+        P.own_extra = P.prefix_extra = kExtra8;
         P.box_log2 = box_log2_of(P.page_size);
         // A slot's heads lie side by side, 128 bytes each: read at different times they cost DRAM more than their
         // bytes. So up to eight heads of the same positions are read in step, by workers that begin together: 16 requests

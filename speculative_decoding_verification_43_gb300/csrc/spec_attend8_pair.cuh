@@ -10,10 +10,15 @@
 // converting V is one operation for two values, and exact. 16-bit floats hold weights from 2^15 down to 2^-14 to 11
 // bits, below to 2^-25, so a row's reference m may stay 2^8 behind its maximum.
 //
-// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 570-630, 0.33 of the measured rate;
-// 64 requests behind 8192 shared positions 122-133, of which the shared ones some 60. Two tiles (both accumulators) take
-// 5000 cycles, 2080 of them products: a row's softmax takes 1900-2600 (the slower in the SM's quarters that convert values
-// too), the scores' way to it 560, and an accumulator's softmax and products follow one another.
+// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 455, 0.43 of
+// the measured rate; 64 requests behind 8192 shared positions 106, of which the shared ones some 50. Two tiles (both
+// accumulators) take 4400 cycles, 2600 of them products (QK by halves: 8 of 49 cycles where whole tiles take 65 for twice
+// the columns, a price for scores that are there before they are needed: 574 us -> 545). The rest is the issuing warp's
+// hand-overs, which find the weights ready but cost it 250 cycles each; a softmax thread works 2600. An item's queries and
+// outputs take 9400 + 7900 cycles (once 21000 + 8500: prompts 545 us). Tried: a second issuing warp, with registers moved
+// between warpgroups for it (470 -> 500), a look at the next weights between product and scores (545 -> 557),
+// conversions without bank conflicts (no difference). Left out one at a time, the exponentials, three quarters of PV,
+// the queries' lower parts or the conversions change the time by 0 to 4 %: no unit is the limit, their chain is.
 //
 // Scales: a column of S has its key's scale as a factor, the same for a box of at least eight columns. The values'
 // scales are applied where the values are converted, as fractions of the tile's largest (rounded up to a power of
@@ -223,14 +228,22 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
                     }
                 } else {
 #pragma unroll 1
-                    for (int r = first; r < n; r += 8) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        float share = 0.0f;
-                        if (item_sees(P, s.keys, x0 + r)) fetch(r, v, share);
-                        found |= isfinite(share) ? 0u : 1u;
-                        found |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                                 __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        put(r, v, share);
+                    for (int r = first; r < n; r += 32) {
+                        uint4 v[4];
+                        float share[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] = make_uint4(0u, 0u, 0u, 0u);
+                            share[i] = 0.0f;
+                            if (item_sees(P, s.keys, x0 + r + 8 * i)) fetch(r + 8 * i, v[i], share[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            found |= isfinite(share[i]) ? 0u : 1u;
+                            found |= __vcmpeq4(v[i].x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v[i].y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                                     __vcmpeq4(v[i].z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v[i].w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            put(r + 8 * i, v[i], share[i]);
+                        }
                     }
                 }
             }
@@ -252,6 +265,9 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
 }
 
 // ---------------------------------------------------------------- softmax (one row per thread)
+
+// The lowest n of 64 bits.
+__device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
 // The second product of a tile with values that are no numbers, on the fp32 units: the row's weights are in tensor
 // memory already, O is complete up to the tile before. first: O holds nothing yet.
@@ -374,7 +390,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 }
             }
             dead = p < 0;
-            const int lim = min(p, s.keys.hi - 1), wlo = P.window > 0 ? p - P.window + 1 : 0, from = s.keys.from;
+            const int lim = min(p, s.keys.hi - 1), wlo = P.window > 0 ? max(p - P.window + 1, 0) : 0, from = s.keys.from;
             if (!have) m = 0.0f;  // lanes without a row never ask for another reference
             const KeyTiles keys = s.keys;
             const int first = s.tile;
@@ -431,11 +447,11 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                             }
                         }
                         if (edge) {
+                            // the positions that the row sees, as bits: up to its own, in the window or among the sinks
+                            const uint64_t seen = below(lim + 1 - xu) & ~below(from - xu) & (~below(wlo - xu) | below(P.n_sink - xu));
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) {
-                                const int xe = xu + e;
-                                if (!(xe >= from && xe <= lim && (xe >= wlo || xe < P.n_sink))) z[e] = -INFINITY;
-                            }
+                            for (int e = 0; e < 64; ++e)
+                                if (!(seen >> e & 1u)) z[e] = -INFINITY;
                         }
 #pragma unroll
                         for (int e = 0; e < 64; e += 8) {
