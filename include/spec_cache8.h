@@ -62,7 +62,7 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  *   A query is divided by the power of two that brings its head's largest element between 224 and 448.
  *   bf16: two e4m3, exact for elements above 2^-9 of the largest, off by at most 2^-17 of the largest below.
  *   fp32: four e4m3, off by at most 2^-19 of the element, or 2^-25 of the largest.
- *   Weights, bf16 with up to 64 packed rows (rows times n_q_heads / n_kv_heads) a request on average: three e5m2 of the
+ *   Weights, bf16 with up to 48 packed rows (rows times n_q_heads / n_kv_heads) a request on average: three e5m2 of the
  *   weight times its position's v_scale, off by at most 2^-11 of itself, or 2^-27 of the row's reference.
  *   bf16 with more, and the shared prefix with more rows in all: a 16-bit float, off by 2^-11 of itself (2^-32 of the
  *   row's reference); a value times its v_scale is a 16-bit float too, off by at most 2^-24 of the largest v_scale within

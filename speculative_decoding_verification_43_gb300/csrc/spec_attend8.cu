@@ -30,15 +30,15 @@ static spec_status attend8_sizes(const spec_attend8_args *a, AttendParams &P) {
 // tensor cores. By the average, because lengths are known on the device alone. Measured with 64 requests of 32 / 8 heads
 // of 128 (us with items of 32, 64 and 256 rows):
 //   packed rows of each request   32            48            64            96             128
-//   up to 2000 positions          69 88 170     104 101 169   112 116 169   155 179 177    200 198 177
-//   up to 8000                    169 202 358   290 239 358   310 277 360   451 469 388    593 529 388
+//   up to 2000 positions          69 89 128     104 101 128   111 114 129   155 175 132    200 195 129
+//   up to 8000                    169 201 279   289 236 283   308 275 284   449 463 302    591 523 305
 //   rows that differ, average     30            34            53            66             93
-//   up to 2000                    86 97 168     87 105 169    114 138 173   132 150 175    171 189 183
-//   up to 8000                    225 243 354   240 267 355   323 357 385   379 389 385    500 510 386
-// Between 32 and 64 the 64 rows win where the requests are alike (a fifth) and lose where they are not (a tenth). fp32
+//   up to 2000                    86 97 127     88 107 128    114 139 127   132 149 130    169 189 151
+//   up to 8000                    226 240 280   238 266 282   324 356 301   378 388 302    500 511 411
+// Between 32 and 48 the 64 rows win where the requests are alike (a fifth) and lose where they are not (a tenth). fp32
 // rows need the room of 64 rows for their further parts.
 static void tensor8_class(bool wide, int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
-    rt_log2 = wide || rows <= 32 * groups ? 5 : rows <= 64 * groups ? 6 : pair8::kRTLog2;
+    rt_log2 = wide || rows <= 32 * groups ? 5 : rows <= 48 * groups ? 6 : pair8::kRTLog2;
     workers = rt_log2 == pair8::kRTLog2 ? kSMs : kSMs * round8::kPerSM;
 }
 

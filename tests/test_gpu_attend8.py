@@ -65,7 +65,7 @@ def test_layouts(name, dtype):
     check8(b, got)
 
 
-@pytest.mark.parametrize("rows,kernel", [([4], "round"), ([16], "round"), ([17], "pair"), ([100], "pair")], ids=str)
+@pytest.mark.parametrize("rows,kernel", [([4], "round"), ([12], "round"), ([13], "pair"), ([100], "pair")], ids=str)
 def test_plan_names_the_kernel(rows, kernel):
     b = Batch8(rows, [200], 8, 2, 64, BF, 16, seed=1).place()
     assert b.attention().plan() == f"spec_attend8_{kernel}_kernel"
