@@ -153,7 +153,7 @@ __device__ __forceinline__ void append_page(const Append8Params &P, int head, in
                                             int lane) {
     using Vec = Piece<E, V>;
     constexpr bool kTwo = KEYS && Task<V, INTER>::kPairs;
-    constexpr int kHold = V == 1 ? 4 : 32 / (kTwo ? 2 * V : V);
+    constexpr int kHold = V == 1 ? 2 : 16 / (kTwo ? 2 * V : V);
     const int per = KEYS && Task<V, INTER>::kPairs ? P.D / V - P.rot / 2 / V : P.D / V;
     const int cols = min(per, kWarp), r_first = lane / cols, r_step = kWarp / cols, x_first = lane - r_first * cols;
     const int rows = r_first < r_step ? n : 0;  // (lanes that are left over have none)
@@ -264,13 +264,14 @@ __device__ __forceinline__ void append_page(const Append8Params &P, int head, in
 // A warp's work is a page's keys or values of one head (a candidate page that is none ends at once), a row's queries, or
 // a request's status. A page's new values stay in registers between the search for the largest and the rounding, so
 // they are read once; pages of one head each, because a scale is one head's, and a warp each, because a round touches a
-// page or two of each request (eight warps a page: prompts 46 us against 38, rounds 9.1 against 8.0).
-// Measured (us a call, back to back): 5 rows of 32 / 8 heads of 128 6.3 (the host's call), 64 requests of 1-8 rows 8.0
+// page or two of each request (a CTA of eight warps a page was slower, for prompts as well).
+// Measured (us a call, back to back): 5 rows of 32 / 8 heads of 128 6.2 (the host's call), 64 requests of 1-8 rows 6.8
 // (7.7 MB; the chain offsets -> candidate -> page -> values -> scale -> stores, launch included), 6 prompts of 500-4000
-// rows, 12 heads of 64, 38 (97 MB, 2.5 TB/s, 0.38 of the copy rate): there the warps wait for their loads (a third of the stalls) and for
-// instructions, as pages and query rows run different code at once; queries alone take 15 of it.
-template <typename E, int V, bool INTER>
-__global__ void __launch_bounds__(kAppend8Threads) spec_append8_kernel(const __grid_constant__ Append8Params P) {
+// rows, 12 heads of 64, 30 (97 MB, 3.3 TB/s, 0.49 of the copy rate): there the warps wait for their loads, so that it
+// counts how many there are (CTAS an SM): 38 us with two (117 registers), 36 with three, 30 with four. Rounds have few, and
+// four's spills cost them more than they bring: 7.9, 6.8, 7.8; 256 requests of 4 fp32 rows 8.5, 8.1, 8.6.
+template <typename E, int V, bool INTER, int CTAS>
+__global__ void __launch_bounds__(kAppend8Threads, CTAS) spec_append8_kernel(const __grid_constant__ Append8Params P) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % kWarp;
@@ -380,10 +381,12 @@ static spec_status launch_append8(Append8Params &P, cudaStream_t stream) {
     P.by_v = FastDiv(P.D / V);
     const int64_t units = static_cast<int64_t>(P.page_units) + P.q_units + P.B;
     const int64_t blocks = (units + kAppend8Warps - 1) / kAppend8Warps;
-    return launch_after(spec_append8_kernel<E, V, INTER>, dim3(static_cast<unsigned>(blocks)), dim3(kAppend8Threads), 0, stream,
-                        P) == cudaSuccess
-               ? SPEC_OK
-               : SPEC_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kAppend8Threads);
+    // four CTAs an SM for prompts: more rows a request than a page has slots
+    const bool prompts = P.T > static_cast<int64_t>(P.B) * P.page_size;
+    const cudaError_t e = prompts ? launch_after(spec_append8_kernel<E, V, INTER, 4>, grid, block, 0, stream, P)
+                                  : launch_after(spec_append8_kernel<E, V, INTER, 3>, grid, block, 0, stream, P);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 template <typename E>

@@ -77,7 +77,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
     // (by the elected lane) S = Q K^T of accumulator w and half u; n positions of the tile are used
     auto score = [&](int w, int u, const Ring &at, int n) {
         const uint64_t k = operand_at(k_op, at.slot * kTile + u * (kHalf * 128)), q = operand_at(q_op, w * kQBytes);
-        const uint32_t shape = mma8_shape(min(n - u * kHalf, kHalf), false, false, false, false);
+        const uint32_t shape = mma8_shape(min(n - u * kHalf, kHalf), false, false, false);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll

@@ -15,7 +15,7 @@
 // the window's items of nine tiles by their ends: some 3 us for the plan, 2 for the first tile's references.
 // What brought it here: hardware barriers between the softmax warps, and keys and values in rings of their own (226 ->
 // 191), heads of the same positions read in step, an edge tile's visible rows as bits (window 74 -> 61).
-// Two softmax warpgroups of 96 registers spilled and were twice as slow; so were three CTAs an SM.
+// Two softmax warpgroups of 96 registers spilled and were twice as slow; three CTAs an SM spilled too.
 //
 // Scales. A thread has one position: its key's scale is one factor of all its scores, and a row's factor (the
 // query's own scale, the softmax's and log2 e) comes from shared memory beside the row's reference. The value's
@@ -122,8 +122,8 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
         if (nrows == 0) return;
         if (nt > 0) {
             const int n16 = (nrows + 15) & ~15;
-            const uint32_t qk_shape = mma8_shape(n16, false, false, false, false),
-                           pv_shape = mma8_shape(n16, false, true, true, true);
+            const uint32_t qk_shape = mma8_shape(n16, false, false, false),
+                           pv_shape = mma8_shape(n16, true, true, true);
             if (!wait_warp(ab, &sh.q_full, q_phase)) return;
             q_phase ^= 1u;
             // step t: tile t's product, and tile t + 1's scores (step -1: the first scores alone). The scores

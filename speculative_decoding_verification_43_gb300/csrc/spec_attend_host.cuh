@@ -19,8 +19,6 @@
 
 namespace spec {
 
-constexpr int kSMs = 152;
-
 // ---------------------------------------------------------------- joining the parts
 
 constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * kWarp;

@@ -7,7 +7,7 @@
 
 namespace spec {
 
-constexpr int kWarp = 32;
+constexpr int kWarp = 32, kSMs = 152;
 
 // ---------------------------------------------------------------- special registers
 

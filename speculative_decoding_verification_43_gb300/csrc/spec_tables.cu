@@ -355,7 +355,7 @@ extern "C" spec_status spec_block_tables(const spec_block_tables_args *a, void *
                    ? SPEC_OK
                    : SPEC_ERR_CUDA;
     cudaError_t e = launch_after(spec_tables_kernel<false>, dim3(1), dim3(kTableThreads), 0, stream, P);
-    if (e == cudaSuccess) e = launch_after(spec_tables_fill_kernel, dim3(2 * 152), dim3(kFillThreads), 0, stream, P);
+    if (e == cudaSuccess) e = launch_after(spec_tables_fill_kernel, dim3(2 * kSMs), dim3(kFillThreads), 0, stream, P);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

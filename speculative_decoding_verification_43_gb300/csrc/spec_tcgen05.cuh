@@ -1,4 +1,4 @@
-// Fifth-generation tensor cores on sm_103a: tensor memory, matrix instructions on bf16 operands with fp32
+// Fifth-generation tensor cores on sm_103a: tensor memory, matrix instructions on operands of 16 and 8 bits with fp32
 // accumulators, and the tensor copies that feed them.
 #pragma once
 
@@ -128,9 +128,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
-// Operands of 8 bits, 32 deep an instruction. e4m3, or e5m2 where said; M = 128 rows, N columns.
-__device__ __forceinline__ uint32_t mma8_shape(int n, bool a_e5m2, bool b_e5m2, bool a_cols, bool b_cols) {
-    return (1u << 4) | (a_e5m2 ? 1u << 7 : 0u) | (b_e5m2 ? 1u << 10 : 0u) | (a_cols ? 1u << 15 : 0u) |
+// Operands of 8 bits, 32 deep an instruction: A e4m3, B the same or e5m2; M = 128 rows, N columns.
+__device__ __forceinline__ uint32_t mma8_shape(int n, bool b_e5m2, bool a_cols, bool b_cols) {
+    return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (a_cols ? 1u << 15 : 0u) |
            (b_cols ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
@@ -138,14 +138,6 @@ __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
-        : "memory");
-}
-// The same with A in tensor memory: lane = row, four values along K per column.
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
 // One arrival on `bar` when every matrix instruction this thread has issued so far is done.
