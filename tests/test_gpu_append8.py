@@ -116,6 +116,20 @@ def test_against_float64(name):
     verify(a, off, rows, kv, page, rot, inter, o.q if Hq else None, before)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "interleaved"])
+@pytest.mark.parametrize("D,rot,pad", [(64, 64, 0), (128, 32, 0), (36, 20, 1), (512, 512, 0)], ids=str)
+def test_more_rows_than_a_page_has_slots(D, rot, pad, inter, dtype):
+    """Every form of the kernel for prompts; their queries in place."""
+    rows, kv = [50, 1, 33], [60, 5, 33]
+    a, off = make(rows, kv, 3, 2, D, dtype, 16, rot, seed=D + inter, pad=pad)
+    before, q0 = saved(a), a["q"].cpu()
+    o = api.kv_append8(**a, rot_dim=rot, interleaved=inter, q_out=a["q"])
+    torch.cuda.synchronize()
+    assert o.q.data_ptr() == a["q"].data_ptr()
+    verify({**a, "q": q0}, off, rows, kv, 16, rot, inter, o.q, before)
+
+
 @pytest.mark.parametrize("page", [1, 2, 5, 8, 24, 128])
 def test_page_sizes(page):
     rows, kv = [9, 1, 130, 3], [70, 128, 200, 3]
