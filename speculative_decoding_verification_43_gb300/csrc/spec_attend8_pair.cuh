@@ -10,11 +10,11 @@
 // converting V is one operation for two values, and exact. 16-bit floats hold weights from 2^15 down to 2^-14 to 11
 // bits, below to 2^-25, so a row's reference m may stay 2^8 behind its maximum.
 //
-// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 455, 0.43 of
+// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 430, 0.46 of
 // the measured rate; 64 requests behind 8192 shared positions 106, of which the shared ones some 50. Two tiles (both
-// accumulators) take 4400 cycles, 2600 of them products (QK by halves: 8 of 49 cycles where whole tiles take 65 for twice
+// accumulators) take some 4200 cycles, 2600 of them products (QK by halves: 8 of 49 cycles where whole tiles take 65 for twice
 // the columns, a price for scores that are there before they are needed: 574 us -> 545). The rest is the issuing warp's
-// hand-overs, which find the weights ready but cost it 250 cycles each; a softmax thread works 2600. An item's queries and
+// hand-overs, which find the weights ready but cost it 250 cycles and more each; a softmax thread works 2600. An item's queries and
 // outputs take 9400 + 7900 cycles (once 21000 + 8500: prompts 545 us). Tried: a second issuing warp, with registers moved
 // between warpgroups for it (470 -> 500), a look at the next weights between product and scores (545 -> 557),
 // conversions without bank conflicts (no difference). Left out one at a time, the exponentials, three quarters of PV,
@@ -116,8 +116,9 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                 __syncwarp();
             }
             ring.step();
-            // Between the waits only one stretch of instructions by the elected lane: what this warp does
-            // beside issuing, the tensor cores wait for.
+            // Between the waits only one stretch of instructions by the elected lane: what this warp does beside issuing, the
+            // tensor cores wait for. So the four stretches of a tile are written out: their operands and barriers are
+            // constants (prompts 452 us -> 430).
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
                 const bool more = t + 1 < nt;  // (only a segment's last tile may be short)
@@ -127,10 +128,12 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
                            : wait_warp(ab, &sh.v_full[values.slot], values.phase)))
                     return;
                 const int halves = n > kHalf ? 2 : 1;
-#pragma unroll 1
-                for (int u = 0; u < halves; ++u) {
-#pragma unroll 1
-                    for (int w = 0; w < accs; ++w) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u >= halves) break;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (w >= accs) break;
                         if (!wait_warp(ab, &sh.p_full[w][u], p_phases >> (2 * u + w) & 1u)) return;
                         p_phases ^= 1u << (2 * u + w);
                         tc_fence_after();
