@@ -65,7 +65,7 @@ typedef struct {
 size_t spec_block_tables_workspace_size(const spec_block_tables_args *args);
 
 /* Enqueues one kernel on `stream`, or two (more than 512 requests, 2048 rows or 65536 entries of block_table).
- * SPEC_ERR_UNSUPPORTED when B * max_blocks or n_pages * page_size exceeds 2^31 - 1. */
+ * SPEC_ERR_UNSUPPORTED when total_rows or B * max_blocks exceeds 2^31 - 2^19, or n_pages * page_size 2^31 - 1. */
 spec_status spec_block_tables(const spec_block_tables_args *args, void *workspace, size_t workspace_bytes,
                               cudaStream_t stream);
 

@@ -39,7 +39,10 @@ constexpr int kTableThreads = 512, kTableWarps = kTableThreads / kWarp;
 // What one block does by itself, its books in shared memory: so many requests, rows, and entries of all tables (how
 // many change is not known here). Larger calls leave entries and rows to a second kernel.
 constexpr int kTableOne = kTableThreads, kTableOneRows = 2048, kTableOneEntries = 1 << 16;
-constexpr int kFillThreads = 256, kRowsAtOnce = 4;
+constexpr int kFillThreads = 256, kRowsAtOnce = 4, kFillBlocks = 2 * kSMs;
+// Rows, entries and requests are gone through in 32-bit steps: one step past the last must not leave them.
+constexpr int kTableMost = INT_MAX - (1 << 19) + 1;
+static_assert(kFillBlocks * kFillThreads * kRowsAtOnce <= 1 << 19 && kTableThreads <= 1 << 19, "a step");
 
 // A request's pages: what it holds, shall hold, takes and gives back.
 struct TableRequest {
@@ -302,7 +305,8 @@ static spec_status table_sizes(const spec_block_tables_args *a) {
     if (a->B < 1 || a->total_rows < 0 || a->page_size < 1 || a->max_blocks < 1 || a->n_pages < 1 || a->n_shared < 0 ||
         a->n_shared > a->max_blocks)
         return SPEC_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(a->B) * a->max_blocks > INT_MAX || static_cast<int64_t>(a->n_pages) * a->page_size > INT_MAX)
+    if (a->total_rows > kTableMost || static_cast<int64_t>(a->B) * a->max_blocks > kTableMost ||
+        static_cast<int64_t>(a->n_pages) * a->page_size > INT_MAX)
         return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
 }
@@ -348,14 +352,14 @@ extern "C" spec_status spec_block_tables(const spec_block_tables_args *a, void *
     P.positions = a->positions;
     P.req_status = a->req_status;
     int32_t *w = static_cast<int32_t *>(workspace);
-    const int n = P.B + 1;
+    const int64_t n = static_cast<int64_t>(P.B) + 1;
     P.books = {w, w + n, w + 2 * n, w + 3 * n, w + 4 * n, w + 5 * n};
     if (one_block(a))
         return launch_after(spec_tables_kernel<true>, dim3(1), dim3(kTableThreads), 0, stream, P) == cudaSuccess
                    ? SPEC_OK
                    : SPEC_ERR_CUDA;
     cudaError_t e = launch_after(spec_tables_kernel<false>, dim3(1), dim3(kTableThreads), 0, stream, P);
-    if (e == cudaSuccess) e = launch_after(spec_tables_fill_kernel, dim3(2 * kSMs), dim3(kFillThreads), 0, stream, P);
+    if (e == cudaSuccess) e = launch_after(spec_tables_fill_kernel, dim3(kFillBlocks), dim3(kFillThreads), 0, stream, P);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

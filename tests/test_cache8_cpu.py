@@ -164,3 +164,27 @@ def test_tables_workspace(lib):
     assert lib.lib.spec_block_tables(ctypes.byref(a), FAKE * 256 + 8, n, None) == -2
     assert lib.lib.spec_block_tables_workspace_size(ctypes.byref(table_args(lib, B=0))) == 0
     assert lib.lib.spec_block_tables_workspace_size(None) == 0 and lib.lib.spec_block_tables(None, None, 0, None) == -1
+
+
+# the most rows, and entries of all tables, that are taken (rows and entries are stepped through in 32 bits)
+TABLES_MOST = (1 << 31) - (1 << 19)
+
+
+@pytest.mark.parametrize("kw", [dict(total_rows=TABLES_MOST + 1), dict(total_rows=(1 << 31) - 1),
+                                dict(total_rows=(1 << 31) - 300000, slot_map=None, positions=None),
+                                dict(B=TABLES_MOST + 1, max_blocks=1, n_shared=1), dict(B=(1 << 31) - 1, max_blocks=1, n_shared=0),
+                                dict(B=1, max_blocks=(1 << 31) - 1), dict(B=1 << 12, max_blocks=(1 << 19) - 127)])
+def test_tables_refuse_steps_beyond_32_bits(lib, kw):
+    a = table_args(lib, **kw)
+    assert lib.lib.spec_block_tables_workspace_size(ctypes.byref(a)) == 0
+    assert lib.lib.spec_block_tables(ctypes.byref(a), FAKE * 256, 1 << 40, None) == -4
+
+
+@pytest.mark.parametrize("kw,B", [(dict(total_rows=TABLES_MOST), 4), (dict(B=TABLES_MOST, max_blocks=1, n_shared=0), TABLES_MOST),
+                                  (dict(B=1 << 12, max_blocks=(1 << 19) - 128), 1 << 12)])
+def test_tables_take_the_largest_sizes(lib, kw, B):
+    """Up to the workspace, which is too small by one byte here, so that nothing is enqueued."""
+    a = table_args(lib, **kw)
+    n = lib.lib.spec_block_tables_workspace_size(ctypes.byref(a))
+    assert n >= 20 * (B + 1)
+    assert lib.lib.spec_block_tables(ctypes.byref(a), FAKE * 256, n - 1, None) == -2
