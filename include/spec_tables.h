@@ -32,9 +32,10 @@ extern "C" {
  * Then row r of the batch, at position p = kv_len[i] - n_i + j of its request i (rows row_off[i] ..
  * row_off[i+1]-1, as for spec_attend), gets positions[r] = p and
  *     slot_map[r] = block_table[i][p / page_size] * page_size + p % page_size,
- * the physical rows that spec_compact takes as cand_kv_rows (for the drafts' rows); padding rows (p < 0) and rows
- * of a request with status bits get -1 in slot_map, padding rows in positions too. Rows of no request are not
- * written.
+ * the physical rows that spec_compact takes as cand_kv_rows (for the drafts' rows). Padding rows (p < 0) get -1 in both,
+ * and so do the rows of a request whose offsets are contradicted (row_off[i] .. row_off[i+1]-1, if 0 <= row_off[i] <=
+ * row_off[i+1] <= T); rows of a request with other status bits get -1 in slot_map. Rows of no request, those beside an
+ * offset outside [0, T] among them, are not written: they keep what the arrays held before.
  *
  * A request with status bits keeps its pages as they are:
  *   SPEC_REQ_BAD_SHAPE   a negative kv_len, n_blocks outside [0, max_blocks]; or offsets that are wrong or

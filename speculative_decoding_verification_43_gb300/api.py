@@ -608,14 +608,16 @@ class TableOutputs:
 
 class BlockTables:
     """A prepared spec_block_tables call for one batch shape: block tables brought to the requests' lengths, and
-    the slots of the rows (see include/spec_tables.h). total_rows 0: tables only."""
+    the slots of the rows (see include/spec_tables.h). total_rows 0: tables only. Rows that belong to no request have
+    slot -1 at first; a later run leaves them as the run before did."""
 
     def __init__(self, B: int, total_rows: int, page_size: int, n_pages: int, device=None):
         self.device = torch.device(device or "cuda")
         i32 = dict(dtype=torch.int32, device=self.device)
         self.B, self.T = B, total_rows
-        self.out = TableOutputs(slot_map=torch.empty(total_rows, **i32), positions=torch.empty(total_rows, **i32),
-                                req_status=torch.empty(B, **i32))
+        # rows that belong to no request are not written
+        self.out = TableOutputs(slot_map=torch.full((total_rows,), -1, **i32),
+                                positions=torch.full((total_rows,), -1, **i32), req_status=torch.empty(B, **i32))
         self.args = SpecBlockTablesArgs()
         a = self.args
         a.B, a.total_rows, a.page_size, a.n_pages = B, total_rows, page_size, n_pages

@@ -126,6 +126,18 @@ __device__ __forceinline__ int table_entry(const TableParams &P, const TableBook
     return P.block_table[static_cast<int64_t>(r) * P.max_blocks + max(K.need[r], P.n_shared) + (z - K.back[r])];
 }
 
+// Whether row r lies between the two offsets of a request that has right ones: where find_request's holder does not
+// have it, such a request is in error, as other offsets contradict its own. Asked only where some request's are wrong.
+static __device__ __noinline__ bool row_in_doubt(const int32_t *row_off, int B, int T, int r) {
+    bool found = false;
+#pragma unroll 4
+    for (int i = 0; i < B; ++i) {
+        const int begin = row_off[i], end = row_off[i + 1];
+        found |= offsets_right(begin, end, T) && r >= begin && r < end;
+    }
+    return found;
+}
+
 // The tables' new entries, the pages given back, and the rows, by threads first, first + step, ..
 template <int AT_ONCE>
 __device__ __forceinline__ void table_fill(const TableParams &P, const TableBooks &K, const int32_t *row_off, int first,
@@ -148,9 +160,9 @@ __device__ __forceinline__ void table_fill(const TableParams &P, const TableBook
                 need = K.need[i];
                 blk = -1;
             }
-            if (!mine) continue;
+            if (!mine && !(K.all[2] && row_in_doubt(row_off, P.B, P.T, r))) continue;
             const int64_t at = static_cast<int64_t>(kv) - (end - begin) + (r - begin);
-            const int p = kv < 0 || at < 0 ? -1 : static_cast<int>(at), b = p < 0 ? 0 : P.by_page(p);
+            const int p = !mine || kv < 0 || at < 0 ? -1 : static_cast<int>(at), b = p < 0 ? 0 : P.by_page(p);
             int slot = -1;
             if (p >= 0 && b < need) {
                 if (b != blk) {

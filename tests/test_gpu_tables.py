@@ -234,3 +234,40 @@ def test_without_outputs():
     torch.cuda.synchronize()
     pool.step([9, 12])
     pool.same()
+
+
+@pytest.mark.parametrize("more", [0, 600], ids=["one block", "two kernels"])
+def test_rows_whose_offsets_are_contradicted_have_no_slot(more):
+    """Requests 1 and 3 have offsets that contradict one another's: their rows get -1, which a reader of slot_map can
+    tell from a slot. Rows of no request keep what was there. `more` requests of a row each behind them."""
+    off = [1, 3, 6, 4, 8, *range(9, 9 + more)]
+    kv = [20, 21, 22, 23] + [5 + i % 30 for i in range(more)]
+    pool = Pool([1, 1, 1, 1] + [0] * more, 8, 20 + 5 * more, width=10).device()
+    T = off[-1] + 2
+    i32 = dict(dtype=torch.int32, device="cuda")
+    t = api.BlockTables(4 + more, T, 8, pool.n_pages).bind(torch.tensor(kv, **i32), *pool.d.values(),
+                                                           row_off=torch.tensor(off, **i32))
+    t.out.slot_map.fill_(-7)
+    t.out.positions.fill_(-7)
+    o = t.run()
+    torch.cuda.synchronize()
+    assert o.req_status.cpu().tolist() == [0, 4, 4, 4] + [0] * more
+    pool.step(kv)
+    pool.same()
+    slots, pos = [-7, 0, 0, -1, -1, -1, -1, -1] + [-7] * (T - 8), [-7, 18, 19, -1, -1, -1, -1, -1] + [-7] * (T - 8)
+    for r in (1, 2):
+        slots[r] = pool.table[0][pos[r] // 8] * 8 + pos[r] % 8
+    for i in range(more):
+        p = pos[8 + i] = kv[4 + i] - 1
+        slots[8 + i] = pool.table[4 + i][p // 8] * 8 + p % 8
+    assert o.slot_map.cpu().tolist() == slots
+    assert o.positions.cpu().tolist() == pos
+
+
+def test_rows_of_no_request_have_no_slot_at_first():
+    pool = Pool([2, 1], 8, 4, width=6).device()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o = api.block_tables(torch.tensor([9, 8], **i32), *pool.d.values(), 8, row_off=torch.tensor([2, 4, 5], **i32), total_rows=8)
+    torch.cuda.synchronize()
+    assert o.slot_map.cpu().tolist()[:2] == [-1, -1] and o.slot_map.cpu().tolist()[5:] == [-1] * 3
+    assert o.positions.cpu().tolist() == [-1, -1, 7, 8, 7, -1, -1, -1]
