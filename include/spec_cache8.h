@@ -64,9 +64,8 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  *   fp32: four e4m3, off by at most 2^-19 of the element, or 2^-25 of the largest.
  *   Weights, bf16 with up to 48 packed rows (rows times n_q_heads / n_kv_heads) a request on average: three e5m2 of the
  *   weight times its position's v_scale, off by at most 2^-11 of itself, or 2^-27 of the row's reference.
- *   bf16 with more, and the shared prefix with more rows in all: a 16-bit float, off by 2^-11 of itself (2^-32 of the
- *   row's reference); a value times its v_scale is a 16-bit float too, off by at most 2^-24 of the largest v_scale within
- *   128 positions, and by 2^-11 of itself where that v_scale is no power of two.
+ *   bf16 with more, and the shared prefix with more rows in all: a 16-bit float of that product, off by 2^-11 of itself, or
+ *   2^-32 of the row's reference; e4m3 is a 16-bit float, so values are exact.
  *   fp32: six e5m2, off by at most 2^-22 of itself, or 2^-38 of the reference; sums leave the tensor cores every
  *   256 positions. (Random batches: off from 64 bits by 7e-7 of the outputs' size; a plain 32-bit form 1.1e-6.)
  * In bf16 a sum of n terms of one sign, all taken by one worker, loses about n 2^-27 of itself by being cut off.

@@ -20,12 +20,12 @@
 // conversions without bank conflicts (no difference). Left out one at a time, the exponentials, three quarters of PV,
 // the queries' lower parts or the conversions change the time by 0 to 4 %: no unit is the limit, their chain is.
 //
-// Scales: a column of S has its key's scale as a factor, the same for a box of at least eight columns. The values'
-// scales are applied where the values are converted, as fractions of the tile's largest (rounded up to a power of
-// two, 2^u): a product of e4m3 and such a fraction is a 16-bit float exactly, or to 11 bits where the scales are no
-// powers of two, or to 2^-25 of 2^u. A tile's weights are 2^(S + u - m), so that what counts is what they contribute,
-// and its part of a row's sum is 2^-u times theirs. The converting warps also set the values of positions that no row
-// sees to 0.
+// Scales: a column of S has its key's scale as a factor, the same for a box of at least eight columns. Its value's scale v
+// goes into the weight, 2^(S + log2 v - m), so that what counts is what a position contributes, and its part of the row's
+// sum is the weight / v. So values are e4m3 as 16-bit floats, exactly, and a row's reference comes from positions
+// that it sees alone. (Scales applied to the values, as fractions of the tile's largest, rounded away a quiet page's values
+// beside a loud page, for rows that did not see that one, too.) The converting warps also set the values of positions that
+// no row sees to 0.
 //
 // Warps: 0-3 and 4-7 the two warpgroups, 8 loads tiles, 9 issues matrix instructions, 10 and 11 convert values
 // (11 keeps the books first: the requests' status).
@@ -53,8 +53,8 @@ struct Shared {
     uint32_t skip[2][2];                // the warpgroup does this half's second product itself
     uint32_t no_number[2][2];           // per slot of values and converting warp: it has found a NaN
     uint32_t tmem;
-    alignas(16) float key_scale[2][kBoxes];  // per slot of values and eight columns
-    float unit[2];                      // per slot of values: log2 of what they are to be taken times
+    // per slot of values and eight columns: scale of the keys, log2 of the values' scale, and its reciprocal
+    alignas(16) float key_scale[2][kBoxes], value_log2[2][kBoxes], value_inv[2][kBoxes];
     float factor[2][kRows];             // of the rows' scores
 };
 
@@ -185,37 +185,25 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
             const float2 *scales = sh.pipe.scale[ring.slot];
             const int group = lane & (kBoxes - 1);
             const bool used = !edge || item_sees(P, s.keys, x0 + 8 * group >> P.box_log2 << P.box_log2, 1 << P.box_log2);
-            const float2 by = used ? scales[8 * group >> P.box_log2] : make_float2(1.0f, 0.0f);
-            // the least power of two that is no less than any of them
-            const float most = redux_max(by.y > 0.0f && by.y < INFINITY ? by.y : 0.0f);
-            const uint32_t bits = __float_as_uint(most);
-            const int unit = most > 0.0f ? static_cast<int>(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0) : 0;
-            const float by_unit = ex2(static_cast<float>(-unit));
+            const float2 by = used ? scales[8 * group >> P.box_log2] : make_float2(1.0f, 1.0f);
             if (which == 0 && lane < kBoxes) {
+                const ValueScale vs = value_scale(by.y);
                 sh.key_scale[values.slot][lane] = by.x;
-                if (lane == 0) sh.unit[values.slot] = static_cast<float>(unit);
+                sh.value_log2[values.slot][lane] = vs.log2;
+                sh.value_inv[values.slot][lane] = vs.inv;
             }
             // 16 values a lane, eight lanes a row: two pieces of eight 16-bit floats in the row's block of columns
             const unsigned char *from = ring_mem + (kStages / 2 + ring.slot) * kTile;
             unsigned char *to = v_mem + values.slot * kValues + (c >> 2) * kBlock;
             const int piece = (c & 3) * 2, first = which * 4 + (lane >> 3);
             uint32_t found = 0u;
-            auto fetch = [&](int r, uint4 &v, float &share) {
-                v = *reinterpret_cast<const uint4 *>(from + r * 128 + ((c ^ (r & 7)) << 4));
-                share = scales[r >> P.box_log2].y * by_unit;
-            };
-            auto put = [&](int r, const uint4 &v, float share) {
-                const __half2 times = __float2half2_rn(share);
-                auto scaled = [&](uint32_t e) -> uint32_t {
-                    const uint32_t h = e4m3_to_half2(e);
-                    const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(h), times);
-                    return reinterpret_cast<const uint32_t &>(y);
-                };
+            auto fetch = [&](int r) { return *reinterpret_cast<const uint4 *>(from + r * 128 + ((c ^ (r & 7)) << 4)); };
+            auto put = [&](int r, const uint4 &v) {
                 unsigned char *row = to + r * 128;
                 *reinterpret_cast<uint4 *>(row + ((piece ^ (r & 7)) << 4)) =
-                    make_uint4(scaled(v.x), scaled(v.x >> 16), scaled(v.y), scaled(v.y >> 16));
+                    make_uint4(e4m3_to_half2(v.x), e4m3_to_half2(v.x >> 16), e4m3_to_half2(v.y), e4m3_to_half2(v.y >> 16));
                 *reinterpret_cast<uint4 *>(row + (((piece + 1) ^ (r & 7)) << 4)) =
-                    make_uint4(scaled(v.z), scaled(v.z >> 16), scaled(v.w), scaled(v.w >> 16));
+                    make_uint4(e4m3_to_half2(v.z), e4m3_to_half2(v.z >> 16), e4m3_to_half2(v.w), e4m3_to_half2(v.w >> 16));
             };
             if (c < P.D / 16) {
                 if (!edge) {
@@ -223,29 +211,23 @@ __device__ __forceinline__ void convert_role(const AttendParams &P, Shared &sh, 
 #pragma unroll 1
                     for (int r = first; r < kKT; r += 64) {
                         uint4 v[8];
-                        float share[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) fetch(r + 8 * i, v[i], share[i]);
+                        for (int i = 0; i < 8; ++i) v[i] = fetch(r + 8 * i);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) put(r + 8 * i, v[i], share[i]);
+                        for (int i = 0; i < 8; ++i) put(r + 8 * i, v[i]);
                     }
                 } else {
 #pragma unroll 1
                     for (int r = first; r < n; r += 32) {
                         uint4 v[4];
-                        float share[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = item_sees(P, s.keys, x0 + r + 8 * i) ? fetch(r + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            v[i] = make_uint4(0u, 0u, 0u, 0u);
-                            share[i] = 0.0f;
-                            if (item_sees(P, s.keys, x0 + r + 8 * i)) fetch(r + 8 * i, v[i], share[i]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            found |= isfinite(share[i]) ? 0u : 1u;
                             found |= __vcmpeq4(v[i].x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v[i].y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                                      __vcmpeq4(v[i].z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v[i].w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                            put(r + 8 * i, v[i], share[i]);
+                            put(r + 8 * i, v[i]);
                         }
                     }
                 }
@@ -409,8 +391,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                 // says counts only if the scores are there, looked at first.
                 if (!wait_two(ab, &sh.s_full[w][0], s_phases & 1u, &sh.v_full[values.slot], values.phase)) return;
                 const unsigned char *v_tile = v_mem + values.slot * kValues;
-                const float *key_scale = sh.key_scale[values.slot];
-                const float unit = sh.unit[values.slot], by_unit = ex2(-unit);
+                const float *key_scale = sh.key_scale[values.slot], *value_log2 = sh.value_log2[values.slot],
+                            *value_inv = sh.value_inv[values.slot];
                 const bool skip = edge && (sh.no_number[values.slot][0] | sh.no_number[values.slot][1]) != 0;
 #pragma unroll 1
                 for (int u = 0; u * kHalf < n; ++u) {
@@ -435,16 +417,18 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         tmem_wait_ld32(z);
                         tmem_wait_ld32(z + 32);
                         // the weights' logarithms under the reference that there is; eight columns share a scale
-                        const float less = unit - (m == -INFINITY ? 0.0f : m);
+                        const float ref = m == -INFINITY ? 0.0f : m;
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int c = 0; c < 8; c += 4) {
                             const float4 k4 = *reinterpret_cast<const float4 *>(key_scale + u * (kHalf / 8) + c);
+                            const float4 v4 = *reinterpret_cast<const float4 *>(value_log2 + u * (kHalf / 8) + c);
                             const float k[4] = {k4.x * factor, k4.y * factor, k4.z * factor, k4.w * factor};
+                            const float less[4] = {v4.x - ref, v4.y - ref, v4.z - ref, v4.w - ref};
 #pragma unroll
                             for (int e = 8 * c; e < 8 * c + 32; e += 2) {
-                                const float kf = k[e / 8 - c];
-                                const float2 y = fma2(make_float2(z[e], z[e + 1]), make_float2(kf, kf), make_float2(less, less));
+                                const float kf = k[e / 8 - c], lf = less[e / 8 - c];
+                                const float2 y = fma2(make_float2(z[e], z[e + 1]), make_float2(kf, kf), make_float2(lf, lf));
                                 z[e] = y.x;
                                 z[e + 1] = y.y;
                             }
@@ -495,15 +479,25 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                         uint32_t pw[32];
 #pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float2 y = make_float2(ex2(z[e]), ex2(z[e + 1]));
-                            sum[e / 2 & 1] = add2(sum[e / 2 & 1], y);
-                            pw[e / 2] = pack_f16(y.x, y.y);
-                            if (e == 30) tmem_st16(s_at, pw);  // over columns that have been read
+                        for (int c = 0; c < 8; c += 4) {
+                            const float4 i4 = *reinterpret_cast<const float4 *>(value_inv + u * (kHalf / 8) + c);
+                            const float inv[4] = {i4.x, i4.y, i4.z, i4.w};
+#pragma unroll
+                            for (int g = c; g < c + 4; ++g) {  // eight columns of one scale
+                                float2 y[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    y[e] = make_float2(ex2(z[8 * g + 2 * e]), ex2(z[8 * g + 2 * e + 1]));
+                                    pw[4 * g + e] = pack_f16(y[e].x, y[e].y);
+                                }
+                                sum[g & 1] = fma2(add2(add2(y[0], y[1]), add2(y[2], y[3])), make_float2(inv[g - c], inv[g - c]),
+                                                  sum[g & 1]);
+                            }
+                            if (c == 0) tmem_st16(s_at, pw);  // over columns that have been read
                         }
                         tmem_st16(s_at + 16, pw + 16);
                         sum[0] = add2(sum[0], sum[1]);
-                        l += (sum[0].x + sum[0].y) * by_unit;
+                        l += sum[0].x + sum[0].y;
                         tmem_wait_st();
                         if (skip) {
                             if (!at_rest()) return;
