@@ -453,8 +453,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared &sh, 
                         if (__any_sync(0xffffffffu, grow)) {
                             if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
                                 if (!at_rest()) return;
-                                const float a = grow && m != -INFINITY ? ex2(kTop - top) : 1.0f;
-                                l *= a;
+                                // (by its root: a sum, divided by scales, may count where 2^(kTop - top) is 0)
+                                const float root = grow && m != -INFINITY ? ex2(0.5f * (kTop - top)) : 1.0f, a = root * root;
+                                l = l * root * root;
 #pragma unroll 1
                                 for (int d = 0; d < P.D; d += 16) {
                                     float o[16];

@@ -31,6 +31,14 @@ struct PartRun {
     __device__ __forceinline__ int64_t row(int x) const { return x == 0 ? base : later + static_cast<int64_t>(x) * pitch; }
 };
 
+// A sum l of a part times w = 2^d, d <= 0. Over a cache in 8 bits a sum is divided by the values' scales and its reference is
+// not, so that l may be 2^75 and count where 2^d itself is 0.
+__device__ __forceinline__ float scaled_sum(float l, float d, float w) {
+    if (d >= -120.0f) return w == 0.0f ? 0.0f : w * l;
+    const float half = ex2(0.5f * d);
+    return half == 0.0f ? 0.0f : l * half * half;
+}
+
 // Joins the parts of one row and writes it; a warp per row. The parts' outputs are asked for together with
 // their maxima, four at a time, and weighed when both are there.
 template <typename E>
@@ -51,7 +59,7 @@ __device__ __forceinline__ void join_row(const AttendParams &P, const PartRun &a
         const float ref = top == -INFINITY ? 0.0f : top;
         // weights of these parts, and of what has been joined so far
         const float w = ex2(ml.x - ref), keep = M == -INFINITY ? 0.0f : ex2(M - ref);
-        L = L * keep + warp_sum(w == 0.0f ? 0.0f : w * ml.y);
+        L = scaled_sum(L, M - ref, keep) + warp_sum(scaled_sum(ml.y, ml.x - ref, w));
         M = top;
 #pragma unroll
         for (int c = 0; c < 2; ++c) o[c] = make_float4(o[c].x * keep, o[c].y * keep, o[c].z * keep, o[c].w * keep);

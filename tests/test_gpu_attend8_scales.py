@@ -1,6 +1,6 @@
-"""GPU: spec_attend8 where the pages' value scales differ as far as they may, 2^-60 .. 2^60, against float64: rows that
-see a quiet page alone beside a loud one of the same tile, loud pages behind the window, positions whose weights are as
-far apart."""
+"""GPU: spec_attend8 where the pages' value scales differ as far as they may, 2^-60 .. 2^30, against float64: rows that
+see a quiet page alone beside a loud one of the same tile, loud pages behind the window, softmax sums whose terms come
+from quiet pages and outputs that come from loud ones, in one worker's tiles and in parts of several workers."""
 import math
 
 import pytest
@@ -21,7 +21,9 @@ class Texts:
     position x's weight, about; vlog[page]: log2 of the values' scale. The first query element is 8 and meets the key's level;
     the others are small, and held whole by two e4m3."""
 
-    def __init__(self, B, rows, n, dtype, level, vlog, G=2, seed=0):
+    def __init__(self, B, rows, n, dtype, level, vlog, G=2, seed=0, adds=None):
+        """adds: at most so many sums on the way of a weight into the row's sum; then keys have the level alone, to two
+        elements' precision."""
         g = torch.Generator(device="cuda").manual_seed(seed)
         rnd = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=F64)  # noqa: E731
         self.B, self.rows, self.n, self.dtype, self.G = B, rows, n, dtype, G
@@ -30,6 +32,12 @@ class Texts:
         key = rnd(pages * PAGE, HKV, D) * 0.125
         key[..., 0] = 0.0
         key[:n, :, 0] = torch.tensor([level(x) for x in range(n)], device="cuda", dtype=F64)[:, None] * math.log(2.0)
+        if adds:
+            at = key[..., 0].clone()
+            key.zero_()
+            key[..., 0] = (at / KSCALE).float().to(E4M3).to(F64) * KSCALE
+            key[..., 1] = 8 * (at - key[..., 0])
+        self.adds = adds
         kq, vq = (key / KSCALE).float().to(E4M3), (rnd(pages * PAGE, HKV, D) * 100).clamp(-448, 448).float().to(E4M3)
         vs = torch.tensor([[2.0 ** vlog(b)] * HKV for b in range(pages)], device="cuda", dtype=F64)
         self.K, self.V = kq.to(F64)[:n] * KSCALE, vq.to(F64)[:n] * vs.repeat_interleave(PAGE, 0)[:n, :, None]
@@ -42,7 +50,7 @@ class Texts:
         self.ks = torch.full((pages, HKV), KSCALE, device="cuda")
         q = rnd(B * rows, HKV * G, D).clamp(-4, 4) * 0.0625
         q = torch.where(q.abs() < 2.0 ** -8, 0.0, q).to(BF)
-        q[..., 0] = 8.0
+        q[..., 0], q[..., 1] = 8.0, 1.0
         self.q = q.to(dtype)
 
     def run(self, window=0):
@@ -58,7 +66,7 @@ class Texts:
         """Bounds. Queries are held whole (fp32: to 2^-19), so a score is off by its additions: at most `ulps` * 2^-22, as
         in attend_ref.check, and a weight and the weights' sum by that each. A weight's logarithm is the sum of score,
         log2 of the scale and reference: three roundings of numbers below 2^8, 2^-17 each. The exponential unit adds 2^-21, the
-        sums over n keys n 2^-24 each. In bf16 a weight is a 16-bit float (2^-11 of itself), and the output is rounded, 2^-8.
+        sums over n keys n 2^-24 each (or `adds`; a score of two products is off by the roundings of four numbers no larger). In bf16 a weight is a 16-bit float (2^-11 of itself), and the output is rounded, 2^-8.
         What the tensor cores add is cut off at 2^-24 of an instruction's largest product, and small weights at 2^-28 of the
         largest: fewer than n / 4 instructions, and n weights, so n 2^-26 of the largest contribution p * 448 * scale."""
         rows, n, scale = self.rows, self.n, D ** -0.5
@@ -74,8 +82,8 @@ class Texts:
             out, mag = (torch.einsum("rhgx,xhd->rhgd", p, v) for v in (self.V, self.V.abs()))
             most = (p * self.loudness.T[None, :, None]).amax(3, keepdim=True)
             ulps = torch.einsum("rhgd,xhd->rhgx", q.abs(), self.K.abs()).masked_fill(~seen, 0).amax(3, keepdim=True) * scale
-            ulps = ulps * D + 4 * z.abs().masked_fill(~seen, 0).amax(3, keepdim=True)
-            weight = 2 * ulps * 2.0 ** -22 + 3 * 2.0 ** -17 + 2.0 ** -20 + nk * 2.0 ** -23
+            ulps = ulps * (4 if self.adds else D) + 4 * z.abs().masked_fill(~seen, 0).amax(3, keepdim=True)
+            weight = 2 * ulps * 2.0 ** -22 + 3 * 2.0 ** -17 + 2.0 ** -20 + (self.adds or nk) * 2.0 ** -23
             tol = mag * weight + nk * 2.0 ** -26 * most + out.abs() * 2.0 ** -24
             if self.dtype == BF:
                 tol = tol + mag * 2.0 ** -11 + out.abs() * 2.0 ** -8
@@ -86,14 +94,14 @@ class Texts:
             assert not bad.any(), (i, int(bad.sum()), bad.nonzero()[:3].tolist(), float((gl - lse).abs().max()))
 
 
-@pytest.mark.parametrize("apart", [26, 40, 120])
+@pytest.mark.parametrize("apart", [26, 40, 90])
 @pytest.mark.parametrize("rows,n,dtype", [(5, 18, BF), (20, 30, BF), (200, 200, BF), (300, 420, BF), (200, 200, F32)], ids=str)
 def test_quiet_page_before_a_loud_one(rows, n, dtype, apart):
     """The rows that see the quiet page alone do not know of the loud one behind it in the same tile."""
-    t = Texts(1, rows, n, dtype, lambda x: 0.25 * (x % 5), lambda b: -apart // 2 if b % 8 == 0 else (apart + 1) // 2)
+    t = Texts(1, rows, n, dtype, lambda x: 0.25 * (x % 5), lambda b: 30 - apart if b % 8 == 0 else 30)
     first = max(0, n - rows)
     if first >= PAGE:  # (nobody sees it alone: the rows of the next page see it with that one)
-        t = Texts(1, rows, n, dtype, lambda x: 0.25 * (x % 5), lambda b: -apart // 2 if b < (n - 100) // PAGE else apart // 2)
+        t = Texts(1, rows, n, dtype, lambda x: 0.25 * (x % 5), lambda b: 30 - apart if b < (n - 100) // PAGE else 30)
     t.check(t.run())
 
 
@@ -105,16 +113,45 @@ def test_loud_page_behind_the_window(rows, dtype, window):
     def level(x):
         return -80.0 if x // PAGE == 14 else 0.5 * (x % 3)
     n = max(rows + 60, 16 * 9 + 30 + window)
-    t = Texts(1, rows, n, dtype, level, lambda b: 50 if b in (9, 14) else 0, seed=1)
+    t = Texts(1, rows, n, dtype, level, lambda b: 30 if b in (9, 14) else -20, seed=1)
     t.check(t.run(window), window)
 
 
 @pytest.mark.parametrize("rows,dtype", KINDS, ids=NAMES)
-@pytest.mark.parametrize("reach", [30, 60])
-def test_what_positions_contribute(rows, dtype, reach):
+@pytest.mark.parametrize("low", [-30, -60])
+def test_what_positions_contribute(rows, dtype, low):
     """Weights as far apart as the scales, the other way round: every position contributes to the output alike."""
     r = torch.Generator().manual_seed(5)
-    vlog = [int(torch.randint(-reach, reach + 1, (1,), generator=r)) for _ in range(40)]
-    vlog[7], vlog[8], vlog[20] = -reach, reach, -reach
+    vlog = [int(torch.randint(low, 31, (1,), generator=r)) for _ in range(40)]
+    vlog[7], vlog[8], vlog[20] = low, 30, low
     t = Texts(20, rows, 640, dtype, lambda x: -float(vlog[x // PAGE]), lambda b: vlog[b], seed=3)
+    t.check(t.run())
+@pytest.mark.parametrize("rows,dtype", KINDS, ids=NAMES)
+@pytest.mark.parametrize("loud", ["first", "last"])
+@pytest.mark.parametrize("level", [-7.0, -18.0, -30.0])
+@pytest.mark.parametrize("many", [True, False], ids=["one worker", "workers"])
+def test_sums_from_quiet_pages(many, level, loud, rows, dtype):
+    """One position of a page at scale 2^30 and all others, 2^level of its weight each, at 2^-60: the output is the
+    first's, the softmax sum is nearly the others'. Many requests on the same positions give a worker several tiles each; one request
+    over 20000 positions falls to many workers."""
+    B, n = (80 if rows == 100 else 300, 1000) if many else (1, 20000)
+    at = 3 if loud == "first" else n - 3
+    page = at // PAGE
+
+    def weight(x):
+        return 0.0 if x == at else -50.0 if x // PAGE == page else level
+    t = Texts(B, rows, n, dtype, weight, lambda b: 30 if b == page else -60, seed=2)
+    t.check(t.run())
+
+
+
+
+@pytest.mark.parametrize("rows,dtype", KINDS, ids=NAMES)
+def test_sums_of_parts_far_below(rows, dtype):
+    """The parts of 400000 positions at 2^-60, beside one at 2^30 that outweighs each of them 2^29 times and more: a part's
+    reference, which its first tile sets, lies 2^126 below that one's, its sum counts. A worker has 1 / 75 of the positions at
+    most (two items, 152 workers or more), and adds 64 or fewer at a time; 512 parts and steps of a tile's own sum beside."""
+    n = 400000
+    t = Texts(1, rows, n, dtype, lambda x: (0.0 if x == 3 else -50.0 if x < PAGE else -36.6 if x // 128 % 2 == 0 else -29.0),
+              lambda b: 30 if b == 0 else -60, seed=4, adds=n // 75 // 64 + 512)
     t.check(t.run())
