@@ -53,8 +53,8 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  *     k_x = k_scale * element, v_x = v_scale * element.
  * attend.dtype is the type of q and out; attend.k_cache and attend.v_cache are the e4m3 arrays. Scales are
  * finite, positive, those of keys within 2^-60 .. 2^60, those of values within 2^-60 .. 2^30 (they need not be powers of
- * two); a page whose scale is not so spoils the rows that see one of its positions, and no others. Elements that are NaN give those rows what the formulas
- * say, and no others.
+ * two); a page whose scale is not so spoils the rows that see one of its positions, and no others. Elements that are NaN
+ * give those rows what the formulas say, and no others.
  *
  * Head sizes above 128, pages that are no multiple of 8 slots, and caches whose heads lie neither side by side in a
  * slot nor a whole number of slots apart: the fp32 units, 32-bit arithmetic throughout (out is rounded once).
@@ -69,8 +69,8 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  *   2^-32 of the row's reference; e4m3 is a 16-bit float, so values are exact.
  *   fp32: six e5m2, off by at most 2^-22 of itself, or 2^-38 of the reference; sums leave the tensor cores every
  *   256 positions. (Random batches: off from 64 bits by 7e-7 of the outputs' size; a plain 32-bit form 1.1e-6.)
- * A position adds less than 2^-43 to a row's sum of weights, relative to it, or is counted: scales may be apart as far as
- * they may be large and small. In bf16 a sum of n terms of one sign, all taken by one worker, loses about n 2^-27 of itself by being cut off.
+ * A position adds less than 2^-32 to a row's sum of weights, relative to it, or is counted, whatever scales within the
+ * range the others have. In bf16 a sum of n terms of one sign, all taken by one worker, loses about n 2^-27 of itself by being cut off.
  * Results do not depend on the order in which CTAs run. */
 typedef struct {
     spec_attend_args attend;

@@ -545,9 +545,10 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                                           fmaxf(scratch.warp[2][tid], scratch.warp[3][tid]));
                     const float old = nref[tid], nw = kTop - v;
                     const bool grow = v != -INFINITY && (old == kNoRef || nw < old);
-                    // a row without weights so far has nothing to rescale
-                    // (its root: a sum, divided by scales, may count where 2^(nw - old) is 0)
-                    scratch.row[tid] = grow && old != kNoRef ? ex2(0.5f * (nw - old)) : 1.0f;
+                    // A row without weights so far has nothing to rescale. Where 2^(nw - old) is 0, sums vanish whose terms are below
+                    // 2^-32 of the new ones' (scales up to 2^90 apart, references up to 2^4 behind their maxima); by the root twice, as in
+                    // the pair kernel, whose references may lag 2^8, windows take 62.3 us instead of 61.1.
+                    scratch.row[tid] = grow && old != kNoRef ? ex2(nw - old) : 1.0f;
                     if (grow) nref[tid] = nw;
                 }
                 bar_sync(1, 128);
@@ -555,8 +556,8 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
 #pragma unroll
                     for (int e = 0; e < RT; e += 2)
                         if ((e & ~15) < nrows) {
-                            l[e / 2].x = l[e / 2].x * scratch.row[e] * scratch.row[e];
-                            l[e / 2].y = l[e / 2].y * scratch.row[e + 1] * scratch.row[e + 1];
+                            l[e / 2].x *= scratch.row[e];
+                            l[e / 2].y *= scratch.row[e + 1];
                         }
 #pragma unroll 1
                     for (int c0 = 0; c0 < (WIDE ? kSets + 1 : 1) * RT; c0 += 16) {  // (and the sums)
@@ -567,7 +568,7 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                         tmem_ld16(o, o_addr + c0);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * scratch.row[r0 + e] * scratch.row[r0 + e]);
+                        for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * scratch.row[r0 + e]);
                         tmem_st16(o_addr + c0, ow);
                     }
                     tmem_wait_st();
