@@ -61,7 +61,7 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  * Otherwise products on the tensor cores, with 32-bit accumulation, which cuts sums off instead of rounding them; q
  * and the weights enter as sums of 8-bit parts. Scores, statistics, the weights' sum and lse are 32-bit.
  *   A query is divided by the power of two that brings its head's largest element between 224 and 448.
- *   bf16: two e4m3, exact for elements above 2^-9 of the largest, off by at most 2^-17 of the largest below.
+ *   bf16: e4m3 and e5m2, exact for elements from 2^-13 of the largest on, off by at most 2^-21 of the largest below.
  *   fp32: four e4m3, off by at most 2^-19 of the element, or 2^-25 of the largest.
  *   Weights, bf16 with up to 48 packed rows (rows times n_q_heads / n_kv_heads) a request on average: three e5m2 of the
  *   weight times its position's v_scale, off by at most 2^-11 of itself, or 2^-27 of the row's reference.

@@ -122,8 +122,10 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
         if (nrows == 0) return;
         if (nt > 0) {
             const int n16 = (nrows + 15) & ~15;
-            const uint32_t qk_shape = mma8_shape(n16, false, false, false),
-                           pv_shape = mma8_shape(n16, true, true, true);
+            // (a bf16 query's second part is e5m2)
+            const uint32_t qk_shapes[2] = {mma8_shape(n16, false, false, false, false),
+                                           mma8_shape(n16, false, !WIDE, false, false)},
+                           pv_shape = mma8_shape(n16, false, true, true, true);
             if (!wait_warp(ab, &sh.q_full, q_phase)) return;
             q_phase ^= 1u;
             // step t: tile t's product, and tile t + 1's scores (step -1: the first scores alone). The scores
@@ -147,7 +149,7 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
                                 for (int i = 0; i < 4; ++i)
                                     if (i < steps)
                                         mma8_ss(s_col + (b * kSets + q / kQ) * RT, operand_at(k, i * 32),
-                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shape, q % kQ < kQ - 1 || i > 0);
+                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shapes[q % kQ], q % kQ < kQ - 1 || i > 0);
                             mma_commit(&sh.s_full[b]);
                             mma_commit(&sh.pipe.k_empty[next.slot]);
                         }

@@ -185,9 +185,11 @@ __device__ __forceinline__ void init_pipe(Pipe<KEYS, VALUES> &pipe, int value_re
 
 // ---------------------------------------------------------------- queries
 // A row of a head is divided by the power of two s that brings its largest element between 224 and 448, and each
-// element becomes hi + lo, hi the nearest e4m3 (four bits) and lo the nearest e4m3 to what that leaves. A bf16
-// element of eight bits is hi + lo exactly while lo's last bit is 2^-9 or more, that is from 2^-2 on (between
-// 1 / 896 and 1 / 1792 of the largest), and off by 2^-10 at most below. Both products go to the same scores, which are then taken times s.
+// element becomes hi + lo, hi the nearest e4m3 (four bits) and lo the nearest e5m2 to what that leaves: of a bf16 element of
+// eight bits at most 8 of its last places, which three bits hold. So hi + lo is the element exactly while hi has its four
+// bits, from 2^-6 on (2^-13 of the largest and more), and off by 2^-14 at most below, where what is left is 2^-10 or less
+// (lo as e4m3, whose least is 2^-9, was off by 2^-10 from 2^-2 on). Both products go to the same scores, which are then
+// taken times s.
 
 constexpr int kLeastQueryLog2 = -100;
 
@@ -213,7 +215,7 @@ __device__ __forceinline__ void split_query(const uint4 &v, float inv, uint2 &hi
         const uint16_t p = to_e4m3(a, b);
         const float2 f = e4m3_to_float2(p);
         h[i] = p;
-        l[i] = to_e4m3(a - f.x, b - f.y);
+        l[i] = to_e5m2(a - f.x, b - f.y);
     }
     hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);

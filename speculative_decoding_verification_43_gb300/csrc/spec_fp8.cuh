@@ -32,6 +32,12 @@ __device__ __forceinline__ uint16_t to_e4m3(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The same to e5m2 (three bits, least 2^-16).
+__device__ __forceinline__ uint16_t to_e5m2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
 // Four weights (16-bit floats' range, below 61440) as sums of three e5m2 each; the words have the first weight in
 // the lowest byte. e5m2 is the upper byte of a 16-bit float, so: the weight is rounded to a 16-bit float (11

@@ -128,9 +128,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
-// Operands of 8 bits, 32 deep an instruction: A e4m3, B the same or e5m2; M = 128 rows, N columns.
-__device__ __forceinline__ uint32_t mma8_shape(int n, bool b_e5m2, bool a_cols, bool b_cols) {
-    return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (a_cols ? 1u << 15 : 0u) |
+// Operands of 8 bits, 32 deep an instruction: e4m3, or e5m2; M = 128 rows, N columns.
+__device__ __forceinline__ uint32_t mma8_shape(int n, bool a_e5m2, bool b_e5m2, bool a_cols, bool b_cols) {
+    return (1u << 4) | (a_e5m2 ? 1u << 7 : 0u) | (b_e5m2 ? 1u << 10 : 0u) | (a_cols ? 1u << 15 : 0u) |
            (b_cols ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {

@@ -19,7 +19,7 @@ NAMES = ["round", "round 64", "pair", "round f32", "many f32"]
 class Texts:
     """B requests of `rows` rows on the same n positions, whose pages lie anywhere in the cache. level[x]: log2 of
     position x's weight, about; vlog[page]: log2 of the values' scale. The first query element is 8 and meets the key's level;
-    the others are small, and held whole by two e4m3."""
+    the others are small, and held whole by two parts."""
 
     def __init__(self, B, rows, n, dtype, level, vlog, G=2, seed=0, adds=None):
         """adds: at most so many sums on the way of a weight into the row's sum; then keys have the level alone, to two
