@@ -608,16 +608,15 @@ class TableOutputs:
 
 class BlockTables:
     """A prepared spec_block_tables call for one batch shape: block tables brought to the requests' lengths, and
-    the slots of the rows (see include/spec_tables.h). total_rows 0: tables only. Rows that belong to no request have
-    slot -1 at first; a later run leaves them as the run before did."""
+    the slots of the rows (see include/spec_tables.h). total_rows 0: tables only. A run does not write the entries of
+    rows that belong to no request: they mean nothing, and say nothing of an error."""
 
     def __init__(self, B: int, total_rows: int, page_size: int, n_pages: int, device=None):
         self.device = torch.device(device or "cuda")
         i32 = dict(dtype=torch.int32, device=self.device)
         self.B, self.T = B, total_rows
-        # rows that belong to no request are not written
-        self.out = TableOutputs(slot_map=torch.full((total_rows,), -1, **i32),
-                                positions=torch.full((total_rows,), -1, **i32), req_status=torch.empty(B, **i32))
+        self.out = TableOutputs(slot_map=torch.empty(total_rows, **i32), positions=torch.empty(total_rows, **i32),
+                                req_status=torch.empty(B, **i32))
         self.args = SpecBlockTablesArgs()
         a = self.args
         a.B, a.total_rows, a.page_size, a.n_pages = B, total_rows, page_size, n_pages
@@ -656,11 +655,14 @@ class BlockTables:
 def block_tables(kv_len, n_blocks, block_table, free_pages, n_free, page_size: int, *, row_off=None, total_rows: int = 0,
                  shared_table=None, stream=None) -> TableOutputs:
     """Brings the block tables to the requests' lengths (see include/spec_tables.h); total_rows rows get their
-    slots. With a stream, workspace and outputs are allocated and written there; who uses the outputs elsewhere
-    waits for it first."""
+    slots; rows that belong to no request have -1. With a stream, workspace and outputs are allocated and written there;
+    who uses the outputs elsewhere waits for it first."""
     with torch.cuda.stream(stream):
         t = BlockTables(kv_len.numel(), total_rows, page_size, free_pages.numel(), device=kv_len.device)
         t.bind(kv_len, n_blocks, block_table, free_pages, n_free, row_off=row_off, shared_table=shared_table)
+        if total_rows:  # (here, where the run's stream is known: a prepared call may run on another than it was made on)
+            t.out.slot_map.fill_(-1)
+            t.out.positions.fill_(-1)
         out = t.run(stream)
     return _hand_over(out, stream)
 

@@ -188,10 +188,3 @@ def test_tables_take_the_largest_sizes(lib, kw, B):
     n = lib.lib.spec_block_tables_workspace_size(ctypes.byref(a))
     assert n >= 20 * (B + 1)
     assert lib.lib.spec_block_tables(ctypes.byref(a), FAKE * 256, n - 1, None) == -2
-
-
-def test_a_row_has_no_slot_until_it_is_given_one(lib):
-    """Rows that belong to no request are not written: a prepared call's arrays begin with -1."""
-    from speculative_decoding_verification_43_gb300 import api
-    out = api.BlockTables(2, 5, 16, 32, device="cpu").out
-    assert out.slot_map.tolist() == [-1] * 5 and out.positions.tolist() == [-1] * 5

@@ -99,3 +99,21 @@ def test_block_tables_on_a_busy_stream():
     torch.cuda.synchronize()
     assert untouched(f)
     assert all(torch.equal(x, y) for x, y in zip([o.slot_map, o.positions, *pool.d.values()], want))
+
+
+def test_tables_made_on_a_busy_stream_and_run_on_another():
+    """Nothing that making a prepared call left on its stream comes after the run."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool = Pool([1, 2], 8, 10, width=6).device()
+    kv, row_off = torch.tensor([20, 25], **i32), torch.tensor([0, 3, 5], **i32)
+    torch.cuda.synchronize()
+    st = busy_stream()
+    with torch.cuda.stream(st):
+        t = api.BlockTables(2, 5, 8, pool.n_pages)
+    t.bind(kv, *pool.d.values(), row_off=row_off)
+    o = t.run()
+    torch.cuda.synchronize()
+    pool.step([20, 25])
+    pool.same()
+    slots, pos = pool.rows([3, 2], [20, 25], [0, 0])
+    assert o.slot_map.cpu().tolist() == slots and o.positions.cpu().tolist() == pos

@@ -264,7 +264,7 @@ def test_rows_whose_offsets_are_contradicted_have_no_slot(more):
     assert o.positions.cpu().tolist() == pos
 
 
-def test_rows_of_no_request_have_no_slot_at_first():
+def test_rows_of_no_request_have_no_slot():
     pool = Pool([2, 1], 8, 4, width=6).device()
     i32 = dict(dtype=torch.int32, device="cuda")
     o = api.block_tables(torch.tensor([9, 8], **i32), *pool.d.values(), 8, row_off=torch.tensor([2, 4, 5], **i32), total_rows=8)
