@@ -29,10 +29,12 @@ extern "C" {
  * need = the least power of two s with a <= 448 s, at least 2^-60. A page that holds no earlier position of the
  * request gets the scale `need`; one that does (the call's first position lies inside it) keeps its own scale if
  * that is larger, else gets `need`, and the earlier positions' elements are brought to it: each becomes the e4m3
- * nearest to element * (old scale / new scale), which is exact (a power of two) down to elements of 2^-6. Slots
- * behind the call's last position mean nothing afterwards (drafts that were refused, for instance). A value that
- * is not finite becomes NaN and leaves the scale alone. (Keys above 448 * 2^60 and values above 448 * 2^30 get scales beyond
- * what spec_attend8 takes.)
+ * nearest to element * (old scale / new scale), which is exact (a power of two) down to elements of 2^-6. A scale does
+ * not shrink again: a row that is refused later (a draft) has raised it for good, and what the page's other positions lose
+ * follows the loudest row appended to it, accepted or not. (Elements of 2^-14 of its largest and more lose nothing.) Slots
+ * behind the call's last position mean nothing afterwards (drafts that were refused, for instance). A value that is not
+ * finite becomes NaN and leaves the scale alone. (Keys above 448 * 2^60 and values above 448 * 2^30 get scales beyond what
+ * spec_attend8 takes.)
  *
  * Rows of one call must not share a page unless they are one request's (a page has one scale: what two requests
  * appending to one page in the same call leave there is not defined). Prefixes are shared in whole pages, or

@@ -262,14 +262,17 @@ __device__ __forceinline__ void append_page(const Append8Params &P, int head, in
 }
 
 // A warp's work is a page's keys or values of one head (a candidate page that is none ends at once), a row's queries, or
-// a request's status. A page's new values stay in registers between the search for the largest and the rounding, so
-// they are read once; pages of one head each, because a scale is one head's, and a warp each, because a round touches a
-// page or two of each request (a CTA of eight warps a page was slower, for prompts as well).
-// Measured (us a call, back to back): 5 rows of 32 / 8 heads of 128 6.2 (the host's call), 64 requests of 1-8 rows 6.8
-// (7.7 MB; the chain offsets -> candidate -> page -> values -> scale -> stores, launch included), 6 prompts of 500-4000
-// rows, 12 heads of 64, 30 (97 MB, 3.3 TB/s, 0.49 of the copy rate): there the warps wait for their loads, so that it
-// counts how many there are (CTAS an SM): 38 us with two (117 registers), 36 with three, 30 with four. Rounds have few, and
-// four's spills cost them more than they bring: 7.9, 6.8, 7.8; 256 requests of 4 fp32 rows 8.5, 8.1, 8.6.
+// a request's status. Between the search for the largest and the rounding 16 values a lane stay in registers: in bf16 the first
+// 4 of a page's 16 rows with heads of 128, 8 of 64 with heads of 64. The other rows are read twice (from L1 or L2 the second
+// time), and keys turned twice, angles included.
+// Pages of one head each, because a scale is one head's, and a warp each, because a round touches a page or two of
+// each request (a CTA of eight warps a page was slower, for prompts as well).
+// Measured (us a call, back to back): 5 rows of 32 / 8 heads of 128 6.3 (the host's call; 4.2 in a graph of calls), 64 requests
+// of 1-8 rows 6.8-7.4 (7.7 MB; the chain offsets -> candidate -> page -> values -> scale -> stores, launch included), 6
+// prompts of 500-4000 rows, 12 heads of 64, 30 (97 MB, 3.3 TB/s, 0.49 of the copy rate): there the warps wait for their
+// loads, the second ones among them, so that it counts how many warps there are (CTAS an SM): 38 us with two (117
+// registers), 36 with three, 30 with four (64). Rounds have few, and four's spills cost them more than they bring: 7.9, 6.8,
+// 7.8; 256 requests of 4 fp32 rows 8.5, 8.1, 8.6.
 template <typename E, int V, bool INTER, int CTAS>
 __global__ void __launch_bounds__(kAppend8Threads, CTAS) spec_append8_kernel(const __grid_constant__ Append8Params P) {
     griddep_launch_dependents();

@@ -35,8 +35,10 @@ static spec_status attend8_sizes(const spec_attend8_args *a, AttendParams &P) {
 //   rows that differ, average     30            34            53            66             93
 //   up to 2000                    86 97 127     88 107 128    114 139 127   132 149 130    169 189 151
 //   up to 8000                    226 240 280   238 266 282   324 356 301   378 388 302    500 511 411
-// Between 32 and 48 the 64 rows win where the requests are alike (a fifth) and lose where they are not (a tenth). fp32
-// rows need the room of 64 rows for their further parts.
+// Between 32 and 48 the 64 rows win where the requests are alike and texts are long (a fifth) and lose where requests differ
+// (a tenth, a fifth on short texts). The rule goes by rows alone: on texts to 2000 positions it gives up 16 % with 64 rows
+// alike and 22 % with 34 that differ. All at one shape; heads of 64, whose products take half and whose weights do not, were
+// not measured. fp32 rows need the room of 64 rows for their further parts.
 static void tensor8_class(bool wide, int64_t rows, int64_t groups, int32_t &rt_log2, int32_t &workers) {
     rt_log2 = wide || rows <= 32 * groups ? 5 : rows <= 48 * groups ? 6 : pair8::kRTLog2;
     workers = rt_log2 == pair8::kRTLog2 ? kSMs : kSMs * round8::kPerSM;

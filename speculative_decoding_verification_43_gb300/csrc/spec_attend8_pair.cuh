@@ -10,7 +10,7 @@
 // converting V is one operation for two values, and exact. 16-bit floats hold weights from 2^15 down to 2^-14 to 11
 // bits, below to 2^-25, so a row's reference m may stay 2^8 behind its maximum.
 //
-// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 430, 0.46 of
+// Measured (us a call): 4 prompts of 1000-2500 rows on up to 6000 positions, 32 / 8 heads of 128 (372 GFLOP) 420-450, 0.45 of
 // the measured rate; 64 requests behind 8192 shared positions 106, of which the shared ones some 50. Two tiles (both
 // accumulators) take some 4200 cycles, 2600 of them products (QK by halves: 8 of 49 cycles where whole tiles take 65 for twice
 // the columns, a price for scores that are there before they are needed: 574 us -> 545). The rest is the issuing warp's
