@@ -72,7 +72,8 @@ spec_status spec_kv_append8(const spec_kv_append8_args *args, cudaStream_t strea
  *   fp32: six e5m2, off by at most 2^-22 of itself, or 2^-38 of the reference; sums leave the tensor cores every
  *   256 positions. (Random batches: off from 64 bits by 7e-7 of the outputs' size; a plain 32-bit form 1.1e-6.)
  * A position adds less than 2^-32 to a row's sum of weights, relative to it, or is counted, whatever scales within the
- * range the others have. In bf16 a sum of n terms of one sign, all taken by one worker, loses about n 2^-27 of itself by being cut off.
+ * range the others have. In bf16 a sum of n terms of one sign, all taken by one worker, loses about n 2^-27 of itself
+ * by being cut off.
  * Results do not depend on the order in which CTAs run. */
 typedef struct {
     spec_attend_args attend;

@@ -609,7 +609,7 @@ class TableOutputs:
 class BlockTables:
     """A prepared spec_block_tables call for one batch shape: block tables brought to the requests' lengths, and
     the slots of the rows (see include/spec_tables.h). total_rows 0: tables only. A run does not write the entries of
-    rows that belong to no request: they mean nothing, and say nothing of an error."""
+    rows that belong to no request: what they hold means nothing."""
 
     def __init__(self, B: int, total_rows: int, page_size: int, n_pages: int, device=None):
         self.device = torch.device(device or "cuda")

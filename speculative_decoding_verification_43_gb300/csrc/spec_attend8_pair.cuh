@@ -2,7 +2,8 @@
 // 16 up to 128): long prompts, and the shared prefix. The work is laid out as in spec_attend_pair.cuh: an item of
 // 256 packed rows in two accumulators of 128 that use the same tiles, a row a thread, one warp issuing the
 // products of both in turn. Per tile of 128 keys and accumulator:
-//   S = Q K^T      Q in two parts, e4m3 and e5m2 (spec_attend8_tiles.cuh), K as it lies in the cache, in two halves of 64 keys
+//   S = Q K^T      Q in two parts, e4m3 and e5m2 (spec_attend8_tiles.cuh), K as it lies in the cache, in two halves of
+//                  64 keys
 //   P = 2^(S - m)  a warpgroup, one row per thread; P (16-bit floats) goes back over S's columns, a half at a time
 //   O += P V       V as 16-bit floats, to which two warps bring each tile once for all 256 rows
 // Taking V as it is would need P in three parts of 8 bits: 12 instructions instead of 8, and five operations a weight
@@ -84,8 +85,8 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared &sh, unsi
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < steps)
-                    mma8_ss(tmem + w * 256 + u * kHalf, operand_at(q, p * kQPart + i * 32), operand_at(k, i * 32), shapes[p],
-                            p + i > 0);
+                    mma8_ss(tmem + w * 256 + u * kHalf, operand_at(q, p * kQPart + i * 32), operand_at(k, i * 32),
+                            shapes[p], p + i > 0);
         mma_commit(&sh.s_full[w][u]);
     };
     // (by the elected lane) O += P V of accumulator w and half u; n positions of the half are used

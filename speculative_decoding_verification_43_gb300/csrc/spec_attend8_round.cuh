@@ -149,7 +149,8 @@ __device__ __forceinline__ void mma_role(const AttendParams &P, Shared<RT, WIDE>
                                 for (int i = 0; i < 4; ++i)
                                     if (i < steps)
                                         mma8_ss(s_col + (b * kSets + q / kQ) * RT, operand_at(k, i * 32),
-                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shapes[q % kQ], q % kQ < kQ - 1 || i > 0);
+                                                operand_at(q_op, q * q_part(RT) + i * 32), qk_shapes[q % kQ],
+                                                q % kQ < kQ - 1 || i > 0);
                             mma_commit(&sh.s_full[b]);
                             mma_commit(&sh.pipe.k_empty[next.slot]);
                         }
@@ -547,9 +548,9 @@ __device__ __forceinline__ void softmax_role(const AttendParams &P, Shared<RT, W
                                           fmaxf(scratch.warp[2][tid], scratch.warp[3][tid]));
                     const float old = nref[tid], nw = kTop - v;
                     const bool grow = v != -INFINITY && (old == kNoRef || nw < old);
-                    // A row without weights so far has nothing to rescale. Where 2^(nw - old) is 0, sums vanish whose terms are below
-                    // 2^-32 of the new ones' (scales up to 2^90 apart, references up to 2^4 behind their maxima); by the root twice, as in
-                    // the pair kernel, whose references may lag 2^8, windows take 62.3 us instead of 61.1.
+                    // A row without weights so far has nothing to rescale. Where 2^(nw - old) is 0, sums vanish whose terms
+                    // are below 2^-32 of the new ones' (scales up to 2^90 apart, references up to 2^4 behind their maxima).
+                    // By the root twice, as in the pair kernel, whose references may lag 2^8, windows take 62.3 us for 61.1.
                     scratch.row[tid] = grow && old != kNoRef ? ex2(nw - old) : 1.0f;
                     if (grow) nref[tid] = nw;
                 }

@@ -277,9 +277,9 @@ __device__ __forceinline__ float tile_value(const unsigned char *v_tile, int k, 
 }
 
 // A position's weight for the output has its value's scale in it, w = 2^(z + log2 v - reference), its part of the row's sum is
-// w / v, and 0 where w is, below 2^-126. With scales up to 2^90 apart such a part is less than 2^-43 of its sum: the largest weight is
-// 2^7 or more, so z + log2 v lies 133 below that one's, log2 v at most 90. (With weights kept 2^40 larger until they are
-// rounded, scales might be 2^120 apart; it cost rounds under a window and fp32 rounds a twentieth.)
+// w / v, and 0 where w is, below 2^-126. With scales up to 2^90 apart such a part is less than 2^-43 of its sum: the largest
+// weight is 2^7 or more, so z + log2 v lies 133 below that one's, log2 v at most 90. (With weights kept 2^40 larger until
+// they are rounded, scales might be 2^120 apart; it cost rounds under a window and fp32 rounds a twentieth.)
 // log2 of a scale and the reciprocal that goes with it: a weight times the scale, and back (exact for powers of two).
 // The reciprocal is finite whatever the scale is: rows that do not see its position add 0 times it to their sums.
 struct ValueScale {

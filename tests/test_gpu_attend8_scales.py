@@ -53,11 +53,12 @@ class Texts:
         q[..., 0], q[..., 1] = 8.0, 1.0
         self.q = q.to(dtype)
 
-    def run(self, window=0):
+    def run(self, window=0, shared=0):
         i32 = dict(dtype=torch.int32, device="cuda")
         B, n = self.B, self.n
         got = api.attend8(self.q, self.kc.view(E4M3), self.vc.view(E4M3), self.ks, self.vs,
-                          torch.arange(B + 1, **i32) * self.rows, torch.full((B,), n, **i32), self.table.repeat(B, 1), window=window)
+                          torch.arange(B + 1, **i32) * self.rows, torch.full((B,), n, **i32), self.table.repeat(B, 1), window=window,
+                          shared_len=shared, shared_table=self.table[:(shared + PAGE - 1) // PAGE].clone() if shared else None)
         torch.cuda.synchronize()
         assert (got.req_status == 0).all()
         return got
@@ -155,3 +156,15 @@ def test_sums_of_parts_far_below(rows, dtype):
     t = Texts(1, rows, n, dtype, lambda x: (0.0 if x == 3 else -50.0 if x < PAGE else -36.6 if x // 128 % 2 == 0 else -29.0),
               lambda b: 30 if b == 0 else -60, seed=4, adds=n // 75 // 64 + 512)
     t.check(t.run())
+
+
+@pytest.mark.parametrize("rows,dtype", KINDS, ids=NAMES)
+@pytest.mark.parametrize("loud", ["prefix", "own"])
+@pytest.mark.parametrize("level", [-7.0, -18.0])
+def test_loud_page_on_one_side_of_the_prefix(level, loud, rows, dtype):
+    """Quiet positions and the loud one in a shared prefix and behind it, whose parts other kernels may leave."""
+    n, shared = 1100, 505
+    at = 40 if loud == "prefix" else 900
+    t = Texts(20, rows, n, dtype, lambda x: 0.0 if x == at else -50.0 if x // PAGE == at // PAGE else level,
+              lambda b: 30 if b == at // PAGE else -60, seed=6)
+    t.check(t.run(shared=shared))
